@@ -20,8 +20,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libshampoo_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "tensor_kernels.hip", "runtime.cpp",
-                                            "roots.cpp", "tensor_runtime.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "tensor_kernels.hip", "layer_gemm.hip",
+                                            "layer_norm.hip", "runtime.cpp", "roots.cpp",
+                                            "tensor_runtime.cpp", "layer_runtime.cpp")]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,483 @@
+// Norms before and after a block, fused with gate, dropout and residual
+// scale, forward and backward; dropout alone. All are bound by HBM: each pass
+// reads every input once and writes every output once, eight elements a lane.
+#include "layer_device.h"
+#include "layer_kernels.h"
+
+namespace shl {
+
+namespace {
+
+// ------------------------------------------------------------------- dropout
+// Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011). Its 128 bits serve eight elements
+// with 16 bits each: the drop probability is a multiple of 2^-16 (the scale
+// uses the rounded one, so expectations stay exact), and the integer
+// multiplications, a quarter of the rate of other instructions, stay below
+// the time of the loads and stores.
+__device__ __forceinline__ void drop_factors(const DropArgs& d, uint64_t row, uint32_t c8, float (&m)[8]) {
+  uint32_t c0 = c8, c1 = static_cast<uint32_t>(row), c2 = static_cast<uint32_t>(row >> 32), c3 = d.offset;
+  uint32_t k0 = d.key0, k1 = d.key1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p0 = static_cast<uint64_t>(c0) * 0xD2511F53u, p1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(p1);
+    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(p0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const uint32_t w[4] = {c0, c1, c2, c3};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[2 * i] = (w[i] & 0xffffu) >= d.threshold ? d.scale : 0.f;
+    m[2 * i + 1] = (w[i] >> 16) >= d.threshold ? d.scale : 0.f;
+  }
+}
+
+// A dropped element is 0 whatever its value (also where it is not finite).
+__device__ __forceinline__ float dropped(float x, float m) { return m != 0.f ? x * m : 0.f; }
+
+// Blocks of bx lanes along a row and 256 / bx rows; kRows rows of a thread are
+// loaded before any is stored.
+constexpr int kRows = 4;
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int bx_log2) {
+  const int bx = 1 << bx_log2, by = 256 >> bx_log2;
+  const int64_t c8 = static_cast<int64_t>(blockIdx.x) * bx + (threadIdx.x & (bx - 1));
+  const int64_t col = c8 * 8;
+  if (col >= a.cols) return;
+  const int n = static_cast<int>(a.cols - col < 8 ? a.cols - col : 8);
+  const int64_t step = static_cast<int64_t>(gridDim.y) * by;
+  for (int64_t row = static_cast<int64_t>(blockIdx.y) * by + (threadIdx.x >> bx_log2); row < a.rows; row += kRows * step) {
+    float v[kRows][8];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (row + k * step < a.rows) load8(a.x, (row + k * step) * a.ldx + col, n, a.f32 != 0, v[k]);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (row + k * step >= a.rows) continue;
+      float m[8];
+      drop_factors(a.drop, static_cast<uint64_t>(row + k * step), static_cast<uint32_t>(c8), m);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = dropped(v[k][i], m[i]);
+      store8(a.y, (row + k * step) * a.ldy + col, n, a.f32 != 0, v[k]);
+    }
+  }
+}
+
+// --------------------------------------------------------------------- norms
+// A workgroup of NT lanes holds a row of up to NT * C * 8 elements in
+// registers, so every sum of the row is taken from them and no input is read
+// twice. Rows go to workgroups in contiguous ranges: a gate's row stays with
+// its workgroup and the backward pass keeps its column sums in registers over
+// the range.
+
+// Sum of x and y over the workgroup, in a fixed order. `turn` alternates two
+// places, so one barrier a sum is enough.
+template <int NT>
+__device__ __forceinline__ void block_sum(float& x, float& y, float (&buf)[2][2][NT / 64 + 1], int& turn) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    x += __shfl_xor(x, o);
+    y += __shfl_xor(y, o);
+  }
+  if (NT == 64) return;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    buf[turn][0][wave] = x;
+    buf[turn][1][wave] = y;
+  }
+  // only LDS is shared here: loads and stores to memory stay in flight
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  x = y = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    x += buf[turn][0][w];
+    y += buf[turn][1][w];
+  }
+  turn ^= 1;
+}
+
+// Row-uniform statistics of v (C chunks of eight a lane): mean (0 for RMS) and
+// 1 / sqrt(mean square + eps). Lanes past the row hold zeros; the centred
+// squares of a layer norm are summed in a second sweep over the registers,
+// which loses no digits to a large mean.
+template <int NT, int C>
+__device__ __forceinline__ void row_stats(const float (&v)[C][8], const int (&n)[C], int kind, int d, float eps, float& mean,
+                                          float& rstd, float (&buf)[2][2][NT / 64 + 1], int& turn) {
+  mean = 0.f;
+  float s = 0.f, q = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[c][i], q += v[c][i] * v[c][i];
+  block_sum<NT>(s, q, buf, turn);
+  if (kind == kNormLayer) {
+    mean = s / d;
+    q = 0.f;
+    float unused = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = i < n[c] ? v[c][i] - mean : 0.f;
+        q += t * t;
+      }
+    block_sum<NT>(q, unused, buf, turn);
+  }
+  rstd = 1.f / sqrtf(q / d + eps);
+}
+
+template <int C, int NT>
+__device__ __forceinline__ void load_vec(const void* p, int64_t off, const int (&n)[C], bool f32, float fill, float (&v)[C][8]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = (c * NT + threadIdx.x) * 8;
+    if (p && n[c] > 0) {
+      load8(p, off + col, n[c], f32, v[c]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = fill;
+    }
+  }
+}
+template <int C, int NT>
+__device__ __forceinline__ void load_row(const void* p, int64_t off, const int (&n)[C], bool f32, float (&v)[C][8]) {
+  load_vec<C, NT>(p, off, n, f32, 0.f, v);
+}
+template <int C, int NT>
+__device__ __forceinline__ void store_row(void* p, int64_t off, const int (&n)[C], bool f32, const float (&v)[C][8]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (n[c] > 0) store8(p, off + (c * NT + threadIdx.x) * 8, n[c], f32, v[c]);
+}
+
+template <bool F32, int NT, int C>
+__global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
+  __shared__ float buf[2][2][NT / 64 + 1];
+  int turn = 0;
+  const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
+  const int64_t first = blockIdx.x * per, last = first + per < a.rows ? first + per : a.rows;
+  int n[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.d - static_cast<int>(c * NT + threadIdx.x) * 8));
+  float wp[C][8], bp[C][8], gate[C][8], wn[C][8], bn[C][8];
+  load_vec<C, NT>(a.w_post, 0, n, F32, 1.f, wp);
+  load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
+  load_vec<C, NT>(a.w_next, 0, n, F32, 1.f, wn);
+  load_vec<C, NT>(a.b_next, 0, n, F32, 0.f, bn);
+  load_vec<C, NT>(nullptr, 0, n, F32, 1.f, gate);
+  int64_t group = -1;
+  float z[C][8], r[C][8];
+  if (first < last) {
+    load_row<C, NT>(a.x, first * a.ldx, n, F32, r);
+    if (a.z) load_row<C, NT>(a.z, first * a.ldz, n, F32, z);
+  }
+  for (int64_t row = first; row < last; ++row) {
+    // the next row's loads pass this row's stores
+    float x2[C][8], z2[C][8];
+    if (row + 1 < last) {
+      load_row<C, NT>(a.x, (row + 1) * a.ldx, n, F32, x2);
+      if (a.z) load_row<C, NT>(a.z, (row + 1) * a.ldz, n, F32, z2);
+    }
+    float mz = 0.f, rz = 1.f, mr = 0.f, rr = 1.f;
+    if (a.z) {
+      if (a.gate && row / a.rows_per_gate != group) {
+        group = row / a.rows_per_gate;
+        load_vec<C, NT>(a.gate, group * a.ld_gate, n, F32, 1.f, gate);
+      }
+      if (a.post_kind != kNormNone) row_stats<NT, C>(z, n, a.post_kind, a.d, a.eps, mz, rz, buf, turn);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = 1.f;
+        if (a.drop.threshold) drop_factors(a.drop, row, c * NT + threadIdx.x, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = (z[c][i] - mz) * rz * wp[c][i] + bp[c][i];
+          r[c][i] = i < n[c] ? a.alpha * r[c][i] + dropped(gate[c][i] * p, m[i]) : 0.f;
+        }
+      }
+      store_row<C, NT>(a.r, row * a.ldr, n, F32, r);
+    }
+    if (a.next_kind != kNormNone) {
+      row_stats<NT, C>(r, n, a.next_kind, a.d, a.eps, mr, rr, buf, turn);
+      float o[C][8];
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[c][i] = (r[c][i] - mr) * rr * wn[c][i] + bn[c][i];
+      store_row<C, NT>(a.n, row * a.ldn, n, F32, o);
+    }
+    if (a.stats && threadIdx.x == 0) {
+      const floatx4 s = {mz, rz, mr, rr};
+      *reinterpret_cast<floatx4*>(a.stats + row * 4) = s;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[c][i] = x2[c][i], z[c][i] = z2[c][i];
+  }
+}
+
+// Backward. With c = dn w', dR = dr + rstd (c - [mean c] - r^ mean(c r^));
+// dx = alpha dR; db = drop(dR); dgate = sum db p; dp = db gate; dz likewise
+// from dp w. The four vectors' sums stay in registers over the workgroup's
+// rows and go to partial[vector][workgroup][d]; norm_sums_kernel joins them in
+// order. A gate row whose tokens all lie in this range is stored at once; one
+// that reaches over an end of the range goes to the partial sums (place 0: it
+// began before the range or fills it, place 1: it goes on after it).
+enum { kSumWNext = 0, kSumBNext = 1, kSumWPost = 2, kSumBPost = 3, kSumGate = 4, kSums = 6 };
+
+template <bool F32, int NT, int C>
+__global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
+  __shared__ float buf[2][2][NT / 64 + 1];
+  int turn = 0;
+  const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
+  const int64_t first = blockIdx.x * per, last = first + per < a.rows ? first + per : a.rows;
+  int n[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.d - static_cast<int>(c * NT + threadIdx.x) * 8));
+  float wp[C][8], bp[C][8], gate[C][8], wn[C][8];
+  load_vec<C, NT>(a.w_post, 0, n, F32, 1.f, wp);
+  load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
+  load_vec<C, NT>(a.w_next, 0, n, F32, 1.f, wn);
+  load_vec<C, NT>(nullptr, 0, n, F32, 1.f, gate);
+  float s_wn[C][8], s_bn[C][8], s_wp[C][8], s_bp[C][8], s_g[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_wn[c][i] = s_bn[c][i] = s_wp[c][i] = s_bp[c][i] = s_g[c][i] = 0.f;
+  const int64_t plane = static_cast<int64_t>(gridDim.x) * a.d;
+  auto put = [&](int what, const float (&v)[C][8]) {
+    store_row<C, NT>(a.partial + what * plane, static_cast<int64_t>(blockIdx.x) * a.d, n, true, v);
+  };
+  int64_t group = -1;
+  auto put_gate = [&]() {
+    const int64_t begin = group * a.rows_per_gate;
+    const int64_t end = begin + a.rows_per_gate < a.rows ? begin + a.rows_per_gate : a.rows;
+    if (begin >= first && end <= last) {
+      store_row<C, NT>(a.dgate, group * a.ld_dgate, n, F32, s_g);
+    } else {
+      put(kSumGate + (begin <= first ? 0 : 1), s_g);
+    }
+  };
+  const float inv_d = 1.f / a.d;
+  for (int64_t row = first; row < last; ++row) {
+    float r[C][8], dn[C][8], dr[C][8], z[C][8];
+    const floatx4 st = *reinterpret_cast<const floatx4*>(a.stats + row * 4);
+    load_row<C, NT>(a.dr, row * a.lddr, n, F32, dr);
+    if (a.next_kind != kNormNone) {
+      load_row<C, NT>(a.r, row * a.ldr, n, F32, r);
+      load_row<C, NT>(a.dn, row * a.lddn, n, F32, dn);
+    }
+    if (a.z) load_row<C, NT>(a.z, row * a.ldz, n, F32, z);
+    if (a.gate && row / a.rows_per_gate != group) {
+      if (a.dgate && group >= 0) {
+        put_gate();
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s_g[c][i] = 0.f;
+      }
+      group = row / a.rows_per_gate;
+      load_vec<C, NT>(a.gate, group * a.ld_gate, n, F32, 1.f, gate);
+    }
+    if (a.next_kind != kNormNone) {
+      const float m = st[2], rs = st[3];
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          r[c][i] = i < n[c] ? (r[c][i] - m) * rs : 0.f;  // r^
+          s_wn[c][i] += dn[c][i] * r[c][i];
+          s_bn[c][i] += dn[c][i];
+          dn[c][i] *= wn[c][i];
+          s1 += dn[c][i];
+          s2 += dn[c][i] * r[c][i];
+        }
+      block_sum<NT>(s1, s2, buf, turn);
+      s1 = a.next_kind == kNormLayer ? s1 * inv_d : 0.f;
+      s2 *= inv_d;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dr[c][i] += rs * (dn[c][i] - s1 - r[c][i] * s2);
+    }
+    if (a.dx) {
+      float o[C][8];
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[c][i] = a.alpha * dr[c][i];
+      store_row<C, NT>(a.dx, row * a.lddx, n, F32, o);
+    }
+    if (a.z) {
+      const bool normed = a.post_kind != kNormNone;
+      const float mz = st[0], rz = st[1];
+      float t1 = 0.f, t2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = 1.f;
+        if (a.drop.threshold) drop_factors(a.drop, row, c * NT + threadIdx.x, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float zh = i < n[c] ? (z[c][i] - mz) * rz : 0.f;
+          const float db = i < n[c] ? dropped(dr[c][i], m[i]) : 0.f;
+          s_g[c][i] += db * (zh * wp[c][i] + bp[c][i]);
+          const float dp = db * gate[c][i];
+          s_wp[c][i] += dp * zh;
+          s_bp[c][i] += dp;
+          z[c][i] = zh;
+          dr[c][i] = dp * wp[c][i];
+          t1 += dr[c][i];
+          t2 += dr[c][i] * zh;
+        }
+      }
+      if (normed) {
+        block_sum<NT>(t1, t2, buf, turn);
+        t1 = a.post_kind == kNormLayer ? t1 * inv_d : 0.f;
+        t2 *= inv_d;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dr[c][i] = rz * (dr[c][i] - t1 - z[c][i] * t2);
+      }
+      if (a.dz) store_row<C, NT>(a.dz, row * a.lddz, n, F32, dr);
+    }
+  }
+  if (a.dw_next) put(kSumWNext, s_wn);
+  if (a.db_next) put(kSumBNext, s_bn);
+  if (a.dw_post) put(kSumWPost, s_wp);
+  if (a.db_post) put(kSumBPost, s_bp);
+  if (a.gate && a.dgate && group >= 0) put_gate();
+}
+
+// Joins the workgroups' column sums: 64 columns a workgroup, its 16 waves take
+// the parts in turn, and the 16 sums are added in order. blockIdx.y: 0..3 the
+// vectors; 3 + k the gate row that reaches over the end of range k - 1, at the
+// first end it reaches over.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int parts) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  const int64_t per = parts ? (a.rows + parts - 1) / parts : 1;
+  const int64_t plane = static_cast<int64_t>(parts) * a.d;
+  void* out;
+  int64_t at = 0;
+  int64_t lo = 0, hi = parts, begin = 0;
+  const bool is_gate = blockIdx.y >= 4;
+  const float* p;
+  if (!is_gate) {
+    out = blockIdx.y == kSumWNext ? a.dw_next : blockIdx.y == kSumBNext ? a.db_next : blockIdx.y == kSumWPost ? a.dw_post : a.db_post;
+    p = a.partial + blockIdx.y * plane;
+  } else {
+    const int64_t k = blockIdx.y - 3;
+    if (k * per >= a.rows) return;
+    const int64_t group = k * per / a.rows_per_gate;
+    begin = group * a.rows_per_gate;
+    const int64_t end = begin + a.rows_per_gate < a.rows ? begin + a.rows_per_gate : a.rows;
+    lo = begin / per;
+    hi = (end + per - 1) / per;
+    if (begin == k * per || lo != k - 1) return;
+    out = a.dgate;
+    at = group * a.ld_dgate;
+    p = a.partial + kSumGate * plane;
+  }
+  if (!out) return;
+  float s = 0.f;
+  if (col < a.d) {
+    for (int64_t k = lo + wave; k < hi; k += 16) {
+      const float* q = p + k * a.d + col;
+      if (is_gate && begin > k * per) q += plane;
+      s += *q;
+    }
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < a.d) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += sums[w][lane];
+    if (a.f32)
+      static_cast<float*>(out)[at + col] = s;
+    else
+      static_cast<uint16_t*>(out)[at + col] = static_cast<uint16_t>(f32_to_bf16(s));
+  }
+}
+
+// Workgroups of the row kernels: enough to fill the card, few enough that the
+// column sums of the backward pass stay a small part of its traffic.
+int64_t norm_grid(const NormArgs& a, bool backward) {
+  const int64_t most = backward ? 1024 : 2048;
+  const int64_t per = (a.rows + most - 1) / most;
+  return per ? (a.rows + per - 1) / per : 0;
+}
+
+template <bool F32, int NT, int C>
+void launch_norm(const NormArgs& a, bool backward, int64_t grid, hipStream_t s) {
+  if (backward)
+    hipLaunchKernelGGL((norm_backward_kernel<F32, NT, C>), dim3(grid), dim3(NT), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_forward_kernel<F32, NT, C>), dim3(grid), dim3(NT), 0, s, a);
+}
+
+template <bool F32>
+hipError_t dispatch_norm(const NormArgs& a, bool backward, int64_t grid, hipStream_t s) {
+  if (a.d <= 512)
+    launch_norm<F32, 64, 1>(a, backward, grid, s);
+  else if (a.d <= 1024)
+    launch_norm<F32, 128, 1>(a, backward, grid, s);
+  else if (a.d <= 2048)
+    launch_norm<F32, 256, 1>(a, backward, grid, s);
+  else if (a.d <= 4096)
+    launch_norm<F32, 512, 1>(a, backward, grid, s);
+  else if (a.d <= kMaxNormWidth)
+    launch_norm<F32, 512, 2>(a, backward, grid, s);
+  else
+    return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_partial_floats(const NormArgs& a) { return kSums * norm_grid(a, true) * a.d; }
+
+hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  return a.f32 ? dispatch_norm<true>(a, false, norm_grid(a, false), s) : dispatch_norm<false>(a, false, norm_grid(a, false), s);
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
+  const int64_t grid = norm_grid(a, true);
+  if (grid) {
+    const hipError_t e = a.f32 ? dispatch_norm<true>(a, true, grid, s) : dispatch_norm<false>(a, true, grid, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dw_next && !a.db_next && !a.dw_post && !a.db_post && !a.dgate) return hipSuccess;
+  const uint32_t ends = a.dgate && grid > 1 ? static_cast<uint32_t>(grid - 1) : 0;
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((a.d + 63) / 64, 4 + ends), dim3(1024), 0, s, a,
+                     static_cast<int>(grid));
+  return hipGetLastError();
+}
+
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
+  if (a.rows == 0 || a.cols == 0) return hipSuccess;
+  const int64_t c8 = (a.cols + 7) / 8;
+  int log2 = 0;
+  while (log2 < 8 && (1 << log2) < c8) ++log2;
+  const int64_t gx = (c8 + (1 << log2) - 1) >> log2, by = 256 >> log2;
+  int64_t gy = (a.rows + by - 1) / by;
+  const int64_t want = (gy + kRows - 1) / kRows;
+  gy = want < 32768 ? want : 32768;
+  if (gx > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(dropout_kernel, dim3(static_cast<uint32_t>(gx), static_cast<uint32_t>(gy)), dim3(256), 0, s, a, log2);
+  return hipGetLastError();
+}
+
+}  // namespace shl

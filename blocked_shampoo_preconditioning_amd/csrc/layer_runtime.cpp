@@ -1,0 +1,472 @@
+// Host side of include/shampoo_layer.h: argument checks, the workspace's
+// layout and the launches of the feed-forward half of a decoder layer.
+#include "../../include/shampoo_layer.h"
+
+#include <cmath>
+#include <exception>
+
+#include "layer_kernels.h"
+#include "runtime_common.h"
+
+using shp_rt::Carver;
+using shp_rt::fail;
+
+namespace {
+
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // 128 rows of an operand stay within 32-bit byte offsets
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esize, int64_t max_ld) {
+  if (rows == 0 || cols == 0) return SHAMPOO_OK;
+  if (!p) return fail(SHAMPOO_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (ld < cols || ld > max_ld)
+    return fail(SHAMPOO_ERR_INVALID_ARG, std::string(name) + ": leading dimension " + std::to_string(ld) +
+                                             " is not in [" + std::to_string(cols) + ", " + std::to_string(max_ld) + "]");
+  if (!aligned(p, esize)) return fail(SHAMPOO_ERR_MISALIGNED, std::string(name) + " is not aligned to its element size");
+  return SHAMPOO_OK;
+}
+
+int check_dtype(int32_t dtype) {
+  if (dtype != SHAMPOO_F32 && dtype != SHAMPOO_BF16)
+    return fail(SHAMPOO_ERR_UNSUPPORTED, "dtype must be SHAMPOO_F32 or SHAMPOO_BF16");
+  return SHAMPOO_OK;
+}
+
+#define RC(expr)                  \
+  do {                            \
+    if (int rc_ = (expr)) return rc_; \
+  } while (0)
+
+// No C++ exception crosses the C boundary.
+template <class F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(SHAMPOO_ERR_INVALID_ARG, e.what());
+  } catch (...) {
+    return fail(SHAMPOO_ERR_INVALID_ARG, "unknown C++ exception");
+  }
+}
+
+// ------------------------------------------------- gated feed-forward block
+struct Planes {
+  const uint16_t* p[3] = {};
+  int64_t ld = 0;
+};
+
+// One pass over the block's launches: with run = false only the workspace is
+// laid out.
+struct Ffn {
+  const shampoo_ffn_t& a;
+  char* ws;
+  hipStream_t stream;
+  bool run;
+  Carver carve{};
+  hipError_t err = hipSuccess;
+  int64_t N, d, f, fp, e;
+  bool f32;
+
+  Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
+    N = a.tokens, d = a.d_model, f = a.d_hidden, fp = round8(f);
+    f32 = a.dtype == SHAMPOO_F32;
+    e = f32 ? 4 : 2;
+  }
+  void* take(int64_t bytes) { return ws + carve.take(bytes); }
+  void ok(hipError_t x) {
+    if (err == hipSuccess) err = x;
+  }
+  int64_t act_bytes() const { return shp_rt::align_up(N * fp * e); }
+
+  // A bf16 operand that loads can take where it is; sums_over_cols: its
+  // columns are the product's summation index.
+  bool usable(const void* p, int64_t cols, int64_t ld, bool sums_over_cols) const {
+    return !f32 && aligned(p, 16) && ld % 8 == 0 && (!sums_over_cols || cols % 8 == 0);
+  }
+  Planes operand(const void* p, int64_t rows, int64_t cols, int64_t ld, bool sums_over_cols) {
+    Planes o;
+    if (usable(p, cols, ld, sums_over_cols)) {
+      o.p[0] = static_cast<const uint16_t*>(p);
+      o.ld = ld;
+      return o;
+    }
+    return copied(p, rows, cols, ld);
+  }
+  Planes copied(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    Planes o;
+    o.ld = round8(cols);
+    uint16_t* out = static_cast<uint16_t*>(take((f32 ? 3 : 1) * rows * o.ld * 2));
+    for (int i = 0; i < (f32 ? 3 : 1); ++i) o.p[i] = out + i * rows * o.ld;
+    if (run) {
+      shl::PackArgs k{p, out, rows, cols, ld, o.ld, f32 ? 1 : 0};
+      ok(shl::launch_pack(k, stream));
+    }
+    return o;
+  }
+  // Both weights of the fused products share one leading dimension.
+  void operands(const void* p, const void* q, int64_t rows, int64_t cols, int64_t ldp, int64_t ldq, bool sums_over_cols, Planes& x,
+                Planes& y) {
+    if (usable(p, cols, ldp, sums_over_cols) && usable(q, cols, ldq, sums_over_cols) && ldp != ldq) {
+      x = copied(p, rows, cols, ldp);
+      y = copied(q, rows, cols, ldq);
+    } else if (usable(p, cols, ldp, sums_over_cols) != usable(q, cols, ldq, sums_over_cols)) {
+      x = copied(p, rows, cols, ldp);
+      y = copied(q, rows, cols, ldq);
+    } else {
+      x = operand(p, rows, cols, ldp, sums_over_cols);
+      y = operand(q, rows, cols, ldq, sums_over_cols);
+    }
+  }
+
+  // Adds the term pairs of one product to the segments, smallest first.
+  void segments(shl::GemmArgs& g, const Planes& A, const Planes& B, const Planes* B1 = nullptr) {
+    static const int kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+    for (int i = f32 ? 0 : 5; i < 6; ++i) {
+      g.a[g.nseg] = A.p[kPairs[i][0]];
+      g.b[0][g.nseg] = B.p[kPairs[i][1]];
+      if (B1) g.b[1][g.nseg] = B1->p[kPairs[i][1]];
+      ++g.nseg;
+    }
+    g.lda = A.ld;
+    g.ldb = B.ld;
+  }
+
+  void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
+    const bool gate = epi == shl::kGate;
+    const int64_t steps = shl::gemm_steps(g.K, g.nseg);
+    int tile = 256;
+    g.splits = 1;
+    if (shl::gemm_tiles(g.M, g.N, g.problems, 256, gate) < 192) {
+      tile = 128;
+      const int64_t tiles = shl::gemm_tiles(g.M, g.N, g.problems, 128, gate);
+      if (tiles < 256) {
+        int64_t s = 512 / (tiles > 0 ? tiles : 1);
+        if (s > steps / 4) s = steps / 4;
+        if (s > 32) s = 32;
+        if (s > 1) g.splits = static_cast<int32_t>(s);
+      }
+    }
+    g.e.f32 = f32 ? 1 : 0;
+    g.e.act = a.activation;
+    if (g.splits > 1)
+      g.partial = static_cast<float*>(take(int64_t(4) * g.splits * g.problems * (gate ? 2 : 1) * g.M * g.N));
+    if (run) ok(shl::launch_gemm(g, tile, a_cols, b_cols, epi, stream));
+  }
+
+  void forward() {
+    const Planes x = operand(a.x, N, d, a.ld_x, true);
+    Planes wg, wu;
+    operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
+    char* saved = static_cast<char*>(a.saved);
+    void* h = saved ? saved + 2 * act_bytes() : take(N * fp * e);
+    {
+      shl::GemmArgs g{};
+      segments(g, x, wg, &wu);
+      g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
+      g.k_real = static_cast<int32_t>(d), g.problems = 1;
+      g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
+      if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
+      product(g, false, true, shl::kGate);
+    }
+    const Planes hp = operand(h, N, f32 ? f : fp, fp, true);
+    const Planes wd = operand(a.w_down, f, d, a.ld_down, false);
+    shl::GemmArgs g{};
+    segments(g, hp, wd);
+    g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
+    g.k_real = static_cast<int32_t>(f), g.problems = 1;
+    g.e.c[0] = a.y, g.e.ldc = a.ld_y;
+    product(g, false, true, shl::kStore);
+  }
+
+  void backward() {
+    char* saved = static_cast<char*>(a.saved);
+    const bool want_gate = a.dx || a.dw_gate || a.dw_up;
+    // dy is read by rows for dh and by columns for dWd: one copy serves both
+    const Planes dy = operand(a.dy, N, d, a.ld_dy, true);
+    void *dg = nullptr, *du = nullptr;
+    if (want_gate) {
+      dg = take(N * fp * e);
+      du = take(N * fp * e);
+      const Planes wd = operand(a.w_down, f, d, a.ld_down, true);
+      shl::GemmArgs g{};
+      segments(g, dy, wd);
+      g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
+      g.k_real = static_cast<int32_t>(d), g.problems = 1;
+      g.e.c[0] = dg, g.e.c[1] = du, g.e.ldc = fp, g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
+      g.e.pad_to = static_cast<int32_t>(fp);
+      product(g, false, false, shl::kActBwd);
+    }
+    if (a.dw_down) {
+      const Planes h = operand(saved + 2 * act_bytes(), N, f, fp, false);
+      shl::GemmArgs g{};
+      segments(g, h, dy);
+      g.M = static_cast<int32_t>(f), g.N = static_cast<int32_t>(d), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 1;
+      g.e.c[0] = a.dw_down, g.e.ldc = a.ld_dw_down;
+      product(g, true, true, shl::kStore);
+    }
+    if (!want_gate) return;
+    const Planes pg = operand(dg, N, f32 ? f : fp, fp, true), pu = operand(du, N, f32 ? f : fp, fp, true);
+    if (a.dx) {
+      Planes wg, wu;
+      operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
+      shl::GemmArgs g{};
+      segments(g, pg, wg);
+      segments(g, pu, wu);
+      g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
+      g.k_real = static_cast<int32_t>(f), g.problems = 1;
+      g.e.c[0] = a.dx, g.e.ldc = a.ld_dx;
+      product(g, false, false, shl::kStore);
+    }
+    if (a.dw_gate) {
+      const Planes x = operand(a.x, N, d, a.ld_x, false);
+      shl::GemmArgs g{};
+      segments(g, x, pg, &pu);
+      g.M = static_cast<int32_t>(d), g.N = static_cast<int32_t>(f), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 2;
+      g.e.c[0] = a.dw_gate, g.e.c[1] = a.dw_up, g.e.ldc = a.ld_dw_gate, g.e.ldc1 = a.ld_dw_up;
+      product(g, true, true, shl::kStore);
+    }
+  }
+};
+
+int check_sizes(const shampoo_ffn_t* a) {
+  if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
+  if (a->tokens < 0 || a->d_model < 1 || a->d_hidden < 1 || a->tokens > kMaxDim || a->d_model > kMaxLd || a->d_hidden > kMaxLd)
+    return fail(SHAMPOO_ERR_INVALID_ARG, "tokens must be in [0, 2^31), d_model and d_hidden in [1, 2^22]");
+  RC(check_dtype(a->dtype));
+  if (a->activation < SHAMPOO_ACT_SILU || a->activation > SHAMPOO_ACT_RELU)
+    return fail(SHAMPOO_ERR_UNSUPPORTED, "activation must be one of shampoo_activation_t");
+  return SHAMPOO_OK;
+}
+
+int check_ffn(const shampoo_ffn_t* a, bool backward) {
+  RC(check_sizes(a));
+  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+  RC(check_matrix("x", a->x, a->tokens, a->d_model, a->ld_x, e, kMaxLd));
+  RC(check_matrix("w_gate", a->w_gate, a->d_model, a->d_hidden, a->ld_gate, e, kMaxLd));
+  RC(check_matrix("w_up", a->w_up, a->d_model, a->d_hidden, a->ld_up, e, kMaxLd));
+  RC(check_matrix("w_down", a->w_down, a->d_hidden, a->d_model, a->ld_down, e, kMaxLd));
+  if (a->saved && !aligned(a->saved, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "saved is not aligned to 256 bytes");
+  if (!backward) return check_matrix("y", a->y, a->tokens, a->d_model, a->ld_y, e, kMaxLd);
+  if (!a->saved && a->tokens) return fail(SHAMPOO_ERR_INVALID_ARG, "saved is NULL: the forward pass has to keep g, u and h");
+  RC(check_matrix("dy", a->dy, a->tokens, a->d_model, a->ld_dy, e, kMaxLd));
+  if (!a->dw_gate != !a->dw_up) return fail(SHAMPOO_ERR_INVALID_ARG, "dw_gate and dw_up are computed together: give both or none");
+  if (a->dx) RC(check_matrix("dx", a->dx, a->tokens, a->d_model, a->ld_dx, e, kMaxLd));
+  if (a->dw_gate) {
+    RC(check_matrix("dw_gate", a->dw_gate, a->d_model, a->d_hidden, a->ld_dw_gate, e, kMaxLd));
+    RC(check_matrix("dw_up", a->dw_up, a->d_model, a->d_hidden, a->ld_dw_up, e, kMaxLd));
+  }
+  if (a->dw_down) RC(check_matrix("dw_down", a->dw_down, a->d_hidden, a->d_model, a->ld_dw_down, e, kMaxLd));
+  return SHAMPOO_OK;
+}
+
+int64_t ffn_workspace(const shampoo_ffn_t* a, bool backward) {
+  Ffn p(*a, nullptr, nullptr, false);
+  backward ? p.backward() : p.forward();
+  return p.carve.o;
+}
+
+int run_ffn(const shampoo_ffn_t* a, void* workspace, size_t bytes, void* stream, bool backward) {
+  return guarded([&]() -> int {
+    RC(check_ffn(a, backward));
+    const int64_t need = ffn_workspace(a, backward);
+    if (need > 0 && !workspace) return fail(SHAMPOO_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "workspace is not aligned to 256 bytes");
+    if (bytes < static_cast<size_t>(need))
+      return fail(SHAMPOO_ERR_WORKSPACE_TOO_SMALL,
+                  "workspace has " + std::to_string(bytes) + " bytes, the call needs " + std::to_string(need));
+    Ffn p(*a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream), true);
+    backward ? p.backward() : p.forward();
+    return p.err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(p.err, backward ? "shampoo_ffn_backward" : "shampoo_ffn_forward");
+  });
+}
+
+// --------------------------------------------------------- norms and dropout
+int make_drop(double p, uint64_t seed, uint32_t offset, shl::DropArgs& d) {
+  if (!(p >= 0.0 && p < 1.0)) return fail(SHAMPOO_ERR_INVALID_ARG, "dropout must be in [0, 1)");
+  const double t = std::nearbyint(p * 65536.0);
+  d.threshold = static_cast<uint32_t>(t > 65535.0 ? 65535.0 : t);
+  d.scale = static_cast<float>(65536.0 / (65536.0 - d.threshold));
+  d.key0 = static_cast<uint32_t>(seed);
+  d.key1 = static_cast<uint32_t>(seed >> 32);
+  d.offset = offset;
+  return SHAMPOO_OK;
+}
+
+constexpr int64_t kAnyLd = int64_t(1) << 40;
+
+int check_vector(const char* name, const void* p, int64_t e) {
+  if (p && !aligned(p, e)) return fail(SHAMPOO_ERR_MISALIGNED, std::string(name) + " is not aligned to its element size");
+  return SHAMPOO_OK;
+}
+
+int check_norm(const shampoo_norm_t* a, bool backward) {
+  if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
+  if (a->rows < 0 || a->rows > (int64_t(1) << 40)) return fail(SHAMPOO_ERR_INVALID_ARG, "rows must be in [0, 2^40]");
+  if (a->width < 1) return fail(SHAMPOO_ERR_INVALID_ARG, "width must be at least 1");
+  if (a->width > shl::kMaxNormWidth)
+    return fail(SHAMPOO_ERR_UNSUPPORTED, "width is over " + std::to_string(shl::kMaxNormWidth) + ": a row stays in one workgroup's registers");
+  RC(check_dtype(a->dtype));
+  for (int32_t k : {a->post_kind, a->next_kind})
+    if (k < SHAMPOO_NORM_NONE || k > SHAMPOO_NORM_LAYER)
+      return fail(SHAMPOO_ERR_UNSUPPORTED, "norm kinds must be of shampoo_norm_kind_t");
+  if (!(a->eps > 0.f) || !std::isfinite(a->eps)) return fail(SHAMPOO_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!std::isfinite(a->residual_scale)) return fail(SHAMPOO_ERR_INVALID_ARG, "residual_scale must be finite");
+  if (a->gate && a->rows_per_gate < 1) return fail(SHAMPOO_ERR_INVALID_ARG, "rows_per_gate must be at least 1");
+  if (!a->z && a->next_kind == SHAMPOO_NORM_NONE) return fail(SHAMPOO_ERR_INVALID_ARG, "neither z nor a next norm: nothing to compute");
+  if (a->post_kind == SHAMPOO_NORM_NONE && (a->post_weight || a->post_bias))
+    return fail(SHAMPOO_ERR_INVALID_ARG, "post_weight and post_bias need a post norm");
+  if (a->next_kind == SHAMPOO_NORM_NONE && (a->next_weight || a->next_bias))
+    return fail(SHAMPOO_ERR_INVALID_ARG, "next_weight and next_bias need a next norm");
+  if (!a->z && (a->gate || a->post_weight || a->post_bias))
+    return fail(SHAMPOO_ERR_INVALID_ARG, "gate, post_weight and post_bias need z");
+  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2, n = a->rows, d = a->width;
+  if (a->z) RC(check_matrix("z", a->z, n, d, a->ld_z, e, kAnyLd));
+  if (a->gate) RC(check_matrix("gate", a->gate, n ? (n - 1) / a->rows_per_gate + 1 : 0, d, a->ld_gate, e, kAnyLd));
+  RC(check_vector("post_weight", a->post_weight, e));
+  RC(check_vector("post_bias", a->post_bias, e));
+  RC(check_vector("next_weight", a->next_weight, e));
+  RC(check_vector("next_bias", a->next_bias, e));
+  if (a->stats && !aligned(a->stats, 16)) return fail(SHAMPOO_ERR_MISALIGNED, "stats is not aligned to 16 bytes");
+  if (!backward) {
+    RC(check_matrix("x", a->x, n, d, a->ld_x, e, kAnyLd));
+    if (a->z) RC(check_matrix("r", a->r, n, d, a->ld_r, e, kAnyLd));
+    if (a->next_kind != SHAMPOO_NORM_NONE) RC(check_matrix("n", a->n, n, d, a->ld_n, e, kAnyLd));
+    return SHAMPOO_OK;
+  }
+  if (!a->stats && n) return fail(SHAMPOO_ERR_INVALID_ARG, "stats is NULL: the forward pass has to keep them");
+  if (a->next_kind != SHAMPOO_NORM_NONE) {
+    if (a->z)
+      RC(check_matrix("r", a->r, n, d, a->ld_r, e, kAnyLd));
+    else
+      RC(check_matrix("x", a->x, n, d, a->ld_x, e, kAnyLd));
+    RC(check_matrix("dn", a->dn, n, d, a->ld_dn, e, kAnyLd));
+  } else if (!a->dr && n) {
+    return fail(SHAMPOO_ERR_INVALID_ARG, "dr is NULL and there is no next norm: no gradient comes in");
+  }
+  if (a->dr) RC(check_matrix("dr", a->dr, n, d, a->ld_dr, e, kAnyLd));
+  if (a->dx) RC(check_matrix("dx", a->dx, n, d, a->ld_dx, e, kAnyLd));
+  if (a->dz) {
+    if (!a->z) return fail(SHAMPOO_ERR_INVALID_ARG, "dz needs z");
+    RC(check_matrix("dz", a->dz, n, d, a->ld_dz, e, kAnyLd));
+  }
+  if (a->d_gate) {
+    if (!a->gate) return fail(SHAMPOO_ERR_INVALID_ARG, "d_gate needs gate");
+    RC(check_matrix("d_gate", a->d_gate, n ? (n - 1) / a->rows_per_gate + 1 : 0, d, a->ld_d_gate, e, kAnyLd));
+  }
+  if ((a->d_post_weight || a->d_post_bias) && (!a->z || a->post_kind == SHAMPOO_NORM_NONE))
+    return fail(SHAMPOO_ERR_INVALID_ARG, "d_post_weight and d_post_bias need z and a post norm");
+  if ((a->d_next_weight || a->d_next_bias) && a->next_kind == SHAMPOO_NORM_NONE)
+    return fail(SHAMPOO_ERR_INVALID_ARG, "d_next_weight and d_next_bias need a next norm");
+  RC(check_vector("d_post_weight", a->d_post_weight, e));
+  RC(check_vector("d_post_bias", a->d_post_bias, e));
+  RC(check_vector("d_next_weight", a->d_next_weight, e));
+  RC(check_vector("d_next_bias", a->d_next_bias, e));
+  return SHAMPOO_OK;
+}
+
+int norm_args(const shampoo_norm_t* a, bool backward, shl::NormArgs& k) {
+  k = shl::NormArgs{};
+  k.z = a->z, k.x = a->x, k.ldz = a->ld_z, k.ldx = a->ld_x;
+  k.r = a->r, k.n = a->n, k.ldr = a->ld_r, k.ldn = a->ld_n;
+  if (backward && !a->z) k.r = const_cast<void*>(a->x), k.ldr = a->ld_x;
+  k.w_post = a->post_weight, k.b_post = a->post_bias, k.gate = a->gate, k.w_next = a->next_weight, k.b_next = a->next_bias;
+  k.ld_gate = a->ld_gate, k.stats = a->stats;
+  k.dr = a->dr, k.dn = a->dn, k.lddr = a->ld_dr, k.lddn = a->ld_dn;
+  k.dx = a->dx, k.dz = a->dz, k.lddx = a->ld_dx, k.lddz = a->ld_dz;
+  k.dw_post = a->d_post_weight, k.db_post = a->d_post_bias, k.dgate = a->d_gate, k.dw_next = a->d_next_weight;
+  k.db_next = a->d_next_bias, k.ld_dgate = a->ld_d_gate;
+  k.rows = a->rows, k.rows_per_gate = a->gate ? a->rows_per_gate : 1;
+  k.d = static_cast<int32_t>(a->width), k.f32 = a->dtype == SHAMPOO_F32 ? 1 : 0;
+  k.post_kind = a->post_kind, k.next_kind = a->next_kind;
+  // without z nothing is scaled: the norm's input is x itself
+  k.eps = a->eps, k.alpha = a->z ? a->residual_scale : 1.f;
+  return make_drop(a->dropout, a->seed, a->offset, k.drop);
+}
+
+}  // namespace
+
+extern "C" {
+
+int shampoo_ffn_saved_size(const shampoo_ffn_t* a, size_t* bytes_out) {
+  RC(check_sizes(a));
+  if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
+  const Ffn p(*a, nullptr, nullptr, false);
+  *bytes_out = static_cast<size_t>(3 * p.act_bytes());
+  return SHAMPOO_OK;
+}
+
+int shampoo_ffn_workspace_size(const shampoo_ffn_t* a, int32_t backward, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    RC(check_ffn(a, backward != 0));
+    if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
+    *bytes_out = static_cast<size_t>(ffn_workspace(a, backward != 0));
+    return SHAMPOO_OK;
+  });
+}
+
+int shampoo_ffn_forward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return run_ffn(a, workspace, workspace_bytes, hip_stream, false);
+}
+
+int shampoo_ffn_backward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return run_ffn(a, workspace, workspace_bytes, hip_stream, true);
+}
+
+int shampoo_norm_workspace_size(const shampoo_norm_t* a, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    RC(check_norm(a, true));
+    if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
+    shl::NormArgs k;
+    RC(norm_args(a, true, k));
+    *bytes_out = static_cast<size_t>(4 * shl::norm_partial_floats(k));
+    return SHAMPOO_OK;
+  });
+}
+
+int shampoo_norm_forward(const shampoo_norm_t* a, void* hip_stream) {
+  return guarded([&]() -> int {
+    RC(check_norm(a, false));
+    shl::NormArgs k;
+    RC(norm_args(a, false, k));
+    const hipError_t e = shl::launch_norm_forward(k, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_norm_forward");
+  });
+}
+
+int shampoo_norm_backward(const shampoo_norm_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    RC(check_norm(a, true));
+    shl::NormArgs k;
+    RC(norm_args(a, true, k));
+    const int64_t need = 4 * shl::norm_partial_floats(k);
+    if (need > 0 && !workspace) return fail(SHAMPOO_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "workspace is not aligned to 256 bytes");
+    if (workspace_bytes < static_cast<size_t>(need))
+      return fail(SHAMPOO_ERR_WORKSPACE_TOO_SMALL,
+                  "workspace has " + std::to_string(workspace_bytes) + " bytes, the call needs " + std::to_string(need));
+    k.partial = static_cast<float*>(workspace);
+    const hipError_t e = shl::launch_norm_backward(k, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_norm_backward");
+  });
+}
+
+int shampoo_dropout(const shampoo_dropout_t* a, void* hip_stream) {
+  return guarded([&]() -> int {
+    if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
+    if (a->rows < 0 || a->cols < 0 || a->cols > kMaxDim || a->rows > (int64_t(1) << 40))
+      return fail(SHAMPOO_ERR_INVALID_ARG, "rows must be in [0, 2^40], cols in [0, 2^31)");
+    RC(check_dtype(a->dtype));
+    const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+    RC(check_matrix("x", a->x, a->rows, a->cols, a->ld_x, e, kAnyLd));
+    RC(check_matrix("y", a->y, a->rows, a->cols, a->ld_y, e, kAnyLd));
+    shl::DropoutArgs k{a->x, a->y, a->rows, a->cols, a->ld_x, a->ld_y, a->dtype == SHAMPOO_F32 ? 1 : 0, {}};
+    RC(make_drop(a->dropout, a->seed, a->offset, k.drop));
+    const hipError_t err = shl::launch_dropout(k, static_cast<hipStream_t>(hip_stream));
+    return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, "shampoo_dropout");
+  });
+}
+
+}  // extern "C"
