@@ -10,16 +10,21 @@ typedef __attribute__((ext_vector_type(4))) float floatx4;
 typedef __attribute__((ext_vector_type(4))) uint32_t uint4v;
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t v) { return __uint_as_float(v << 16); }
-// Round to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-  return (u & 0x7fffffffu) > 0x7f800000u ? (u >> 16) | 0x40u : r;
+// Two fp32 values to bf16, to nearest even (the hardware's conversion; NaN
+// stays NaN), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) float f2;
+  typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+  const f2 x = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2));
 }
+__device__ __forceinline__ uint16_t f32_to_bf16(float x) { return static_cast<uint16_t>(pack_bf16(x, 0.f)); }
 
 // Eight consecutive elements of a row, or its last n < 8 (the others 0).
 // Whole groups go as 16-byte accesses whatever their alignment (global memory
-// takes unaligned ones).
+// takes unaligned ones). A row's last group goes element by element in a
+// rolled loop over a shifting register file: these lines are in every kernel
+// many times, and instructions that are fetched cost more than that loop.
 __device__ __forceinline__ void load8(const void* p, int64_t off, int n, bool f32, float (&v)[8]) {
   if (f32) {
     const float* q = static_cast<const float*>(p) + off;
@@ -29,9 +34,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t off, int n, bool f3
       __builtin_memcpy(&b, q + 4, 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? q[i] : 0.f;
+      return;
     }
   } else {
     const uint16_t* q = static_cast<const uint16_t*>(p) + off;
@@ -40,39 +43,97 @@ __device__ __forceinline__ void load8(const void* p, int64_t off, int n, bool f3
       __builtin_memcpy(&w, q, 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[2 * i] = bf16_to_f32(w[i] & 0xffffu), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_to_f32(q[i]) : 0.f;
+      return;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll 1
+  for (int k = n - 1; k >= 0; --k) {
+#pragma unroll
+    for (int i = 7; i > 0; --i) v[i] = v[i - 1];
+    v[0] = f32 ? static_cast<const float*>(p)[off + k] : bf16_to_f32(static_cast<const uint16_t*>(p)[off + k]);
   }
 }
 
 __device__ __forceinline__ void store8(void* p, int64_t off, int n, bool f32, const float (&v)[8]) {
-  if (f32) {
-    float* q = static_cast<float*>(p) + off;
-    if (n == 8) {
+  if (n == 8) {
+    if (f32) {
+      float* q = static_cast<float*>(p) + off;
       floatx4 a, b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = v[i], b[i] = v[4 + i];
       __builtin_memcpy(q, &a, 16);
       __builtin_memcpy(q + 4, &b, 16);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) q[i] = v[i];
-    }
-  } else {
-    uint16_t* q = static_cast<uint16_t*>(p) + off;
-    if (n == 8) {
       uint4v w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(v[2 * i]) | (f32_to_bf16(v[2 * i + 1]) << 16);
-      __builtin_memcpy(q, &w, 16);
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      __builtin_memcpy(static_cast<uint16_t*>(p) + off, &w, 16);
+    }
+    return;
+  }
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v[i];
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    if (f32)
+      static_cast<float*>(p)[off + k] = x[0];
+    else
+      static_cast<uint16_t*>(p)[off + k] = f32_to_bf16(x[0]);
+#pragma unroll
+    for (int i = 0; i < 7; ++i) x[i] = x[i + 1];
+  }
+}
+
+// Eight elements as they lie in memory: held so, a row on its way takes half
+// (bf16) or as many registers as its values.
+template <bool F32>
+struct Raw8 {
+  uint4v w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t off, int n) {
+  Raw8<F32> r;
+  if (n == 8) {
+    if constexpr (F32) {
+      const float* q = static_cast<const float*>(p) + off;
+      __builtin_memcpy(&r.w[0], q, 16);
+      __builtin_memcpy(&r.w[1], q + 4, 16);
+    } else {
+      __builtin_memcpy(&r.w[0], static_cast<const uint16_t*>(p) + off, 16);
+    }
+    return r;
+  }
+  constexpr int W = F32 ? 8 : 4;
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll 1
+  for (int k = n - 1; k >= 0; --k) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 7; i > 0; --i) w[i] = w[i - 1];
+      w[0] = __float_as_uint(static_cast<const float*>(p)[off + k]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) q[i] = static_cast<uint16_t>(f32_to_bf16(v[i]));
+      for (int i = 3; i > 0; --i) w[i] = w[i] << 16 | w[i - 1] >> 16;
+      w[0] = w[0] << 16 | static_cast<const uint16_t*>(p)[off + k];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (F32)
+      v[i] = __uint_as_float(r.w[F32 ? i / 4 : 0][i % 4]);
+    else
+      v[i] = __uint_as_float(i % 2 ? r.w[0][i / 2] & 0xffff0000u : r.w[0][i / 2] << 16);
   }
 }
 

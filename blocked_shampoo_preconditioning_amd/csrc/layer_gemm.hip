@@ -1,4 +1,4 @@
-// The gated feed-forward block's products on the bf16 matrix cores.
+// The gated feed-forward block's products on the 16-bit matrix cores.
 //
 // One tiled product serves the block's six: forward [g u] = x [Wg Wu] and
 // y = h Wd; backward dh = dy Wd^T, dx = dg Wg^T + du Wu^T, [dWg dWu] = x^T [dg
@@ -6,7 +6,9 @@
 // registers (buffer loads with an LDS destination, 16 bytes a lane), double
 // buffered over K steps of 64; fragments leave LDS as 16-byte rows (K
 // contiguous) or through the transposing 8-byte read (K the slow index), so no
-// operand is ever transposed in memory.
+// operand is ever transposed in memory. fp32 operands come as two fp16 planes
+// each (pack_kernel): three products of them in a row, the small ones first,
+// give fp32 accuracy at three bf16 products' cost.
 #include "layer_device.h"
 #include "layer_kernels.h"
 
@@ -16,6 +18,7 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) int int4v;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 halfx8;
 typedef __attribute__((ext_vector_type(4))) short short4v;
 typedef __attribute__((ext_vector_type(16))) float floatx16;
 typedef __attribute__((address_space(3))) char lds_char;
@@ -24,68 +27,110 @@ constexpr int kBK = 64;                 // K step
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ---------------------------------------------------------------- activation
-__device__ __forceinline__ float sigmoidf(float x) { return 1.f / (1.f + __expf(-x)); }
-
-// Value and derivative of the activation at g. The tanh form of GELU is
-// g sigmoid(2 k (g + c g^3)), k = sqrt(2 / pi), c = 0.044715, since
-// (1 + tanh(t)) / 2 = sigmoid(2 t).
-__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
-  if (act == kSilu) {
-    const float s = sigmoidf(g);
-    a = g * s;
-    da = s * (1.f + g * (1.f - s));
-  } else if (act == kGelu) {
-    const float k = 0.7978845608028654f, c = 0.044715f;
-    const float s = sigmoidf(2.f * k * g * (1.f + c * g * g));
-    a = g * s;
-    da = s + a * (1.f - s) * 2.f * k * (1.f + 3.f * c * g * g);
-  } else {
-    a = g > 0.f ? g : (g != g ? g : 0.f);
-    da = g > 0.f ? 1.f : 0.f;
+// Value a and derivative da at g. SiLU is g s(g), s the logistic function; the
+// tanh form of GELU is g s(t), t = 2 k (g + c g^3), k = sqrt(2 / pi), c =
+// 0.044715, since (1 + tanh(x)) / 2 = s(2 x). So both are g s(g (p + q g^2)).
+struct Activation {
+  float p, q;
+  bool relu;
+  __device__ __forceinline__ explicit Activation(int act) {
+    const float k2 = 1.5957691216057308f;
+    p = act == kGelu ? k2 : 1.f;
+    q = act == kGelu ? k2 * 0.044715f : 0.f;
+    relu = act == kRelu;
   }
+  __device__ __forceinline__ void operator()(float g, float& a, float& da) const {
+    const float g2 = fminf(g * g, 1e30f);  // q g^2 stays a number where q = 0
+    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-g * (p + q * g2)));
+    a = g * s;
+    da = s + a * (1.f - s) * (p + 3.f * q * g2);
+    if (relu) {
+      a = g > 0.f ? g : g != g ? g : 0.f;
+      da = g > 0.f ? 1.f : 0.f;
+    }
+  }
+};
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < __builtin_inff() ? a : 0.f;
+}
+
+// Raises a maximum word by a wave's largest finite |value|. The order of the
+// atomics does not change the result; a wave that finds the word as high
+// leaves it (2048 unconditional atomics on one word took 90 us).
+__device__ __forceinline__ void raise_max(uint32_t* word, float m) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  const uint32_t bits = __float_as_uint(m);
+  if ((threadIdx.x & 63) == 0 && bits > __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(word, bits);
+}
+
+// Power of two that an operand's planes are scaled by: its largest finite
+// |value| comes into [2^14, 2^15).
+__device__ __forceinline__ int scale_exp(uint32_t word) {
+  if (word == 0) return 0;
+  const int e = static_cast<int>(word >> 23);
+  return 14 - ((e ? e : 1) - 127);
 }
 
 // The epilogue on columns [col, col + 8) of one row: v (and for kGate also w,
-// the same columns of u). Columns from N to pad_to get zeros.
-template <int EPI>
-__device__ __forceinline__ void finish8(const EpiArgs& e, int problem, int64_t row, int col, int N, float (&v)[8],
-                                        float (&w)[8]) {
+// the same columns of u; for kActBwd g and u as they lie in memory). oc, og: the
+// place in the results and in g and u. Columns from N to pad_to get zeros. Returns the largest finite |value| of a result
+// that a later product reads.
+template <bool F32, int EPI>
+__device__ __forceinline__ float finish8(const EpiArgs& e, const Activation& act, int problem, int64_t oc, int64_t og, int col, int N,
+                                         float (&v)[8], float (&w)[8], const Raw8<F32>& gr, const Raw8<F32>& ur) {
   const int width = e.pad_to > N ? e.pad_to : N;
-  const int n = min(8, width - col);
-  if (n <= 0) return;
+  // all but a kStore's rows are padded to whole groups of eight
+  const int n = EPI == kStore ? min(8, width - col) : col < width ? 8 : 0;
+  float m = 0.f;
+  if (n <= 0) return m;
   if (col + 8 > N) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (col + i >= N) v[i] = 0.f, w[i] = 0.f;
   }
-  const bool f32 = e.f32 != 0;
   if (EPI == kStore) {
-    store8(problem ? e.c[1] : e.c[0], row * (problem ? e.ldc1 : e.ldc) + col, n, f32, v);
+    store8(problem ? e.c[1] : e.c[0], oc, n, F32, v);
   } else if (EPI == kGate) {
     if (e.g) {
-      store8(e.g, row * e.ldg + col, n, f32, v);
-      store8(e.u, row * e.ldg + col, n, f32, w);
+      store8(e.g, og, 8, F32, v);
+      store8(e.u, og, 8, F32, w);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, da;
-      activate(e.act, v[i], a, da);
+      act(v[i], a, da);
       v[i] = a * w[i];
+      if (F32) m = fmaxf(m, finite_abs(v[i]));
     }
-    store8(e.c[0], row * e.ldc + col, n, f32, v);
+    store8(e.c[0], oc, 8, F32, v);
   } else {
     float g[8], u[8];
-    load8(e.g, row * e.ldg + col, n, f32, g);
-    load8(e.u, row * e.ldg + col, n, f32, u);
+    unpack8<F32>(gr, g);
+    unpack8<F32>(ur, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, da;
-      activate(e.act, g[i], a, da);
+      act(g[i], a, da);
       g[i] = v[i] * u[i] * da;
       u[i] = v[i] * a;
+      if (F32) m = fmaxf(m, fmaxf(finite_abs(g[i]), finite_abs(u[i])));
     }
-    store8(e.c[0], row * e.ldc + col, n, f32, g);
-    store8(e.c[1], row * e.ldc + col, n, f32, u);
+    store8(e.c[0], oc, 8, F32, g);
+    store8(e.c[1], oc, 8, F32, u);
+  }
+  return m;
+}
+
+// What kActBwd reads of g and u for eight columns of a row.
+template <bool F32>
+__device__ __forceinline__ void load_gu(const EpiArgs& e, bool row_in, int64_t og, int col, int N, Raw8<F32>& g, Raw8<F32>& u) {
+  const int width = e.pad_to > N ? e.pad_to : N;
+  if (row_in && col < width) {
+    g = load_raw8<F32>(e.g, og, 8);
+    u = load_raw8<F32>(e.u, og, 8);
   }
 }
 
@@ -98,6 +143,8 @@ struct Tile {
   static constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
   static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int PITCH = FN * 32 + 4;  // floats of a row of the epilogue's strips
+  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
 };
 
 // LDS order of 16-byte chunks. A row operand's tile is [rows][64 k] (8 chunks
@@ -111,21 +158,17 @@ __device__ __forceinline__ int swz_col(int k) {
   return WIDTH == 128 ? ((k & 3) << 1) ^ ((k & 3) << 2) : (k & 3) << 1;
 }
 
-// One panel of an operand on its way to LDS: `rows` rows of 128 (or WIDTH * 2)
-// bytes, brought by all waves, 1 KiB an instruction.
-struct Panel {
-  const char* base;   // first byte of the panel at the current K step
-  int64_t left;       // bytes from base to the operand's end
-};
-
+// A buffer of `left` bytes from base (below 2 GiB are enough: a tile's offsets
+// stay under that); loads past it give zeros. Its length is rounded up to a
+// whole word, which the hardware checks.
 __device__ __forceinline__ int4v make_rsrc(const char* base, int64_t left) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   int64_t n = left < 0 ? 0 : (left + 3) & ~int64_t(3);
   n = n > 0x7ffffff0 ? 0x7ffffff0 : n;
   int4v r;
-  r[0] = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
-  r[1] = __builtin_amdgcn_readfirstlane(static_cast<int>(b >> 32) & 0xffff);
-  r[2] = __builtin_amdgcn_readfirstlane(static_cast<int>(n));
+  r[0] = static_cast<int>(b);
+  r[1] = static_cast<int>(b >> 32) & 0xffff;
+  r[2] = static_cast<int>(n);
   r[3] = 0x00020000;
   return r;
 }
@@ -153,16 +196,23 @@ __device__ __forceinline__ bf16x8 lds_read_tr(const char* p, int second) {
   return x.v;
 }
 
-template <class T, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(T::NT, T::NT == 512 ? 2 : 2) void gemm_kernel(GemmArgs g) {
+// The operands' 16 bits are bf16, or fp16 for the planes of fp32 values.
+template <bool F16>
+__device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const floatx16& c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(T::NT, T::FM * T::FN > 8 ? 1 : 2) void gemm_kernel(GemmArgs g) {
   constexpr bool GATE = EPI == kGate;
   constexpr int HN = GATE ? T::BN / 2 : T::BN;       // result columns of a tile
-  constexpr int AP = T::BM / 128;                    // A panels of 128 rows / columns
   constexpr int BW = GATE ? T::BN / 2 : 128;         // width of a B panel
-  constexpr int BP = T::BN / BW;
   static_assert(BW == 128 || BW == 64, "");
   static_assert(!GATE || BCOL, "");
-  __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -172,77 +222,111 @@ __global__ __launch_bounds__(T::NT, T::NT == 512 ? 2 : 2) void gemm_kernel(GemmA
   // work, in groups of four row tiles, so that the tiles in flight on one XCD
   // share their operands in its L2.
   const int tm = (g.M + T::BM - 1) / T::BM, tn = (g.N + HN - 1) / HN;
-  const int64_t total = static_cast<int64_t>(tm) * tn * g.problems * g.splits;
-  const int64_t per = (total + 7) / 8;
-  int64_t id = static_cast<int64_t>(blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (id >= total || static_cast<int64_t>(blockIdx.x / 8) >= per) return;
-  const int split = static_cast<int>(id / (static_cast<int64_t>(tm) * tn * g.problems));
-  id -= static_cast<int64_t>(split) * tm * tn * g.problems;
-  const int problem = static_cast<int>(id / (static_cast<int64_t>(tm) * tn));
-  int t = static_cast<int>(id - static_cast<int64_t>(problem) * tm * tn);
-  const int group = t / (4 * tn);
-  const int in_group = min(4, tm - 4 * group);
-  t -= group * 4 * tn;
-  const int m0 = (4 * group + t % in_group) * T::BM, n0 = (t / in_group) * HN;
+  const uint32_t per = gridDim.x / 8;
+  uint32_t id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  const uint32_t tiles = static_cast<uint32_t>(tm) * tn;
+  if (id >= tiles * g.problems * g.splits) return;
+  int split = 0, problem = 0;
+  if (g.splits > 1) {
+    split = id / (tiles * g.problems);
+    id -= split * (tiles * g.problems);
+  }
+  if (g.problems > 1 && id >= tiles) {
+    problem = 1;
+    id -= tiles;
+  }
+  const uint32_t group = id / (4 * static_cast<uint32_t>(tn));
+  const uint32_t in_group = min(4u, tm - 4 * group);
+  id -= group * 4 * tn;
+  const uint32_t tcol = id / in_group;
+  const int m0 = (4 * group + id - tcol * in_group) * T::BM, n0 = tcol * HN;
 
-  // K steps of this split: segments of ksteps each
-  const int ksteps = (g.K + kBK - 1) / kBK;
-  const int steps = ksteps * g.nseg;
-  const int first = static_cast<int>(static_cast<int64_t>(steps) * split / g.splits);
-  const int last = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / g.splits);
+  // K steps of this split, cut as evenly as they go
+  const int ksteps = (g.K + kBK - 1) / kBK, steps = ksteps * g.nseg;
+  int first = 0, last = steps;
+  if (g.splits > 1) {
+    const int each = steps / g.splits, rest = steps - each * g.splits;
+    first = each * split + min(split, rest);
+    last = first + each + (split < rest ? 1 : 0);
+  }
 
-  // a lane's place in the loads: offsets inside a panel, in bytes
-  constexpr int A_INST = 16;                    // 1 KiB instructions of a 128-panel
-  constexpr int B_INST = BW * kBK * 2 / 1024;
+  // Loads: 1 KiB an instruction, NW instructions at a time. A row operand's
+  // buffer starts at the tile's first row and its offsets move along K; a
+  // column operand's starts at the step's first K row and its offsets stay.
+  constexpr int NA = T::A_BYTES / 1024 / T::NW, NB = T::B_BYTES / 1024 / T::NW;
+  constexpr int BPP = BW * kBK * 2 / 1024 / T::NW;  // instructions of one B panel
   const int64_t lda2 = g.lda * 2, ldb2 = g.ldb * 2;
-  const uint32_t rsw = (lane & 7) ^ swz_row((lane >> 3) + 8 * wave);
-  // rows a wave's instruction j covers: (j * NW + wave) * 8 (row operand) or * (1024 / row bytes)
-  auto row_off = [&](int64_t ld2) { return static_cast<uint32_t>((wave * 8 + (lane >> 3)) * ld2 + rsw * 16); };
-  auto col_off = [&](int64_t ld2, int width) {
-    const int per_row = width / 8, rows = 64 / per_row;
-    const int k = wave * rows + lane / per_row, p = lane % per_row;
-    const int c = p ^ (width == 128 ? swz_col<128>(k) : swz_col<64>(k));
-    return static_cast<uint32_t>(k * ld2 + c * 16);
+  // row operand: row (instruction * NW + wave) * 8 + lane / 8, chunk lane % 8 (swizzled)
+  const int rchunk = (lane & 7) ^ swz_row((lane >> 3) + 8 * wave);
+  auto row_off = [&](int64_t ld2, int j) {
+    return static_cast<uint32_t>(((j * T::NW + wave) * 8 + (lane >> 3)) * ld2 + rchunk * 16);
   };
-  const uint32_t a_off = ACOL ? col_off(lda2, 128) : row_off(lda2);
-  const uint32_t b_off = BCOL ? col_off(ldb2, BW) : row_off(ldb2);
-  const uint32_t a_jump = static_cast<uint32_t>((ACOL ? T::NW * 4 : T::NW * 8) * lda2);
-  const uint32_t b_jump = static_cast<uint32_t>((BCOL ? T::NW * (512 / BW) : T::NW * 8) * ldb2);
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
+  // column operand of panels `width` wide: K row of the panel, chunk (swizzled)
+  auto col_off = [&](int64_t ld2, int width, int j, int panel) {
+    const int per_row = width / 8, rows = 64 / per_row;
+    const int k = (j * T::NW + wave) * rows + lane / per_row;
+    const int c = (lane % per_row) ^ (width == 128 ? swz_col<128>(k) : swz_col<64>(k));
+    return static_cast<uint32_t>(k * ld2 + c * 16 + panel * width * 2);
+  };
+  uint32_t va[NA], vb[NB];
+#pragma unroll
+  for (int j = 0; j < NA; ++j) va[j] = ACOL ? col_off(lda2, 128, j % (16 / T::NW), j / (16 / T::NW)) : row_off(lda2, j);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) vb[j] = BCOL ? col_off(ldb2, BW, j % BPP, GATE ? 0 : j / BPP) : row_off(ldb2, j);
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds)) + wave * 1024;
+  const int64_t a_start = ACOL ? 2 * static_cast<int64_t>(m0) : m0 * lda2;
+  const int64_t b_start = BCOL ? 2 * static_cast<int64_t>(n0) : n0 * ldb2;
+  const int64_t a_size = (ACOL ? (static_cast<int64_t>(g.k_real) - 1) * lda2 + 2 * static_cast<int64_t>(g.M)
+                               : (static_cast<int64_t>(g.M) - 1) * lda2 + 2 * static_cast<int64_t>(g.K)) - a_start;
+  const int64_t b_size = (BCOL ? (static_cast<int64_t>(g.k_real) - 1) * ldb2 + 2 * static_cast<int64_t>(g.N)
+                               : (static_cast<int64_t>(g.N) - 1) * ldb2 + 2 * static_cast<int64_t>(g.K)) - b_start;
 
-  auto issue = [&](int step, int buf) {
-    const int seg = step / ksteps, k0 = (step - seg * ksteps) * kBK;
-    const bool k_ok = k0 + static_cast<int>(rsw) * 8 < g.K;
-    const uint32_t at = lds0 + buf * T::STAGE + wave * 1024;
-#pragma unroll
-    for (int p = 0; p < AP; ++p) {
-      const char* base = reinterpret_cast<const char*>(g.a[seg]);
-      const int64_t size = ACOL ? (static_cast<int64_t>(g.k_real) - 1) * lda2 + 2 * g.M
-                                : (static_cast<int64_t>(g.M) - 1) * lda2 + 2 * g.K;
-      const int64_t o = ACOL ? k0 * lda2 + 2 * (m0 + p * 128) : (m0 + p * 128) * lda2 + 2 * k0;
-      const int4v rs = make_rsrc(base + o, size - o);
-#pragma unroll
-      for (int j = 0; j < A_INST / T::NW; ++j) {
-        uint32_t v = a_off + j * a_jump;
-        if (!ACOL) v = k_ok ? v : kOutOfRange;
-        load_lds(rs, v, at + p * 16384 + j * T::NW * 1024);
-      }
+  // where the loads are: segment, K of the step, the operands' buffers
+  int seg = 0;
+  if (first) seg = first / ksteps;
+  int k0 = (first - seg * ksteps) * kBK;
+  const char *pa, *pb, *pb1;
+  auto enter = [&]() {
+    pa = reinterpret_cast<const char*>(g.a[seg]) + a_start;
+    pb = reinterpret_cast<const char*>(GATE ? g.b[0][seg] : g.b[problem][seg]) + b_start;
+    pb1 = GATE ? reinterpret_cast<const char*>(g.b[1][seg]) + b_start : nullptr;
+  };
+  enter();
+  // One step's loads: the buffers, then NA + NB instructions, then the move to
+  // the next step.
+  int4v ra, rb, rb1;
+  uint32_t ko = 0, at = 0;
+  bool tail = false, in = false;
+  auto aim = [&](int buf, bool more) {
+    at = lds0 + buf * T::STAGE;
+    const int64_t ka = ACOL ? k0 * lda2 : 0, kb = BCOL ? k0 * ldb2 : 0;
+    // past the last step nothing is read: zeros go to a buffer that nobody reads
+    ra = make_rsrc(pa + ka, more ? a_size - ka : 0);
+    rb = make_rsrc(pb + kb, more ? b_size - kb : 0);
+    if (GATE) rb1 = make_rsrc(pb1 + kb, more ? b_size - kb : 0);
+    ko = static_cast<uint32_t>(k0) * 2;
+    tail = (!ACOL || !BCOL) && k0 + kBK > g.K;  // some chunks of a row are past K
+    in = k0 + rchunk * 8 < g.K;
+    k0 += kBK;
+    if (k0 >= g.K && more && ++seg < g.nseg) {
+      k0 = 0;
+      enter();
     }
-#pragma unroll
-    for (int p = 0; p < BP; ++p) {
-      const char* base = reinterpret_cast<const char*>(GATE ? g.b[p][seg] : g.b[problem][seg]);
-      const int64_t size = BCOL ? (static_cast<int64_t>(g.k_real) - 1) * ldb2 + 2 * g.N
-                                : (static_cast<int64_t>(g.N) - 1) * ldb2 + 2 * g.K;
-      const int col = n0 + (GATE ? 0 : p * 128);
-      const int64_t o = BCOL ? k0 * ldb2 + 2 * col : col * ldb2 + 2 * k0;
-      const int4v rs = make_rsrc(base + o, size - o);
-#pragma unroll
-      for (int j = 0; j < B_INST / T::NW; ++j) {
-        uint32_t v = b_off + j * b_jump;
-        if (!BCOL) v = k_ok ? v : kOutOfRange;
-        load_lds(rs, v, at + T::A_BYTES + p * (B_INST * 1024) + j * T::NW * 1024);
-      }
+  };
+  auto load = [&](int q) {
+    const int j = q < NA ? q : q - NA;
+    const bool rows = q < NA ? !ACOL : !BCOL;
+    uint32_t v = q < NA ? va[j] : vb[j];
+    if (rows) {
+      v += ko;
+      if (tail) v = in ? v : kOutOfRange;
     }
+    load_lds(q < NA ? ra : (GATE && j >= BPP ? rb1 : rb), v, at + (q < NA ? 0 : T::A_BYTES) + j * T::NW * 1024);
+  };
+  auto issue = [&](int buf, bool more) {
+    aim(buf, more);
+#pragma unroll
+    for (int q = 0; q < NA + NB; ++q) load(q);
   };
 
   // a lane's place in the fragment reads
@@ -269,7 +353,7 @@ __global__ __launch_bounds__(T::NT, T::NT == 512 ? 2 : 2) void gemm_kernel(GemmA
     const char* bt = st + T::A_BYTES;
     if (GATE) {  // even fragments: gate panel, odd: up panel
       const int col = wn * (T::FN / 2) * 32 + (j >> 1) * 32;
-      return frag_col(bt + (j & 1) * (B_INST * 1024), BW, col, ks);
+      return frag_col(bt + (j & 1) * (BW * kBK * 2), BW, col, ks);
     }
     const int col = wn * T::FN * 32 + j * 32;
     if (BCOL) return frag_col(bt + (col >> 7) * 16384, 128, col & 127, ks);
@@ -284,40 +368,105 @@ __global__ __launch_bounds__(T::NT, T::NT == 512 ? 2 : 2) void gemm_kernel(GemmA
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-  if (first < last) issue(first, 0);
+  // The K loop, software-pipelined: a K step is four slices of 16; each
+  // slice's fragments are read from LDS while the matrix cores work on the one
+  // before, also across the barrier between two steps. At the barrier a wave's
+  // loads of the next step have landed and its reads of this step are done, so
+  // after it the next step can be read and this step's buffer be filled again.
+  bf16x8 a0[T::FM], b0[T::FN], a1[T::FM], b1[T::FN];
+  auto read = [&](const char* st, int ks, bf16x8(&a)[T::FM], bf16x8(&b)[T::FN]) {
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) b[j] = frag_b(st, j, ks);
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) a[i] = frag_a(st, i, ks);
+  };
+  // one slice's products, with the LDS reads before them in the program spread between them
+  constexpr int kReads = (ACOL ? 2 : 1) * T::FM + (BCOL ? 2 : 1) * T::FN, kMma = T::FM * T::FN;
+  auto mma = [&](const bf16x8(&a)[T::FM], const bf16x8(&b)[T::FN]) {
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) acc[i][j] = mfma<F32>(b[j], a[i], acc[i][j]);
+#pragma unroll
+    for (int q = 0; q < kMma; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMma - 1) / kMma, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // the same with a step's loads between them
+  auto mma_load = [&](const bf16x8(&a)[T::FM], const bf16x8(&b)[T::FN]) {
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) {
+        acc[i][j] = mfma<F32>(b[j], a[i], acc[i][j]);
+        constexpr int kEach = (NA + NB + kMma - 1) / kMma;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+          if ((i * T::FN + j) * kEach + e < NA + NB) load((i * T::FN + j) * kEach + e);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (first < last) {
+    issue(0, true);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    issue(1, first + 1 < last);
+    read(lds, 0, a0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   for (int step = first; step < last; ++step) {
     const int buf = (step - first) & 1;
-    // this wave's loads of the step have landed and its reads of the other
-    // buffer are done; after the barrier that holds for all waves
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (step + 1 < last) issue(step + 1, buf ^ 1);
     const char* st = lds + buf * T::STAGE;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      bf16x8 a[T::FM], b[T::FN];
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i) a[i] = frag_a(st, i, ks);
-#pragma unroll
-      for (int j = 0; j < T::FN; ++j) b[j] = frag_b(st, j, ks);
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
-    }
+    aim(buf, step + 2 < last);
+    read(st, 1, a1, b1);
+    mma(a0, b0);
+    read(st, 2, a0, b0);
+    mma(a1, b1);
+    read(st, 3, a1, b1);
+    mma(a0, b0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    read(lds + (buf ^ 1) * T::STAGE, 0, a0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    mma_load(a1, b1);
   }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // Epilogue. A lane's accumulators are column r32 (row m of the result) and
   // rows 8 q + 4 half + 0..3 (result columns n) of each fragment: FN fragments
   // pass through a wave-private LDS strip and come back as eight columns of
   // one row a lane, so that stores are 16 bytes a lane and whole row segments.
-  constexpr int PITCH = T::FN * 32 + 4;
+  // kActBwd reads g and u one fragment row ahead, since a load waits for the
+  // stores before it (fp32: its own row, for want of registers).
+  constexpr int AHEAD = F32 ? 0 : 1;
+  constexpr int PITCH = T::PITCH;
+  constexpr int COLS = GATE ? T::FN * 16 : T::FN * 32;           // result columns of a wave
+  constexpr int LR = COLS / 8, RP = 64 / LR, NP = 32 / RP;       // lanes a row, rows a pass, passes
+  const int row0 = m0 + wm * T::FM * 32 + lane / LR;
+  const int c8 = (lane % LR) * 8, col = n0 + wn * COLS + c8;
+  const int64_t ldc = EPI == kStore && problem ? g.e.ldc1 : g.e.ldc;
+  const int64_t oc = row0 * ldc + col, og = row0 * g.e.ldg + col;
+  const Activation act(g.e.act);
+  Raw8<F32> gr[1 + AHEAD][NP], ur[1 + AHEAD][NP];
+  const bool act_bwd = EPI == kActBwd && g.splits == 1;
+  if (act_bwd && AHEAD) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) load_gu<F32>(g.e, row0 + p * RP < g.M, og + p * RP * g.e.ldg, col, g.N, gr[0][p], ur[0][p]);
+  }
+  // the last loads (zeros) have landed and all reads are done: LDS is free
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   float* strip = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
-  static_assert(T::NW * 32 * PITCH * 4 <= 2 * T::STAGE, "");
-  const EpiArgs& e = g.e;
+  int exponent = 0;
+  if (F32) exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
+  float largest = 0.f;
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
+    if (act_bwd && i + AHEAD < T::FM) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        load_gu<F32>(g.e, row0 + (i + AHEAD) * 32 + p * RP < g.M, og + ((i + AHEAD) * 32 + p * RP) * g.e.ldg, col, g.N,
+                     gr[(i + AHEAD) & AHEAD][p], ur[(i + AHEAD) & AHEAD][p]);
+    }
 #pragma unroll
     for (int j = 0; j < T::FN; ++j)
 #pragma unroll
@@ -329,127 +478,208 @@ __global__ __launch_bounds__(T::NT, T::NT == 512 ? 2 : 2) void gemm_kernel(GemmA
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    constexpr int COLS = GATE ? T::FN * 16 : T::FN * 32;   // result columns of a wave
-    constexpr int LR = COLS / 8, RP = 64 / LR;             // lanes a row, rows a pass
+    auto strip8 = [&](int p, float(&v)[8], float(&w)[8]) {
+      const float* x = strip + (p * RP + lane / LR) * PITCH + (GATE ? (c8 >> 5) * 64 + (c8 & 31) : c8);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = x[q], w[q] = GATE ? x[32 + q] : 0.f;
+    };
+    if (g.splits > 1) {
+      constexpr int parts = GATE ? 2 : 1;
+      const int64_t plane = static_cast<int64_t>(g.M) * g.N;
+      float* part = g.partial + (static_cast<int64_t>(split) * g.problems + problem) * parts * plane + col;
+      const int n = min(8, g.N - col);
 #pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += RP) {
-      const int r = r0 + lane / LR, c8 = (lane % LR) * 8;
-      const int64_t row = m0 + wm * T::FM * 32 + i * 32 + r;
-      const int col = n0 + wn * COLS + c8;
-      float v[8], w[8];
-      if (GATE) {
-        const float* p = strip + r * PITCH + (c8 >> 5) * 64 + (c8 & 31);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = p[q], w[q] = p[32 + q];
-      } else {
-        const float* p = strip + r * PITCH + c8;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = p[q], w[q] = 0.f;
-      }
-      if (row < g.M) {
-        if (g.splits > 1) {
-          constexpr int parts = GATE ? 2 : 1;
-          const int n = min(8, g.N - col);
-          float* q = g.partial + ((static_cast<int64_t>(split) * g.problems + problem) * parts) * g.M * g.N + row * g.N + col;
-          if (n > 0) {
-            store8(q, 0, n, true, v);
-            if (GATE) store8(q + static_cast<int64_t>(g.M) * g.N, 0, n, true, w);
-          }
-        } else {
-          finish8<EPI>(e, problem, row, col, g.N, v, w);
+      for (int p = 0; p < NP; ++p) {
+        const int row = row0 + i * 32 + p * RP;
+        float v[8], w[8];
+        strip8(p, v, w);
+        if (row < g.M && n > 0) {
+          store8(part, static_cast<int64_t>(row) * g.N, n, true, v);
+          if (GATE) store8(part + plane, static_cast<int64_t>(row) * g.N, n, true, w);
         }
+      }
+    } else {
+      auto pass = [&](int p) {
+        const int down = i * 32 + p * RP;
+        float v[8], w[8];
+        strip8(p, v, w);
+        if (row0 + down >= g.M) return;
+        if (F32) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = ldexpf(v[q], exponent), w[q] = ldexpf(w[q], exponent);
+        }
+        largest = fmaxf(largest, finish8<F32, EPI>(g.e, act, problem, oc + down * ldc, og + down * g.e.ldg, col, g.N, v, w,
+                                                   gr[i & AHEAD][p], ur[i & AHEAD][p]));
+      };
+      if (EPI == kActBwd) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) pass(p);
+      } else {
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) pass(p);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
+  if (F32 && EPI != kStore && g.splits == 1) raise_max(g.max_c, largest);
 }
 
 // Joins the parts of a split product in their order and runs the epilogue.
-template <int EPI>
+template <bool F32, int EPI>
 __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
   const int width = max(g.N, g.e.pad_to);
   const int c8 = (width + 7) / 8;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(c8) * g.M) return;
   const int problem = blockIdx.y;
   const int64_t row = i / c8;
   const int col = static_cast<int>(i - row * c8) * 8;
+  const int64_t oc = row * (EPI == kStore && problem ? g.e.ldc1 : g.e.ldc) + col, og = row * g.e.ldg + col;
   constexpr int parts = EPI == kGate ? 2 : 1;
   const int64_t plane = static_cast<int64_t>(g.M) * g.N;
   const int n = max(0, min(8, g.N - col));
-  float v[8], w[8], x[8];
+  float largest = 0.f;
+  if (i < static_cast<int64_t>(c8) * g.M) {
+    Raw8<F32> gr, ur;
+    if (EPI == kActBwd) load_gu<F32>(g.e, true, og, col, g.N, gr, ur);
+    float v[8], w[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] = w[q] = 0.f;
-  for (int s = 0; s < g.splits; ++s) {
-    const float* p = g.partial + (static_cast<int64_t>(s) * g.problems + problem) * parts * plane + row * g.N + col;
-    load8(p, 0, n, true, x);
+    for (int q = 0; q < 8; ++q) v[q] = w[q] = 0.f;
+    const int64_t jump = plane * g.problems * parts;
+    const float* p = g.partial + static_cast<int64_t>(problem) * parts * plane + row * g.N + col;
+    constexpr int U = 4;  // parts in flight
+    for (int s = 0; s < g.splits; s += U, p += U * jump) {
+      float x[U][8], y[U][8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] += x[q];
-    if (EPI == kGate) {
-      load8(p + plane, 0, n, true, x);
+      for (int k = 0; k < U; ++k) {
+        const int m = s + k < g.splits ? n : 0;
+        load8(p + k * jump, 0, m, true, x[k]);
+        if (EPI == kGate) load8(p + k * jump + plane, 0, m, true, y[k]);
+      }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] += x[q];
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] += x[k][q];
+          if (EPI == kGate) w[q] += y[k][q];
+        }
     }
+    if (F32) {
+      const int exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = ldexpf(v[q], exponent), w[q] = ldexpf(w[q], exponent);
+    }
+    largest = finish8<F32, EPI>(g.e, Activation(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
   }
-  finish8<EPI>(g.e, problem, row, col, g.N, v, w);
+  if (F32 && EPI != kStore) raise_max(g.max_c, largest);
 }
 
-// ------------------------------------------------------------------- packing
-// x = h + m + l exactly, each term bf16: h and m by cutting the low 16 bits,
-// l what is left (at most 8 significant bits). Infinities and NaN stay in h.
-__global__ __launch_bounds__(256) void pack_planes_kernel(PackArgs p) {
-  const int64_t c8 = p.ld_out / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= c8 * p.rows) return;
-  const int64_t row = i / c8;
-  const int col = static_cast<int>(i - row * c8) * 8;
-  const int n = static_cast<int>(p.cols - col < 8 ? (p.cols - col < 0 ? 0 : p.cols - col) : 8);
-  float v[8];
-  load8(p.src, row * p.ld + col, n, p.f32 != 0, v);
-  const int64_t at = row * p.ld_out + col, plane = p.rows * p.ld_out;
-  uint4v h, m, l;
+// ------------------------------------------------------------------- copies
+__global__ __launch_bounds__(64) void zero_words_kernel(uint32_t* words, int n) {
+  for (int i = threadIdx.x; i < n; i += 64) words[i] = 0;
+}
+
+// Raises each operand's maximum word; an operand takes blockIdx.y.
+__global__ __launch_bounds__(256) void max_kernel(PackList l) {
+  const PackArgs& p = l.t[blockIdx.y];
+  const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, step = static_cast<int64_t>(gridDim.x) * 256;
+  float m = 0.f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
+    float v[4][8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t t[2][3];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const float x = v[2 * q + b];
-      const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-      float d = x - hx;
-      if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) d = 0.f;
-      const float mx = __uint_as_float(__float_as_uint(d) & 0xffff0000u);
-      // a NaN whose payload lies in the low bits only stays a NaN
-      t[b][0] = (__float_as_uint(hx) >> 16) | ((x != x) ? 0x40u : 0u);
-      t[b][1] = __float_as_uint(mx) >> 16;
-      t[b][2] = __float_as_uint(d - mx) >> 16;
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = i + k * step, row = at / c8;
+      const int col = static_cast<int>(at - row * c8) * 8;
+      load8(p.src, row * p.ld + col, at < total ? static_cast<int>(min<int64_t>(8, p.cols - col)) : 0, true, v[k]);
     }
-    h[q] = t[0][0] | t[1][0] << 16;
-    m[q] = t[0][1] | t[1][1] << 16;
-    l[q] = t[0][2] | t[1][2] << 16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, finite_abs(v[k][q]));
   }
-  *reinterpret_cast<uint4v*>(p.out + at) = h;
-  if (p.f32) {
-    *reinterpret_cast<uint4v*>(p.out + plane + at) = m;
-    *reinterpret_cast<uint4v*>(p.out + 2 * plane + at) = l;
+  __shared__ float waves[4];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x < 64) raise_max(p.word, fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3])));
+}
+
+// Copies operands into rows that loads can take (16-byte aligned, padded with
+// zeros to whole 16 bytes). fp32 values become two fp16 planes: x 2^e = h + l
+// + d with e from the operand's largest finite |value| (scale_exp), |d| <=
+// 2^-22 |x 2^e| (or 2^-25 for the smallest). Infinities and NaN go to h alone,
+// so a product they enter is not finite and no other is touched.
+template <bool F32>
+__global__ __launch_bounds__(256) void pack_kernel(PackList list) {
+  const PackArgs& p = list.t[blockIdx.y];
+  const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, plane = p.rows * p.ld_out;
+  const int e = F32 ? scale_exp(*p.word) : 0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / c8;
+    const int col = static_cast<int>(i - row * c8) * 8;
+    const int n = static_cast<int>(min<int64_t>(8, p.cols - col));
+    const Raw8<F32> raw = load_raw8<F32>(p.src, row * p.ld + col, n);
+    uint16_t* out = p.out + row * p.ld_out + col;
+    if (!F32) {
+      *reinterpret_cast<uint4v*>(out) = raw.w[0];
+      continue;
+    }
+    float v[8];
+    unpack8<F32>(raw, v);
+    halfx8 h, l;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float x = ldexpf(v[q], e);
+      h[q] = static_cast<_Float16>(x);
+      l[q] = fabsf(v[q]) < __builtin_inff() ? static_cast<_Float16>(x - static_cast<float>(h[q])) : static_cast<_Float16>(0.f);
+    }
+    *reinterpret_cast<halfx8*>(out) = h;
+    *reinterpret_cast<halfx8*>(out + plane) = l;
   }
 }
 
-using Tile256 = Tile<4, 2, 2, 4>;
+// 256 tiles run as eight waves of 128 x 64 (kGate: 64 x 128, so that a wave's
+// rows of h are whole 128-byte segments).
+template <int EPI>
+using Tile256 = Tile<EPI == kGate ? 2 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
 using Tile128 = Tile<2, 2, 2, 2>;
 
-template <class T, bool ACOL, bool BCOL, int EPI>
+template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
   const int64_t tiles = gemm_tiles(g.M, g.N, g.problems, T::BM, EPI == kGate) * g.splits;
   const int64_t grid = (tiles + 7) / 8 * 8;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_kernel<T, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
+  if (grid > 0x7fffffff || gemm_steps(g.K, g.nseg) > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_kernel<T, F32, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || g.splits == 1) return err;
   const int64_t c8 = (((g.e.pad_to > g.N) ? g.e.pad_to : g.N) + 7) / 8;
   const int64_t blocks = (c8 * g.M + 255) / 256;
-  hipLaunchKernelGGL((gemm_finish_kernel<EPI>), dim3(static_cast<uint32_t>(blocks), g.problems), dim3(256), 0, s, g);
+  hipLaunchKernelGGL((gemm_finish_kernel<F32, EPI>), dim3(static_cast<uint32_t>(blocks), g.problems), dim3(256), 0, s, g);
   return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_typed(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
+#define SHL_CASE(AC, BC, E)                              \
+  if (a_cols == AC && b_cols == BC && epi == E)          \
+    return tile == 256 ? launch_one<Tile256<E>, F32, AC, BC, E>(g, s) : launch_one<Tile128, F32, AC, BC, E>(g, s);
+  SHL_CASE(false, true, kGate)
+  SHL_CASE(false, true, kStore)
+  SHL_CASE(false, false, kActBwd)
+  SHL_CASE(false, false, kStore)
+  SHL_CASE(true, true, kStore)
+#undef SHL_CASE
+  return hipErrorInvalidValue;
+}
+
+uint32_t pack_grid(const PackList& l) {
+  int64_t most = 1;
+  for (int i = 0; i < l.n; ++i) {
+    const int64_t b = (l.t[i].rows * (l.t[i].ld_out / 8) + 255) / 256;
+    most = b > most ? b : most;
+  }
+  return static_cast<uint32_t>(most < 4096 ? most : 4096);
 }
 
 }  // namespace
@@ -463,22 +693,28 @@ int64_t gemm_steps(int64_t K, int nseg) { return (K + kBK - 1) / kBK * nseg; }
 
 hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
-#define SHL_CASE(AC, BC, E)                                              \
-  if (a_cols == AC && b_cols == BC && epi == E)                          \
-    return tile == 256 ? launch_one<Tile256, AC, BC, E>(g, s) : launch_one<Tile128, AC, BC, E>(g, s);
-  SHL_CASE(false, true, kGate)
-  SHL_CASE(false, true, kStore)
-  SHL_CASE(false, false, kActBwd)
-  SHL_CASE(false, false, kStore)
-  SHL_CASE(true, true, kStore)
-#undef SHL_CASE
-  return hipErrorInvalidValue;
+  return g.f32 ? launch_typed<true>(g, tile, a_cols, b_cols, epi, s) : launch_typed<false>(g, tile, a_cols, b_cols, epi, s);
 }
 
-hipError_t launch_pack(const PackArgs& p, hipStream_t s) {
-  const int64_t n = p.rows * (p.ld_out / 8);
-  if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(pack_planes_kernel, dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s, p);
+hipError_t launch_zero_words(uint32_t* words, int n, hipStream_t s) {
+  hipLaunchKernelGGL(zero_words_kernel, dim3(1), dim3(64), 0, s, words, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_max(const PackList& l, hipStream_t s) {
+  if (l.n == 0) return hipSuccess;
+  const uint32_t grid = pack_grid(l);
+  hipLaunchKernelGGL(max_kernel, dim3(grid < 256 ? grid : 256, l.n), dim3(256), 0, s, l);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack(const PackList& l, hipStream_t s) {
+  if (l.n == 0) return hipSuccess;
+  const dim3 grid(pack_grid(l), l.n);
+  if (l.f32)
+    hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(256), 0, s, l);
+  else
+    hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(256), 0, s, l);
   return hipGetLastError();
 }
 

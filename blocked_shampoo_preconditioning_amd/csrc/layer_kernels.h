@@ -7,7 +7,7 @@
 
 namespace shl {
 
-constexpr int kMaxSeg = 12;  // two products of six term pairs (gradient of x, fp32)
+constexpr int kMaxSeg = 6;  // two products of three plane pairs (gradient of x, fp32)
 
 enum Act { kSilu = 0, kGelu = 1, kRelu = 2 };
 
@@ -24,18 +24,21 @@ struct EpiArgs {
   void* u;
   int64_t ldc, ldc1;   // elements; ldc1: problem 1's (kStore)
   int64_t ldg;
-  int32_t f32;         // element type of every array here (0: bf16)
   int32_t act;
   int32_t pad_to;      // columns [N, pad_to) are written as zeros (rows padded for a later product)
 };
 
-// sum over segments s of A_s B_s, A_s [M][K], B_s [K][N], bf16 with fp32
-// accumulation. An operand is read by rows (K contiguous) or by columns (K is
-// the slow index).
+// sum over segments s of A_s B_s, A_s [M][K], B_s [K][N], 16-bit operands with
+// fp32 accumulation. An operand is read by rows (K contiguous) or by columns (K
+// is the slow index). f32 = 0: bf16 operands and bf16 arrays in the epilogue; 1:
+// fp16 planes of scaled fp32 values and fp32 arrays.
 struct GemmArgs {
   const uint16_t* a[kMaxSeg];
   const uint16_t* b[2][kMaxSeg];  // [1]: u's weights (kGate) or problem 1's operand
+  const uint32_t *max_a, *max_b;  // f32: the operands' maximum words (PackArgs)
+  uint32_t* max_c;                // f32: raised by h (kGate), dg and du (kActBwd)
   int64_t lda, ldb;
+  int32_t f32;
   int32_t nseg;
   int32_t M, N;        // N: columns of one result
   int32_t K;           // a multiple of 8: rows of a row operand are whole 16-byte chunks
@@ -53,15 +56,24 @@ int64_t gemm_tiles(int64_t M, int64_t N, int problems, int tile, bool gate);
 // K steps of one launch (all segments).
 int64_t gemm_steps(int64_t K, int nseg);
 
-// bf16 planes of a matrix: out[p][rows][ld_out], cols zero-padded to ld_out.
-// f32 sources give three planes whose sum is the value; bf16 sources one.
+// A copy of an operand: out[rows][ld_out], columns zero-padded to ld_out (a
+// multiple of 8). fp32 sources give two fp16 planes, out[2][rows][ld_out],
+// scaled by the power of two that brings the value in `word` (the bits of the
+// largest finite |value| of all that share the scale) into [2^14, 2^15).
 struct PackArgs {
   const void* src;
   uint16_t* out;
+  uint32_t* word;
   int64_t rows, cols, ld, ld_out;
-  int32_t f32;
 };
-hipError_t launch_pack(const PackArgs& p, hipStream_t s);
+constexpr int kMaxPack = 6;
+struct PackList {
+  PackArgs t[kMaxPack];
+  int32_t n, f32;
+};
+hipError_t launch_zero_words(uint32_t* words, int n, hipStream_t s);
+hipError_t launch_max(const PackList& l, hipStream_t s);  // raises every word by its operand
+hipError_t launch_pack(const PackList& l, hipStream_t s);
 
 enum NormKind { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
 

@@ -142,9 +142,22 @@ __device__ __forceinline__ void load_vec(const void* p, int64_t off, const int (
     }
   }
 }
-template <int C, int NT>
-__device__ __forceinline__ void load_row(const void* p, int64_t off, const int (&n)[C], bool f32, float (&v)[C][8]) {
-  load_vec<C, NT>(p, off, n, f32, 0.f, v);
+template <bool F32, int C, int NT>
+__device__ __forceinline__ void load_raw(const void* p, int64_t off, const int (&n)[C], Raw8<F32> (&v)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = load_raw8<F32>(p, off + (c * NT + threadIdx.x) * 8, n[c]);
+}
+template <bool F32, int C>
+__device__ __forceinline__ void unpack(const Raw8<F32> (&w)[C], float (&v)[C][8]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) unpack8<F32>(w[c], v[c]);
+}
+template <int C>
+__device__ __forceinline__ void fill(float (&v)[C][8], float x) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[c][i] = x;
 }
 template <int C, int NT>
 __device__ __forceinline__ void store_row(void* p, int64_t off, const int (&n)[C], bool f32, const float (&v)[C][8]) {
@@ -153,37 +166,46 @@ __device__ __forceinline__ void store_row(void* p, int64_t off, const int (&n)[C
     if (n[c] > 0) store8(p, off + (c * NT + threadIdx.x) * 8, n[c], f32, v[c]);
 }
 
-template <bool F32, int NT, int C>
+// Lanes past a row's end hold zeros: n is what a chunk has of the row (0..8).
+template <int C, int NT>
+__device__ __forceinline__ void chunk_sizes(int d, int (&n)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, d - static_cast<int>(c * NT + threadIdx.x) * 8));
+}
+
+// BIAS: there is a post or a next bias (without, their registers are saved).
+template <bool F32, int NT, int C, bool BIAS>
 __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
   __shared__ float buf[2][2][NT / 64 + 1];
   int turn = 0;
   const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
   const int64_t first = blockIdx.x * per, last = first + per < a.rows ? first + per : a.rows;
+  if (first >= last) return;
   int n[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.d - static_cast<int>(c * NT + threadIdx.x) * 8));
+  chunk_sizes<C, NT>(a.d, n);
+  Raw8<F32> xr[C], zr[C];
+  load_raw<F32, C, NT>(a.x, first * a.ldx, n, xr);
+  if (a.z) load_raw<F32, C, NT>(a.z, first * a.ldz, n, zr);
   float wp[C][8], bp[C][8], gate[C][8], wn[C][8], bn[C][8];
   load_vec<C, NT>(a.w_post, 0, n, F32, 1.f, wp);
-  load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
   load_vec<C, NT>(a.w_next, 0, n, F32, 1.f, wn);
-  load_vec<C, NT>(a.b_next, 0, n, F32, 0.f, bn);
-  load_vec<C, NT>(nullptr, 0, n, F32, 1.f, gate);
-  int64_t group = -1;
-  float z[C][8], r[C][8];
-  if (first < last) {
-    load_row<C, NT>(a.x, first * a.ldx, n, F32, r);
-    if (a.z) load_row<C, NT>(a.z, first * a.ldz, n, F32, z);
+  if (BIAS) {
+    load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
+    load_vec<C, NT>(a.b_next, 0, n, F32, 0.f, bn);
   }
+  fill<C>(gate, 1.f);
+  int64_t group = -1;
   for (int64_t row = first; row < last; ++row) {
-    // the next row's loads pass this row's stores
-    float x2[C][8], z2[C][8];
-    if (row + 1 < last) {
-      load_row<C, NT>(a.x, (row + 1) * a.ldx, n, F32, x2);
-      if (a.z) load_row<C, NT>(a.z, (row + 1) * a.ldz, n, F32, z2);
+    float z[C][8], r[C][8];
+    unpack<F32, C>(xr, r);
+    unpack<F32, C>(zr, z);
+    if (row + 1 < last) {  // the next row's loads go ahead of this row's stores
+      load_raw<F32, C, NT>(a.x, (row + 1) * a.ldx, n, xr);
+      if (a.z) load_raw<F32, C, NT>(a.z, (row + 1) * a.ldz, n, zr);
     }
     float mz = 0.f, rz = 1.f, mr = 0.f, rr = 1.f;
     if (a.z) {
-      if (a.gate && row / a.rows_per_gate != group) {
+      if (a.gate && (group < 0 || row >= (group + 1) * a.rows_per_gate)) {
         group = row / a.rows_per_gate;
         load_vec<C, NT>(a.gate, group * a.ld_gate, n, F32, 1.f, gate);
       }
@@ -196,7 +218,8 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
         if (a.drop.threshold) drop_factors(a.drop, row, c * NT + threadIdx.x, m);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p = (z[c][i] - mz) * rz * wp[c][i] + bp[c][i];
+          float p = (z[c][i] - mz) * rz * wp[c][i];
+          if (BIAS) p += bp[c][i];
           r[c][i] = i < n[c] ? a.alpha * r[c][i] + dropped(gate[c][i] * p, m[i]) : 0.f;
         }
       }
@@ -204,21 +227,19 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
     }
     if (a.next_kind != kNormNone) {
       row_stats<NT, C>(r, n, a.next_kind, a.d, a.eps, mr, rr, buf, turn);
-      float o[C][8];
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[c][i] = (r[c][i] - mr) * rr * wn[c][i] + bn[c][i];
-      store_row<C, NT>(a.n, row * a.ldn, n, F32, o);
+        for (int i = 0; i < 8; ++i) {
+          r[c][i] = (r[c][i] - mr) * rr * wn[c][i];
+          if (BIAS) r[c][i] += bn[c][i];
+        }
+      store_row<C, NT>(a.n, row * a.ldn, n, F32, r);
     }
     if (a.stats && threadIdx.x == 0) {
       const floatx4 s = {mz, rz, mr, rr};
       *reinterpret_cast<floatx4*>(a.stats + row * 4) = s;
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[c][i] = x2[c][i], z[c][i] = z2[c][i];
   }
 }
 
@@ -231,25 +252,40 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
 // began before the range or fills it, place 1: it goes on after it).
 enum { kSumWNext = 0, kSumBNext = 1, kSumWPost = 2, kSumBPost = 3, kSumGate = 4, kSums = 6 };
 
-template <bool F32, int NT, int C>
-__global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
+template <bool F32, int NT, int C, bool BIAS>
+__global__ __launch_bounds__(NT, NT == 512 ? 2 : 3) void norm_backward_kernel(NormArgs a) {
   __shared__ float buf[2][2][NT / 64 + 1];
   int turn = 0;
   const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
   const int64_t first = blockIdx.x * per, last = first + per < a.rows ? first + per : a.rows;
   int n[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.d - static_cast<int>(c * NT + threadIdx.x) * 8));
+  chunk_sizes<C, NT>(a.d, n);
+  const bool has_next = a.next_kind != kNormNone;
+  Raw8<F32> rw[C], dnw[C], drw[C], zw[C];
+  floatx4 st;
+  auto load = [&](int64_t row) {
+    st = *reinterpret_cast<const floatx4*>(a.stats + row * 4);
+    if (has_next) {
+      load_raw<F32, C, NT>(a.r, row * a.ldr, n, rw);
+      load_raw<F32, C, NT>(a.dn, row * a.lddn, n, dnw);
+    }
+    if (a.dr) load_raw<F32, C, NT>(a.dr, row * a.lddr, n, drw);
+    if (a.z) load_raw<F32, C, NT>(a.z, row * a.ldz, n, zw);
+  };
+  if (first < last) load(first);
   float wp[C][8], bp[C][8], gate[C][8], wn[C][8];
   load_vec<C, NT>(a.w_post, 0, n, F32, 1.f, wp);
-  load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
   load_vec<C, NT>(a.w_next, 0, n, F32, 1.f, wn);
-  load_vec<C, NT>(nullptr, 0, n, F32, 1.f, gate);
+  if (BIAS) load_vec<C, NT>(a.b_post, 0, n, F32, 0.f, bp);
+  fill<C>(gate, 1.f);
   float s_wn[C][8], s_bn[C][8], s_wp[C][8], s_bp[C][8], s_g[C][8];
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_wn[c][i] = s_bn[c][i] = s_wp[c][i] = s_bp[c][i] = s_g[c][i] = 0.f;
+  fill<C>(s_wn, 0.f);
+  fill<C>(s_wp, 0.f);
+  fill<C>(s_g, 0.f);
+  if (BIAS) {
+    fill<C>(s_bn, 0.f);
+    fill<C>(s_bp, 0.f);
+  }
   const int64_t plane = static_cast<int64_t>(gridDim.x) * a.d;
   auto put = [&](int what, const float (&v)[C][8]) {
     store_row<C, NT>(a.partial + what * plane, static_cast<int64_t>(blockIdx.x) * a.d, n, true, v);
@@ -267,26 +303,26 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
   const float inv_d = 1.f / a.d;
   for (int64_t row = first; row < last; ++row) {
     float r[C][8], dn[C][8], dr[C][8], z[C][8];
-    const floatx4 st = *reinterpret_cast<const floatx4*>(a.stats + row * 4);
-    load_row<C, NT>(a.dr, row * a.lddr, n, F32, dr);
-    if (a.next_kind != kNormNone) {
-      load_row<C, NT>(a.r, row * a.ldr, n, F32, r);
-      load_row<C, NT>(a.dn, row * a.lddn, n, F32, dn);
+    const float m = st[2], rs = st[3], mz = st[0], rz = st[1];
+    if (has_next) {
+      unpack<F32, C>(rw, r);
+      unpack<F32, C>(dnw, dn);
     }
-    if (a.z) load_row<C, NT>(a.z, row * a.ldz, n, F32, z);
-    if (a.gate && row / a.rows_per_gate != group) {
+    if (a.dr)
+      unpack<F32, C>(drw, dr);
+    else
+      fill<C>(dr, 0.f);
+    if (a.z) unpack<F32, C>(zw, z);
+    if (row + 1 < last) load(row + 1);  // ahead of this row's stores
+    if (a.gate && (group < 0 || row >= (group + 1) * a.rows_per_gate)) {
       if (a.dgate && group >= 0) {
         put_gate();
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s_g[c][i] = 0.f;
+        fill<C>(s_g, 0.f);
       }
       group = row / a.rows_per_gate;
       load_vec<C, NT>(a.gate, group * a.ld_gate, n, F32, 1.f, gate);
     }
-    if (a.next_kind != kNormNone) {
-      const float m = st[2], rs = st[3];
+    if (has_next) {
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -294,7 +330,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
         for (int i = 0; i < 8; ++i) {
           r[c][i] = i < n[c] ? (r[c][i] - m) * rs : 0.f;  // r^
           s_wn[c][i] += dn[c][i] * r[c][i];
-          s_bn[c][i] += dn[c][i];
+          if (BIAS) s_bn[c][i] += dn[c][i];
           dn[c][i] *= wn[c][i];
           s1 += dn[c][i];
           s2 += dn[c][i] * r[c][i];
@@ -316,30 +352,30 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
       store_row<C, NT>(a.dx, row * a.lddx, n, F32, o);
     }
     if (a.z) {
-      const bool normed = a.post_kind != kNormNone;
-      const float mz = st[0], rz = st[1];
       float t1 = 0.f, t2 = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float m[8];
+        float mk[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = 1.f;
-        if (a.drop.threshold) drop_factors(a.drop, row, c * NT + threadIdx.x, m);
+        for (int i = 0; i < 8; ++i) mk[i] = 1.f;
+        if (a.drop.threshold) drop_factors(a.drop, row, c * NT + threadIdx.x, mk);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float zh = i < n[c] ? (z[c][i] - mz) * rz : 0.f;
-          const float db = i < n[c] ? dropped(dr[c][i], m[i]) : 0.f;
-          s_g[c][i] += db * (zh * wp[c][i] + bp[c][i]);
+          const float db = i < n[c] ? dropped(dr[c][i], mk[i]) : 0.f;
+          float p = zh * wp[c][i];
+          if (BIAS) p += bp[c][i];
+          s_g[c][i] += db * p;
           const float dp = db * gate[c][i];
           s_wp[c][i] += dp * zh;
-          s_bp[c][i] += dp;
+          if (BIAS) s_bp[c][i] += dp;
           z[c][i] = zh;
           dr[c][i] = dp * wp[c][i];
           t1 += dr[c][i];
           t2 += dr[c][i] * zh;
         }
       }
-      if (normed) {
+      if (a.post_kind != kNormNone) {
         block_sum<NT>(t1, t2, buf, turn);
         t1 = a.post_kind == kNormLayer ? t1 * inv_d : 0.f;
         t2 *= inv_d;
@@ -352,95 +388,124 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a) {
     }
   }
   if (a.dw_next) put(kSumWNext, s_wn);
-  if (a.db_next) put(kSumBNext, s_bn);
   if (a.dw_post) put(kSumWPost, s_wp);
-  if (a.db_post) put(kSumBPost, s_bp);
+  if (BIAS) {
+    if (a.db_next) put(kSumBNext, s_bn);
+    if (a.db_post) put(kSumBPost, s_bp);
+  }
   if (a.gate && a.dgate && group >= 0) put_gate();
 }
 
-// Joins the workgroups' column sums: 64 columns a workgroup, its 16 waves take
-// the parts in turn, and the 16 sums are added in order. blockIdx.y: 0..3 the
-// vectors; 3 + k the gate row that reaches over the end of range k - 1, at the
-// first end it reaches over.
-__global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int parts) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+// Joins the workgroups' column sums: 32 columns a workgroup, its 32 half-waves
+// take the parts in turn with eight loads in flight, and the 32 sums are added
+// in order. blockIdx.y: the vectors of `what`; then the gate's rows that reach
+// over an end of a range: each row in turn (by_row), or for more rows than
+// ends each end, where the first one that a row reaches over stands for it.
+struct SumList {
+  int32_t n;
+  int32_t what[4];
+  int32_t by_row;
+};
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int parts, SumList list) {
+  __shared__ float sums[32][33];
+  const int c32 = threadIdx.x & 31, slot = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + c32;
   const int64_t per = parts ? (a.rows + parts - 1) / parts : 1;
   const int64_t plane = static_cast<int64_t>(parts) * a.d;
   void* out;
   int64_t at = 0;
-  int64_t lo = 0, hi = parts, begin = 0;
-  const bool is_gate = blockIdx.y >= 4;
+  int64_t lo = 0, hi = parts, begin = -1;
   const float* p;
-  if (!is_gate) {
-    out = blockIdx.y == kSumWNext ? a.dw_next : blockIdx.y == kSumBNext ? a.db_next : blockIdx.y == kSumWPost ? a.dw_post : a.db_post;
-    p = a.partial + blockIdx.y * plane;
+  if (static_cast<int>(blockIdx.y) < list.n) {
+    const int what = list.what[blockIdx.y];
+    out = what == kSumWNext ? a.dw_next : what == kSumBNext ? a.db_next : what == kSumWPost ? a.dw_post : a.db_post;
+    p = a.partial + what * plane;
   } else {
-    const int64_t k = blockIdx.y - 3;
-    if (k * per >= a.rows) return;
-    const int64_t group = k * per / a.rows_per_gate;
+    const int64_t k = blockIdx.y - list.n;
+    int64_t group = k;
+    if (!list.by_row) {
+      if ((k + 1) * per >= a.rows) return;
+      group = (k + 1) * per / a.rows_per_gate;
+    }
     begin = group * a.rows_per_gate;
     const int64_t end = begin + a.rows_per_gate < a.rows ? begin + a.rows_per_gate : a.rows;
     lo = begin / per;
     hi = (end + per - 1) / per;
-    if (begin == k * per || lo != k - 1) return;
+    if (hi - lo <= 1 || (!list.by_row && lo != k)) return;
     out = a.dgate;
     at = group * a.ld_dgate;
     p = a.partial + kSumGate * plane;
   }
-  if (!out) return;
   float s = 0.f;
   if (col < a.d) {
-    for (int64_t k = lo + wave; k < hi; k += 16) {
-      const float* q = p + k * a.d + col;
-      if (is_gate && begin > k * per) q += plane;
-      s += *q;
+    for (int64_t k = lo + slot; k < hi; k += 256) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t q = k + 32 * i;
+        x[i] = q < hi ? p[q * a.d + col + (begin > q * per ? plane : 0)] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
     }
   }
-  sums[wave][lane] = s;
+  sums[slot][c32] = s;
   __syncthreads();
-  if (wave == 0 && col < a.d) {
+  if (slot == 0 && col < a.d) {
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += sums[w][lane];
+    for (int w = 0; w < 32; ++w) s += sums[w][c32];
     if (a.f32)
       static_cast<float*>(out)[at + col] = s;
     else
-      static_cast<uint16_t*>(out)[at + col] = static_cast<uint16_t>(f32_to_bf16(s));
+      static_cast<uint16_t*>(out)[at + col] = f32_to_bf16(s);
   }
 }
 
-// Workgroups of the row kernels: enough to fill the card, few enough that the
-// column sums of the backward pass stay a small part of its traffic.
+int norm_lanes(int d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512; }
+
+// Workgroups of the row kernels: as many as the card holds at once (twice that
+// in the forward pass), and in the backward pass at least four rows each where there are
+// rows enough, so that the column sums stay a small part of the traffic.
 int64_t norm_grid(const NormArgs& a, bool backward) {
-  const int64_t most = backward ? 1024 : 2048;
-  const int64_t per = (a.rows + most - 1) / most;
+  const int lanes = norm_lanes(a.d);
+  const int64_t most = backward ? 256 * (lanes == 512 ? 8 : 12) * 64 / lanes : 2 * 256 * 16 * 64 / lanes;
+  int64_t per = (a.rows + most - 1) / most;
+  if (backward) {
+    const int64_t least = (a.rows + 511) / 512;
+    per = per > (least < 4 ? least : 4) ? per : (least < 4 ? least : 4);
+  }
   return per ? (a.rows + per - 1) / per : 0;
 }
 
 template <bool F32, int NT, int C>
 void launch_norm(const NormArgs& a, bool backward, int64_t grid, hipStream_t s) {
-  if (backward)
-    hipLaunchKernelGGL((norm_backward_kernel<F32, NT, C>), dim3(grid), dim3(NT), 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_forward_kernel<F32, NT, C>), dim3(grid), dim3(NT), 0, s, a);
+  const dim3 g(static_cast<uint32_t>(grid)), b(NT);
+  if (backward) {
+    if (a.b_post || a.db_post || a.db_next)
+      hipLaunchKernelGGL((norm_backward_kernel<F32, NT, C, true>), g, b, 0, s, a);
+    else
+      hipLaunchKernelGGL((norm_backward_kernel<F32, NT, C, false>), g, b, 0, s, a);
+  } else if (a.b_post || a.b_next) {
+    hipLaunchKernelGGL((norm_forward_kernel<F32, NT, C, true>), g, b, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((norm_forward_kernel<F32, NT, C, false>), g, b, 0, s, a);
+  }
 }
 
 template <bool F32>
 hipError_t dispatch_norm(const NormArgs& a, bool backward, int64_t grid, hipStream_t s) {
-  if (a.d <= 512)
-    launch_norm<F32, 64, 1>(a, backward, grid, s);
-  else if (a.d <= 1024)
-    launch_norm<F32, 128, 1>(a, backward, grid, s);
-  else if (a.d <= 2048)
-    launch_norm<F32, 256, 1>(a, backward, grid, s);
-  else if (a.d <= 4096)
-    launch_norm<F32, 512, 1>(a, backward, grid, s);
-  else if (a.d <= kMaxNormWidth)
-    launch_norm<F32, 512, 2>(a, backward, grid, s);
-  else
-    return hipErrorInvalidValue;
+  if (a.d > kMaxNormWidth) return hipErrorInvalidValue;
+  switch (norm_lanes(a.d)) {
+    case 64: launch_norm<F32, 64, 1>(a, backward, grid, s); break;
+    case 128: launch_norm<F32, 128, 1>(a, backward, grid, s); break;
+    case 256: launch_norm<F32, 256, 1>(a, backward, grid, s); break;
+    default:
+      if (a.d <= 4096)
+        launch_norm<F32, 512, 1>(a, backward, grid, s);
+      else
+        launch_norm<F32, 512, 2>(a, backward, grid, s);
+  }
   return hipGetLastError();
 }
 
@@ -459,10 +524,20 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
     const hipError_t e = a.f32 ? dispatch_norm<true>(a, true, grid, s) : dispatch_norm<false>(a, true, grid, s);
     if (e != hipSuccess) return e;
   }
-  if (!a.dw_next && !a.db_next && !a.dw_post && !a.db_post && !a.dgate) return hipSuccess;
-  const uint32_t ends = a.dgate && grid > 1 ? static_cast<uint32_t>(grid - 1) : 0;
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((a.d + 63) / 64, 4 + ends), dim3(1024), 0, s, a,
-                     static_cast<int>(grid));
+  SumList list{};
+  if (a.dw_next) list.what[list.n++] = kSumWNext;
+  if (a.db_next) list.what[list.n++] = kSumBNext;
+  if (a.dw_post) list.what[list.n++] = kSumWPost;
+  if (a.db_post) list.what[list.n++] = kSumBPost;
+  int64_t ends = 0;
+  if (a.dgate && grid > 1) {
+    const int64_t groups = (a.rows + a.rows_per_gate - 1) / a.rows_per_gate;
+    list.by_row = groups <= grid - 1;
+    ends = list.by_row ? groups : grid - 1;
+  }
+  if (list.n + ends == 0) return hipSuccess;
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((a.d + 31) / 32, static_cast<uint32_t>(list.n + ends)), dim3(1024), 0, s, a,
+                     static_cast<int>(grid), list);
   return hipGetLastError();
 }
 

@@ -13,7 +13,7 @@ using shp_rt::fail;
 
 namespace {
 
-constexpr int64_t kMaxLd = int64_t(1) << 22;  // 128 rows of an operand stay within 32-bit byte offsets
+constexpr int64_t kMaxLd = int64_t(1) << 21;  // 256 rows of an operand stay within 32-bit byte offsets
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 
 int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
@@ -54,13 +54,17 @@ int guarded(F&& f) {
 
 // ------------------------------------------------- gated feed-forward block
 struct Planes {
-  const uint16_t* p[3] = {};
+  const uint16_t* p[2] = {};
   int64_t ld = 0;
+  const uint32_t* word = nullptr;
 };
 
 // One pass over the block's launches: with run = false only the workspace is
 // laid out.
 struct Ffn {
+  // maximum words of the fp32 operands
+  enum Word { kX, kWIn, kWDown, kH, kDy, kDgu, kWords };
+
   const shampoo_ffn_t& a;
   char* ws;
   hipStream_t stream;
@@ -69,11 +73,14 @@ struct Ffn {
   hipError_t err = hipSuccess;
   int64_t N, d, f, fp, e;
   bool f32;
+  uint32_t* words = nullptr;
+  shl::PackList list{};
 
   Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
     N = a.tokens, d = a.d_model, f = a.d_hidden, fp = round8(f);
     f32 = a.dtype == SHAMPOO_F32;
     e = f32 ? 4 : 2;
+    list.f32 = f32;
   }
   void* take(int64_t bytes) { return ws + carve.take(bytes); }
   void ok(hipError_t x) {
@@ -86,52 +93,53 @@ struct Ffn {
   bool usable(const void* p, int64_t cols, int64_t ld, bool sums_over_cols) const {
     return !f32 && aligned(p, 16) && ld % 8 == 0 && (!sums_over_cols || cols % 8 == 0);
   }
-  Planes operand(const void* p, int64_t rows, int64_t cols, int64_t ld, bool sums_over_cols) {
+  Planes operand(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld, bool sums_over_cols) {
+    if (!usable(p, cols, ld, sums_over_cols)) return copied(w, p, rows, cols, ld);
     Planes o;
-    if (usable(p, cols, ld, sums_over_cols)) {
-      o.p[0] = static_cast<const uint16_t*>(p);
-      o.ld = ld;
-      return o;
-    }
-    return copied(p, rows, cols, ld);
-  }
-  Planes copied(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-    Planes o;
-    o.ld = round8(cols);
-    uint16_t* out = static_cast<uint16_t*>(take((f32 ? 3 : 1) * rows * o.ld * 2));
-    for (int i = 0; i < (f32 ? 3 : 1); ++i) o.p[i] = out + i * rows * o.ld;
-    if (run) {
-      shl::PackArgs k{p, out, rows, cols, ld, o.ld, f32 ? 1 : 0};
-      ok(shl::launch_pack(k, stream));
-    }
+    o.p[0] = static_cast<const uint16_t*>(p);
+    o.ld = ld;
     return o;
   }
-  // Both weights of the fused products share one leading dimension.
+  // Puts a copy on the list; flush() makes it.
+  Planes copied(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    Planes o;
+    o.ld = round8(cols);
+    uint16_t* out = static_cast<uint16_t*>(take((f32 ? 2 : 1) * rows * o.ld * 2));
+    o.p[0] = out;
+    if (f32) o.p[1] = out + rows * o.ld, o.word = words + w;
+    if (rows) list.t[list.n++] = shl::PackArgs{p, out, words + w, rows, cols, ld, o.ld};
+    return o;
+  }
+  // Both weights of the fused products share one leading dimension (and scale).
   void operands(const void* p, const void* q, int64_t rows, int64_t cols, int64_t ldp, int64_t ldq, bool sums_over_cols, Planes& x,
                 Planes& y) {
-    if (usable(p, cols, ldp, sums_over_cols) && usable(q, cols, ldq, sums_over_cols) && ldp != ldq) {
-      x = copied(p, rows, cols, ldp);
-      y = copied(q, rows, cols, ldq);
-    } else if (usable(p, cols, ldp, sums_over_cols) != usable(q, cols, ldq, sums_over_cols)) {
-      x = copied(p, rows, cols, ldp);
-      y = copied(q, rows, cols, ldq);
-    } else {
-      x = operand(p, rows, cols, ldp, sums_over_cols);
-      y = operand(q, rows, cols, ldq, sums_over_cols);
-    }
+    const bool in_place = ldp == ldq && usable(p, cols, ldp, sums_over_cols) && usable(q, cols, ldq, sums_over_cols);
+    x = in_place ? operand(kWIn, p, rows, cols, ldp, sums_over_cols) : copied(kWIn, p, rows, cols, ldp);
+    y = in_place ? operand(kWIn, q, rows, cols, ldq, sums_over_cols) : copied(kWIn, q, rows, cols, ldq);
+  }
+  void start_words() {
+    if (!f32) return;
+    words = static_cast<uint32_t*>(take(kWords * 4));
+    if (run) ok(shl::launch_zero_words(words, kWords, stream));
+  }
+  // Makes the listed copies; fp32 ones after their maxima are known (the
+  // maxima of h, dg and du come from the product that wrote them).
+  void flush(bool maxima) {
+    if (run && f32 && maxima) ok(shl::launch_max(list, stream));
+    if (run) ok(shl::launch_pack(list, stream));
+    list.n = 0;
   }
 
-  // Adds the term pairs of one product to the segments, smallest first.
+  // Adds one product's plane pairs to the segments, the smaller terms first.
   void segments(shl::GemmArgs& g, const Planes& A, const Planes& B, const Planes* B1 = nullptr) {
-    static const int kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
-    for (int i = f32 ? 0 : 5; i < 6; ++i) {
+    static const int kPairs[3][2] = {{0, 1}, {1, 0}, {0, 0}};
+    for (int i = f32 ? 0 : 2; i < 3; ++i) {
       g.a[g.nseg] = A.p[kPairs[i][0]];
       g.b[0][g.nseg] = B.p[kPairs[i][1]];
       if (B1) g.b[1][g.nseg] = B1->p[kPairs[i][1]];
       ++g.nseg;
     }
-    g.lda = A.ld;
-    g.ldb = B.ld;
+    g.lda = A.ld, g.ldb = B.ld, g.max_a = A.word, g.max_b = B.word;
   }
 
   void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
@@ -149,7 +157,7 @@ struct Ffn {
         if (s > 1) g.splits = static_cast<int32_t>(s);
       }
     }
-    g.e.f32 = f32 ? 1 : 0;
+    g.f32 = f32 ? 1 : 0;
     g.e.act = a.activation;
     if (g.splits > 1)
       g.partial = static_cast<float*>(take(int64_t(4) * g.splits * g.problems * (gate ? 2 : 1) * g.M * g.N));
@@ -157,9 +165,12 @@ struct Ffn {
   }
 
   void forward() {
-    const Planes x = operand(a.x, N, d, a.ld_x, true);
+    start_words();
+    const Planes x = operand(kX, a.x, N, d, a.ld_x, true);
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
+    const Planes wd = operand(kWDown, a.w_down, f, d, a.ld_down, false);
+    flush(true);
     char* saved = static_cast<char*>(a.saved);
     void* h = saved ? saved + 2 * act_bytes() : take(N * fp * e);
     {
@@ -169,10 +180,11 @@ struct Ffn {
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
       if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
+      if (f32) g.max_c = words + kH;
       product(g, false, true, shl::kGate);
     }
-    const Planes hp = operand(h, N, f32 ? f : fp, fp, true);
-    const Planes wd = operand(a.w_down, f, d, a.ld_down, false);
+    const Planes hp = operand(kH, h, N, fp, fp, true);
+    flush(false);
     shl::GemmArgs g{};
     segments(g, hp, wd);
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
@@ -182,25 +194,31 @@ struct Ffn {
   }
 
   void backward() {
+    start_words();
     char* saved = static_cast<char*>(a.saved);
-    const bool want_gate = a.dx || a.dw_gate || a.dw_up;
+    const bool want_gate = a.dx || a.dw_gate;
     // dy is read by rows for dh and by columns for dWd: one copy serves both
-    const Planes dy = operand(a.dy, N, d, a.ld_dy, true);
+    const Planes dy = operand(kDy, a.dy, N, d, a.ld_dy, true);
+    Planes wd, h, wg, wu, x;
+    if (want_gate) wd = operand(kWDown, a.w_down, f, d, a.ld_down, true);
+    if (a.dw_down) h = operand(kH, saved + 2 * act_bytes(), N, fp, fp, false);
+    if (a.dx) operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
+    if (a.dw_gate) x = operand(kX, a.x, N, d, a.ld_x, false);
+    flush(true);
     void *dg = nullptr, *du = nullptr;
     if (want_gate) {
       dg = take(N * fp * e);
       du = take(N * fp * e);
-      const Planes wd = operand(a.w_down, f, d, a.ld_down, true);
       shl::GemmArgs g{};
       segments(g, dy, wd);
       g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = dg, g.e.c[1] = du, g.e.ldc = fp, g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
       g.e.pad_to = static_cast<int32_t>(fp);
+      if (f32) g.max_c = words + kDgu;
       product(g, false, false, shl::kActBwd);
     }
     if (a.dw_down) {
-      const Planes h = operand(saved + 2 * act_bytes(), N, f, fp, false);
       shl::GemmArgs g{};
       segments(g, h, dy);
       g.M = static_cast<int32_t>(f), g.N = static_cast<int32_t>(d), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 1;
@@ -208,10 +226,9 @@ struct Ffn {
       product(g, true, true, shl::kStore);
     }
     if (!want_gate) return;
-    const Planes pg = operand(dg, N, f32 ? f : fp, fp, true), pu = operand(du, N, f32 ? f : fp, fp, true);
+    const Planes pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
+    flush(false);
     if (a.dx) {
-      Planes wg, wu;
-      operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
       shl::GemmArgs g{};
       segments(g, pg, wg);
       segments(g, pu, wu);
@@ -221,7 +238,6 @@ struct Ffn {
       product(g, false, false, shl::kStore);
     }
     if (a.dw_gate) {
-      const Planes x = operand(a.x, N, d, a.ld_x, false);
       shl::GemmArgs g{};
       segments(g, x, pg, &pu);
       g.M = static_cast<int32_t>(d), g.N = static_cast<int32_t>(f), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 2;
@@ -234,7 +250,7 @@ struct Ffn {
 int check_sizes(const shampoo_ffn_t* a) {
   if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
   if (a->tokens < 0 || a->d_model < 1 || a->d_hidden < 1 || a->tokens > kMaxDim || a->d_model > kMaxLd || a->d_hidden > kMaxLd)
-    return fail(SHAMPOO_ERR_INVALID_ARG, "tokens must be in [0, 2^31), d_model and d_hidden in [1, 2^22]");
+    return fail(SHAMPOO_ERR_INVALID_ARG, "tokens must be in [0, 2^31), d_model and d_hidden in [1, 2^21]");
   RC(check_dtype(a->dtype));
   if (a->activation < SHAMPOO_ACT_SILU || a->activation > SHAMPOO_ACT_RELU)
     return fail(SHAMPOO_ERR_UNSUPPORTED, "activation must be one of shampoo_activation_t");

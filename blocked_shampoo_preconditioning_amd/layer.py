@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -26,48 +27,23 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 NORMS = {"none": 0, None: 0, "rms": 1, "layer": 2}
 MAX_NORM_WIDTH = 8192
 
-_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
-_U32, _U64 = ctypes.c_uint32, ctypes.c_uint64
-_F, _D = ctypes.c_float, ctypes.c_double
+# The C argument structs, field by field (native sizes and alignment); packing
+# one takes a fraction of the time of filling a ctypes structure, which counts
+# where a call is a few microseconds. "P" is a pointer, 0 for NULL.
+_FFN = struct.Struct("@qqq ii PPPP qqqq P q P P q PPPP qqqq")
+_NORM = struct.Struct("@qq iii f f d Q I q PP qq PP qq PPPPP q P PP qq PP qq PPPPP q")
+_DROP = struct.Struct("@qq i I d Q PP qq")
 
-
-class FFNArgs(ctypes.Structure):
-    _fields_ = [("tokens", _I64), ("d_model", _I64), ("d_hidden", _I64), ("dtype", _I32), ("activation", _I32),
-                ("x", _P), ("w_gate", _P), ("w_up", _P), ("w_down", _P),
-                ("ld_x", _I64), ("ld_gate", _I64), ("ld_up", _I64), ("ld_down", _I64),
-                ("y", _P), ("ld_y", _I64), ("saved", _P),
-                ("dy", _P), ("ld_dy", _I64), ("dx", _P), ("dw_gate", _P), ("dw_up", _P), ("dw_down", _P),
-                ("ld_dx", _I64), ("ld_dw_gate", _I64), ("ld_dw_up", _I64), ("ld_dw_down", _I64)]
-
-
-class NormArgs(ctypes.Structure):
-    _fields_ = [("rows", _I64), ("width", _I64), ("dtype", _I32), ("post_kind", _I32), ("next_kind", _I32),
-                ("eps", _F), ("residual_scale", _F), ("dropout", _D), ("seed", _U64), ("offset", _U32),
-                ("rows_per_gate", _I64),
-                ("z", _P), ("x", _P), ("ld_z", _I64), ("ld_x", _I64), ("r", _P), ("n", _P), ("ld_r", _I64), ("ld_n", _I64),
-                ("post_weight", _P), ("post_bias", _P), ("gate", _P), ("next_weight", _P), ("next_bias", _P),
-                ("ld_gate", _I64), ("stats", _P),
-                ("dr", _P), ("dn", _P), ("ld_dr", _I64), ("ld_dn", _I64), ("dx", _P), ("dz", _P), ("ld_dx", _I64), ("ld_dz", _I64),
-                ("d_post_weight", _P), ("d_post_bias", _P), ("d_gate", _P), ("d_next_weight", _P), ("d_next_bias", _P),
-                ("ld_d_gate", _I64)]
-
-
-class DropoutArgs(ctypes.Structure):
-    _fields_ = [("rows", _I64), ("cols", _I64), ("dtype", _I32), ("offset", _U32), ("dropout", _D), ("seed", _U64),
-                ("x", _P), ("y", _P), ("ld_x", _I64), ("ld_y", _I64)]
-
-
-_SIZE = ctypes.POINTER(ctypes.c_size_t)
-_FFN, _NORM, _DROP = (ctypes.POINTER(t) for t in (FFNArgs, NormArgs, DropoutArgs))
+_A, _SIZE = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
 _SIGNATURES = {
-    "shampoo_ffn_saved_size": [_FFN, _SIZE],
-    "shampoo_ffn_workspace_size": [_FFN, _I32, _SIZE],
-    "shampoo_ffn_forward": [_FFN, _P, ctypes.c_size_t, _P],
-    "shampoo_ffn_backward": [_FFN, _P, ctypes.c_size_t, _P],
-    "shampoo_norm_workspace_size": [_NORM, _SIZE],
-    "shampoo_norm_forward": [_NORM, _P],
-    "shampoo_norm_backward": [_NORM, _P, ctypes.c_size_t, _P],
-    "shampoo_dropout": [_DROP, _P],
+    "shampoo_ffn_saved_size": [_A, _SIZE],
+    "shampoo_ffn_workspace_size": [_A, ctypes.c_int32, _SIZE],
+    "shampoo_ffn_forward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "shampoo_ffn_backward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "shampoo_norm_workspace_size": [_A, _SIZE],
+    "shampoo_norm_forward": [_A, ctypes.c_void_p],
+    "shampoo_norm_backward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "shampoo_dropout": [_A, ctypes.c_void_p],
 }
 _lib = None
 
@@ -84,21 +60,51 @@ def load_library():
     return _lib
 
 
-def _check(code):
+_DTYPES = {torch.bfloat16: SHAMPOO_BF16, torch.float32: SHAMPOO_F32}
+_U64, _U32 = 0xFFFFFFFFFFFFFFFF, 0xFFFFFFFF
+
+
+def _call(name, args, like, *more):
+    """Runs an entry point on `like`'s device and torch's current stream there."""
+    fn = getattr(_lib or load_library(), name)
+    dev = like.get_device()
+    if dev == torch.cuda.current_device():
+        code = fn(args, *more, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(args, *more, torch.cuda.current_stream(dev).cuda_stream)
     if code:
         _s._check(code)
 
 
-_DTYPES = {torch.bfloat16: SHAMPOO_BF16, torch.float32: SHAMPOO_F32}
+def _size(name, args, *more):
+    out = ctypes.c_size_t()
+    code = getattr(_lib or load_library(), name)(args, *more, ctypes.byref(out))
+    if code:
+        _s._check(code)
+    return out.value
 
 
-def _matrix(name, t, rows, cols, like=None):
-    """(pointer, leading dimension) of a 2-D tensor of that shape."""
+def _first(name, t):
+    """dtype code, rows and columns of the tensor that sets a call's dtype and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} is {t.dtype}: float32 and bfloat16 are supported")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (tokens, width), got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    return code, rows, cols
+
+
+def _matrix(name, t, rows, cols, like):
+    """(pointer, leading dimension) of a 2-D tensor of that shape, dtype and device."""
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
     shape = t.shape
     if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")
-    if like is not None:
-        _same(name, t, like)
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous (stride {t.stride()})")
@@ -111,62 +117,60 @@ def _matrix(name, t, rows, cols, like=None):
 
 
 def _vector(name, t, n, like):
-    """Pointer of a 1-D tensor of n elements (None: NULL)."""
+    """Pointer of a 1-D tensor of n elements (None: 0)."""
     if t is None:
-        return None
+        return 0
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n} elements, got shape {tuple(t.shape)}")
-    _same(name, t, like)
     return t.data_ptr()
 
 
-def _same(name, t, like):
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-
-
-def _dtype(name, t):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} is {t.dtype}: float32 and bfloat16 are supported")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D (tokens, width), got shape {tuple(t.shape)}")
-    return _DTYPES[t.dtype]
-
-
-def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _new(like, rows, cols):
+    return like.new_empty((rows, cols))
 
 
 def _workspace(nbytes, like):
-    return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    """(pointer, tensor that owns it)."""
+    if not nbytes:
+        return 0, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return ws.data_ptr(), ws
 
 
 # ------------------------------------------------------ gated feed-forward block
-def _ffn_args(x, w_gate, w_up, w_down, activation):
-    dt = _dtype("x", x)
-    if activation not in ACTIVATIONS:
+def _ffn_inputs(x, w_gate, w_up, w_down, activation):
+    """The leading fields of the C struct, tokens to ld_down."""
+    dt, n, d = _first("x", x)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
-    n, d = x.shape
     if w_gate.dim() != 2:
         raise ValueError(f"w_gate must be 2-D, got shape {tuple(w_gate.shape)}")
     f = w_gate.shape[1]
-    px, lx = _matrix("x", x, n, d)
+    px, lx = _matrix("x", x, n, d, x)
     pg, lg = _matrix("w_gate", w_gate, d, f, x)
     pu, lu = _matrix("w_up", w_up, d, f, x)
     pd, ld = _matrix("w_down", w_down, f, d, x)
-    return FFNArgs(n, d, f, dt, ACTIVATIONS[activation], px, pg, pu, pd, lx, lg, lu, ld)
+    return n, d, f, dt, act, px, pg, pu, pd, lx, lg, lu, ld
 
 
-def _ffn_call(a, backward, like):
-    lib, size = load_library(), ctypes.c_size_t()
-    ref = ctypes.byref(a)
-    with torch.cuda.device(like.device):
-        _check(lib.shampoo_ffn_workspace_size(ref, backward, ctypes.byref(size)))
-        ws = _workspace(size.value, like) if size.value else None
-        fn = lib.shampoo_ffn_backward if backward else lib.shampoo_ffn_forward
-        _check(fn(ref, ws.data_ptr() if ws is not None else None, size.value, _stream(like)))
+_sizes = {}  # (sizes and dtype, direction, leading dimensions, alignments) -> bytes of workspace
+
+
+def _ffn_workspace(fields, args, backward, more):
+    """Workspace bytes of a call: asked once for each combination of what they go by."""
+    key = (fields[:4], backward, fields[9:], fields[5] & 15, fields[6] & 15, fields[7] & 15, fields[8] & 15, more)
+    size = _sizes.get(key)
+    if size is None:
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        size = _sizes[key] = _size("shampoo_ffn_workspace_size", args, backward)
+    return size
+
+
+_NO_GRADIENTS = (0,) * 10
 
 
 def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
@@ -174,82 +178,69 @@ def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
     [d, f], w_down [f, d]. With `save` returns (y, saved), `saved` being what
     `ffn_backward` needs (an opaque tensor of three f-wide rows a token).
     activation: "silu", "gelu" (tanh form) or "relu"."""
-    a = _ffn_args(x, w_gate, w_up, w_down, activation)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.y, a.ld_y = y.data_ptr(), x.shape[1]
+    fields = _ffn_inputs(x, w_gate, w_up, w_down, activation)
+    n, d, f = fields[:3]
+    y = _new(x, n, d)
     saved = None
     if save:
-        size = ctypes.c_size_t()
-        _check(load_library().shampoo_ffn_saved_size(ctypes.byref(a), ctypes.byref(size)))
-        saved = torch.empty(size.value, dtype=torch.uint8, device=x.device)
-        a.saved = saved.data_ptr()
-    _ffn_call(a, 0, x)
+        saved = torch.empty(_saved_size(fields), dtype=torch.uint8, device=x.device)
+    args = _FFN.pack(*fields, y.data_ptr() or 256, d, saved.data_ptr() if save else 0, *_NO_GRADIENTS)
+    size = _ffn_workspace(fields, args, 0, save)
+    ws, keep = _workspace(size, x)
+    _call("shampoo_ffn_forward", args, x, ws, size)
     return (y, saved) if save else y
+
+
+def _saved_size(fields):
+    key = fields[:4]
+    size = _sizes.get(key)
+    if size is None:
+        size = _sizes[key] = _size("shampoo_ffn_saved_size", _FFN.pack(*fields, *(0,) * 13))
+    return size
 
 
 def ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation="silu", need_dx=True, need_dw=True):
     """(dx, dw_gate, dw_up, dw_down) from dy, the forward pass's inputs and what
     it saved. need_dx / need_dw: None is returned for what is not needed."""
-    a = _ffn_args(x, w_gate, w_up, w_down, activation)
-    n, d, f = a.tokens, a.d_model, a.d_hidden
-    a.dy, a.ld_dy = _matrix("dy", dy, n, d, x)
-    size = ctypes.c_size_t()
-    _check(load_library().shampoo_ffn_saved_size(ctypes.byref(a), ctypes.byref(size)))
-    if saved.dtype != torch.uint8 or saved.numel() != size.value or saved.device != x.device:
+    fields = _ffn_inputs(x, w_gate, w_up, w_down, activation)
+    n, d, f = fields[:3]
+    pdy, ldy = _matrix("dy", dy, n, d, x)
+    if saved.dtype is not torch.uint8 or saved.numel() != _saved_size(fields) or saved.get_device() != x.get_device():
         raise ValueError("saved is not what ffn_forward kept for these sizes")
-    a.saved = saved.data_ptr()
-
-    def new(rows, cols):
-        return torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    dx = dwg = dwu = dwd = None
-    if need_dx:
-        dx = new(n, d)
-        a.dx, a.ld_dx = dx.data_ptr(), d
+    dx = _new(x, n, d) if need_dx else None
+    dwg = dwu = dwd = None
+    pointers = (dx.data_ptr() or 256 if need_dx else 0, 0, 0, 0)
     if need_dw:
-        dwg, dwu, dwd = new(d, f), new(d, f), new(f, d)
-        a.dw_gate, a.dw_up, a.dw_down = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
-        a.ld_dw_gate, a.ld_dw_up, a.ld_dw_down = f, f, d
+        dwg, dwu, dwd = _new(x, d, f), _new(x, d, f), _new(x, f, d)
+        pointers = (pointers[0], dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr())
     if need_dx or need_dw:
-        _ffn_call(a, 1, x)
+        args = _FFN.pack(*fields, 0, 0, saved.data_ptr(), pdy, ldy, *pointers, d, f, f, d)
+        size = _ffn_workspace(fields, args, 1, (need_dx, need_dw, ldy, pdy & 15))
+        ws, keep = _workspace(size, x)
+        _call("shampoo_ffn_backward", args, x, ws, size)
     return dx, dwg, dwu, dwd
 
 
 # ------------------------------------------------------- norms around a block
-def _norm_args(x, z, post, post_weight, post_bias, gate, rows_per_gate, residual_scale, dropout, seed, offset, next,
-               next_weight, next_bias, eps):
-    dt = _dtype("x", x)
-    n, d = x.shape
-    if post not in NORMS or next not in NORMS:
+def _norm_head(dt, n, d, post, next, eps, residual_scale, dropout, seed, offset, rows_per_gate):
+    kp, kn = NORMS.get(post), NORMS.get(next)
+    if kp is None or kn is None:
         raise ValueError("post and next are one of 'none', 'rms', 'layer'")
-    a = NormArgs(n, d, dt, NORMS[post], NORMS[next], eps, residual_scale, dropout, seed & 0xFFFFFFFFFFFFFFFF,
-                 offset & 0xFFFFFFFF, 1)
-    a.x, a.ld_x = _matrix("x", x, n, d)
-    if z is not None:
-        a.z, a.ld_z = _matrix("z", z, n, d, x)
-    if gate is not None:
-        a.rows_per_gate = max(n, 1) if rows_per_gate is None else rows_per_gate
-        if a.rows_per_gate < 1:
-            raise ValueError("rows_per_gate must be at least 1")
-        a.gate, a.ld_gate = _matrix("gate", gate, -(-n // a.rows_per_gate), d, x)
-    a.post_weight = _vector("post_weight", post_weight, d, x)
-    a.post_bias = _vector("post_bias", post_bias, d, x)
-    a.next_weight = _vector("next_weight", next_weight, d, x)
-    a.next_bias = _vector("next_bias", next_bias, d, x)
-    return a
+    if rows_per_gate is None:
+        rows_per_gate = n or 1
+    elif rows_per_gate < 1:
+        raise ValueError("rows_per_gate must be at least 1")
+    return n, d, dt, kp, kn, eps, residual_scale, dropout, seed & _U64, offset & _U32, rows_per_gate
 
 
-def _norm_forward(a, x, r, stats):
-    n = torch.empty(x.shape, dtype=x.dtype, device=x.device) if a.next_kind else None
-    if n is not None:
-        a.n, a.ld_n = n.data_ptr(), x.shape[1]
-    if r is not None:
-        a.r, a.ld_r = r.data_ptr(), x.shape[1]
-    if stats:
-        stats = torch.empty((x.shape[0], 4), dtype=torch.float32, device=x.device)
-        a.stats = stats.data_ptr()
-    with torch.cuda.device(x.device):
-        _check(load_library().shampoo_norm_forward(ctypes.byref(a), _stream(x)))
-    return n, stats
+def _norm_vectors(like, n, d, post_weight, post_bias, gate, rows_per_gate, next_weight, next_bias):
+    """Pointers of weights, biases and gate, and the gate's leading dimension."""
+    pg, lg = _matrix("gate", gate, -(-n // rows_per_gate), d, like) if gate is not None else (0, 0)
+    return (_vector("post_weight", post_weight, d, like), _vector("post_bias", post_bias, d, like), pg,
+            _vector("next_weight", next_weight, d, like), _vector("next_bias", next_bias, d, like), lg)
+
+
+_NO_NORM_GRADIENTS = (0,) * 14
 
 
 def residual_forward(x, z, *, post="rms", post_weight=None, post_bias=None, gate=None, rows_per_gate=None,
@@ -263,56 +254,66 @@ def residual_forward(x, z, *, post="rms", post_weight=None, post_bias=None, gate
     for row i (rows_per_gate None: one row for all). dropout: probability, under
     the 64-bit `seed` and 32-bit `offset`. Returns (r, n, stats); n is None for
     next="none"; stats go to `residual_backward`."""
-    a = _norm_args(x, z, post, post_weight, post_bias, gate, rows_per_gate, residual_scale, dropout, seed, offset, next,
-                   next_weight, next_bias, eps)
+    dt, n, d = _first("x", x)
     if z is None:
         raise ValueError("z is None: norm_forward is the norm alone")
-    r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    n, stats = _norm_forward(a, x, r, True)
-    return r, n, stats
+    head = _norm_head(dt, n, d, post, next, eps, residual_scale, dropout, seed, offset, rows_per_gate)
+    px, lx = _matrix("x", x, n, d, x)
+    pz, lz = _matrix("z", z, n, d, x)
+    vectors = _norm_vectors(x, n, d, post_weight, post_bias, gate, head[-1], next_weight, next_bias)
+    r = _new(x, n, d)
+    out = _new(x, n, d) if head[4] else None
+    stats = torch.empty((n, 4), dtype=torch.float32, device=x.device)
+    args = _NORM.pack(*head, pz, px, lz, lx, r.data_ptr(), out.data_ptr() if out is not None else 0, d, d, *vectors,
+                      stats.data_ptr(), *_NO_NORM_GRADIENTS)
+    _call("shampoo_norm_forward", args, x)
+    return r, out, stats
 
 
 def norm_forward(x, kind="rms", weight=None, bias=None, eps=1e-6):
     """n = norm(x), [rows, width]; returns (n, stats for `norm_backward`)."""
     if kind in ("none", None):
         raise ValueError("kind must be 'rms' or 'layer'")
-    a = _norm_args(x, None, "none", None, None, None, None, 1.0, 0.0, 0, 0, kind, weight, bias, eps)
-    return _norm_forward(a, x, None, True)
+    dt, n, d = _first("x", x)
+    head = _norm_head(dt, n, d, "none", kind, eps, 1.0, 0.0, 0, 0, None)
+    px, lx = _matrix("x", x, n, d, x)
+    vectors = _norm_vectors(x, n, d, None, None, None, 1, weight, bias)
+    out = _new(x, n, d)
+    stats = torch.empty((n, 4), dtype=torch.float32, device=x.device)
+    args = _NORM.pack(*head, 0, px, 0, lx, 0, out.data_ptr(), d, d, *vectors, stats.data_ptr(), *_NO_NORM_GRADIENTS)
+    _call("shampoo_norm_forward", args, x)
+    return out, stats
 
 
-def _norm_backward(a, x, z, dr, dn, stats):
-    n, d = x.shape
-    if stats.shape != (n, 4) or stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != x.device:
+def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
+    """x: the forward pass's r (or its input, where there is no z)."""
+    n, d = head[:2]
+    if stats.shape != (n, 4) or stats.dtype is not torch.float32 or not stats.is_contiguous() or \
+            stats.get_device() != x.get_device():
         raise ValueError("stats is not what the forward pass returned for these sizes")
-    a.stats = stats.data_ptr()
-    if dr is not None:
-        a.dr, a.ld_dr = _matrix("dr", dr, n, d, x)
-    if a.next_kind:
+    pz, lz = _matrix("z", z, n, d, x) if z is not None else (0, 0)
+    pdr, ldr = _matrix("dr", dr, n, d, x) if dr is not None else (0, 0)
+    pdn, ldn = 0, 0
+    if head[4]:
         if dn is None:
             raise ValueError("dn is None: the next norm's gradient is needed")
-        a.dn, a.ld_dn = _matrix("dn", dn, n, d, x)
-
-    def new(*shape):
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
-    g = dict.fromkeys(("x", "z", "post_weight", "post_bias", "gate", "next_weight", "next_bias"))
-    g["x"] = new(n, d)
-    a.dx, a.ld_dx = g["x"].data_ptr(), d
-    if z is not None:
-        g["z"] = new(n, d)
-        a.dz, a.ld_dz = g["z"].data_ptr(), d
-    for name in ("post_weight", "post_bias", "next_weight", "next_bias"):
-        if getattr(a, name):
-            g[name] = new(d)
-            setattr(a, "d_" + name, g[name].data_ptr())
-    if a.gate:
-        g["gate"] = new(-(-n // a.rows_per_gate), d)
-        a.d_gate, a.ld_d_gate = g["gate"].data_ptr(), d
-    lib, size = load_library(), ctypes.c_size_t()
-    with torch.cuda.device(x.device):
-        _check(lib.shampoo_norm_workspace_size(ctypes.byref(a), ctypes.byref(size)))
-        ws = _workspace(size.value, x) if size.value else None
-        _check(lib.shampoo_norm_backward(ctypes.byref(a), ws.data_ptr() if ws is not None else None, size.value, _stream(x)))
-    return g
+        pdn, ldn = _matrix("dn", dn, n, d, x)
+    dx = _new(x, n, d)
+    dz = _new(x, n, d) if z is not None else None
+    # the vectors' gradients, in the struct's order: post weight, post bias, gate, next weight, next bias
+    grads = [x.new_empty(d) if vectors[i] else None for i in (0, 1, 2, 3, 4)]
+    if vectors[2]:
+        grads[2] = _new(x, -(-n // head[10]), d)
+    pointers = [g.data_ptr() if g is not None else 0 for g in grads]
+    args = _NORM.pack(*head, pz, px, lz, lx, px if z is not None else 0, 0, lx, 0, *vectors, stats.data_ptr(), pdr, pdn, ldr,
+                      ldn, dx.data_ptr(), dz.data_ptr() if z is not None else 0, d, d, *pointers, d)
+    key = (head[:3], vectors[2] != 0)
+    size = _sizes.get(key)
+    if size is None:
+        size = _sizes[key] = _size("shampoo_norm_workspace_size", args)
+    ws, keep = _workspace(size, x)
+    _call("shampoo_norm_backward", args, x, ws, size)
+    return dx, dz, grads
 
 
 def residual_backward(dr, dn, r, z, stats, *, post="rms", post_weight=None, post_bias=None, gate=None, rows_per_gate=None,
@@ -322,10 +323,12 @@ def residual_backward(dr, dn, r, z, stats, *, post="rms", post_weight=None, post
     its r, z and stats, with the same settings: a dict with "x", "z",
     "post_weight", "post_bias", "gate", "next_weight", "next_bias" (None for
     what was not given)."""
-    a = _norm_args(r, z, post, post_weight, post_bias, gate, rows_per_gate, residual_scale, dropout, seed, offset, next,
-                   next_weight, next_bias, eps)
-    a.r, a.ld_r = a.x, a.ld_x
-    return _norm_backward(a, r, z, dr, dn, stats)
+    dt, n, d = _first("r", r)
+    head = _norm_head(dt, n, d, post, next, eps, residual_scale, dropout, seed, offset, rows_per_gate)
+    px, lx = _matrix("r", r, n, d, r)
+    vectors = _norm_vectors(r, n, d, post_weight, post_bias, gate, head[-1], next_weight, next_bias)
+    dx, dz, g = _norm_backward(head, r, z, px, lx, vectors, dr, dn, stats)
+    return {"x": dx, "z": dz, "post_weight": g[0], "post_bias": g[1], "gate": g[2], "next_weight": g[3], "next_bias": g[4]}
 
 
 def norm_backward(dn, x, stats, dr=None, kind="rms", weight=None, bias=None, eps=1e-6):
@@ -333,9 +336,12 @@ def norm_backward(dn, x, stats, dr=None, kind="rms", weight=None, bias=None, eps
     way (the residual stream) added: a dict with "x", "weight", "bias"."""
     if kind in ("none", None):
         raise ValueError("kind must be 'rms' or 'layer'")
-    a = _norm_args(x, None, "none", None, None, None, None, 1.0, 0.0, 0, 0, kind, weight, bias, eps)
-    g = _norm_backward(a, x, None, dr, dn, stats)
-    return {"x": g["x"], "weight": g["next_weight"], "bias": g["next_bias"]}
+    dt, n, d = _first("x", x)
+    head = _norm_head(dt, n, d, "none", kind, eps, 1.0, 0.0, 0, 0, None)
+    px, lx = _matrix("x", x, n, d, x)
+    vectors = _norm_vectors(x, n, d, None, None, None, 1, weight, bias)
+    dx, _, g = _norm_backward(head, x, None, px, lx, vectors, dr, dn, stats)
+    return {"x": dx, "weight": g[3], "bias": g[4]}
 
 
 # -------------------------------------------------------------------- dropout
@@ -344,12 +350,13 @@ def dropout(x, p, seed, offset=0, out=None):
     others scaled to keep the expectation. Which ones goes by (row, column,
     seed, offset) alone, so the gradient is the same call on the gradient.
     out: a tensor to write to (may be x)."""
-    dt = _dtype("x", x)
-    n, d = x.shape
-    px, lx = _matrix("x", x, n, d)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    py, ly = _matrix("out", y, n, d, x)
-    a = DropoutArgs(n, d, dt, offset & 0xFFFFFFFF, p, seed & 0xFFFFFFFFFFFFFFFF, px, py, lx, ly)
-    with torch.cuda.device(x.device):
-        _check(load_library().shampoo_dropout(ctypes.byref(a), _stream(x)))
-    return y
+    dt, n, d = _first("x", x)
+    px, lx = _matrix("x", x, n, d, x)
+    if out is None:
+        out, ly = _new(x, n, d), d
+        py = out.data_ptr()
+    else:
+        py, ly = _matrix("out", out, n, d, x)
+    args = _DROP.pack(n, d, dt, offset & _U32, p, seed & _U64, px, py, lx, ly)
+    _call("shampoo_dropout", args, x)
+    return out

@@ -37,9 +37,11 @@ extern "C" {
  *     dWg = x^T dg,  dWu = x^T du,  dWd = h^T dy.
  * x, y, dy, dx: tokens x d_model; Wg, Wu: d_model x d_hidden; Wd: d_hidden x
  * d_model. All of one dtype. bf16 products run on the bf16 matrix cores; fp32
- * operands are split exactly into three bf16 terms and six products of them
- * accumulate in fp32 (the dropped terms are below 2^-24 of |x y|). An
- * infinite or NaN operand makes every result it enters non-finite. */
+ * operands are scaled by a power of two that brings their largest finite
+ * |value| into [2^14, 2^15) and split into two fp16 terms (as
+ * SHAMPOO_GEMM_SPLIT_F16), three products of which accumulate in fp32. An
+ * infinite or NaN operand makes every result it enters non-finite, and leaves
+ * the others as they are. */
 typedef enum {
   SHAMPOO_ACT_SILU = 0, /* g / (1 + exp(-g))                               */
   SHAMPOO_ACT_GELU = 1, /* tanh form                                       */
@@ -51,7 +53,7 @@ typedef struct {
   int32_t dtype;                     /* shampoo_dtype_t                      */
   int32_t activation;                /* shampoo_activation_t                 */
   const void *x, *w_gate, *w_up, *w_down;
-  int64_t ld_x, ld_gate, ld_up, ld_down; /* cols <= ld <= 2^22, as all lds   */
+  int64_t ld_x, ld_gate, ld_up, ld_down; /* cols <= ld <= 2^21, as all lds   */
   /* forward */
   void* y;
   int64_t ld_y;
