@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libshampoo_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "tensor_kernels.hip", "layer_gemm.hip",
-                                            "layer_norm.hip", "runtime.cpp", "roots.cpp",
+                                            "layer_decode.hip", "layer_norm.hip", "runtime.cpp", "roots.cpp",
                                             "tensor_runtime.cpp", "layer_runtime.cpp")]
 ARCH = "gfx950"
 

@@ -1,0 +1,233 @@
+// The feed-forward block's forward products for a few tokens (serving).
+//
+// Every weight is read once for at most 16 T rows of x, so the kernel is bound
+// by HBM. The weights' rows [k][n] go from memory into registers, two columns a
+// lane: the 16 lanes of a row read 32 columns in whole 64-byte pieces, and
+// each wave has 16 loads a matrix in flight with no LDS in their way. The
+// matrix cores take them as they come: the weights are the "A" operand (16 rows
+// of one 16 x 16 product are columns 2 j + i, j the lane of a row), x the "B"
+// operand (16 tokens). fp32 uses the fp32 matrix instruction, so it is exact to
+// fp32 accumulation.
+#include "layer_epilogue.h"
+#include "layer_kernels.h"
+
+namespace shl {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) short short4v;
+
+constexpr int kCols = 32;       // columns of a workgroup
+constexpr int kBatch = 64;      // K rows in flight at once in a wave
+
+// A batch's K rows go to the 16-lane groups q = 0..3 in runs of sixteen, so that
+// a lane's values of x lie together: step s of the products takes row 16 q + s
+// (fp32, four rows a product) or rows 16 q + 4 s + 0..3 (bf16, sixteen).
+//
+// Sixteen values of x of one token; those from K on are zeros.
+template <bool F32>
+__device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K, uint32_t (&v)[F32 ? 16 : 8]) {
+  if (k + 16 <= K) {
+    __builtin_memcpy(v, static_cast<const char*>(x) + (row + k) * (F32 ? 4 : 2), F32 ? 64 : 32);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < (F32 ? 16 : 8); ++i) v[i] = 0;
+#pragma unroll 1
+  for (int e = K - k - 1; e >= 0; --e) {  // shifted in from the last one
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 15; i > 0; --i) v[i] = v[i - 1];
+      v[0] = static_cast<const uint32_t*>(x)[row + k + e];
+    } else {
+#pragma unroll
+      for (int i = 7; i > 0; --i) v[i] = v[i] << 16 | v[i - 1] >> 16;
+      v[0] = v[0] << 16 | static_cast<const uint16_t*>(x)[row + k + e];
+    }
+  }
+}
+
+// kBatch rows of K from k0 for MATS matrices and 16 T tokens. Rows from K on lie
+// past the weights' end and read as zeros; what a lane reads past a row's last
+// column belongs to columns that are not stored.
+template <bool F32, int MATS, int T>
+__device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)[T], int k0, const uint32_t (&off)[MATS],
+                                      floatx4 (&acc)[MATS][2][T]) {
+  constexpr int E = F32 ? 4 : 2;
+  const int q = (threadIdx.x & 63) >> 4;
+  uint32_t v[MATS][16][F32 ? 2 : 1], xv[T][F32 ? 16 : 8];
+#pragma unroll
+  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + 16 * q, a.K, xv[t]);
+#pragma unroll
+  for (int m = 0; m < MATS; ++m) {
+    const int64_t at = k0 * a.ldw[m] * E, end = ((a.K - 1) * a.ldw[m] + a.N) * E;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(a.w[m]) + at), 0, static_cast<int>(max<int64_t>(0, min<int64_t>(end - at, 0x7ffffff0))), 0x00020000);
+    const uint32_t step = static_cast<uint32_t>(a.ldw[m]) * E;
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      if constexpr (F32) {
+        typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
+        const uint2v w = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(r, off[m] + s * step, 0, 0));
+        v[m][s][0] = w[0], v[m][s][1] = w[1];
+      } else {
+        v[m][s][0] = __builtin_amdgcn_raw_buffer_load_b32(r, off[m] + s * step, 0, 0);
+      }
+    }
+  }
+  if constexpr (F32) {
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+            acc[m][i][t] =
+                __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[m][s][i]), __uint_as_float(xv[t][s]), acc[m][i][t], 0, 0, 0);
+  } else {
+    typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        const uint32_t w0 = v[m][4 * s][0], w1 = v[m][4 * s + 1][0], w2 = v[m][4 * s + 2][0], w3 = v[m][4 * s + 3][0];
+        // four rows of the lane's first and second column
+        const uint2v c0 = {__builtin_amdgcn_perm(w1, w0, 0x05040100u), __builtin_amdgcn_perm(w3, w2, 0x05040100u)};
+        const uint2v c1 = {__builtin_amdgcn_perm(w1, w0, 0x07060302u), __builtin_amdgcn_perm(w3, w2, 0x07060302u)};
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const uint2v xx = {xv[t][2 * s], xv[t][2 * s + 1]};
+          const short4v b = __builtin_bit_cast(short4v, xx);
+          acc[m][0][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c0), b, acc[m][0][t], 0, 0, 0);
+          acc[m][1][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c1), b, acc[m][1][t], 0, 0, 0);
+        }
+      }
+  }
+}
+
+// Workgroup: kCols columns (of both weights for kGate), one of a.splits parts
+// of K, cut again over the waves; the waves' sums are added in order through
+// LDS. One part: the epilogue follows; more: the sums go to a.partial in
+// GemmArgs' layout and the finish kernel joins them.
+template <bool F32, int EPI, int T, int W>
+__global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
+  constexpr int MATS = EPI == kGate ? 2 : 1;
+  constexpr int PITCH = kCols + 4;
+  __shared__ float sums[W][MATS * 16][PITCH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // neighbouring columns, whose rows share cache lines, go to one XCD
+  const uint32_t per = gridDim.x / 8;
+  const uint32_t id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  const uint32_t groups = (a.N + kCols - 1) / kCols;
+  if (id >= groups * a.splits) return;
+  const uint32_t group = id / a.splits, split = id - group * a.splits;
+  // a lane's two columns; the last lanes repeat the last two of the matrix
+  const int n0 = group * kCols, col = min(n0 + 2 * (lane & 15), a.N - 2);
+  uint32_t off[MATS];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+    off[m] = (16 * (lane >> 4) * static_cast<uint32_t>(a.ldw[m]) + static_cast<uint32_t>(col)) * (F32 ? 4 : 2);
+  // batches of this wave
+  const int batches = (a.K + kBatch - 1) / kBatch, parts = a.splits * W;
+  const int part = split * W + wave, each = batches / parts, rest = batches - each * parts;
+  const int first = each * part + min(part, rest), last = first + each + (part < rest ? 1 : 0);
+  int64_t xrow[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) xrow[t] = static_cast<int64_t>(min(16 * t + (lane & 15), a.M - 1)) * a.ldx;
+  floatx4 acc[MATS][2][T];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[m][i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int b = first; b < last; ++b) batch<F32, MATS, T>(a, xrow, b * kBatch, off, acc);
+  const Activation act(a.e.act);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int rows = min(16, a.M - 16 * t);
+    if (rows <= 0) break;
+    if (t > 0) __syncthreads();
+    // a lane's sums: token lane % 16, columns of the lanes 4 (lane / 16) + r
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = min(n0 + 2 * (4 * (lane >> 4) + r), a.N - 2) + i - n0;
+        if (c >= 0) {
+#pragma unroll
+          for (int m = 0; m < MATS; ++m) sums[wave][m * 16 + (lane & 15)][c] = acc[m][i][t][r];
+        }
+      }
+    __syncthreads();
+    // the waves' sums in order, one column of one token a lane
+#pragma unroll 1
+    for (int u = threadIdx.x; u < MATS * rows * kCols; u += W * 64) {
+      const int c = u % kCols, y = u / kCols, row = y < rows ? y : y - rows + 16;
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) x += sums[k][row][c];
+      sums[0][row][c] = x;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int u = threadIdx.x; u < rows * (kCols / 8); u += W * 64) {
+      const int row = u / (kCols / 8), c = u % (kCols / 8) * 8, token = 16 * t + row;
+      float v[8], w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[q] = sums[0][row][c + q];
+        w[q] = MATS == 2 ? sums[0][(MATS - 1) * 16 + row][c + q] : 0.f;
+      }
+      if (a.splits > 1) {
+        const int n = min(8, a.N - n0 - c);
+        const int64_t plane = static_cast<int64_t>(a.M) * a.N;
+        float* p = a.partial + static_cast<int64_t>(split) * MATS * plane + static_cast<int64_t>(token) * a.N + n0 + c;
+        if (n > 0) {
+          store8(p, 0, n, true, v);
+          if (MATS == 2) store8(p + plane, 0, n, true, w);
+        }
+      } else {
+        const Raw8<F32> none{};
+        finish8<F32, EPI>(a.e, act, 0, token * a.e.ldc + n0 + c, token * a.e.ldg + n0 + c, n0 + c, a.N, v, w, none, none);
+      }
+    }
+  }
+}
+
+template <bool F32, int EPI>
+hipError_t launch_decode_tokens(const DecodeArgs& a, dim3 grid, hipStream_t s) {
+  // more tokens take more registers a wave, so fewer waves
+  if (a.M <= 16)
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 1, F32 ? 8 : 16>), grid, dim3(F32 ? 512 : 1024), 0, s, a);
+  else if (a.M <= 32)
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 2, 8>), grid, dim3(512), 0, s, a);
+  else if constexpr (F32)
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 4, 8>), grid, dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t decode_groups(int64_t N) { return (N + kCols - 1) / kCols; }
+int64_t decode_batches(int64_t K) { return (K + kBatch - 1) / kBatch; }
+
+hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s) {
+  if (a.M <= 0 || a.N <= 0) return hipSuccess;
+  if (a.M > decode_tokens(f32) || (epi != kGate && epi != kStore)) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<uint32_t>((decode_groups(a.N) * a.splits + 7) / 8 * 8));
+  hipError_t e;
+  if (epi == kGate)
+    e = f32 ? launch_decode_tokens<true, kGate>(a, grid, s) : launch_decode_tokens<false, kGate>(a, grid, s);
+  else
+    e = f32 ? launch_decode_tokens<true, kStore>(a, grid, s) : launch_decode_tokens<false, kStore>(a, grid, s);
+  if (e != hipSuccess || a.splits == 1) return e;
+  GemmArgs g{};
+  g.M = a.M, g.N = a.N, g.problems = 1, g.splits = a.splits, g.partial = a.partial, g.e = a.e, g.f32 = f32;
+  return launch_finish(g, epi, s);
+}
+
+}  // namespace shl

@@ -56,6 +56,25 @@ int64_t gemm_tiles(int64_t M, int64_t N, int problems, int tile, bool gate);
 // K steps of one launch (all segments).
 int64_t gemm_steps(int64_t K, int nseg);
 
+// Joins a split product's parts and runs the epilogue.
+hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s);
+
+// A forward product for at most decode_tokens rows of x, operands as the caller
+// has them: x [M][K], w [K][N] (kGate: both weights), bf16 weights with 4-byte
+// aligned rows; K, N >= 2.
+constexpr int decode_tokens(bool f32) { return f32 ? 64 : 32; }
+struct DecodeArgs {
+  const void* x;
+  const void* w[2];
+  int64_t ldx, ldw[2];
+  int32_t M, N, K, splits;
+  float* partial;      // [splits][1 or 2][M][N], splits > 1
+  EpiArgs e;
+};
+int64_t decode_groups(int64_t N);   // workgroups before splitting
+int64_t decode_batches(int64_t K);  // the smallest parts K is cut into
+hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s);
+
 // A copy of an operand: out[rows][ld_out], columns zero-padded to ld_out (a
 // multiple of 8). fp32 sources give two fp16 planes, out[2][rows][ld_out],
 // scaled by the power of two that brings the value in `word` (the bits of the

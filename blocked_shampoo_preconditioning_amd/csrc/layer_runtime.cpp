@@ -164,7 +164,46 @@ struct Ffn {
     if (run) ok(shl::launch_gemm(g, tile, a_cols, b_cols, epi, stream));
   }
 
+  // Whether the forward pass takes the few-token kernels: they read two columns
+  // of a row in one aligned access.
+  bool few() const {
+    auto pairs = [&](const void* p, int64_t ld) { return f32 || (aligned(p, 4) && ld % 2 == 0); };
+    return N <= shl::decode_tokens(f32) && d >= 2 && f >= 2 && pairs(a.w_gate, a.ld_gate) && pairs(a.w_up, a.ld_up) &&
+           pairs(a.w_down, a.ld_down);
+  }
+  // The forward products of a few tokens, weights as the caller has them.
+  void few_product(shl::DecodeArgs& g, shl::Epi epi) {
+    const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K);
+    int64_t s = 1;
+    if (groups < 192) {
+      s = 512 / groups;
+      if (s > batches / 16) s = batches / 16;
+      if (s > 32) s = 32;
+    }
+    g.splits = static_cast<int32_t>(s < 1 ? 1 : s);
+    g.e.act = a.activation;
+    if (g.splits > 1)
+      g.partial = static_cast<float*>(take(int64_t(4) * g.splits * (epi == shl::kGate ? 2 : 1) * g.M * g.N));
+    if (run) ok(shl::launch_decode(g, f32, epi, stream));
+  }
+  void forward_few() {
+    char* saved = static_cast<char*>(a.saved);
+    void* h = saved ? saved + 2 * act_bytes() : take(N * fp * e);
+    shl::DecodeArgs g{};
+    g.x = a.x, g.ldx = a.ld_x, g.w[0] = a.w_gate, g.w[1] = a.w_up, g.ldw[0] = a.ld_gate, g.ldw[1] = a.ld_up;
+    g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(d);
+    g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
+    if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
+    few_product(g, shl::kGate);
+    shl::DecodeArgs y{};
+    y.x = h, y.ldx = fp, y.w[0] = a.w_down, y.ldw[0] = a.ld_down;
+    y.M = static_cast<int32_t>(N), y.N = static_cast<int32_t>(d), y.K = static_cast<int32_t>(f);
+    y.e.c[0] = a.y, y.e.ldc = a.ld_y;
+    few_product(y, shl::kStore);
+  }
+
   void forward() {
+    if (few()) return forward_few();
     start_words();
     const Planes x = operand(kX, a.x, N, d, a.ld_x, true);
     Planes wg, wu;

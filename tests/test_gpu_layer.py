@@ -93,6 +93,20 @@ def test_ffn_strided(pad, dtype):
     check_ffn(150, 136, 264, "silu", dtype, pad=pad, seed=4)
 
 
+@pytest.mark.parametrize("n", [13, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("d,f", [(66, 70), (768, 513), (258, 2048)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ffn_few_tokens(n, d, f, dtype):
+    """Around every token count where another kernel takes over; last columns that make half a pair."""
+    check_ffn(n, d, f, "gelu", dtype, seed=6)
+
+
+@pytest.mark.parametrize("pad", [1, 2, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ffn_few_tokens_strided(pad, dtype):
+    check_ffn(9, 131, 77, "silu", dtype, pad=pad, seed=7)
+
+
 def test_ffn_256_tiles():
     """Enough rows and columns that the largest tiles run, ragged at every edge."""
     check_ffn(4000, 520, 3000, "silu", "bf16", seed=5)
