@@ -53,6 +53,41 @@ int guarded(F&& f) {
 }
 
 // ------------------------------------------------- gated feed-forward block
+// Tile and K split of a product, by an estimate of its time in microseconds.
+// Measured on the products of 300..8192 tokens, 256..2048 x 1024..8192: a CU
+// does a K step (64) of 128 x 128 results in 0.47 us; 256 tiles run at that
+// rate, one to a CU; 128 tiles at 0.8 of it with two on a CU and at 0.5 with
+// one. A round of tiles costs 5 or 3 us to fill and empty. A split costs a
+// second launch and its sums' way through memory at 4 TB/s. Of the listed sizes
+// this takes 256 tiles alone where they fill the card (8192 x 2048 x 8192), 256
+// tiles in 4 or 5 parts for long sums over few tiles (dx of 2048 x 2048 x 8192:
+// 656 us a step, with 128 tiles unsplit 709), 128 tiles unsplit for short ones
+// (1024 x 768 x 2048: dWg, dWu 114 us, in two parts 122) and split 128 tiles
+// where those are under about 100 (y of 1024 x 768 x 2048: 118, unsplit 124).
+int choose_tile(int64_t M, int64_t N, int problems, bool gate, int64_t steps, int32_t& splits) {
+  const double unit = 0.47 * static_cast<double>(steps);
+  const double sums = static_cast<double>(M) * static_cast<double>(N) * problems * (gate ? 2 : 1) * 8 / 4e6;
+  int tile = 256;
+  double best = 0;
+  splits = 0;
+  for (int t : {256, 128}) {
+    const int64_t tiles = shl::gemm_tiles(M, N, problems, t, gate);
+    for (int64_t s = 1; s <= 16 && (s == 1 || s * 4 <= steps); ++s) {
+      const int64_t n = tiles * s;
+      double us;
+      if (t == 256) {
+        us = static_cast<double>((n + 255) / 256) * (4 * unit / s + 5);
+      } else {
+        const int64_t rest = n % 512;
+        us = static_cast<double>(n / 512) * (2.5 * unit / s + 3) + (rest == 0 ? 0 : (rest <= 256 ? 2.0 : 2.5) * unit / s + 3);
+      }
+      if (s > 1) us += 4 + sums * s;
+      if (splits == 0 || us < best) best = us, tile = t, splits = static_cast<int32_t>(s);
+    }
+  }
+  return tile;
+}
+
 struct Planes {
   const uint16_t* p[2] = {};
   int64_t ld = 0;
@@ -145,18 +180,7 @@ struct Ffn {
   void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
     const bool gate = epi == shl::kGate;
     const int64_t steps = shl::gemm_steps(g.K, g.nseg);
-    int tile = 256;
-    g.splits = 1;
-    if (shl::gemm_tiles(g.M, g.N, g.problems, 256, gate) < 192) {
-      tile = 128;
-      const int64_t tiles = shl::gemm_tiles(g.M, g.N, g.problems, 128, gate);
-      if (tiles < 256) {
-        int64_t s = 512 / (tiles > 0 ? tiles : 1);
-        if (s > steps / 4) s = steps / 4;
-        if (s > 32) s = 32;
-        if (s > 1) g.splits = static_cast<int32_t>(s);
-      }
-    }
+    const int tile = choose_tile(g.M, g.N, g.problems, gate, steps, g.splits);
     g.f32 = f32 ? 1 : 0;
     g.e.act = a.activation;
     if (g.splits > 1)
