@@ -471,6 +471,19 @@ __global__ __launch_bounds__(64) void zero_words_kernel(uint32_t* words, int n) 
   for (int i = threadIdx.x; i < n; i += 64) words[i] = 0;
 }
 
+// Row and first column of an operand's i-th group of eight columns, c8 a row. A
+// 64-bit division takes longer than the group's load.
+__device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total, int64_t& row, int& col) {
+  if (total <= 0x7fffffff) {
+    const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(c8);
+    row = r;
+    col = static_cast<int>(static_cast<uint32_t>(i) - r * static_cast<uint32_t>(c8)) * 8;
+  } else {
+    row = i / c8;
+    col = static_cast<int>(i - row * c8) * 8;
+  }
+}
+
 // Raises each operand's maximum word; an operand takes blockIdx.y.
 __global__ __launch_bounds__(256) void max_kernel(PackList l) {
   const PackArgs& p = l.t[blockIdx.y];
@@ -480,8 +493,10 @@ __global__ __launch_bounds__(256) void max_kernel(PackList l) {
     float v[4][8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t at = i + k * step, row = at / c8;
-      const int col = static_cast<int>(at - row * c8) * 8;
+      const int64_t at = i + k * step;
+      int64_t row;
+      int col;
+      group_place(at < total ? at : 0, c8, total, row, col);
       load8(p.src, row * p.ld + col, at < total ? static_cast<int>(min<int64_t>(8, p.cols - col)) : 0, true, v[k]);
     }
 #pragma unroll
@@ -508,8 +523,9 @@ __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, plane = p.rows * p.ld_out;
   const int e = F32 ? scale_exp(*p.word) : 0;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = i / c8;
-    const int col = static_cast<int>(i - row * c8) * 8;
+    int64_t row;
+    int col;
+    group_place(i, c8, total, row, col);
     const int n = static_cast<int>(min<int64_t>(8, p.cols - col));
     const Raw8<F32> raw = load_raw8<F32>(p.src, row * p.ld + col, n);
     uint16_t* out = p.out + row * p.ld_out + col;

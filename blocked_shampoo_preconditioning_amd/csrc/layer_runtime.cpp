@@ -97,7 +97,8 @@ struct Planes {
 // One pass over the block's launches: with run = false only the workspace is
 // laid out.
 struct Ffn {
-  // maximum words of the fp32 operands
+  // maximum words of the fp32 operands; the forward pass's (up to kH) are kept
+  // behind h in `saved`
   enum Word { kX, kWIn, kWDown, kH, kDy, kDgu, kWords };
 
   const shampoo_ffn_t& a;
@@ -108,7 +109,7 @@ struct Ffn {
   hipError_t err = hipSuccess;
   int64_t N, d, f, fp, e;
   bool f32;
-  uint32_t* words = nullptr;
+  uint32_t *words = nullptr, *kept = nullptr;
   shl::PackList list{};
 
   Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
@@ -141,8 +142,8 @@ struct Ffn {
     o.ld = round8(cols);
     uint16_t* out = static_cast<uint16_t*>(take((f32 ? 2 : 1) * rows * o.ld * 2));
     o.p[0] = out;
-    if (f32) o.p[1] = out + rows * o.ld, o.word = words + w;
-    if (rows) list.t[list.n++] = shl::PackArgs{p, out, words + w, rows, cols, ld, o.ld};
+    if (f32) o.p[1] = out + rows * o.ld, o.word = word(w);
+    if (rows) list.t[list.n++] = shl::PackArgs{p, out, word(w), rows, cols, ld, o.ld};
     return o;
   }
   // Both weights of the fused products share one leading dimension (and scale).
@@ -152,15 +153,25 @@ struct Ffn {
     x = in_place ? operand(kWIn, p, rows, cols, ldp, sums_over_cols) : copied(kWIn, p, rows, cols, ldp);
     y = in_place ? operand(kWIn, q, rows, cols, ldq, sums_over_cols) : copied(kWIn, q, rows, cols, ldq);
   }
-  void start_words() {
+  uint32_t* saved_words() const { return reinterpret_cast<uint32_t*>(static_cast<char*>(a.saved) + 3 * act_bytes()); }
+  void start_words(bool backward) {
     if (!f32) return;
-    words = static_cast<uint32_t*>(take(kWords * 4));
+    words = !backward && a.saved ? saved_words() : static_cast<uint32_t*>(take(kWords * 4));
     if (run) ok(shl::launch_zero_words(words, kWords, stream));
+    kept = backward && !few() ? saved_words() : nullptr;
   }
-  // Makes the listed copies; fp32 ones after their maxima are known (the
-  // maxima of h, dg and du come from the product that wrote them).
+  uint32_t* word(Word w) const { return kept && w <= kH ? kept + w : words + w; }
+  // Makes the listed copies; fp32 ones after their maxima are known (those of
+  // h, dg and du come from the product that wrote them, and the backward pass
+  // has the forward pass's).
   void flush(bool maxima) {
-    if (run && f32 && maxima) ok(shl::launch_max(list, stream));
+    if (run && f32 && maxima) {
+      shl::PackList scan{};
+      scan.f32 = 1;
+      for (int i = 0; i < list.n; ++i)
+        if (!kept || list.t[i].word < kept || list.t[i].word > kept + kH) scan.t[scan.n++] = list.t[i];
+      ok(shl::launch_max(scan, stream));
+    }
     if (run) ok(shl::launch_pack(list, stream));
     list.n = 0;
   }
@@ -228,7 +239,7 @@ struct Ffn {
 
   void forward() {
     if (few()) return forward_few();
-    start_words();
+    start_words(false);
     const Planes x = operand(kX, a.x, N, d, a.ld_x, true);
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
@@ -243,7 +254,7 @@ struct Ffn {
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
       if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
-      if (f32) g.max_c = words + kH;
+      if (f32) g.max_c = word(kH);
       product(g, false, true, shl::kGate);
     }
     const Planes hp = operand(kH, h, N, fp, fp, true);
@@ -257,7 +268,7 @@ struct Ffn {
   }
 
   void backward() {
-    start_words();
+    start_words(true);
     char* saved = static_cast<char*>(a.saved);
     const bool want_gate = a.dx || a.dw_gate;
     // dy is read by rows for dh and by columns for dWd: one copy serves both
@@ -278,7 +289,7 @@ struct Ffn {
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = dg, g.e.c[1] = du, g.e.ldc = fp, g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
       g.e.pad_to = static_cast<int32_t>(fp);
-      if (f32) g.max_c = words + kDgu;
+      if (f32) g.max_c = word(kDgu);
       product(g, false, false, shl::kActBwd);
     }
     if (a.dw_down) {
@@ -473,7 +484,7 @@ int shampoo_ffn_saved_size(const shampoo_ffn_t* a, size_t* bytes_out) {
   RC(check_sizes(a));
   if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
   const Ffn p(*a, nullptr, nullptr, false);
-  *bytes_out = static_cast<size_t>(3 * p.act_bytes());
+  *bytes_out = static_cast<size_t>(3 * p.act_bytes() + 256);
   return SHAMPOO_OK;
 }
 
