@@ -20,42 +20,83 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ uint16_t f32_to_bf16(float x) { return static_cast<uint16_t>(pack_bf16(x, 0.f)); }
 
-// Eight consecutive elements of a row, or its last n < 8 (the others 0).
-// Whole groups go as 16-byte accesses whatever their alignment (global memory
-// takes unaligned ones). A row's last group goes element by element in a
-// rolled loop over a shifting register file: these lines are in every kernel
-// many times, and instructions that are fetched cost more than that loop.
-__device__ __forceinline__ void load8(const void* p, int64_t off, int n, bool f32, float (&v)[8]) {
-  if (f32) {
-    const float* q = static_cast<const float*>(p) + off;
-    if (n == 8) {
-      floatx4 a, b;
-      __builtin_memcpy(&a, q, 16);
-      __builtin_memcpy(&b, q + 4, 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-      return;
-    }
+// Eight elements as they lie in memory: held so, a row on its way takes half
+// (bf16) or as many registers as its values.
+template <bool F32>
+struct Raw8 {
+  uint4v w[F32 ? 2 : 1];
+};
+
+// Elements [col, col + n) of a row that starts at p + row, n <= 8 of them (the
+// others 0). Whole groups go as 16-byte accesses whatever their alignment
+// (global memory takes unaligned ones). A row's last group n < 8 reads the
+// row's last eight and moves them down, since a loop over single elements
+// would wait for each; only rows shorter than eight are read so.
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t row, int col, int n) {
+  constexpr int E = F32 ? 4 : 2, W = F32 ? 8 : 4;
+  Raw8<F32> r;
+  uint32_t w[W];
+  const int up = col >= 8 || n == 8 ? 8 - n : 0;  // elements to read before col
+  if (n > 0 && (n == 8 || col >= 8)) {
+    __builtin_memcpy(w, static_cast<const char*>(p) + (row + col - up) * E, 8 * E);
   } else {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + off;
-    if (n == 8) {
-      uint4v w;
-      __builtin_memcpy(&w, q, 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[2 * i] = bf16_to_f32(w[i] & 0xffffu), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      return;
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    if (n > 0) {
+#pragma unroll 1
+      for (int k = n - 1; k >= 0; --k) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 7; i > 0; --i) w[i] = w[i - 1];
+          w[0] = static_cast<const uint32_t*>(p)[row + col + k];
+        } else {
+#pragma unroll
+          for (int i = 3; i > 0; --i) w[i] = w[i] << 16 | w[i - 1] >> 16;
+          w[0] = w[0] << 16 | static_cast<const uint16_t*>(p)[row + col + k];
+        }
+      }
+    }
+  }
+  if (up > 0 && up < 8) {
+#pragma unroll
+    for (int b = 4; b > 0; b >>= 1) {
+      if (up & b) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = i + b < 8 ? w[i + b < 8 ? i + b : 7] : 0u;
+        } else if (b == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = w[i] >> 16 | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = i + b / 2 < 4 ? w[i + b / 2 < 4 ? i + b / 2 : 3] : 0u;
+        }
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll 1
-  for (int k = n - 1; k >= 0; --k) {
+  for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {
 #pragma unroll
-    for (int i = 7; i > 0; --i) v[i] = v[i - 1];
-    v[0] = f32 ? static_cast<const float*>(p)[off + k] : bf16_to_f32(static_cast<const uint16_t*>(p)[off + k]);
+  for (int i = 0; i < 8; ++i) {
+    if (F32)
+      v[i] = __uint_as_float(r.w[F32 ? i / 4 : 0][i % 4]);
+    else
+      v[i] = __uint_as_float(i % 2 ? r.w[0][i / 2] & 0xffff0000u : r.w[0][i / 2] << 16);
   }
 }
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t row, int col, int n, float (&v)[8]) {
+  unpack8<F32>(load_raw8<F32>(p, row, col, n), v);
+}
 
+// Eight elements to a row, or its last n < 8: one by one in a rolled loop over
+// a shifting register file, since these lines are in every kernel many times and
+// fetching instructions costs more than that loop.
 __device__ __forceinline__ void store8(void* p, int64_t off, int n, bool f32, const float (&v)[8]) {
   if (n == 8) {
     if (f32) {
@@ -84,56 +125,6 @@ __device__ __forceinline__ void store8(void* p, int64_t off, int n, bool f32, co
       static_cast<uint16_t*>(p)[off + k] = f32_to_bf16(x[0]);
 #pragma unroll
     for (int i = 0; i < 7; ++i) x[i] = x[i + 1];
-  }
-}
-
-// Eight elements as they lie in memory: held so, a row on its way takes half
-// (bf16) or as many registers as its values.
-template <bool F32>
-struct Raw8 {
-  uint4v w[F32 ? 2 : 1];
-};
-template <bool F32>
-__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t off, int n) {
-  Raw8<F32> r;
-  if (n == 8) {
-    if constexpr (F32) {
-      const float* q = static_cast<const float*>(p) + off;
-      __builtin_memcpy(&r.w[0], q, 16);
-      __builtin_memcpy(&r.w[1], q + 4, 16);
-    } else {
-      __builtin_memcpy(&r.w[0], static_cast<const uint16_t*>(p) + off, 16);
-    }
-    return r;
-  }
-  constexpr int W = F32 ? 8 : 4;
-  uint32_t w[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) w[i] = 0;
-#pragma unroll 1
-  for (int k = n - 1; k >= 0; --k) {
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 7; i > 0; --i) w[i] = w[i - 1];
-      w[0] = __float_as_uint(static_cast<const float*>(p)[off + k]);
-    } else {
-#pragma unroll
-      for (int i = 3; i > 0; --i) w[i] = w[i] << 16 | w[i - 1] >> 16;
-      w[0] = w[0] << 16 | static_cast<const uint16_t*>(p)[off + k];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
-  return r;
-}
-template <bool F32>
-__device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (F32)
-      v[i] = __uint_as_float(r.w[F32 ? i / 4 : 0][i % 4]);
-    else
-      v[i] = __uint_as_float(i % 2 ? r.w[0][i / 2] & 0xffff0000u : r.w[0][i / 2] << 16);
   }
 }
 

@@ -110,8 +110,8 @@ template <bool F32>
 __device__ __forceinline__ void load_gu(const EpiArgs& e, bool row_in, int64_t og, int col, int N, Raw8<F32>& g, Raw8<F32>& u) {
   const int width = e.pad_to > N ? e.pad_to : N;
   if (row_in && col < width) {
-    g = load_raw8<F32>(e.g, og, 8);
-    u = load_raw8<F32>(e.u, og, 8);
+    g = load_raw8<F32>(e.g, og, 0, 8);
+    u = load_raw8<F32>(e.u, og, 0, 8);
   }
 }
 

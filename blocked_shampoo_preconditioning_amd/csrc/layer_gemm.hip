@@ -438,15 +438,15 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = w[q] = 0.f;
     const int64_t jump = plane * g.problems * parts;
-    const float* p = g.partial + static_cast<int64_t>(problem) * parts * plane + row * g.N + col;
+    const float* p = g.partial + static_cast<int64_t>(problem) * parts * plane;
     constexpr int U = 4;  // parts in flight
     for (int s = 0; s < g.splits; s += U, p += U * jump) {
       float x[U][8], y[U][8];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int m = s + k < g.splits ? n : 0;
-        load8(p + k * jump, 0, m, true, x[k]);
-        if (EPI == kGate) load8(p + k * jump + plane, 0, m, true, y[k]);
+        load8<true>(p + k * jump, row * g.N, col, m, x[k]);
+        if (EPI == kGate) load8<true>(p + k * jump + plane, row * g.N, col, m, y[k]);
       }
 #pragma unroll
       for (int k = 0; k < U; ++k)
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(256) void max_kernel(PackList l) {
       int64_t row;
       int col;
       group_place(at < total ? at : 0, c8, total, row, col);
-      load8(p.src, row * p.ld + col, at < total ? static_cast<int>(min<int64_t>(8, p.cols - col)) : 0, true, v[k]);
+      load8<true>(p.src, row * p.ld, col, at < total ? static_cast<int>(min<int64_t>(8, p.cols - col)) : 0, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
     int col;
     group_place(i, c8, total, row, col);
     const int n = static_cast<int>(min<int64_t>(8, p.cols - col));
-    const Raw8<F32> raw = load_raw8<F32>(p.src, row * p.ld + col, n);
+    const Raw8<F32> raw = load_raw8<F32>(p.src, row * p.ld, col, n);
     uint16_t* out = p.out + row * p.ld_out + col;
     if (!F32) {
       *reinterpret_cast<uint4v*>(out) = raw.w[0];

@@ -208,11 +208,12 @@ struct Ffn {
   }
   // The forward products of a few tokens, weights as the caller has them.
   void few_product(shl::DecodeArgs& g, shl::Epi epi) {
-    const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K);
+    const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K, f32);
     int64_t s = 1;
     if (groups < 192) {
       s = 512 / groups;
-      if (s > batches / 16) s = batches / 16;
+      const int64_t most = f32 || N > 16 ? batches / 8 : batches / 16;  // a batch for each wave
+      if (s > most) s = most;
       if (s > 32) s = 32;
     }
     g.splits = static_cast<int32_t>(s < 1 ? 1 : s);

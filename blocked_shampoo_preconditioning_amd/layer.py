@@ -64,15 +64,18 @@ _DTYPES = {torch.bfloat16: SHAMPOO_BF16, torch.float32: SHAMPOO_F32}
 _U64, _U32 = 0xFFFFFFFFFFFFFFFF, 0xFFFFFFFF
 
 
-def _call(name, args, like, *more):
-    """Runs an entry point on `like`'s device and torch's current stream there."""
+# The current stream's handle: torch.cuda.current_stream builds a Stream object for it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(name, args, dev, *more):
+    """Runs an entry point on device `dev` and torch's current stream there."""
     fn = getattr(_lib or load_library(), name)
-    dev = like.get_device()
     if dev == torch.cuda.current_device():
-        code = fn(args, *more, torch.cuda.current_stream(dev).cuda_stream)
+        code = fn(args, *more, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(args, *more, torch.cuda.current_stream(dev).cuda_stream)
+            code = fn(args, *more, _raw_stream(dev))
     if code:
         _s._check(code)
 
@@ -98,13 +101,16 @@ def _first(name, t):
     return code, rows, cols
 
 
+def _unlike(name, t, like):
+    return ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+
+
 def _matrix(name, t, rows, cols, like):
     """(pointer, leading dimension) of a 2-D tensor of that shape, dtype and device."""
     if t.dtype is not like.dtype or t.get_device() != like.get_device():
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({rows}, {cols})")
+        raise _unlike(name, t, like)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous (stride {t.stride()})")
@@ -121,14 +127,22 @@ def _vector(name, t, n, like):
     if t is None:
         return 0
     if t.dtype is not like.dtype or t.get_device() != like.get_device():
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise _unlike(name, t, like)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements, got shape {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _new(like, rows, cols):
     return like.new_empty((rows, cols))
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape, dtype and device."""
+    return torch.empty_like(t, memory_format=_CONTIGUOUS)
+
+
+_CONTIGUOUS = torch.contiguous_format
 
 
 def _workspace(nbytes, like):
@@ -180,14 +194,14 @@ def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
     activation: "silu", "gelu" (tanh form) or "relu"."""
     fields = _ffn_inputs(x, w_gate, w_up, w_down, activation)
     n, d, f = fields[:3]
-    y = _new(x, n, d)
+    y = _new_like(x)
     saved = None
     if save:
         saved = torch.empty(_saved_size(fields), dtype=torch.uint8, device=x.device)
     args = _FFN.pack(*fields, y.data_ptr() or 256, d, saved.data_ptr() if save else 0, *_NO_GRADIENTS)
     size = _ffn_workspace(fields, args, 0, save)
     ws, keep = _workspace(size, x)
-    _call("shampoo_ffn_forward", args, x, ws, size)
+    _call("shampoo_ffn_forward", args, x.get_device(), ws, size)
     return (y, saved) if save else y
 
 
@@ -207,17 +221,17 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation="silu", need_dx=
     pdy, ldy = _matrix("dy", dy, n, d, x)
     if saved.dtype is not torch.uint8 or saved.numel() != _saved_size(fields) or saved.get_device() != x.get_device():
         raise ValueError("saved is not what ffn_forward kept for these sizes")
-    dx = _new(x, n, d) if need_dx else None
+    dx = _new_like(x) if need_dx else None
     dwg = dwu = dwd = None
     pointers = (dx.data_ptr() or 256 if need_dx else 0, 0, 0, 0)
     if need_dw:
-        dwg, dwu, dwd = _new(x, d, f), _new(x, d, f), _new(x, f, d)
+        dwg, dwu, dwd = _new_like(w_gate), _new_like(w_up), _new_like(w_down)
         pointers = (pointers[0], dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr())
     if need_dx or need_dw:
         args = _FFN.pack(*fields, 0, 0, saved.data_ptr(), pdy, ldy, *pointers, d, f, f, d)
         size = _ffn_workspace(fields, args, 1, (need_dx, need_dw, ldy, pdy & 15))
         ws, keep = _workspace(size, x)
-        _call("shampoo_ffn_backward", args, x, ws, size)
+        _call("shampoo_ffn_backward", args, x.get_device(), ws, size)
     return dx, dwg, dwu, dwd
 
 
@@ -261,12 +275,12 @@ def residual_forward(x, z, *, post="rms", post_weight=None, post_bias=None, gate
     px, lx = _matrix("x", x, n, d, x)
     pz, lz = _matrix("z", z, n, d, x)
     vectors = _norm_vectors(x, n, d, post_weight, post_bias, gate, head[-1], next_weight, next_bias)
-    r = _new(x, n, d)
-    out = _new(x, n, d) if head[4] else None
+    r = _new_like(x)
+    out = _new_like(x) if head[4] else None
     stats = torch.empty((n, 4), dtype=torch.float32, device=x.device)
     args = _NORM.pack(*head, pz, px, lz, lx, r.data_ptr(), out.data_ptr() if out is not None else 0, d, d, *vectors,
                       stats.data_ptr(), *_NO_NORM_GRADIENTS)
-    _call("shampoo_norm_forward", args, x)
+    _call("shampoo_norm_forward", args, x.get_device())
     return r, out, stats
 
 
@@ -278,10 +292,10 @@ def norm_forward(x, kind="rms", weight=None, bias=None, eps=1e-6):
     head = _norm_head(dt, n, d, "none", kind, eps, 1.0, 0.0, 0, 0, None)
     px, lx = _matrix("x", x, n, d, x)
     vectors = _norm_vectors(x, n, d, None, None, None, 1, weight, bias)
-    out = _new(x, n, d)
+    out = _new_like(x)
     stats = torch.empty((n, 4), dtype=torch.float32, device=x.device)
     args = _NORM.pack(*head, 0, px, 0, lx, 0, out.data_ptr(), d, d, *vectors, stats.data_ptr(), *_NO_NORM_GRADIENTS)
-    _call("shampoo_norm_forward", args, x)
+    _call("shampoo_norm_forward", args, x.get_device())
     return out, stats
 
 
@@ -298,10 +312,10 @@ def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
         if dn is None:
             raise ValueError("dn is None: the next norm's gradient is needed")
         pdn, ldn = _matrix("dn", dn, n, d, x)
-    dx = _new(x, n, d)
-    dz = _new(x, n, d) if z is not None else None
+    dx = _new_like(x)
+    dz = _new_like(x) if z is not None else None
     # the vectors' gradients, in the struct's order: post weight, post bias, gate, next weight, next bias
-    grads = [x.new_empty(d) if vectors[i] else None for i in (0, 1, 2, 3, 4)]
+    grads = [x.new_empty(d) if v else None for v in vectors[:5]]
     if vectors[2]:
         grads[2] = _new(x, -(-n // head[10]), d)
     pointers = [g.data_ptr() if g is not None else 0 for g in grads]
@@ -312,7 +326,7 @@ def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
     if size is None:
         size = _sizes[key] = _size("shampoo_norm_workspace_size", args)
     ws, keep = _workspace(size, x)
-    _call("shampoo_norm_backward", args, x, ws, size)
+    _call("shampoo_norm_backward", args, x.get_device(), ws, size)
     return dx, dz, grads
 
 
@@ -353,10 +367,10 @@ def dropout(x, p, seed, offset=0, out=None):
     dt, n, d = _first("x", x)
     px, lx = _matrix("x", x, n, d, x)
     if out is None:
-        out, ly = _new(x, n, d), d
+        out, ly = _new_like(x), d
         py = out.data_ptr()
     else:
         py, ly = _matrix("out", out, n, d, x)
     args = _DROP.pack(n, d, dt, offset & _U32, p, seed & _U64, px, py, lx, ly)
-    _call("shampoo_dropout", args, x)
+    _call("shampoo_dropout", args, x.get_device())
     return out
