@@ -20,23 +20,22 @@ typedef __attribute__((ext_vector_type(4))) int int4v;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 halfx8;
 typedef __attribute__((ext_vector_type(4))) short short4v;
-typedef __attribute__((ext_vector_type(16))) float floatx16;
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kBK = 64;                 // K step
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ------------------------------------------------------------------ the tile
-// WM x WN waves of FM x FN fragments of 32 x 32.
-template <int FM_, int FN_, int WM_, int WN_>
+// WM x WN waves of FM x FN fragments of 16 x 16.
+template <int FM_, int FN_, int WM_, int WN_, int STAGES_ = 2>
 struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int NW = WM * WN, NT = NW * 64;
-  static constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
+  static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
   static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int PITCH = FN * 32 + 4;  // floats of a row of the epilogue's strips
-  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
+  static constexpr int PITCH = FN * 16 + 4;  // floats of a row of the epilogue's strips
+  static constexpr int LDS = STAGES * STAGE > NW * 32 * PITCH * 4 ? STAGES * STAGE : NW * 32 * PITCH * 4;
 };
 
 // LDS order of 16-byte chunks. A row operand's tile is [rows][64 k] (8 chunks
@@ -47,7 +46,7 @@ struct Tile {
 __device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 template <int WIDTH>
 __device__ __forceinline__ int swz_col(int k) {
-  return WIDTH == 128 ? ((k & 3) << 1) ^ ((k & 3) << 2) : (k & 3) << 1;
+  return WIDTH == 128 ? ((k & 3) << 1) ^ ((k & 3) << 2) ^ ((k >> 1) & 4) : ((k & 3) << 1) ^ ((k >> 2) & 2);
 }
 
 // A buffer of `left` bytes from base (below 2 GiB are enough: a tile's offsets
@@ -88,17 +87,20 @@ __device__ __forceinline__ bf16x8 lds_read_tr(const char* p, int second) {
   return x.v;
 }
 
-// The operands' 16 bits are bf16, or fp16 for the planes of fp32 values.
+// The operands' 16 bits are bf16, or fp16 for the planes of fp32 values. The
+// 16 x 16 x 32 instruction takes less power than the 32 x 32 x 16 one (2090
+// against 1860 TFLOP/s sustained from registers), and power is what limits the
+// large products.
 template <bool F16>
-__device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const floatx16& c) {
+__device__ __forceinline__ floatx4 mfma(const bf16x8& a, const bf16x8& b, const floatx4& c) {
   if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(T::NT, T::FM * T::FN > 8 ? 1 : 2) void gemm_kernel(GemmArgs g) {
+__global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
   constexpr bool GATE = EPI == kGate;
   constexpr int HN = GATE ? T::BN / 2 : T::BN;       // result columns of a tile
   constexpr int BW = GATE ? T::BN / 2 : 128;         // width of a B panel
@@ -221,120 +223,151 @@ __global__ __launch_bounds__(T::NT, T::FM * T::FN > 8 ? 1 : 2) void gemm_kernel(
     for (int q = 0; q < NA + NB; ++q) load(q);
   };
 
-  // a lane's place in the fragment reads
-  const int half = lane >> 5, r32 = lane & 31;
-  // row operand: row r32 of a fragment, chunk 2 ks + half
+  // A lane's place in the fragment reads (16 rows or columns x 32 k, eight k of
+  // one row a lane).
+  const int r16 = lane & 15, q4 = lane >> 4;
+  // row operand: row r16, chunk 4 ks + q4
   auto frag_row = [&](const char* tile, int row0, int ks) {
-    return lds_read16(tile + (row0 + r32) * 128 + (((2 * ks + half) ^ swz_row(r32)) << 4));
+    return lds_read16(tile + (row0 + r16) * 128 + (((4 * ks + q4) ^ swz_row(r16)) << 4));
   };
-  // column operand: k = 16 ks + 8 half + (lane % 16) / 4 (+ 4 in the second
-  // read), columns 16 ((lane / 16) % 2) + 4 (lane % 4)
-  const int kk = (lane & 15) >> 2;
+  // column operand: k = 32 ks + 8 q4 + (lane % 16) / 4 (+ 4 in the second
+  // read), columns 4 (lane % 4) on
+  const int kk = 8 * q4 + (r16 >> 2);
   auto frag_col = [&](const char* tile, int width, int col0, int ks) {
-    const int c = (col0 >> 3) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int c = (col0 >> 3) + ((lane & 3) >> 1);
     const int s = width == 128 ? swz_col<128>(kk) : swz_col<64>(kk);
-    const char* p = tile + (16 * ks + 8 * half + kk) * (width * 2) + ((c ^ s) << 4) + (lane & 1) * 8;
+    const char* p = tile + (32 * ks + kk) * (width * 2) + ((c ^ s) << 4) + (lane & 1) * 8;
     return lds_read_tr(p, 4 * width * 2);
   };
   auto frag_a = [&](const char* st, int i, int ks) {
-    const int row = wm * T::FM * 32 + i * 32;  // within the tile
+    const int row = (wm * T::FM + i) * 16;  // within the tile
     if (ACOL) return frag_col(st + (row >> 7) * 16384, 128, row & 127, ks);
     return frag_row(st, row, ks);
   };
   auto frag_b = [&](const char* st, int j, int ks) {
     const char* bt = st + T::A_BYTES;
-    if (GATE) {  // even fragments: gate panel, odd: up panel
-      const int col = wn * (T::FN / 2) * 32 + (j >> 1) * 32;
-      return frag_col(bt + (j & 1) * (BW * kBK * 2), BW, col, ks);
+    if (GATE) {  // a wave's first half of the fragments: gate panel, second: up panel
+      constexpr int H = T::FN / 2;
+      return frag_col(bt + (j / H) * (BW * kBK * 2), BW, (wn * H + j % H) * 16, ks);
     }
-    const int col = wn * T::FN * 32 + j * 32;
+    const int col = (wn * T::FN + j) * 16;
     if (BCOL) return frag_col(bt + (col >> 7) * 16384, 128, col & 127, ks);
     return frag_row(bt, col, ks);
   };
 
-  floatx16 acc[T::FM][T::FN];
+  floatx4 acc[T::FM][T::FN];
 #pragma unroll
   for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    for (int j = 0; j < T::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // The K loop, software-pipelined: a K step is four slices of 16; each
-  // slice's fragments are read from LDS while the matrix cores work on the one
-  // before, also across the barrier between two steps. At the barrier a wave's
-  // loads of the next step have landed and its reads of this step are done, so
-  // after it the next step can be read and this step's buffer be filled again.
-  bf16x8 a0[T::FM], b0[T::FN], a1[T::FM], b1[T::FN];
-  auto read = [&](const char* st, int ks, bf16x8(&a)[T::FM], bf16x8(&b)[T::FN]) {
+  // The K loop, software-pipelined. A K step is two slices of 32, a slice two
+  // phases: the fragments of the operand that has more of them (M: x rows, else
+  // columns) come in two halves, the other's whole. Each phase's fragments are
+  // read from LDS while the matrix cores work on the phase before, also across
+  // the barrier between two steps. At the barrier a wave's loads of the next
+  // step have landed and its reads of this step are done, so after it the next
+  // step can be read and this step's buffer be filled again, which the last
+  // phase does with its loads between the products.
+  constexpr bool HALVE_A = T::FM >= T::FN;
+  constexpr int H = (HALVE_A ? T::FM : T::FN) / 2, F = HALVE_A ? T::FN : T::FM;
+  bf16x8 lo[H], hi[H], full0[F], full1[F];
+  auto read_half = [&](const char* st, int ks, int half, bf16x8(&x)[H]) {
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) b[j] = frag_b(st, j, ks);
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i) a[i] = frag_a(st, i, ks);
+    for (int i = 0; i < H; ++i) x[i] = HALVE_A ? frag_a(st, half * H + i, ks) : frag_b(st, half * H + i, ks);
   };
-  // one slice's products, with the LDS reads before them in the program spread between them
-  constexpr int kReads = (ACOL ? 2 : 1) * T::FM + (BCOL ? 2 : 1) * T::FN, kMma = T::FM * T::FN;
-  auto mma = [&](const bf16x8(&a)[T::FM], const bf16x8(&b)[T::FN]) {
+  auto read_full = [&](const char* st, int ks, bf16x8(&x)[F]) {
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i)
+    for (int i = 0; i < F; ++i) x[i] = HALVE_A ? frag_b(st, i, ks) : frag_a(st, i, ks);
+  };
+  constexpr int kMma = H * F;
+  auto product = [&](int half, int q, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
+    const int h = q / F, f = q % F;
+    if (HALVE_A) {
+      floatx4& c = acc[half * H + h][f];
+      c = mfma<F32>(y[f], x[h], c);
+    } else {
+      floatx4& c = acc[f][half * H + h];
+      c = mfma<F32>(x[h], y[f], c);
+    }
+  };
+  // one phase's products, with the LDS reads before them in the program spread
+  // between them (a read of a row operand is one instruction, of a column
+  // operand two)
+  constexpr int kHalfReads = H * ((HALVE_A ? ACOL : BCOL) ? 2 : 1), kFullReads = F * ((HALVE_A ? BCOL : ACOL) ? 2 : 1);
+  auto mma = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F], int reads) {
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j) acc[i][j] = mfma<F32>(b[j], a[i], acc[i][j]);
+    for (int q = 0; q < kMma; ++q) product(half, q, x, y);
+    if (reads == kHalfReads) {
 #pragma unroll
-    for (int q = 0; q < kMma; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMma - 1) / kMma, 0);
+      for (int q = 0; q < kMma; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kMma / 2 - 1) / (kMma / 2), 0);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kMma; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kFullReads + kMma / 2 - 1) / (kMma / 2), 0);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   // the same with a step's loads between them
-  auto mma_load = [&](const bf16x8(&a)[T::FM], const bf16x8(&b)[T::FN]) {
+  auto mma_load = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
+    constexpr int kEach = (NA + NB + kMma - 1) / kMma;
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < T::FN; ++j) {
-        acc[i][j] = mfma<F32>(b[j], a[i], acc[i][j]);
-        constexpr int kEach = (NA + NB + kMma - 1) / kMma;
+    for (int q = 0; q < kMma; ++q) {
+      product(half, q, x, y);
+      if (q * kEach < NA + NB) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e)
-          if ((i * T::FN + j) * kEach + e < NA + NB) load((i * T::FN + j) * kEach + e);
+          if (q * kEach + e < NA + NB) load(q * kEach + e);
         __builtin_amdgcn_sched_barrier(0);
       }
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
+  // loads that may be on their way when the next step has landed
+  constexpr int kAhead = (T::STAGES - 2) * (NA + NB);
   if (first < last) {
-    issue(0, true);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    issue(1, first + 1 < last);
-    read(lds, 0, a0, b0);
+#pragma unroll
+    for (int i = 0; i < T::STAGES; ++i) issue(i, first + i < last);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kAhead + NA + NB) : "memory");
+    read_half(lds, 0, 0, lo);
+    read_full(lds, 0, full0);
     __builtin_amdgcn_sched_barrier(0);
   }
+  int buf = 0;
   for (int step = first; step < last; ++step) {
-    const int buf = (step - first) & 1;
     const char* st = lds + buf * T::STAGE;
-    aim(buf, step + 2 < last);
-    read(st, 1, a1, b1);
-    mma(a0, b0);
-    read(st, 2, a0, b0);
-    mma(a1, b1);
-    read(st, 3, a1, b1);
-    mma(a0, b0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read(lds + (buf ^ 1) * T::STAGE, 0, a0, b0);
+    aim(buf, step + T::STAGES < last);
+    buf = buf + 1 == T::STAGES ? 0 : buf + 1;
+    read_half(st, 0, 1, hi);
+    mma(0, lo, full0, kHalfReads);
+    read_half(st, 1, 0, lo);
+    read_full(st, 1, full1);
+    mma(1, hi, full0, kHalfReads + kFullReads);
+    read_half(st, 1, 1, hi);
+    mma(0, lo, full1, kHalfReads);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead) : "memory");
+    read_half(lds + buf * T::STAGE, 0, 0, lo);
+    read_full(lds + buf * T::STAGE, 0, full0);
     __builtin_amdgcn_sched_barrier(0);
-    mma_load(a1, b1);
+    mma_load(1, hi, full1);
   }
 
-  // Epilogue. A lane's accumulators are column r32 (row m of the result) and
-  // rows 8 q + 4 half + 0..3 (result columns n) of each fragment: FN fragments
-  // pass through a wave-private LDS strip and come back as eight columns of
-  // one row a lane, so that stores are 16 bytes a lane and whole row segments.
-  // kActBwd reads g and u one fragment row ahead, since a load waits for the
-  // stores before it (fp32: its own row, for want of registers).
+  // Epilogue. A lane's accumulators are column r16 (row m of the result) and
+  // rows 4 q4 + 0..3 (result columns n) of each fragment: two rows of FN
+  // fragments pass through a wave-private LDS strip and come back as eight
+  // columns of one row a lane, so that stores are 16 bytes a lane and whole row
+  // segments. kActBwd reads g and u one strip ahead, since a load waits for the
+  // stores before it (fp32: its own strip, for want of registers).
   constexpr int AHEAD = F32 ? 0 : 1;
   constexpr int PITCH = T::PITCH;
-  constexpr int COLS = GATE ? T::FN * 16 : T::FN * 32;           // result columns of a wave
+  constexpr int COLS = GATE ? T::FN * 8 : T::FN * 16;            // result columns of a wave
   constexpr int LR = COLS / 8, RP = 64 / LR, NP = 32 / RP;       // lanes a row, rows a pass, passes
-  const int row0 = m0 + wm * T::FM * 32 + lane / LR;
+  const int row0 = m0 + wm * T::FM * 16 + lane / LR;
   const int c8 = (lane % LR) * 8, col = n0 + wn * COLS + c8;
   const int64_t ldc = EPI == kStore && problem ? g.e.ldc1 : g.e.ldc;
   const int64_t oc = row0 * ldc + col, og = row0 * g.e.ldg + col;
@@ -352,28 +385,23 @@ __global__ __launch_bounds__(T::NT, T::FM * T::FN > 8 ? 1 : 2) void gemm_kernel(
   if (F32) exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
   float largest = 0.f;
 #pragma unroll
-  for (int i = 0; i < T::FM; ++i) {
-    if (act_bwd && i + AHEAD < T::FM) {
+  for (int i = 0; i < T::FM / 2; ++i) {
+    if (act_bwd && i + AHEAD < T::FM / 2) {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
         load_gu<F32>(g.e, row0 + (i + AHEAD) * 32 + p * RP < g.M, og + ((i + AHEAD) * 32 + p * RP) * g.e.ldg, col, g.N,
                      gr[(i + AHEAD) & AHEAD][p], ur[(i + AHEAD) & AHEAD][p]);
     }
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        floatx4 x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = acc[i][j][4 * q + r];
-        *reinterpret_cast<floatx4*>(strip + r32 * PITCH + j * 32 + 8 * q + 4 * half) = x;
-      }
+      for (int j = 0; j < T::FN; ++j) *reinterpret_cast<floatx4*>(strip + (h * 16 + r16) * PITCH + j * 16 + 4 * q4) = acc[2 * i + h][j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     auto strip8 = [&](int p, float(&v)[8], float(&w)[8]) {
-      const float* x = strip + (p * RP + lane / LR) * PITCH + (GATE ? (c8 >> 5) * 64 + (c8 & 31) : c8);
+      const float* x = strip + (p * RP + lane / LR) * PITCH + c8;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = x[q], w[q] = GATE ? x[32 + q] : 0.f;
+      for (int q = 0; q < 8; ++q) v[q] = x[q], w[q] = GATE ? x[COLS + q] : 0.f;
     };
     if (g.splits > 1) {
       constexpr int parts = GATE ? 2 : 1;
@@ -550,8 +578,8 @@ __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
 // 256 tiles run as eight waves of 128 x 64 (kGate: 64 x 128, so that a wave's
 // rows of h are whole 128-byte segments).
 template <int EPI>
-using Tile256 = Tile<EPI == kGate ? 2 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
-using Tile128 = Tile<2, 2, 2, 2>;
+using Tile256 = Tile<EPI == kGate ? 4 : 8, EPI == kGate ? 8 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
+using Tile128 = Tile<4, 4, 2, 2>;
 
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
