@@ -27,15 +27,15 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ------------------------------------------------------------------ the tile
 // WM x WN waves of FM x FN fragments of 16 x 16.
-template <int FM_, int FN_, int WM_, int WN_, int STAGES_ = 2>
+template <int FM_, int FN_, int WM_, int WN_>
 struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
   static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int PITCH = FN * 16 + 4;  // floats of a row of the epilogue's strips
-  static constexpr int LDS = STAGES * STAGE > NW * 32 * PITCH * 4 ? STAGES * STAGE : NW * 32 * PITCH * 4;
+  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
 };
 
 // LDS order of 16-byte chunks. A row operand's tile is [rows][64 k] (8 chunks
@@ -49,41 +49,40 @@ __device__ __forceinline__ int swz_col(int k) {
   return WIDTH == 128 ? ((k & 3) << 1) ^ ((k & 3) << 2) ^ ((k >> 1) & 4) : ((k & 3) << 1) ^ ((k >> 2) & 2);
 }
 
-// A buffer of `left` bytes from base (below 2 GiB are enough: a tile's offsets
-// stay under that); loads past it give zeros. Its length is rounded up to a
-// whole word, which the hardware checks.
-__device__ __forceinline__ int4v make_rsrc(const char* base, int64_t left) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  int64_t n = left < 0 ? 0 : (left + 3) & ~int64_t(3);
-  n = n > 0x7ffffff0 ? 0x7ffffff0 : n;
+// A buffer of `left` >= 0 bytes from base (2 GiB of them are enough: a tile's
+// offsets stay under that); loads past it give zeros. The hardware checks whole
+// words, so its length is rounded up to one.
+__device__ __forceinline__ int4v make_rsrc(uint64_t base, int64_t left) {
+  const uint32_t n = static_cast<uint32_t>(left) + 3u & ~3u;
   int4v r;
-  r[0] = static_cast<int>(b);
-  r[1] = static_cast<int>(b >> 32) & 0xffff;
-  r[2] = static_cast<int>(n);
+  r[0] = static_cast<int>(base);
+  r[1] = static_cast<int>(base >> 32);
+  r[2] = static_cast<int>(static_cast<uint32_t>(left >> 30) > 1u ? 0x7ffffff0u : n);
   r[3] = 0x00020000;
   return r;
 }
 
-// 64 x 16 bytes from rsrc + voff (a lane's own) to LDS at `lds` + 16 * lane.
-// Written as asm because the compiler would wait for every such load before
-// any transposing LDS read; it has no register results, and its arrival is
-// waited for at the barrier of the next K step.
-__device__ __forceinline__ void load_lds(const int4v& rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+// 64 x 16 bytes from rsrc + voff (a lane's own) to LDS at `lds` + plus + 16 *
+// lane. Written as asm because the compiler would wait for every such load
+// before any transposing LDS read; it has no register results, and its arrival
+// is waited for at the barrier of the next K step.
+__device__ __forceinline__ void load_lds(const int4v& rsrc, uint32_t voff, uint32_t lds, int plus) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
-               : "s"(lds), "v"(voff), "s"(rsrc)
-               : "memory");
+               : "s"(lds), "v"(voff), "s"(rsrc), "i"(plus)
+               : "memory", "scc");
 }
 
-__device__ __forceinline__ bf16x8 lds_read16(const char* p) { return *reinterpret_cast<const bf16x8*>(p); }
-__device__ __forceinline__ bf16x8 lds_read_tr(const char* p, int second) {
-  typedef __attribute__((address_space(3))) short4v* P;
+typedef __attribute__((address_space(3))) const bf16x8* lds_frag;
+typedef __attribute__((address_space(3))) short4v* lds_quad;
+__device__ __forceinline__ bf16x8 lds_read16(uint32_t at) { return *reinterpret_cast<lds_frag>(at); }
+__device__ __forceinline__ bf16x8 lds_read_tr(uint32_t at, int second) {
   union {
     short4v s[2];
     bf16x8 v;
   } x;
-  x.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p));
-  x.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + second));
+  x.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_quad>(at));
+  x.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_quad>(at + second));
   return x.v;
 }
 
@@ -175,84 +174,123 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
   const int64_t b_size = (BCOL ? (static_cast<int64_t>(g.k_real) - 1) * ldb2 + 2 * static_cast<int64_t>(g.N)
                                : (static_cast<int64_t>(g.N) - 1) * ldb2 + 2 * static_cast<int64_t>(g.K)) - b_start;
 
-  // where the loads are: segment, K of the step, the operands' buffers
+  // Where the loads are: segment, K of the step, the operands' buffers. Every
+  // instruction here is paid for in every K step, so a step moves the buffers by
+  // a few scalar additions; a row operand's chunks past K, which only a
+  // segment's last step can have, get an offset out of range once.
+  const int64_t a_step = ACOL ? kBK * lda2 : kBK * 2, b_step = BCOL ? kBK * ldb2 : kBK * 2;
   int seg = 0;
   if (first) seg = first / ksteps;
   int k0 = (first - seg * ksteps) * kBK;
-  const char *pa, *pb, *pb1;
-  auto enter = [&]() {
-    pa = reinterpret_cast<const char*>(g.a[seg]) + a_start;
-    pb = reinterpret_cast<const char*>(GATE ? g.b[0][seg] : g.b[problem][seg]) + b_start;
-    pb1 = GATE ? reinterpret_cast<const char*>(g.b[1][seg]) + b_start : nullptr;
+  int loads = last - first;  // steps still to be loaded
+  uint64_t pa = 0, pb = 0, pb1 = 0;
+  int64_t left_a = 0, left_b = 0;
+  bool cut = false;
+  auto cut_chunks = [&]() {
+    const bool now = (!ACOL || !BCOL) && k0 + kBK > g.K;
+    if (now == cut) return;
+    cut = now;
+    const uint32_t bit = now && k0 + rchunk * 8 >= g.K ? kOutOfRange : 0u;
+#pragma unroll
+    for (int j = 0; j < NA; ++j)
+      if (!ACOL) va[j] = (va[j] & ~kOutOfRange) | bit;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      if (!BCOL) vb[j] = (vb[j] & ~kOutOfRange) | bit;
   };
-  enter();
-  // One step's loads: the buffers, then NA + NB instructions, then the move to
-  // the next step.
+  auto enter = [&]() {
+    const int64_t ka = k0 / kBK * a_step, kb = k0 / kBK * b_step;
+    pa = reinterpret_cast<uint64_t>(g.a[seg]) + a_start + ka;
+    pb = reinterpret_cast<uint64_t>(GATE ? g.b[0][seg] : g.b[problem][seg]) + b_start + kb;
+    if (GATE) pb1 = reinterpret_cast<uint64_t>(g.b[1][seg]) + b_start + kb;
+    left_a = a_size - ka;
+    left_b = b_size - kb;
+    cut_chunks();
+  };
   int4v ra, rb, rb1;
-  uint32_t ko = 0, at = 0;
-  bool tail = false, in = false;
-  auto aim = [&](int buf, bool more) {
+  uint32_t at = 0;
+  auto aim = [&](int buf) {
     at = lds0 + buf * T::STAGE;
-    const int64_t ka = ACOL ? k0 * lda2 : 0, kb = BCOL ? k0 * ldb2 : 0;
     // past the last step nothing is read: zeros go to a buffer that nobody reads
-    ra = make_rsrc(pa + ka, more ? a_size - ka : 0);
-    rb = make_rsrc(pb + kb, more ? b_size - kb : 0);
-    if (GATE) rb1 = make_rsrc(pb1 + kb, more ? b_size - kb : 0);
-    ko = static_cast<uint32_t>(k0) * 2;
-    tail = (!ACOL || !BCOL) && k0 + kBK > g.K;  // some chunks of a row are past K
-    in = k0 + rchunk * 8 < g.K;
+    ra = make_rsrc(pa, loads > 0 ? left_a : 0);
+    rb = make_rsrc(pb, loads > 0 ? left_b : 0);
+    if (GATE) rb1 = make_rsrc(pb1, loads > 0 ? left_b : 0);
+  };
+  auto load = [&](int q) {
+    const int j = q < NA ? q : q - NA;
+    load_lds(q < NA ? ra : (GATE && j >= BPP ? rb1 : rb), q < NA ? va[j] : vb[j], at,
+             (q < NA ? 0 : T::A_BYTES) + j * T::NW * 1024);
+  };
+  auto advance = [&]() {
+    if (--loads <= 0) return;
     k0 += kBK;
-    if (k0 >= g.K && more && ++seg < g.nseg) {
+    if (k0 < g.K) {
+      pa += a_step, pb += b_step;
+      if (GATE) pb1 += b_step;
+      left_a -= a_step, left_b -= b_step;
+      if (k0 + kBK > g.K) cut_chunks();
+    } else {
+      ++seg;
       k0 = 0;
       enter();
     }
   };
-  auto load = [&](int q) {
-    const int j = q < NA ? q : q - NA;
-    const bool rows = q < NA ? !ACOL : !BCOL;
-    uint32_t v = q < NA ? va[j] : vb[j];
-    if (rows) {
-      v += ko;
-      if (tail) v = in ? v : kOutOfRange;
-    }
-    load_lds(q < NA ? ra : (GATE && j >= BPP ? rb1 : rb), v, at + (q < NA ? 0 : T::A_BYTES) + j * T::NW * 1024);
-  };
-  auto issue = [&](int buf, bool more) {
-    aim(buf, more);
-#pragma unroll
-    for (int q = 0; q < NA + NB; ++q) load(q);
-  };
 
-  // A lane's place in the fragment reads (16 rows or columns x 32 k, eight k of
-  // one row a lane).
+  // A lane's places in the fragment reads (16 rows or columns x 32 k, eight k of
+  // one row a lane), as LDS addresses of the buffer that is read.
   const int r16 = lane & 15, q4 = lane >> 4;
-  // row operand: row r16, chunk 4 ks + q4
-  auto frag_row = [&](const char* tile, int row0, int ks) {
-    return lds_read16(tile + (row0 + r16) * 128 + (((4 * ks + q4) ^ swz_row(r16)) << 4));
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
+  // row operand: row r16 of a fragment, chunk 4 ks + q4; fragments 2 KiB apart
+  auto row_at = [&](uint32_t tile, int row0, int ks) {
+    return static_cast<uint32_t>(tile + (row0 + r16) * 128 + (((4 * ks + q4) ^ swz_row(r16)) << 4));
   };
   // column operand: k = 32 ks + 8 q4 + (lane % 16) / 4 (+ 4 in the second
   // read), columns 4 (lane % 4) on
   const int kk = 8 * q4 + (r16 >> 2);
-  auto frag_col = [&](const char* tile, int width, int col0, int ks) {
+  auto col_at = [&](uint32_t tile, int width, int col0) {
     const int c = (col0 >> 3) + ((lane & 3) >> 1);
     const int s = width == 128 ? swz_col<128>(kk) : swz_col<64>(kk);
-    const char* p = tile + (32 * ks + kk) * (width * 2) + ((c ^ s) << 4) + (lane & 1) * 8;
-    return lds_read_tr(p, 4 * width * 2);
+    return static_cast<uint32_t>(tile + kk * (width * 2) + ((c ^ s) << 4) + (lane & 1) * 8);
   };
-  auto frag_a = [&](const char* st, int i, int ks) {
-    const int row = (wm * T::FM + i) * 16;  // within the tile
-    if (ACOL) return frag_col(st + (row >> 7) * 16384, 128, row & 127, ks);
-    return frag_row(st, row, ks);
-  };
-  auto frag_b = [&](const char* st, int j, int ks) {
-    const char* bt = st + T::A_BYTES;
-    if (GATE) {  // a wave's first half of the fragments: gate panel, second: up panel
-      constexpr int H = T::FN / 2;
-      return frag_col(bt + (j / H) * (BW * kBK * 2), BW, (wn * H + j % H) * 16, ks);
+  uint32_t fa[ACOL ? T::FM : 2], fb[BCOL ? T::FN : 2];
+  if (ACOL) {
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) {
+      const int row = (wm * T::FM + i) * 16;
+      fa[ACOL ? i : 0] = col_at(lds_base + (row >> 7) * 16384, 128, row & 127);
     }
-    const int col = (wn * T::FN + j) * 16;
-    if (BCOL) return frag_col(bt + (col >> 7) * 16384, 128, col & 127, ks);
-    return frag_row(bt, col, ks);
+  } else {
+    fa[0] = row_at(lds_base, wm * T::FM * 16, 0);
+    fa[1] = row_at(lds_base, wm * T::FM * 16, 1);
+  }
+  if (BCOL) {
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) {
+      // kGate: a wave's first half of the fragments gate panel, second: up panel
+      constexpr int H2 = T::FN / 2;
+      const int col = GATE ? (wn * H2 + j % H2) * 16 : (wn * T::FN + j) * 16;
+      const int panel = GATE ? j / H2 : col >> 7;
+      fb[BCOL ? j : 0] = col_at(lds_base + T::A_BYTES + panel * (BW * kBK * 2), BW, GATE ? col : col & 127);
+    }
+  } else {
+    fb[0] = row_at(lds_base + T::A_BYTES, wn * T::FN * 16, 0);
+    fb[1] = row_at(lds_base + T::A_BYTES, wn * T::FN * 16, 1);
+  }
+  auto frag_a = [&](int i, int ks) {
+    if (ACOL) return lds_read_tr(fa[ACOL ? i : 0] + ks * (32 * 256), 4 * 256);
+    return lds_read16(fa[ks] + i * 2048);
+  };
+  auto frag_b = [&](int j, int ks) {
+    if (BCOL) return lds_read_tr(fb[BCOL ? j : 0] + ks * (32 * BW * 2), 4 * BW * 2);
+    return lds_read16(fb[ks] + j * 2048);
+  };
+  uint32_t flip = T::STAGE;
+  auto other_buffer = [&]() {
+#pragma unroll
+    for (uint32_t& x : fa) x += flip;
+#pragma unroll
+    for (uint32_t& x : fb) x += flip;
+    flip = 0u - flip;
   };
 
   floatx4 acc[T::FM][T::FN];
@@ -261,24 +299,26 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // The K loop, software-pipelined. A K step is two slices of 32, a slice two
-  // phases: the fragments of the operand that has more of them (M: x rows, else
-  // columns) come in two halves, the other's whole. Each phase's fragments are
-  // read from LDS while the matrix cores work on the phase before, also across
-  // the barrier between two steps. At the barrier a wave's loads of the next
-  // step have landed and its reads of this step are done, so after it the next
-  // step can be read and this step's buffer be filled again, which the last
-  // phase does with its loads between the products.
-  constexpr bool HALVE_A = T::FM >= T::FN;
-  constexpr int H = (HALVE_A ? T::FM : T::FN) / 2, F = HALVE_A ? T::FN : T::FM;
+  // The K loop, software-pipelined. A K step is two slices of 32. In the large
+  // tiles a slice is two phases, for want of registers: the fragments of the
+  // operand that has more of them come in two halves, the other's whole; in the
+  // small ones it is one (H: fragments of the first operand at a time, F: of
+  // the other). Each phase's fragments are read from LDS while the matrix cores
+  // work on the phase before, also across the barrier between two steps. At the
+  // barrier a wave's loads of the next step have landed and its reads of this
+  // step are done, so after it the next step can be read and this step's buffer
+  // be filled again, which the last phase does with its loads between the
+  // products.
+  constexpr bool HALVE_A = T::FM >= T::FN, TWO = T::FM * T::FN > 16;
+  constexpr int H = (HALVE_A ? T::FM : T::FN) / (TWO ? 2 : 1), F = HALVE_A ? T::FN : T::FM;
   bf16x8 lo[H], hi[H], full0[F], full1[F];
-  auto read_half = [&](const char* st, int ks, int half, bf16x8(&x)[H]) {
+  auto read_half = [&](int ks, int half, bf16x8(&x)[H]) {
 #pragma unroll
-    for (int i = 0; i < H; ++i) x[i] = HALVE_A ? frag_a(st, half * H + i, ks) : frag_b(st, half * H + i, ks);
+    for (int i = 0; i < H; ++i) x[i] = HALVE_A ? frag_a(half * H + i, ks) : frag_b(half * H + i, ks);
   };
-  auto read_full = [&](const char* st, int ks, bf16x8(&x)[F]) {
+  auto read_full = [&](int ks, bf16x8(&x)[F]) {
 #pragma unroll
-    for (int i = 0; i < F; ++i) x[i] = HALVE_A ? frag_b(st, i, ks) : frag_a(st, i, ks);
+    for (int i = 0; i < F; ++i) x[i] = HALVE_A ? frag_b(i, ks) : frag_a(i, ks);
   };
   constexpr int kMma = H * F;
   auto product = [&](int half, int q, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
@@ -328,33 +368,44 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // loads that may be on their way when the next step has landed
-  constexpr int kAhead = (T::STAGES - 2) * (NA + NB);
   if (first < last) {
+    enter();
 #pragma unroll
-    for (int i = 0; i < T::STAGES; ++i) issue(i, first + i < last);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kAhead + NA + NB) : "memory");
-    read_half(lds, 0, 0, lo);
-    read_full(lds, 0, full0);
+    for (int i = 0; i < 2; ++i) {
+      aim(i);
+#pragma unroll
+      for (int q = 0; q < NA + NB; ++q) load(q);
+      advance();
+    }
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NA + NB) : "memory");
+    read_half(0, 0, lo);
+    read_full(0, full0);
     __builtin_amdgcn_sched_barrier(0);
   }
   int buf = 0;
   for (int step = first; step < last; ++step) {
-    const char* st = lds + buf * T::STAGE;
-    aim(buf, step + T::STAGES < last);
-    buf = buf + 1 == T::STAGES ? 0 : buf + 1;
-    read_half(st, 0, 1, hi);
-    mma(0, lo, full0, kHalfReads);
-    read_half(st, 1, 0, lo);
-    read_full(st, 1, full1);
-    mma(1, hi, full0, kHalfReads + kFullReads);
-    read_half(st, 1, 1, hi);
-    mma(0, lo, full1, kHalfReads);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead) : "memory");
-    read_half(lds + buf * T::STAGE, 0, 0, lo);
-    read_full(lds + buf * T::STAGE, 0, full0);
+    aim(buf);
+    buf ^= 1;
+    if (TWO) {
+      read_half(0, 1, hi);
+      mma(0, lo, full0, kHalfReads);
+      read_half(1, 0, lo);
+      read_full(1, full1);
+      mma(1, hi, full0, kHalfReads + kFullReads);
+      read_half(1, 1, hi);
+      mma(0, lo, full1, kHalfReads);
+    } else {
+      read_half(1, 0, hi);
+      read_full(1, full1);
+      mma(0, lo, full0, kHalfReads + kFullReads);
+    }
+    other_buffer();
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    read_half(0, 0, lo);
+    read_full(0, full0);
     __builtin_amdgcn_sched_barrier(0);
-    mma_load(1, hi, full1);
+    mma_load(TWO ? 1 : 0, hi, full1);
+    advance();
   }
 
   // Epilogue. A lane's accumulators are column r16 (row m of the result) and
