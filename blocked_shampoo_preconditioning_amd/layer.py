@@ -314,11 +314,16 @@ def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
         pdn, ldn = _matrix("dn", dn, n, d, x)
     dx = _new_like(x)
     dz = _new_like(x) if z is not None else None
-    # the vectors' gradients, in the struct's order: post weight, post bias, gate, next weight, next bias
-    grads = [x.new_empty(d) if v else None for v in vectors[:5]]
-    if vectors[2]:
-        grads[2] = _new(x, -(-n // head[10]), d)
-    pointers = [g.data_ptr() if g is not None else 0 for g in grads]
+    # the vectors' gradients, in the struct's order: post weight, post bias, gate, next weight, next bias;
+    # those of one row come from one allocation
+    gate_rows = -(-n // head[10]) if vectors[2] else 0
+    rows = [gate_rows if i == 2 else 1 if v else 0 for i, v in enumerate(vectors[:5])]
+    one = sum(r == 1 for r in rows)
+    shared = iter(()) if not one else iter(x.new_empty((one, d)).unbind(0))
+    grads = [None if r == 0 else next(shared) if r == 1 else _new(x, r, d) for r in rows]
+    if vectors[2] and rows[2] < 2:
+        grads[2] = grads[2].view(1, d) if rows[2] else _new(x, 0, d)
+    pointers = [g.data_ptr() if g is not None else 0 for g in grads]  # an empty one: 0, nothing to write
     args = _NORM.pack(*head, pz, px, lz, lx, px if z is not None else 0, 0, lx, 0, *vectors, stats.data_ptr(), pdr, pdn, ldr,
                       ldn, dx.data_ptr(), dz.data_ptr() if z is not None else 0, d, d, *pointers, d)
     key = (head[:3], vectors[2] != 0)
