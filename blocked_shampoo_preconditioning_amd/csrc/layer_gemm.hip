@@ -98,15 +98,15 @@ __device__ __forceinline__ floatx4 mfma(const bf16x8& a, const bf16x8& b, const 
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// One workgroup's tile (or its part of K) of a product: `block` of `blocks`
+// workgroups, a multiple of 8.
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uint32_t blocks, char* lds) {
   constexpr bool GATE = EPI == kGate;
   constexpr int HN = GATE ? T::BN / 2 : T::BN;       // result columns of a tile
   constexpr int BW = GATE ? T::BN / 2 : 128;         // width of a B panel
   static_assert(BW == 128 || BW == 64, "");
   static_assert(!GATE || BCOL, "");
-  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
-
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM;
@@ -115,8 +115,8 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
   // work, in groups of four row tiles, so that the tiles in flight on one XCD
   // share their operands in its L2.
   const int tm = (g.M + T::BM - 1) / T::BM, tn = (g.N + HN - 1) / HN;
-  const uint32_t per = gridDim.x / 8;
-  uint32_t id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  const uint32_t per = blocks / 8;
+  uint32_t id = block % 8 * per + block / 8;
   const uint32_t tiles = static_cast<uint32_t>(tm) * tn;
   if (id >= tiles * g.problems * g.splits) return;
   int split = 0, problem = 0;
@@ -496,6 +496,28 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
   if (F32 && EPI != kStore && g.splits == 1) raise_max(g.max_c, largest);
 }
 
+template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+  gemm_tile<T, F32, ACOL, BCOL, EPI>(g, blockIdx.x, gridDim.x, lds);
+}
+
+// The backward pass's last three products in one launch: dx (operands by rows),
+// dWd, and dWg with dWu (operands by columns). None fills the card alone at
+// ordinary sizes (1024..4096 tokens of 768 x 2048: 48..192 tiles of 128), all
+// together nearly do, with fewer splits and no gaps between launches.
+template <class T, bool F32>
+__global__ __launch_bounds__(T::NT, 2) void gemm_group_kernel(GroupArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+  const uint32_t b = blockIdx.x;
+  if (b < a.start[1])
+    gemm_tile<T, F32, false, false, kStore>(a.g[0], b, a.start[1], lds);
+  else if (b < a.start[2])
+    gemm_tile<T, F32, true, true, kStore>(a.g[1], b - a.start[1], a.start[2] - a.start[1], lds);
+  else
+    gemm_tile<T, F32, true, true, kStore>(a.g[2], b - a.start[2], a.start[3] - a.start[2], lds);
+}
+
 // Joins the parts of a split product in their order and runs the epilogue.
 template <bool F32, int EPI>
 __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
@@ -632,15 +654,37 @@ template <int EPI>
 using Tile256 = Tile<EPI == kGate ? 4 : 8, EPI == kGate ? 8 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
 using Tile128 = Tile<4, 4, 2, 2>;
 
+// Workgroups of a product, a multiple of 8 (one for each XCD).
+int64_t gemm_blocks(const GemmArgs& g, int tile, bool gate) {
+  if (g.M <= 0 || g.N <= 0) return 0;
+  return (gemm_tiles(g.M, g.N, g.problems, tile, gate) * g.splits + 7) / 8 * 8;
+}
+
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
-  const int64_t tiles = gemm_tiles(g.M, g.N, g.problems, T::BM, EPI == kGate) * g.splits;
-  const int64_t grid = (tiles + 7) / 8 * 8;
+  const int64_t grid = gemm_blocks(g, T::BM, EPI == kGate);
   if (grid > 0x7fffffff || gemm_steps(g.K, g.nseg) > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemm_kernel<T, F32, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || g.splits == 1) return err;
   return launch_finish(g, static_cast<Epi>(EPI), s);
+}
+
+template <class T, bool F32>
+hipError_t launch_group_tiles(GroupArgs& a, hipStream_t s) {
+  int64_t at = 0;
+  for (int i = 0; i < 3; ++i) {
+    a.start[i] = static_cast<uint32_t>(at);
+    at += gemm_blocks(a.g[i], T::BM, false);
+    if (at > 0x7fffffff || gemm_steps(a.g[i].K, a.g[i].nseg) > 0x7fffffff) return hipErrorInvalidValue;
+  }
+  a.start[3] = static_cast<uint32_t>(at);
+  if (at == 0) return hipSuccess;
+  hipLaunchKernelGGL((gemm_group_kernel<T, F32>), dim3(static_cast<uint32_t>(at)), dim3(T::NT), 0, s, a);
+  hipError_t e = hipGetLastError();
+  for (int i = 0; i < 3 && e == hipSuccess; ++i)
+    if (a.g[i].splits > 1 && a.g[i].M > 0) e = launch_finish(a.g[i], kStore, s);
+  return e;
 }
 
 template <bool F32>
@@ -651,8 +695,6 @@ hipError_t launch_typed(const GemmArgs& g, int tile, bool a_cols, bool b_cols, E
   SHL_CASE(false, true, kGate)
   SHL_CASE(false, true, kStore)
   SHL_CASE(false, false, kActBwd)
-  SHL_CASE(false, false, kStore)
-  SHL_CASE(true, true, kStore)
 #undef SHL_CASE
   return hipErrorInvalidValue;
 }
@@ -678,6 +720,11 @@ int64_t gemm_steps(int64_t K, int nseg) { return (K + kBK - 1) / kBK * nseg; }
 hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   return g.f32 ? launch_typed<true>(g, tile, a_cols, b_cols, epi, s) : launch_typed<false>(g, tile, a_cols, b_cols, epi, s);
+}
+
+hipError_t launch_group(GroupArgs& a, int tile, bool f32, hipStream_t s) {
+  if (tile == 256) return f32 ? launch_group_tiles<Tile256<kStore>, true>(a, s) : launch_group_tiles<Tile256<kStore>, false>(a, s);
+  return f32 ? launch_group_tiles<Tile128, true>(a, s) : launch_group_tiles<Tile128, false>(a, s);
 }
 
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s) {

@@ -56,6 +56,13 @@ int64_t gemm_tiles(int64_t M, int64_t N, int problems, int tile, bool gate);
 // K steps of one launch (all segments).
 int64_t gemm_steps(int64_t K, int nseg);
 
+// Three products of one launch: g[0] reads both operands by rows, g[1] and g[2]
+// by columns; all store (M = 0: left out). start is filled by the launch.
+struct GroupArgs {
+  GemmArgs g[3];
+  uint32_t start[4];
+};
+hipError_t launch_group(GroupArgs& a, int tile, bool f32, hipStream_t s);
 // Joins a split product's parts and runs the epilogue.
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s);
 

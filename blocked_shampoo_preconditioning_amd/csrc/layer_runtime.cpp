@@ -53,38 +53,78 @@ int guarded(F&& f) {
 }
 
 // ------------------------------------------------- gated feed-forward block
-// Tile and K split of a product, by an estimate of its time in microseconds.
-// Measured on the products of 300..8192 tokens, 256..2048 x 1024..8192: a CU
-// does a K step (64) of 128 x 128 results in 0.47 us; 256 tiles run at that
-// rate, one to a CU; 128 tiles at 0.8 of it with two on a CU and at 0.5 with
-// one. A round of tiles costs 5 or 3 us to fill and empty. A split costs a
-// second launch and its sums' way through memory at 4 TB/s. Of the listed sizes
-// this takes 256 tiles alone where they fill the card (8192 x 2048 x 8192), 256
-// tiles in 4 or 5 parts for long sums over few tiles (dx of 2048 x 2048 x 8192:
-// 656 us a step, with 128 tiles unsplit 709), 128 tiles unsplit for short ones
-// (1024 x 768 x 2048: dWg, dWu 114 us, in two parts 122) and split 128 tiles
-// where those are under about 100 (y of 1024 x 768 x 2048: 118, unsplit 124).
-int choose_tile(int64_t M, int64_t N, int problems, bool gate, int64_t steps, int32_t& splits) {
-  const double unit = 0.47 * static_cast<double>(steps);
-  const double sums = static_cast<double>(M) * static_cast<double>(N) * problems * (gate ? 2 : 1) * 8 / 4e6;
-  int tile = 256;
-  double best = 0;
-  splits = 0;
-  for (int t : {256, 128}) {
-    const int64_t tiles = shl::gemm_tiles(M, N, problems, t, gate);
-    for (int64_t s = 1; s <= 16 && (s == 1 || s * 4 <= steps); ++s) {
-      const int64_t n = tiles * s;
-      double us;
-      if (t == 256) {
-        us = static_cast<double>((n + 255) / 256) * (4 * unit / s + 5);
-      } else {
-        const int64_t rest = n % 512;
-        us = static_cast<double>(n / 512) * (2.5 * unit / s + 3) + (rest == 0 ? 0 : (rest <= 256 ? 2.0 : 2.5) * unit / s + 3);
-      }
-      if (s > 1) us += 4 + sums * s;
-      if (splits == 0 || us < best) best = us, tile = t, splits = static_cast<int32_t>(s);
-    }
+// Tile and K splits of the products of one launch, by an estimate of its time in
+// microseconds from what the K loop was measured to take for a step of 64: 1.6
+// for a 256 tile alone on its CU; for 128 tiles 0.92 with two on the CU and 0.72
+// with one. Workgroups of unequal length fill the card about as well as equal
+// ones of the same total, but the launch takes at least its longest one's time.
+// Filling and emptying costs 5 or 3, a split another launch and its sums' way
+// through memory at 4 TB/s. Measured with the choices left open: dx of 2048 x
+// 2048 x 8192 as 256 tiles in 4 parts (the step took 656 against 709 with 128
+// tiles unsplit), dWg and dWu of 1024 x 768 x 2048 as unsplit 128 tiles (114
+// against 122 in two parts), y of that size in 4 parts (118 against 124).
+struct Shape {
+  int64_t M, N;
+  int problems;
+  bool gate;
+  int64_t steps;
+  int32_t splits;
+};
+
+double estimate(const Shape* p, int n, int tile) {
+  double work = 0, longest = 0, extra = 0;
+  int64_t groups = 0;
+  for (int i = 0; i < n; ++i) {
+    if (p[i].M == 0) continue;
+    const int64_t tiles = shl::gemm_tiles(p[i].M, p[i].N, p[i].problems, tile, p[i].gate);
+    const double each = static_cast<double>((p[i].steps + p[i].splits - 1) / p[i].splits);
+    groups += tiles * p[i].splits;
+    work += static_cast<double>(tiles * p[i].splits) * each;
+    longest = each > longest ? each : longest;
+    if (p[i].splits > 1)
+      extra += 4 + static_cast<double>(p[i].M) * static_cast<double>(p[i].N) * p[i].problems * (p[i].gate ? 2 : 1) * 8 / 4e6 * p[i].splits;
   }
+  const bool alone = tile == 256 || groups <= 256;
+  const double step = tile == 256 ? 1.6 : alone ? 0.72 : 0.92, slots = alone ? 256 : 512;
+  // equal workgroups go in whole rounds; unequal ones about half a round apart
+  const double mean = work / static_cast<double>(groups > 0 ? groups : 1);
+  double rounds = static_cast<double>(groups) / slots;
+  rounds = n == 1 ? static_cast<double>(static_cast<int64_t>(rounds + 0.999)) : rounds < 1 ? 1 : rounds + 0.25;
+  double t = rounds * mean * step;
+  t = t > longest * step ? t : longest * step;
+  return t + (tile == 256 ? 5 : 3) * (rounds > 1 ? rounds : 1) + extra;
+}
+
+// One product.
+int choose_tile(Shape p, int32_t& splits) {
+  int tile = 256;
+  double best = -1;
+  for (int t : {256, 128})
+    for (int32_t s = 1; s <= 16 && (s == 1 || s * 4 <= p.steps); ++s) {
+      p.splits = s;
+      const double us = estimate(&p, 1, t);
+      if (best < 0 || us < best) best = us, tile = t, splits = s;
+    }
+  return tile;
+}
+
+// dx (p[0]) with dWd and dWg, dWu (p[1], p[2], whose sums are equally long).
+int choose_group(Shape (&p)[3]) {
+  static const int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  int tile = 256;
+  double best = -1;
+  int32_t a = 1, b = 1;
+  for (int t : {256, 128})
+    for (int32_t sa : kSplits) {
+      if (sa > 1 && (p[0].M == 0 || sa * 4 > p[0].steps)) break;
+      for (int32_t sb : kSplits) {
+        if (sb > 1 && (p[1].M + p[2].M == 0 || sb * 4 > p[2].steps || sb > 8)) break;
+        p[0].splits = sa, p[1].splits = p[2].splits = sb;
+        const double us = estimate(p, 3, t);
+        if (best < 0 || us < best) best = us, tile = t, a = sa, b = sb;
+      }
+    }
+  p[0].splits = a, p[1].splits = p[2].splits = b;
   return tile;
 }
 
@@ -188,15 +228,29 @@ struct Ffn {
     g.lda = A.ld, g.ldb = B.ld, g.max_a = A.word, g.max_b = B.word;
   }
 
-  void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
-    const bool gate = epi == shl::kGate;
-    const int64_t steps = shl::gemm_steps(g.K, g.nseg);
-    const int tile = choose_tile(g.M, g.N, g.problems, gate, steps, g.splits);
+  Shape shape(const shl::GemmArgs& g, bool gate) const {
+    return {g.M, g.M ? g.N : 0, g.problems, gate, shl::gemm_steps(g.K, g.nseg), 1};
+  }
+  void settle(shl::GemmArgs& g, bool gate) {
     g.f32 = f32 ? 1 : 0;
     g.e.act = a.activation;
     if (g.splits > 1)
       g.partial = static_cast<float*>(take(int64_t(4) * g.splits * g.problems * (gate ? 2 : 1) * g.M * g.N));
+  }
+  void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
+    const bool gate = epi == shl::kGate;
+    const int tile = choose_tile(shape(g, gate), g.splits);
+    settle(g, gate);
     if (run) ok(shl::launch_gemm(g, tile, a_cols, b_cols, epi, stream));
+  }
+  void group(shl::GroupArgs& q) {
+    Shape p[3] = {shape(q.g[0], false), shape(q.g[1], false), shape(q.g[2], false)};
+    const int tile = choose_group(p);
+    for (int i = 0; i < 3; ++i) {
+      q.g[i].splits = p[i].splits;
+      settle(q.g[i], false);
+    }
+    if (run) ok(shl::launch_group(q, tile, f32, stream));
   }
 
   // Whether the forward pass takes the few-token kernels: they read two columns
@@ -293,32 +347,33 @@ struct Ffn {
       if (f32) g.max_c = word(kDgu);
       product(g, false, false, shl::kActBwd);
     }
-    if (a.dw_down) {
-      shl::GemmArgs g{};
-      segments(g, h, dy);
-      g.M = static_cast<int32_t>(f), g.N = static_cast<int32_t>(d), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 1;
-      g.e.c[0] = a.dw_down, g.e.ldc = a.ld_dw_down;
-      product(g, true, true, shl::kStore);
+    Planes pg, pu;
+    if (want_gate) {
+      pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
+      flush(false);
     }
-    if (!want_gate) return;
-    const Planes pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
-    flush(false);
+    shl::GroupArgs q{};
     if (a.dx) {
-      shl::GemmArgs g{};
+      shl::GemmArgs& g = q.g[0];
       segments(g, pg, wg);
       segments(g, pu, wu);
       g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
       g.k_real = static_cast<int32_t>(f), g.problems = 1;
       g.e.c[0] = a.dx, g.e.ldc = a.ld_dx;
-      product(g, false, false, shl::kStore);
+    }
+    if (a.dw_down) {
+      shl::GemmArgs& g = q.g[1];
+      segments(g, h, dy);
+      g.M = static_cast<int32_t>(f), g.N = static_cast<int32_t>(d), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 1;
+      g.e.c[0] = a.dw_down, g.e.ldc = a.ld_dw_down;
     }
     if (a.dw_gate) {
-      shl::GemmArgs g{};
+      shl::GemmArgs& g = q.g[2];
       segments(g, x, pg, &pu);
       g.M = static_cast<int32_t>(d), g.N = static_cast<int32_t>(f), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 2;
       g.e.c[0] = a.dw_gate, g.e.c[1] = a.dw_up, g.e.ldc = a.ld_dw_gate, g.e.ldc1 = a.ld_dw_up;
-      product(g, true, true, shl::kStore);
     }
+    group(q);
   }
 };
 
