@@ -568,8 +568,14 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
 }
 
 // ------------------------------------------------------------------- copies
-__global__ __launch_bounds__(64) void zero_words_kernel(uint32_t* words, int n) {
-  for (int i = threadIdx.x; i < n; i += 64) words[i] = 0;
+// The largest of a workgroup's values (256 threads), in every thread.
+__device__ __forceinline__ float block_max(float m) {
+  __shared__ float waves[4];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
+  __syncthreads();
+  return fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
 }
 
 // Row and first column of an operand's i-th group of eight columns, c8 a row. A
@@ -585,9 +591,12 @@ __device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total
   }
 }
 
-// Raises each operand's maximum word; an operand takes blockIdx.y.
+// Largest finite |value| of what each workgroup reads of an operand
+// (blockIdx.y), to the operand's kMaxParts places: 1024 atomics on three words
+// took longer than the reads. Clears the words that products will raise.
 __global__ __launch_bounds__(256) void max_kernel(PackList l) {
   const PackArgs& p = l.t[blockIdx.y];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < l.n_clear) l.clear[threadIdx.x] = 0;
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, step = static_cast<int64_t>(gridDim.x) * 256;
   float m = 0.f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
@@ -605,12 +614,8 @@ __global__ __launch_bounds__(256) void max_kernel(PackList l) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) m = fmaxf(m, finite_abs(v[k][q]));
   }
-  __shared__ float waves[4];
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x < 64) raise_max(p.word, fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3])));
+  m = block_max(m);
+  if (threadIdx.x == 0) p.parts[blockIdx.x] = __float_as_uint(m);
 }
 
 // Copies operands into rows that loads can take (16-byte aligned, padded with
@@ -622,7 +627,16 @@ template <bool F32>
 __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
   const PackArgs& p = list.t[blockIdx.y];
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, plane = p.rows * p.ld_out;
-  const int e = F32 ? scale_exp(*p.word) : 0;
+  int e = 0;
+  if (F32 && p.n_parts > 0) {  // the word comes from the parts of all operands that share it
+    float m = 0.f;
+    for (int i = threadIdx.x; i < p.n_parts; i += 256) m = fmaxf(m, __uint_as_float(p.parts[p.first_part + i]));
+    const uint32_t word = __float_as_uint(block_max(m));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.word = word;
+    e = scale_exp(word);
+  } else if (F32) {
+    e = scale_exp(*p.word);
+  }
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
     int64_t row;
     int col;
@@ -745,15 +759,9 @@ hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_zero_words(uint32_t* words, int n, hipStream_t s) {
-  hipLaunchKernelGGL(zero_words_kernel, dim3(1), dim3(64), 0, s, words, n);
-  return hipGetLastError();
-}
-
 hipError_t launch_max(const PackList& l, hipStream_t s) {
   if (l.n == 0) return hipSuccess;
-  const uint32_t grid = pack_grid(l);
-  hipLaunchKernelGGL(max_kernel, dim3(grid < 256 ? grid : 256, l.n), dim3(256), 0, s, l);
+  hipLaunchKernelGGL(max_kernel, dim3(kMaxParts, l.n), dim3(256), 0, s, l);
   return hipGetLastError();
 }
 

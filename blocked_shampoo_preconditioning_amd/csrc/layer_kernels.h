@@ -86,19 +86,25 @@ hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s);
 // multiple of 8). fp32 sources give two fp16 planes, out[2][rows][ld_out],
 // scaled by the power of two that brings the value in `word` (the bits of the
 // largest finite |value| of all that share the scale) into [2^14, 2^15).
+constexpr int kMaxParts = 256;
 struct PackArgs {
   const void* src;
   uint16_t* out;
   uint32_t* word;
   int64_t rows, cols, ld, ld_out;
+  // launch_max writes the operand's kMaxParts partial maxima to parts; with
+  // n_parts > 0 launch_pack takes the word from parts[first_part..] and stores it
+  uint32_t* parts;
+  int32_t first_part, n_parts;
 };
 constexpr int kMaxPack = 6;
 struct PackList {
   PackArgs t[kMaxPack];
+  uint32_t* clear;  // launch_max: words to be cleared
+  int32_t n_clear;
   int32_t n, f32;
 };
-hipError_t launch_zero_words(uint32_t* words, int n, hipStream_t s);
-hipError_t launch_max(const PackList& l, hipStream_t s);  // raises every word by its operand
+hipError_t launch_max(const PackList& l, hipStream_t s);
 hipError_t launch_pack(const PackList& l, hipStream_t s);
 
 enum NormKind { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };

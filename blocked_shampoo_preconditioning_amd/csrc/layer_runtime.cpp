@@ -137,8 +137,8 @@ struct Planes {
 // One pass over the block's launches: with run = false only the workspace is
 // laid out.
 struct Ffn {
-  // maximum words of the fp32 operands; the forward pass's (up to kH) are kept
-  // behind h in `saved`
+  // Maximum words of the fp32 operands. The forward pass keeps its own (up to kH)
+  // behind h in `saved`, and h as the planes that its second product read.
   enum Word { kX, kWIn, kWDown, kH, kDy, kDgu, kWords };
 
   const shampoo_ffn_t& a;
@@ -177,13 +177,13 @@ struct Ffn {
     return o;
   }
   // Puts a copy on the list; flush() makes it.
-  Planes copied(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  Planes copied(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld, void* to = nullptr) {
     Planes o;
     o.ld = round8(cols);
-    uint16_t* out = static_cast<uint16_t*>(take((f32 ? 2 : 1) * rows * o.ld * 2));
+    uint16_t* out = static_cast<uint16_t*>(to ? to : take((f32 ? 2 : 1) * rows * o.ld * 2));
     o.p[0] = out;
     if (f32) o.p[1] = out + rows * o.ld, o.word = word(w);
-    if (rows) list.t[list.n++] = shl::PackArgs{p, out, word(w), rows, cols, ld, o.ld};
+    if (rows) list.t[list.n++] = shl::PackArgs{p, out, word(w), rows, cols, ld, o.ld, nullptr, 0, 0};
     return o;
   }
   // Both weights of the fused products share one leading dimension (and scale).
@@ -197,20 +197,31 @@ struct Ffn {
   void start_words(bool backward) {
     if (!f32) return;
     words = !backward && a.saved ? saved_words() : static_cast<uint32_t*>(take(kWords * 4));
-    if (run) ok(shl::launch_zero_words(words, kWords, stream));
     kept = backward && !few() ? saved_words() : nullptr;
   }
   uint32_t* word(Word w) const { return kept && w <= kH ? kept + w : words + w; }
-  // Makes the listed copies; fp32 ones after their maxima are known (those of
-  // h, dg and du come from the product that wrote them, and the backward pass
-  // has the forward pass's).
-  void flush(bool maxima) {
-    if (run && f32 && maxima) {
+  bool is_kept(const uint32_t* w) const { return kept && w >= kept && w <= kept + kH; }
+  // Makes the listed copies. maxima: those of fp32 operands are found first (the
+  // backward pass has the forward pass's) and `raised`, the word of a later
+  // product's results, is cleared; else they come from the product that wrote
+  // the operands.
+  void flush(bool maxima, Word raised) {
+    if (f32 && maxima) {
       shl::PackList scan{};
       scan.f32 = 1;
+      scan.clear = words + raised, scan.n_clear = 1;
       for (int i = 0; i < list.n; ++i)
-        if (!kept || list.t[i].word < kept || list.t[i].word > kept + kH) scan.t[scan.n++] = list.t[i];
-      ok(shl::launch_max(scan, stream));
+        if (!is_kept(list.t[i].word)) scan.t[scan.n++] = list.t[i];
+      uint32_t* parts = static_cast<uint32_t*>(take(int64_t(4) * shl::kMaxParts * shl::kMaxPack));
+      // operands that share a word are next to each other
+      for (int i = 0; i < scan.n; ++i) scan.t[i].parts = parts + i * shl::kMaxParts;
+      for (int i = 0; i < list.n; ++i) {
+        shl::PackArgs& p = list.t[i];
+        p.parts = parts, p.n_parts = 0;
+        for (int k = scan.n - 1; k >= 0; --k)
+          if (scan.t[k].word == p.word) p.first_part = k * shl::kMaxParts, p.n_parts += shl::kMaxParts;
+      }
+      if (run) ok(shl::launch_max(scan, stream));
     }
     if (run) ok(shl::launch_pack(list, stream));
     list.n = 0;
@@ -254,7 +265,8 @@ struct Ffn {
   }
 
   // Whether the forward pass takes the few-token kernels: they read two columns
-  // of a row in one aligned access.
+  // of a row in one aligned access. For fp32 the sizes alone decide, so that the
+  // backward pass knows in which form h was kept.
   bool few() const {
     auto pairs = [&](const void* p, int64_t ld) { return f32 || (aligned(p, 4) && ld % 2 == 0); };
     return N <= shl::decode_tokens(f32) && d >= 2 && f >= 2 && pairs(a.w_gate, a.ld_gate) && pairs(a.w_up, a.ld_up) &&
@@ -299,9 +311,10 @@ struct Ffn {
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
     const Planes wd = operand(kWDown, a.w_down, f, d, a.ld_down, false);
-    flush(true);
+    flush(true, kH);
     char* saved = static_cast<char*>(a.saved);
-    void* h = saved ? saved + 2 * act_bytes() : take(N * fp * e);
+    // bf16 h is kept as it is, fp32 h as its planes, which take as much
+    void* h = saved && !f32 ? saved + 2 * act_bytes() : take(N * fp * e);
     {
       shl::GemmArgs g{};
       segments(g, x, wg, &wu);
@@ -312,8 +325,8 @@ struct Ffn {
       if (f32) g.max_c = word(kH);
       product(g, false, true, shl::kGate);
     }
-    const Planes hp = operand(kH, h, N, fp, fp, true);
-    flush(false);
+    const Planes hp = f32 && saved ? copied(kH, h, N, fp, fp, saved + 2 * act_bytes()) : operand(kH, h, N, fp, fp, true);
+    flush(false, kH);
     shl::GemmArgs g{};
     segments(g, hp, wd);
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
@@ -330,10 +343,16 @@ struct Ffn {
     const Planes dy = operand(kDy, a.dy, N, d, a.ld_dy, true);
     Planes wd, h, wg, wu, x;
     if (want_gate) wd = operand(kWDown, a.w_down, f, d, a.ld_down, true);
-    if (a.dw_down) h = operand(kH, saved + 2 * act_bytes(), N, fp, fp, false);
+    if (a.dw_down && kept) {
+      h.ld = fp, h.word = word(kH);
+      h.p[0] = reinterpret_cast<const uint16_t*>(saved + 2 * act_bytes());
+      h.p[1] = h.p[0] + N * fp;
+    } else if (a.dw_down) {
+      h = operand(kH, saved + 2 * act_bytes(), N, fp, fp, false);
+    }
     if (a.dx) operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
     if (a.dw_gate) x = operand(kX, a.x, N, d, a.ld_x, false);
-    flush(true);
+    flush(true, kDgu);
     void *dg = nullptr, *du = nullptr;
     if (want_gate) {
       dg = take(N * fp * e);
@@ -350,7 +369,7 @@ struct Ffn {
     Planes pg, pu;
     if (want_gate) {
       pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
-      flush(false);
+      flush(false, kDgu);
     }
     shl::GroupArgs q{};
     if (a.dx) {
