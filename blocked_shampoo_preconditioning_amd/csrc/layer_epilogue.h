@@ -38,13 +38,14 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // Raises a maximum word by a wave's largest finite |value|. The order of the
-// atomics does not change the result; a wave that finds the word as high
-// leaves it (2048 unconditional atomics on one word took 90 us).
+// atomics does not change the result. They queue up at a word, so that every
+// workgroup has one of kMaxParts (1024 on one word: 42 us for a finish kernel
+// that now takes 12), and it does not look at the word first (16 us).
 __device__ __forceinline__ void raise_max(uint32_t* word, float m) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   const uint32_t bits = __float_as_uint(m);
-  if ((threadIdx.x & 63) == 0 && bits > __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(word, bits);
+  if ((threadIdx.x & 63) == 0 && bits) atomicMax(word, bits);
 }
 
 // Power of two that an operand's planes are scaled by: its largest finite

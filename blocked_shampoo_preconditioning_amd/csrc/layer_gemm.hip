@@ -493,7 +493,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  if (F32 && EPI != kStore && g.splits == 1) raise_max(g.max_c, largest);
+  if (F32 && EPI != kStore && g.splits == 1) raise_max(g.max_parts + blockIdx.x % kMaxParts, largest);
 }
 
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
@@ -516,6 +516,16 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_group_kernel(GroupArgs a) {
     gemm_tile<T, F32, true, true, kStore>(a.g[1], b - a.start[1], a.start[2] - a.start[1], lds);
   else
     gemm_tile<T, F32, true, true, kStore>(a.g[2], b - a.start[2], a.start[3] - a.start[2], lds);
+}
+
+// The largest of a workgroup's values (256 threads), in every thread.
+__device__ __forceinline__ float block_max(float m) {
+  __shared__ float waves[4];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
+  __syncthreads();
+  return fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
 }
 
 // Joins the parts of a split product in their order and runs the epilogue.
@@ -564,20 +574,13 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
     }
     largest = finish8<F32, EPI>(g.e, Activation(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
   }
-  if (F32 && EPI != kStore && g.max_c) raise_max(g.max_c, largest);
+  if (F32 && EPI != kStore && g.max_parts) {
+    largest = block_max(largest);
+    if (threadIdx.x < 64) raise_max(g.max_parts + blockIdx.x % kMaxParts, largest);
+  }
 }
 
 // ------------------------------------------------------------------- copies
-// The largest of a workgroup's values (256 threads), in every thread.
-__device__ __forceinline__ float block_max(float m) {
-  __shared__ float waves[4];
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
-  __syncthreads();
-  return fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
-}
-
 // Row and first column of an operand's i-th group of eight columns, c8 a row. A
 // 64-bit division takes longer than the group's load.
 __device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total, int64_t& row, int& col) {
@@ -596,7 +599,7 @@ __device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total
 // took longer than the reads. Clears the words that products will raise.
 __global__ __launch_bounds__(256) void max_kernel(PackList l) {
   const PackArgs& p = l.t[blockIdx.y];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < l.n_clear) l.clear[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kMaxParts) l.clear[threadIdx.x] = 0;
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, step = static_cast<int64_t>(gridDim.x) * 256;
   float m = 0.f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {

@@ -28,6 +28,9 @@ struct EpiArgs {
   int32_t pad_to;      // columns [N, pad_to) are written as zeros (rows padded for a later product)
 };
 
+// Partial maxima that an operand's largest |value| is put together from.
+constexpr int kMaxParts = 256;
+
 // sum over segments s of A_s B_s, A_s [M][K], B_s [K][N], 16-bit operands with
 // fp32 accumulation. An operand is read by rows (K contiguous) or by columns (K
 // is the slow index). f32 = 0: bf16 operands and bf16 arrays in the epilogue; 1:
@@ -36,7 +39,7 @@ struct GemmArgs {
   const uint16_t* a[kMaxSeg];
   const uint16_t* b[2][kMaxSeg];  // [1]: u's weights (kGate) or problem 1's operand
   const uint32_t *max_a, *max_b;  // f32: the operands' maximum words (PackArgs)
-  uint32_t* max_c;                // f32: raised by h (kGate), dg and du (kActBwd)
+  uint32_t* max_parts;            // f32: kMaxParts words raised by h (kGate), dg and du (kActBwd)
   int64_t lda, ldb;
   int32_t f32;
   int32_t nseg;
@@ -86,7 +89,6 @@ hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s);
 // multiple of 8). fp32 sources give two fp16 planes, out[2][rows][ld_out],
 // scaled by the power of two that brings the value in `word` (the bits of the
 // largest finite |value| of all that share the scale) into [2^14, 2^15).
-constexpr int kMaxParts = 256;
 struct PackArgs {
   const void* src;
   uint16_t* out;
@@ -100,8 +102,7 @@ struct PackArgs {
 constexpr int kMaxPack = 6;
 struct PackList {
   PackArgs t[kMaxPack];
-  uint32_t* clear;  // launch_max: words to be cleared
-  int32_t n_clear;
+  uint32_t* clear;  // launch_max: kMaxParts words to be cleared
   int32_t n, f32;
 };
 hipError_t launch_max(const PackList& l, hipStream_t s);

@@ -82,7 +82,7 @@ double estimate(const Shape* p, int n, int tile) {
     work += static_cast<double>(tiles * p[i].splits) * each;
     longest = each > longest ? each : longest;
     if (p[i].splits > 1)
-      extra += 4 + static_cast<double>(p[i].M) * static_cast<double>(p[i].N) * p[i].problems * (p[i].gate ? 2 : 1) * 8 / 4e6 * p[i].splits;
+      extra += 4 + static_cast<double>(p[i].M) * static_cast<double>(p[i].N) * p[i].problems * (p[i].gate ? 2 : 1) * 6 / 4e6 * p[i].splits;
   }
   const bool alone = tile == 256 || groups <= 256;
   const double step = tile == 256 ? 1.6 : alone ? 0.72 : 0.92, slots = alone ? 256 : 512;
@@ -100,7 +100,7 @@ int choose_tile(Shape p, int32_t& splits) {
   int tile = 256;
   double best = -1;
   for (int t : {256, 128})
-    for (int32_t s = 1; s <= 16 && (s == 1 || s * 4 <= p.steps); ++s) {
+    for (int32_t s = 1; s <= 32 && (s == 1 || s * 4 <= p.steps); ++s) {
       p.splits = s;
       const double us = estimate(&p, 1, t);
       if (best < 0 || us < best) best = us, tile = t, splits = s;
@@ -110,7 +110,7 @@ int choose_tile(Shape p, int32_t& splits) {
 
 // dx (p[0]) with dWd and dWg, dWu (p[1], p[2], whose sums are equally long).
 int choose_group(Shape (&p)[3]) {
-  static const int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  static const int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   int tile = 256;
   double best = -1;
   int32_t a = 1, b = 1;
@@ -118,7 +118,7 @@ int choose_group(Shape (&p)[3]) {
     for (int32_t sa : kSplits) {
       if (sa > 1 && (p[0].M == 0 || sa * 4 > p[0].steps)) break;
       for (int32_t sb : kSplits) {
-        if (sb > 1 && (p[1].M + p[2].M == 0 || sb * 4 > p[2].steps || sb > 8)) break;
+        if (sb > 1 && (p[1].M + p[2].M == 0 || sb * 4 > p[2].steps)) break;
         p[0].splits = sa, p[1].splits = p[2].splits = sb;
         const double us = estimate(p, 3, t);
         if (best < 0 || us < best) best = us, tile = t, a = sa, b = sb;
@@ -149,7 +149,7 @@ struct Ffn {
   hipError_t err = hipSuccess;
   int64_t N, d, f, fp, e;
   bool f32;
-  uint32_t *words = nullptr, *kept = nullptr;
+  uint32_t *words = nullptr, *kept = nullptr, *raised = nullptr;
   shl::PackList list{};
 
   Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
@@ -198,18 +198,19 @@ struct Ffn {
     if (!f32) return;
     words = !backward && a.saved ? saved_words() : static_cast<uint32_t*>(take(kWords * 4));
     kept = backward && !few() ? saved_words() : nullptr;
+    raised = static_cast<uint32_t*>(take(4 * shl::kMaxParts));
   }
   uint32_t* word(Word w) const { return kept && w <= kH ? kept + w : words + w; }
   bool is_kept(const uint32_t* w) const { return kept && w >= kept && w <= kept + kH; }
   // Makes the listed copies. maxima: those of fp32 operands are found first (the
-  // backward pass has the forward pass's) and `raised`, the word of a later
-  // product's results, is cleared; else they come from the product that wrote
-  // the operands.
-  void flush(bool maxima, Word raised) {
+  // backward pass has the forward pass's) and `raised` is cleared for the
+  // product that follows; else they are in `raised`, from the product that
+  // wrote the operands.
+  void flush(bool maxima) {
     if (f32 && maxima) {
       shl::PackList scan{};
       scan.f32 = 1;
-      scan.clear = words + raised, scan.n_clear = 1;
+      scan.clear = raised;
       for (int i = 0; i < list.n; ++i)
         if (!is_kept(list.t[i].word)) scan.t[scan.n++] = list.t[i];
       uint32_t* parts = static_cast<uint32_t*>(take(int64_t(4) * shl::kMaxParts * shl::kMaxPack));
@@ -222,6 +223,8 @@ struct Ffn {
           if (scan.t[k].word == p.word) p.first_part = k * shl::kMaxParts, p.n_parts += shl::kMaxParts;
       }
       if (run) ok(shl::launch_max(scan, stream));
+    } else if (f32) {
+      for (int i = 0; i < list.n; ++i) list.t[i].parts = raised, list.t[i].first_part = 0, list.t[i].n_parts = shl::kMaxParts;
     }
     if (run) ok(shl::launch_pack(list, stream));
     list.n = 0;
@@ -311,7 +314,7 @@ struct Ffn {
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
     const Planes wd = operand(kWDown, a.w_down, f, d, a.ld_down, false);
-    flush(true, kH);
+    flush(true);
     char* saved = static_cast<char*>(a.saved);
     // bf16 h is kept as it is, fp32 h as its planes, which take as much
     void* h = saved && !f32 ? saved + 2 * act_bytes() : take(N * fp * e);
@@ -322,11 +325,11 @@ struct Ffn {
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
       if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
-      if (f32) g.max_c = word(kH);
+      g.max_parts = raised;
       product(g, false, true, shl::kGate);
     }
     const Planes hp = f32 && saved ? copied(kH, h, N, fp, fp, saved + 2 * act_bytes()) : operand(kH, h, N, fp, fp, true);
-    flush(false, kH);
+    flush(false);
     shl::GemmArgs g{};
     segments(g, hp, wd);
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
@@ -352,7 +355,7 @@ struct Ffn {
     }
     if (a.dx) operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
     if (a.dw_gate) x = operand(kX, a.x, N, d, a.ld_x, false);
-    flush(true, kDgu);
+    flush(true);
     void *dg = nullptr, *du = nullptr;
     if (want_gate) {
       dg = take(N * fp * e);
@@ -363,13 +366,13 @@ struct Ffn {
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
       g.e.c[0] = dg, g.e.c[1] = du, g.e.ldc = fp, g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
       g.e.pad_to = static_cast<int32_t>(fp);
-      if (f32) g.max_c = word(kDgu);
+      g.max_parts = raised;
       product(g, false, false, shl::kActBwd);
     }
     Planes pg, pu;
     if (want_gate) {
       pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
-      flush(false, kDgu);
+      flush(false);
     }
     shl::GroupArgs q{};
     if (a.dx) {
