@@ -26,16 +26,22 @@ constexpr int kBK = 64;                 // K step
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ------------------------------------------------------------------ the tile
-// WM x WN waves of FM x FN fragments of 16 x 16.
-template <int FM_, int FN_, int WM_, int WN_>
+// WM x WN waves of FM x FN fragments of 16 x 16. With KG = 2 there are two such
+// sets of waves, each with half of the K steps and buffers of its own, whose
+// sums are joined through LDS: four waves alone on a CU leave its matrix cores
+// idle between their phases (a 128 tile takes 0.6 us a K step with them, half of
+// 0.85 with eight; y of 4096 x 2048 x 768, 192 tiles: 26.5 against 22.8 us).
+template <int FM_, int FN_, int WM_, int WN_, int KG_ = 1>
 struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
-  static constexpr int NW = WM * WN, NT = NW * 64;
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, KG = KG_;
+  static constexpr int NW = WM * WN, NT = NW * 64 * KG;
+  static_assert(KG == 1 || (KG == 2 && FM == 4), "");
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
   static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int PITCH = FN * 16 + 4;  // floats of a row of the epilogue's strips
-  static constexpr int LDS = 2 * STAGE > NW * 32 * PITCH * 4 ? 2 * STAGE : NW * 32 * PITCH * 4;
+  static constexpr int STRIPS = NT / 64 * 32 * PITCH * 4;
+  static constexpr int LDS = KG * 2 * STAGE > STRIPS ? KG * 2 * STAGE : STRIPS;
 };
 
 // LDS order of 16-byte chunks. A row operand's tile is [rows][64 k] (8 chunks
@@ -107,8 +113,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   constexpr int BW = GATE ? T::BN / 2 : 128;         // width of a B panel
   static_assert(BW == 128 || BW == 64, "");
   static_assert(!GATE || BCOL, "");
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63;
+  const int any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kgroup = any_wave / T::NW, wave = any_wave - kgroup * T::NW;
   const int wm = wave % T::WM, wn = wave / T::WM;
 
   // Workgroups go round the 8 XCDs; each XCD takes a contiguous range of the
@@ -142,6 +149,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     first = each * split + min(split, rest);
     last = first + each + (split < rest ? 1 : 0);
   }
+  // the second set of waves may have a step less: it adds zeros in its last one
+  const int turns = (last - first + T::KG - 1) / T::KG;
+  first += kgroup * turns;
+  int loads = min(turns, last - first);  // steps still to be loaded
 
   // Loads: 1 KiB an instruction, NW instructions at a time. A row operand's
   // buffer starts at the tile's first row and its offsets move along K; a
@@ -166,7 +177,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   for (int j = 0; j < NA; ++j) va[j] = ACOL ? col_off(lda2, 128, j % (16 / T::NW), j / (16 / T::NW)) : row_off(lda2, j);
 #pragma unroll
   for (int j = 0; j < NB; ++j) vb[j] = BCOL ? col_off(ldb2, BW, j % BPP, GATE ? 0 : j / BPP) : row_off(ldb2, j);
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds)) + wave * 1024;
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds)) + kgroup * (2 * T::STAGE);
+  const uint32_t lds0 = lds_base + wave * 1024;
   const int64_t a_start = ACOL ? 2 * static_cast<int64_t>(m0) : m0 * lda2;
   const int64_t b_start = BCOL ? 2 * static_cast<int64_t>(n0) : n0 * ldb2;
   const int64_t a_size = (ACOL ? (static_cast<int64_t>(g.k_real) - 1) * lda2 + 2 * static_cast<int64_t>(g.M)
@@ -180,9 +192,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   // segment's last step can have, get an offset out of range once.
   const int64_t a_step = ACOL ? kBK * lda2 : kBK * 2, b_step = BCOL ? kBK * ldb2 : kBK * 2;
   int seg = 0;
-  if (first) seg = first / ksteps;
+  if (first) seg = min(first, steps - 1) / ksteps;
   int k0 = (first - seg * ksteps) * kBK;
-  int loads = last - first;  // steps still to be loaded
   uint64_t pa = 0, pb = 0, pb1 = 0;
   int64_t left_a = 0, left_b = 0;
   bool cut = false;
@@ -211,7 +222,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   uint32_t at = 0;
   auto aim = [&](int buf) {
     at = lds0 + buf * T::STAGE;
-    // past the last step nothing is read: zeros go to a buffer that nobody reads
+    // past the last step nothing is read: the buffer gets zeros
     ra = make_rsrc(pa, loads > 0 ? left_a : 0);
     rb = make_rsrc(pb, loads > 0 ? left_b : 0);
     if (GATE) rb1 = make_rsrc(pb1, loads > 0 ? left_b : 0);
@@ -239,7 +250,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   // A lane's places in the fragment reads (16 rows or columns x 32 k, eight k of
   // one row a lane), as LDS addresses of the buffer that is read.
   const int r16 = lane & 15, q4 = lane >> 4;
-  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
   // row operand: row r16 of a fragment, chunk 4 ks + q4; fragments 2 KiB apart
   auto row_at = [&](uint32_t tile, int row0, int ks) {
     return static_cast<uint32_t>(tile + (row0 + r16) * 128 + (((4 * ks + q4) ^ swz_row(r16)) << 4));
@@ -368,7 +378,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  if (first < last) {
+  if (turns > 0) {
     enter();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -383,7 +393,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     __builtin_amdgcn_sched_barrier(0);
   }
   int buf = 0;
-  for (int step = first; step < last; ++step) {
+  for (int turn = 0; turn < turns; ++turn) {
     aim(buf);
     buf ^= 1;
     if (TWO) {
@@ -418,7 +428,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   constexpr int PITCH = T::PITCH;
   constexpr int COLS = GATE ? T::FN * 8 : T::FN * 16;            // result columns of a wave
   constexpr int LR = COLS / 8, RP = 64 / LR, NP = 32 / RP;       // lanes a row, rows a pass, passes
-  const int row0 = m0 + wm * T::FM * 16 + lane / LR;
+  constexpr int STRIPS = T::FM / 2 / T::KG;                      // of a wave
+  const int row0 = m0 + wm * T::FM * 16 + kgroup * 32 + lane / LR;
   const int c8 = (lane % LR) * 8, col = n0 + wn * COLS + c8;
   const int64_t ldc = EPI == kStore && problem ? g.e.ldc1 : g.e.ldc;
   const int64_t oc = row0 * ldc + col, og = row0 * g.e.ldg + col;
@@ -431,13 +442,31 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   }
   // the last loads (zeros) have landed and all reads are done: LDS is free
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  float* strip = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
+  if constexpr (T::KG == 2) {
+    // each set joins one strip: it gives the other's and takes its own
+    floatx4* give = reinterpret_cast<floatx4*>(lds) + any_wave * (2 * T::FN * 64) + lane;
+    const floatx4* get = reinterpret_cast<floatx4*>(lds) + (any_wave ^ T::NW) * (2 * T::FN * 64) + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) {
+        give[(h * T::FN + j) * 64] = kgroup ? acc[h][j] : acc[2 + h][j];
+        acc[h][j] = kgroup ? acc[2 + h][j] : acc[h][j];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) acc[h][j] += get[(h * T::FN + j) * 64];
+    __syncthreads();
+  }
+  float* strip = reinterpret_cast<float*>(lds) + any_wave * (32 * PITCH);
   int exponent = 0;
   if (F32) exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
   float largest = 0.f;
 #pragma unroll
-  for (int i = 0; i < T::FM / 2; ++i) {
-    if (act_bwd && i + AHEAD < T::FM / 2) {
+  for (int i = 0; i < STRIPS; ++i) {
+    if (act_bwd && i + AHEAD < STRIPS) {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
         load_gu<F32>(g.e, row0 + (i + AHEAD) * 32 + p * RP < g.M, og + ((i + AHEAD) * 32 + p * RP) * g.e.ldg, col, g.N,
@@ -670,16 +699,17 @@ __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
 template <int EPI>
 using Tile256 = Tile<EPI == kGate ? 4 : 8, EPI == kGate ? 8 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
 using Tile128 = Tile<4, 4, 2, 2>;
+using Tile128x2 = Tile<4, 4, 2, 2, 2>;
 
 // Workgroups of a product, a multiple of 8 (one for each XCD).
-int64_t gemm_blocks(const GemmArgs& g, int tile, bool gate) {
+int64_t gemm_blocks(const GemmArgs& g, TileKind tile, bool gate) {
   if (g.M <= 0 || g.N <= 0) return 0;
   return (gemm_tiles(g.M, g.N, g.problems, tile, gate) * g.splits + 7) / 8 * 8;
 }
 
 template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
-hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
-  const int64_t grid = gemm_blocks(g, T::BM, EPI == kGate);
+hipError_t launch_one(const GemmArgs& g, TileKind tile, hipStream_t s) {
+  const int64_t grid = gemm_blocks(g, tile, EPI == kGate);
   if (grid > 0x7fffffff || gemm_steps(g.K, g.nseg) > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemm_kernel<T, F32, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
   hipError_t err = hipGetLastError();
@@ -688,11 +718,11 @@ hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
 }
 
 template <class T, bool F32>
-hipError_t launch_group_tiles(GroupArgs& a, hipStream_t s) {
+hipError_t launch_group_tiles(GroupArgs& a, TileKind tile, hipStream_t s) {
   int64_t at = 0;
   for (int i = 0; i < 3; ++i) {
     a.start[i] = static_cast<uint32_t>(at);
-    at += gemm_blocks(a.g[i], T::BM, false);
+    at += gemm_blocks(a.g[i], tile, false);
     if (at > 0x7fffffff || gemm_steps(a.g[i].K, a.g[i].nseg) > 0x7fffffff) return hipErrorInvalidValue;
   }
   a.start[3] = static_cast<uint32_t>(at);
@@ -705,10 +735,12 @@ hipError_t launch_group_tiles(GroupArgs& a, hipStream_t s) {
 }
 
 template <bool F32>
-hipError_t launch_typed(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
-#define SHL_CASE(AC, BC, E)                              \
-  if (a_cols == AC && b_cols == BC && epi == E)          \
-    return tile == 256 ? launch_one<Tile256<E>, F32, AC, BC, E>(g, s) : launch_one<Tile128, F32, AC, BC, E>(g, s);
+hipError_t launch_typed(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
+#define SHL_CASE(AC, BC, E)                                                                           \
+  if (a_cols == AC && b_cols == BC && epi == E)                                                       \
+    return tile == kTile256 ? launch_one<Tile256<E>, F32, AC, BC, E>(g, tile, s)                      \
+                            : tile == kTile128 ? launch_one<Tile128, F32, AC, BC, E>(g, tile, s)      \
+                                               : launch_one<Tile128x2, F32, AC, BC, E>(g, tile, s);
   SHL_CASE(false, true, kGate)
   SHL_CASE(false, true, kStore)
   SHL_CASE(false, false, kActBwd)
@@ -727,21 +759,27 @@ uint32_t pack_grid(const PackList& l) {
 
 }  // namespace
 
-int64_t gemm_tiles(int64_t M, int64_t N, int problems, int tile, bool gate) {
-  const int64_t hn = gate ? tile / 2 : tile;
-  return ((M + tile - 1) / tile) * ((N + hn - 1) / hn) * problems;
+int64_t gemm_tiles(int64_t M, int64_t N, int problems, TileKind tile, bool gate) {
+  const int64_t w = tile == kTile256 ? 256 : 128, hn = gate ? w / 2 : w;
+  return ((M + w - 1) / w) * ((N + hn - 1) / hn) * problems;
 }
 
 int64_t gemm_steps(int64_t K, int nseg) { return (K + kBK - 1) / kBK * nseg; }
 
-hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
+hipError_t launch_gemm(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   return g.f32 ? launch_typed<true>(g, tile, a_cols, b_cols, epi, s) : launch_typed<false>(g, tile, a_cols, b_cols, epi, s);
 }
 
-hipError_t launch_group(GroupArgs& a, int tile, bool f32, hipStream_t s) {
-  if (tile == 256) return f32 ? launch_group_tiles<Tile256<kStore>, true>(a, s) : launch_group_tiles<Tile256<kStore>, false>(a, s);
-  return f32 ? launch_group_tiles<Tile128, true>(a, s) : launch_group_tiles<Tile128, false>(a, s);
+template <class T>
+static hipError_t launch_group_typed(GroupArgs& a, TileKind tile, bool f32, hipStream_t s) {
+  return f32 ? launch_group_tiles<T, true>(a, tile, s) : launch_group_tiles<T, false>(a, tile, s);
+}
+
+hipError_t launch_group(GroupArgs& a, TileKind tile, bool f32, hipStream_t s) {
+  return tile == kTile256   ? launch_group_typed<Tile256<kStore>>(a, tile, f32, s)
+         : tile == kTile128 ? launch_group_typed<Tile128>(a, tile, f32, s)
+                            : launch_group_typed<Tile128x2>(a, tile, f32, s);
 }
 
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s) {

@@ -52,10 +52,12 @@ struct GemmArgs {
   EpiArgs e;
 };
 
-// Tile of 256 x 256 or 128 x 128 results (kGate: 128 or 64 columns of h).
-hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s);
+// Results of a workgroup: 256 x 256 or 128 x 128 (kGate: 128 or 64 columns of
+// h); x2: by two sets of waves with half of K each.
+enum TileKind { kTile256, kTile128, kTile128x2 };
+hipError_t launch_gemm(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s);
 // Tiles of one launch before splitting.
-int64_t gemm_tiles(int64_t M, int64_t N, int problems, int tile, bool gate);
+int64_t gemm_tiles(int64_t M, int64_t N, int problems, TileKind tile, bool gate);
 // K steps of one launch (all segments).
 int64_t gemm_steps(int64_t K, int nseg);
 
@@ -65,7 +67,7 @@ struct GroupArgs {
   GemmArgs g[3];
   uint32_t start[4];
 };
-hipError_t launch_group(GroupArgs& a, int tile, bool f32, hipStream_t s);
+hipError_t launch_group(GroupArgs& a, TileKind tile, bool f32, hipStream_t s);
 // Joins a split product's parts and runs the epilogue.
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s);
 

@@ -54,15 +54,18 @@ int guarded(F&& f) {
 
 // ------------------------------------------------- gated feed-forward block
 // Tile and K splits of the products of one launch, by an estimate of its time in
-// microseconds from what the K loop was measured to take for a step of 64: 1.6
-// for a 256 tile alone on its CU; for 128 tiles 0.92 with two on the CU and 0.72
-// with one. Workgroups of unequal length fill the card about as well as equal
-// ones of the same total, but the launch takes at least its longest one's time.
-// Filling and emptying costs 5 or 3, a split another launch and its sums' way
-// through memory at 4 TB/s. Measured with the choices left open: dx of 2048 x
-// 2048 x 8192 as 256 tiles in 4 parts (the step took 656 against 709 with 128
-// tiles unsplit), dWg and dWu of 1024 x 768 x 2048 as unsplit 128 tiles (114
-// against 122 in two parts), y of that size in 4 parts (118 against 124).
+// microseconds. A K step of 64 takes 1.6 for a 256 tile alone on its CU, 0.92
+// for two 128 tiles on one and 0.72 for one alone, with two sets of waves 0.43
+// on a part of the card and 0.55 on the whole (the L2s' rate). Workgroups of
+// unequal length fill the card about as well as equal ones of the same total,
+// but the launch takes at least its longest one's time. Filling and emptying
+// costs 5, 3 or 4, a split another launch and its sums' way through memory.
+// Measured with the choices left open (a whole step, us): dx of 2048 x 2048 x
+// 8192 as 256 tiles in 4 parts 656, as 128 tiles unsplit 709; dWg and dWu of
+// 1024 x 768 x 2048 as unsplit 128 tiles 114, in two parts 122, y of that size
+// unsplit 124, in 4 parts 118; y of 4096 x 768 x 2048 with one set of waves 159,
+// with two 156; f32 of 1536 x 1000 x 2728 with the whole card's 0.55 388, with
+// 0.43 throughout 425 and more.
 struct Shape {
   int64_t M, N;
   int problems;
@@ -71,7 +74,7 @@ struct Shape {
   int32_t splits;
 };
 
-double estimate(const Shape* p, int n, int tile) {
+double estimate(const Shape* p, int n, shl::TileKind tile) {
   double work = 0, longest = 0, extra = 0;
   int64_t groups = 0;
   for (int i = 0; i < n; ++i) {
@@ -84,22 +87,22 @@ double estimate(const Shape* p, int n, int tile) {
     if (p[i].splits > 1)
       extra += 4 + static_cast<double>(p[i].M) * static_cast<double>(p[i].N) * p[i].problems * (p[i].gate ? 2 : 1) * 6 / 4e6 * p[i].splits;
   }
-  const bool alone = tile == 256 || groups <= 256;
-  const double step = tile == 256 ? 1.6 : alone ? 0.72 : 0.92, slots = alone ? 256 : 512;
+  const bool big = tile == shl::kTile256, alone = tile != shl::kTile128 || groups <= 256;
+  const double step = big ? 1.6 : tile == shl::kTile128x2 ? 0.55 : alone ? 0.72 : 0.92, slots = alone ? 256 : 512;
   // equal workgroups go in whole rounds; unequal ones about half a round apart
   const double mean = work / static_cast<double>(groups > 0 ? groups : 1);
   double rounds = static_cast<double>(groups) / slots;
   rounds = n == 1 ? static_cast<double>(static_cast<int64_t>(rounds + 0.999)) : rounds < 1 ? 1 : rounds + 0.25;
   double t = rounds * mean * step;
   t = t > longest * step ? t : longest * step;
-  return t + (tile == 256 ? 5 : 3) * (rounds > 1 ? rounds : 1) + extra;
+  return t + (big ? 5 : tile == shl::kTile128x2 ? 4 : 3) * (rounds > 1 ? rounds : 1) + extra;
 }
 
 // One product.
-int choose_tile(Shape p, int32_t& splits) {
-  int tile = 256;
+shl::TileKind choose_tile(Shape p, int32_t& splits) {
+  shl::TileKind tile = shl::kTile256;
   double best = -1;
-  for (int t : {256, 128})
+  for (shl::TileKind t : {shl::kTile256, shl::kTile128, shl::kTile128x2})
     for (int32_t s = 1; s <= 32 && (s == 1 || s * 4 <= p.steps); ++s) {
       p.splits = s;
       const double us = estimate(&p, 1, t);
@@ -109,12 +112,12 @@ int choose_tile(Shape p, int32_t& splits) {
 }
 
 // dx (p[0]) with dWd and dWg, dWu (p[1], p[2], whose sums are equally long).
-int choose_group(Shape (&p)[3]) {
+shl::TileKind choose_group(Shape (&p)[3]) {
   static const int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-  int tile = 256;
+  shl::TileKind tile = shl::kTile256;
   double best = -1;
   int32_t a = 1, b = 1;
-  for (int t : {256, 128})
+  for (shl::TileKind t : {shl::kTile256, shl::kTile128, shl::kTile128x2})
     for (int32_t sa : kSplits) {
       if (sa > 1 && (p[0].M == 0 || sa * 4 > p[0].steps)) break;
       for (int32_t sb : kSplits) {
@@ -253,13 +256,13 @@ struct Ffn {
   }
   void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
     const bool gate = epi == shl::kGate;
-    const int tile = choose_tile(shape(g, gate), g.splits);
+    const shl::TileKind tile = choose_tile(shape(g, gate), g.splits);
     settle(g, gate);
     if (run) ok(shl::launch_gemm(g, tile, a_cols, b_cols, epi, stream));
   }
   void group(shl::GroupArgs& q) {
     Shape p[3] = {shape(q.g[0], false), shape(q.g[1], false), shape(q.g[2], false)};
-    const int tile = choose_group(p);
+    const shl::TileKind tile = choose_group(p);
     for (int i = 0; i < 3; ++i) {
       q.g[i].splits = p[i].splits;
       settle(q.g[i], false);
