@@ -2,9 +2,10 @@
 
     python -m blocked_shampoo_preconditioning_amd.build
 
-Compiles the HIP kernels (csrc/kernels.hip, csrc/tensor_kernels.hip) and the
-host runtime (csrc/runtime.cpp, roots.cpp, tensor_runtime.cpp) with hipcc into
-one shared library next to this file. Packed fp32 instructions are disabled for the
+Compiles the HIP kernels (csrc/kernels.hip, csrc/tensor_kernels.hip and the
+layer operators' csrc/layer_gemm.hip, layer_decode.hip, layer_norm.hip) and the
+host runtime (csrc/runtime.cpp, roots.cpp, tensor_runtime.cpp, layer_runtime.cpp)
+with hipcc into one shared library next to this file. Packed fp32 instructions are disabled for the
 device code (-packed-fp32-ops); hipcc's host pass warns that it does not know
 that feature, which is harmless.
 """

@@ -3,11 +3,17 @@
 // Every weight is read once for at most 16 T rows of x, so the kernel is bound
 // by HBM. The weights' rows [k][n] go from memory into registers, two columns a
 // lane: the 16 lanes of a row read 32 columns in whole 64-byte pieces, and
-// each wave has 16 (fp32) or 32 loads a matrix in flight with no LDS in their way. The
+// each wave has 16 loads a matrix in flight with no LDS in their way. The
 // matrix cores take them as they come: the weights are the "A" operand (16 rows
 // of one 16 x 16 product are columns 2 j + i, j the lane of a row), x the "B"
 // operand (16 tokens). fp32 uses the fp32 matrix instruction, so it is exact to
 // fp32 accumulation.
+//
+// One token of 2048 x 8192 bf16: g, u and h (67 MB) in 20 us, y (34 MB) in 10 and
+// 4 to join its 32 parts of K (16 and 8 for the products when the last-level
+// cache still has the weights); 13 tokens of 768 x 2048 fp32 (19 MB): 10, 5 and 3,
+// where the launches are more than half. Batches of 128 rows spill;
+// non-temporal loads are no faster.
 #include "layer_epilogue.h"
 #include "layer_kernels.h"
 
@@ -18,11 +24,8 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) short short4v;
 
 constexpr int kCols = 32;       // columns of a workgroup
-// K rows in flight at once in a wave, and the run of them that a lane has
-template <bool F32>
-constexpr int kBatch = 64;
-template <bool F32>
-constexpr int kRun = kBatch<F32> / 4;
+constexpr int kBatch = 64;      // K rows that a wave has in flight at once
+constexpr int kRun = kBatch / 4;  // the run of them that a lane has
 
 // A batch's K rows go to the 16-lane groups q = 0..3 in runs of kRun, so that a
 // lane's values of x lie together: step s of the products takes row kRun q + s
@@ -31,7 +34,7 @@ constexpr int kRun = kBatch<F32> / 4;
 // kRun values of x of one token (64 bytes); those from K on are zeros.
 template <bool F32>
 __device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K, uint32_t (&v)[F32 ? 16 : 8]) {
-  if (k + kRun<F32> <= K) {
+  if (k + kRun <= K) {
     __builtin_memcpy(v, static_cast<const char*>(x) + (row + k) * (F32 ? 4 : 2), F32 ? 64 : 32);
     return;
   }
@@ -56,9 +59,9 @@ __device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)
                                       floatx4 (&acc)[MATS][2][T]) {
   constexpr int E = F32 ? 4 : 2;
   const int q = (threadIdx.x & 63) >> 4;
-  uint32_t v[MATS][kRun<F32>][F32 ? 2 : 1], xv[T][F32 ? 16 : 8];
+  uint32_t v[MATS][kRun][F32 ? 2 : 1], xv[T][F32 ? 16 : 8];
 #pragma unroll
-  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + kRun<F32> * q, a.K, xv[t]);
+  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + kRun * q, a.K, xv[t]);
 #pragma unroll
   for (int m = 0; m < MATS; ++m) {
     const int64_t at = k0 * a.ldw[m] * E, end = ((a.K - 1) * a.ldw[m] + a.N) * E;
@@ -66,7 +69,7 @@ __device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)
         const_cast<char*>(static_cast<const char*>(a.w[m]) + at), 0, static_cast<int>(max<int64_t>(0, min<int64_t>(end - at, 0x7ffffff0))), 0x00020000);
     const uint32_t step = static_cast<uint32_t>(a.ldw[m]) * E;
 #pragma unroll
-    for (int s = 0; s < kRun<F32>; ++s) {
+    for (int s = 0; s < kRun; ++s) {
       if constexpr (F32) {
         typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
         const uint2v w = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(r, off[m] + s * step, 0, 0));
@@ -90,7 +93,7 @@ __device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)
   } else {
     typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
 #pragma unroll
-    for (int s = 0; s < kRun<F32> / 4; ++s)
+    for (int s = 0; s < kRun / 4; ++s)
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
         const uint32_t w0 = v[m][4 * s][0], w1 = v[m][4 * s + 1][0], w2 = v[m][4 * s + 2][0], w3 = v[m][4 * s + 3][0];
@@ -129,9 +132,9 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
   uint32_t off[MATS];
 #pragma unroll
   for (int m = 0; m < MATS; ++m)
-    off[m] = (kRun<F32> * (lane >> 4) * static_cast<uint32_t>(a.ldw[m]) + static_cast<uint32_t>(col)) * (F32 ? 4 : 2);
+    off[m] = (kRun * (lane >> 4) * static_cast<uint32_t>(a.ldw[m]) + static_cast<uint32_t>(col)) * (F32 ? 4 : 2);
   // batches of this wave
-  const int batches = (a.K + kBatch<F32> - 1) / kBatch<F32>, parts = a.splits * W;
+  const int batches = (a.K + kBatch - 1) / kBatch, parts = a.splits * W;
   const int part = split * W + wave, each = batches / parts, rest = batches - each * parts;
   const int first = each * part + min(part, rest), last = first + each + (part < rest ? 1 : 0);
   int64_t xrow[T];
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int t = 0; t < T; ++t) acc[m][i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-  for (int b = first; b < last; ++b) batch<F32, MATS, T>(a, xrow, b * kBatch<F32>, off, acc);
+  for (int b = first; b < last; ++b) batch<F32, MATS, T>(a, xrow, b * kBatch, off, acc);
   const Activation act(a.e.act);
 #pragma unroll
   for (int t = 0; t < T; ++t) {
@@ -214,7 +217,7 @@ hipError_t launch_decode_tokens(const DecodeArgs& a, dim3 grid, hipStream_t s) {
 }  // namespace
 
 int64_t decode_groups(int64_t N) { return (N + kCols - 1) / kCols; }
-int64_t decode_batches(int64_t K, bool f32) { return f32 ? (K + kBatch<true> - 1) / kBatch<true> : (K + kBatch<false> - 1) / kBatch<false>; }
+int64_t decode_batches(int64_t K) { return (K + kBatch - 1) / kBatch; }
 
 hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s) {
   if (a.M <= 0 || a.N <= 0) return hipSuccess;

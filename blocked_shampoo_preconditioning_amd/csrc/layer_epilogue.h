@@ -58,8 +58,11 @@ __device__ __forceinline__ int scale_exp(uint32_t word) {
 
 // The epilogue on columns [col, col + 8) of one row: v (and for kGate also w,
 // the same columns of u; for kActBwd g and u as they lie in memory). oc, og: the
-// place in the results and in g and u. Columns from N to pad_to get zeros. Returns the largest finite |value| of a result
-// that a later product reads.
+// place in the results and in g and u. Columns from N to pad_to get zeros.
+// Returns the largest finite |value| of a result that a later product reads.
+// bf16 g and u are rounded where they are kept (the activation takes them before
+// that): the kept state and this epilogue's traffic, which is as long as its
+// product at ordinary widths, would double without.
 template <bool F32, int EPI>
 __device__ __forceinline__ float finish8(const EpiArgs& e, const Activation& act, int problem, int64_t oc, int64_t og, int col, int N,
                                          float (&v)[8], float (&w)[8], const Raw8<F32>& gr, const Raw8<F32>& ur) {

@@ -84,7 +84,7 @@ struct DecodeArgs {
   EpiArgs e;
 };
 int64_t decode_groups(int64_t N);   // workgroups before splitting
-int64_t decode_batches(int64_t K, bool f32);  // the smallest parts K is cut into
+int64_t decode_batches(int64_t K);  // the smallest parts K is cut into
 hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s);
 
 // A copy of an operand: out[rows][ld_out], columns zero-padded to ld_out (a

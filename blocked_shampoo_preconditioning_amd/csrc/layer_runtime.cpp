@@ -56,16 +56,16 @@ int guarded(F&& f) {
 // Tile and K splits of the products of one launch, by an estimate of its time in
 // microseconds. A K step of 64 takes 1.6 for a 256 tile alone on its CU, 0.92
 // for two 128 tiles on one and 0.72 for one alone, with two sets of waves 0.43
-// on a part of the card and 0.55 on the whole (the L2s' rate). Workgroups of
-// unequal length fill the card about as well as equal ones of the same total,
+// on a part of the card and 0.55 on the whole (the L2s' rate), which is what is
+// reckoned with. Workgroups of unequal length fill the card about as well as equal ones of the same total,
 // but the launch takes at least its longest one's time. Filling and emptying
 // costs 5, 3 or 4, a split another launch and its sums' way through memory.
 // Measured with the choices left open (a whole step, us): dx of 2048 x 2048 x
 // 8192 as 256 tiles in 4 parts 656, as 128 tiles unsplit 709; dWg and dWu of
 // 1024 x 768 x 2048 as unsplit 128 tiles 114, in two parts 122, y of that size
 // unsplit 124, in 4 parts 118; y of 4096 x 768 x 2048 with one set of waves 159,
-// with two 156; f32 of 1536 x 1000 x 2728 with the whole card's 0.55 388, with
-// 0.43 throughout 425 and more.
+// with two 156, its g, u and h as 256 tiles 155, as 128 tiles 161; f32 of 1536 x
+// 1000 x 2728 with 0.55 388, with 0.46 425.
 struct Shape {
   int64_t M, N;
   int problems;
@@ -280,7 +280,7 @@ struct Ffn {
   }
   // The forward products of a few tokens, weights as the caller has them.
   void few_product(shl::DecodeArgs& g, shl::Epi epi) {
-    const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K, f32);
+    const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K);
     int64_t s = 1;
     if (groups < 192) {
       s = 512 / groups;

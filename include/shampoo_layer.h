@@ -8,7 +8,8 @@
  * Conventions are shampoo.h's: status codes, shampoo_last_error, device
  * memory owned by the caller, every call asynchronous on the given stream,
  * row-major matrices with a leading dimension in elements. In addition:
- *  - Results are deterministic: no atomics, every sum in a fixed order.
+ *  - Results are deterministic: every sum is taken in a fixed order, and
+ *    atomics only take maxima.
  *  - Sums, statistics and products accumulate in fp32; an element is rounded
  *    (to nearest even) when it is stored in bf16.
  *  - A workspace is scratch: nothing is kept in it after the call's work on
@@ -41,7 +42,11 @@ extern "C" {
  * |value| into [2^14, 2^15) and split into two fp16 terms (as
  * SHAMPOO_GEMM_SPLIT_F16), three products of which accumulate in fp32. An
  * infinite or NaN operand makes every result it enters non-finite, and leaves
- * the others as they are. */
+ * the others as they are. In bf16, g, u, h, dg and du are rounded when they are
+ * stored between the products (h from unrounded g and u): the matrix cores
+ * take no more of h, dg and du, and g and u are what a step keeps. dx, dWg and
+ * dWu then differ from fp32 intermediates' by 0.003 in relative norm, where
+ * rounding the results alone gives 0.0017. */
 typedef enum {
   SHAMPOO_ACT_SILU = 0, /* g / (1 + exp(-g))                               */
   SHAMPOO_ACT_GELU = 1, /* tanh form                                       */
