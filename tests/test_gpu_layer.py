@@ -112,6 +112,15 @@ def test_ffn_256_tiles():
     check_ffn(4000, 520, 3000, "silu", "bf16", seed=5)
 
 
+@pytest.mark.parametrize("n,d,f", [(4612, 72, 843), (5383, 1491, 72), (757, 975, 3156), (500, 588, 4184), (1537, 520, 900),
+                                   (4097, 40, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ffn_tiles(n, d, f, dtype):
+    """The first sizes at which each product takes each tile: one set of waves or two (with an odd number of K steps), K whole or
+    in up to 32 parts."""
+    check_ffn(n, d, f, "gelu", dtype, seed=8)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_dropout_alone(dtype):
     g = torch.Generator().manual_seed(1)
