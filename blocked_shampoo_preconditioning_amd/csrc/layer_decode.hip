@@ -3,17 +3,19 @@
 // Every weight is read once for at most 16 T rows of x, so the kernel is bound
 // by HBM. The weights' rows [k][n] go from memory into registers, two columns a
 // lane: the 16 lanes of a row read 32 columns in whole 64-byte pieces, and
-// each wave has 16 loads a matrix in flight with no LDS in their way. The
+// each wave has 8 to 16 loads a matrix in flight with no LDS in their way. The
 // matrix cores take them as they come: the weights are the "A" operand (16 rows
 // of one 16 x 16 product are columns 2 j + i, j the lane of a row), x the "B"
 // operand (16 tokens). fp32 uses the fp32 matrix instruction, so it is exact to
 // fp32 accumulation.
 //
 // One token of 2048 x 8192 bf16: g, u and h (67 MB) in 20 us, y (34 MB) in 10 and
-// 4 to join its 32 parts of K (16 and 8 for the products when the last-level
+// 4 to join its 8 parts of K (16 and 8 for the products when the last-level
 // cache still has the weights); 13 tokens of 768 x 2048 fp32 (19 MB): 10, 5 and 3,
-// where the launches are more than half. Batches of 128 rows spill;
-// non-temporal loads are no faster.
+// where the launches are more than half; 64 tokens of 2048 x 8192 fp32 (201 MB) in
+// 105. Loaded as one batch of 64 rows at a time: 33.5 us against 32.4 for the
+// one token, 120 against 105 for the 64. Two batches of 64 spill; non-temporal
+// loads are no faster.
 #include "layer_epilogue.h"
 #include "layer_kernels.h"
 
@@ -24,26 +26,28 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) short short4v;
 
 constexpr int kCols = 32;       // columns of a workgroup
-constexpr int kBatch = 64;      // K rows that a wave has in flight at once
+constexpr int kBatch = 32;      // K rows of a load; a wave has one or two of them in flight
 constexpr int kRun = kBatch / 4;  // the run of them that a lane has
 
 // A batch's K rows go to the 16-lane groups q = 0..3 in runs of kRun, so that a
 // lane's values of x lie together: step s of the products takes row kRun q + s
 // (fp32, four rows a product) or rows kRun q + 4 s + 0..3 (bf16, sixteen).
 //
-// kRun values of x of one token (64 bytes); those from K on are zeros.
+// kRun values of x of one token; those from K on are zeros.
 template <bool F32>
-__device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K, uint32_t (&v)[F32 ? 16 : 8]) {
+constexpr int kWords = F32 ? kRun : kRun / 2;
+template <bool F32>
+__device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K, uint32_t (&v)[kWords<F32>]) {
   if (k + kRun <= K) {
-    __builtin_memcpy(v, static_cast<const char*>(x) + (row + k) * (F32 ? 4 : 2), F32 ? 64 : 32);
+    __builtin_memcpy(v, static_cast<const char*>(x) + (row + k) * (F32 ? 4 : 2), 4 * kWords<F32>);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < (F32 ? 16 : 8); ++i) v[i] = 0;
+  for (int i = 0; i < kWords<F32>; ++i) v[i] = 0;
 #pragma unroll 1
   for (int e = K - k - 1; e >= 0; --e) {  // shifted in from the last one
 #pragma unroll
-    for (int i = (F32 ? 15 : 7); i > 0; --i) v[i] = F32 ? v[i - 1] : v[i] << 16 | v[i - 1] >> 16;
+    for (int i = kWords<F32> - 1; i > 0; --i) v[i] = F32 ? v[i - 1] : v[i] << 16 | v[i - 1] >> 16;
     if constexpr (F32)
       v[0] = static_cast<const uint32_t*>(x)[row + k + e];
     else
@@ -55,13 +59,15 @@ __device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K,
 // past the weights' end and read as zeros; what a lane reads past a row's last
 // column belongs to columns that are not stored.
 template <bool F32, int MATS, int T>
-__device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)[T], int k0, const uint32_t (&off)[MATS],
-                                      floatx4 (&acc)[MATS][2][T]) {
+struct Batch {
+  uint32_t w[MATS][kRun][F32 ? 2 : 1], x[T][kWords<F32>];
+};
+template <bool F32, int MATS, int T>
+__device__ __forceinline__ void load(const DecodeArgs& a, const int64_t (&xrow)[T], int k0, const uint32_t (&off)[MATS], Batch<F32, MATS, T>& b) {
   constexpr int E = F32 ? 4 : 2;
   const int q = (threadIdx.x & 63) >> 4;
-  uint32_t v[MATS][kRun][F32 ? 2 : 1], xv[T][F32 ? 16 : 8];
 #pragma unroll
-  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + kRun * q, a.K, xv[t]);
+  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + kRun * q, a.K, b.x[t]);
 #pragma unroll
   for (int m = 0; m < MATS; ++m) {
     const int64_t at = k0 * a.ldw[m] * E, end = ((a.K - 1) * a.ldw[m] + a.N) * E;
@@ -73,15 +79,20 @@ __device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)
       if constexpr (F32) {
         typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
         const uint2v w = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(r, off[m] + s * step, 0, 0));
-        v[m][s][0] = w[0], v[m][s][1] = w[1];
+        b.w[m][s][0] = w[0], b.w[m][s][1] = w[1];
       } else {
-        v[m][s][0] = __builtin_amdgcn_raw_buffer_load_b32(r, off[m] + s * step, 0, 0);
+        b.w[m][s][0] = __builtin_amdgcn_raw_buffer_load_b32(r, off[m] + s * step, 0, 0);
       }
     }
   }
+}
+
+// Their products.
+template <bool F32, int MATS, int T>
+__device__ __forceinline__ void use(const Batch<F32, MATS, T>& b, floatx4 (&acc)[MATS][2][T]) {
   if constexpr (F32) {
 #pragma unroll
-    for (int s = 0; s < 16; ++s)
+    for (int s = 0; s < kRun; ++s)
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -89,23 +100,23 @@ __device__ __forceinline__ void batch(const DecodeArgs& a, const int64_t (&xrow)
 #pragma unroll
           for (int t = 0; t < T; ++t)
             acc[m][i][t] =
-                __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[m][s][i]), __uint_as_float(xv[t][s]), acc[m][i][t], 0, 0, 0);
+                __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b.w[m][s][i]), __uint_as_float(b.x[t][s]), acc[m][i][t], 0, 0, 0);
   } else {
     typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
 #pragma unroll
     for (int s = 0; s < kRun / 4; ++s)
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
-        const uint32_t w0 = v[m][4 * s][0], w1 = v[m][4 * s + 1][0], w2 = v[m][4 * s + 2][0], w3 = v[m][4 * s + 3][0];
+        const uint32_t w0 = b.w[m][4 * s][0], w1 = b.w[m][4 * s + 1][0], w2 = b.w[m][4 * s + 2][0], w3 = b.w[m][4 * s + 3][0];
         // four rows of the lane's first and second column
         const uint2v c0 = {__builtin_amdgcn_perm(w1, w0, 0x05040100u), __builtin_amdgcn_perm(w3, w2, 0x05040100u)};
         const uint2v c1 = {__builtin_amdgcn_perm(w1, w0, 0x07060302u), __builtin_amdgcn_perm(w3, w2, 0x07060302u)};
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          const uint2v xx = {xv[t][2 * s], xv[t][2 * s + 1]};
-          const short4v b = __builtin_bit_cast(short4v, xx);
-          acc[m][0][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c0), b, acc[m][0][t], 0, 0, 0);
-          acc[m][1][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c1), b, acc[m][1][t], 0, 0, 0);
+          const uint2v xx = {b.x[t][2 * s], b.x[t][2 * s + 1]};
+          const short4v x4 = __builtin_bit_cast(short4v, xx);
+          acc[m][0][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c0), x4, acc[m][0][t], 0, 0, 0);
+          acc[m][1][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c1), x4, acc[m][1][t], 0, 0, 0);
         }
       }
   }
@@ -147,8 +158,20 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int t = 0; t < T; ++t) acc[m][i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // one batch is loaded while the one before it is multiplied
+  Batch<F32, MATS, T> even, odd;
+  int b = first;
+  if (b < last) load<F32, MATS, T>(a, xrow, b * kBatch, off, even);
 #pragma unroll 1
-  for (int b = first; b < last; ++b) batch<F32, MATS, T>(a, xrow, b * kBatch, off, acc);
+  for (; b + 2 < last; b += 2) {
+    load<F32, MATS, T>(a, xrow, (b + 1) * kBatch, off, odd);
+    use<F32, MATS, T>(even, acc);
+    load<F32, MATS, T>(a, xrow, (b + 2) * kBatch, off, even);
+    use<F32, MATS, T>(odd, acc);
+  }
+  if (b + 1 < last) load<F32, MATS, T>(a, xrow, (b + 1) * kBatch, off, odd);
+  if (b < last) use<F32, MATS, T>(even, acc);
+  if (b + 1 < last) use<F32, MATS, T>(odd, acc);
   const Activation act(a.e.act);
 #pragma unroll
   for (int t = 0; t < T; ++t) {

@@ -284,7 +284,7 @@ struct Ffn {
     int64_t s = 1;
     if (groups < 192) {
       s = 512 / groups;
-      const int64_t most = f32 || N > 16 ? batches / 8 : batches / 16;  // a batch for each wave
+      const int64_t most = f32 || N > 16 ? batches / 16 : batches / 32;  // two batches for each wave
       if (s > most) s = most;
       if (s > 32) s = 32;
     }
