@@ -30,16 +30,16 @@ struct Raw8 {
 // Elements [col, col + n) of a row that starts at p + row, n <= 8 of them (the
 // others 0). Whole groups go as 16-byte accesses whatever their alignment
 // (global memory takes unaligned ones). A row's last group n < 8 reads the
-// row's last eight and moves them down, since a loop over single elements
-// would wait for each; only rows shorter than eight are read so.
+// row's last eight, which settle8 moves down, since a loop over single elements
+// would wait for each; only rows shorter than eight are read so. Loads that
+// are to be in flight together are all fetched before the first is settled.
 template <bool F32>
-__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t row, int col, int n) {
+__device__ __forceinline__ Raw8<F32> fetch8(const void* p, int64_t row, int col, int n) {
   constexpr int E = F32 ? 4 : 2, W = F32 ? 8 : 4;
   Raw8<F32> r;
   uint32_t w[W];
-  const int up = col >= 8 || n == 8 ? 8 - n : 0;  // elements to read before col
   if (n > 0 && (n == 8 || col >= 8)) {
-    __builtin_memcpy(w, static_cast<const char*>(p) + (row + col - up) * E, 8 * E);
+    __builtin_memcpy(w, static_cast<const char*>(p) + (row + col - (8 - n)) * E, 8 * E);
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0;
@@ -58,7 +58,18 @@ __device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t row, int c
       }
     }
   }
-  if (up > 0 && up < 8) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> settle8(Raw8<F32> r, int col, int n) {
+  constexpr int W = F32 ? 8 : 4;
+  const int up = 8 - n;  // elements that were read before col
+  if (n > 0 && n < 8 && col >= 8) {
+    uint32_t w[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = r.w[i / 4][i % 4];
 #pragma unroll
     for (int b = 4; b > 0; b >>= 1) {
       if (up & b) {
@@ -74,10 +85,14 @@ __device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t row, int c
         }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
+    for (int i = 0; i < W; ++i) r.w[i / 4][i % 4] = w[i];
+  }
   return r;
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t row, int col, int n) {
+  return settle8<F32>(fetch8<F32>(p, row, col, n), col, n);
 }
 template <bool F32>
 __device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {

@@ -56,13 +56,13 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int bx_log2
     Raw8<F32> w[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
-      if (row + k * step < a.rows) w[k] = load_raw8<F32>(a.x, (row + k * step) * a.ldx, static_cast<int>(col), n);
+      if (row + k * step < a.rows) w[k] = fetch8<F32>(a.x, (row + k * step) * a.ldx, static_cast<int>(col), n);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (row + k * step >= a.rows) continue;
       float m[8], v[8];
       drop_factors(a.drop, static_cast<uint64_t>(row + k * step), static_cast<uint32_t>(c8), m);
-      unpack8<F32>(w[k], v);
+      unpack8<F32>(settle8<F32>(w[k], static_cast<int>(col), n), v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = dropped(v[i], m[i]);
       store8(a.y, (row + k * step) * a.ldy + col, n, F32, v);
@@ -77,15 +77,28 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int bx_log2
 // its workgroup and the backward pass keeps its column sums in registers over
 // the range.
 
+// A wave's sum, in a fixed order, through the lanes' own data paths: quads, the
+// halves and the whole of a row of 16, then rows 0 to 1 and 2 to 3, 1 to 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float from_lane(float x) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x += from_lane<0xb1, 0xf>(x);
+  x += from_lane<0x4e, 0xf>(x);
+  x += from_lane<0x141, 0xf>(x);
+  x += from_lane<0x140, 0xf>(x);
+  x += from_lane<0x142, 0xa>(x);
+  x += from_lane<0x143, 0xc>(x);
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+
 // Sum of x and y over the workgroup, in a fixed order. `turn` alternates two
 // places, so one barrier a sum is enough.
 template <int NT>
 __device__ __forceinline__ void block_sum(float& x, float& y, float (&buf)[2][2][NT / 64 + 1], int& turn) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    x += __shfl_xor(x, o);
-    y += __shfl_xor(y, o);
-  }
+  x = wave_sum(x);
+  y = wave_sum(y);
   if (NT == 64) return;
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
@@ -133,36 +146,47 @@ __device__ __forceinline__ void row_stats(const float (&v)[C][8], const int (&n)
   rstd = 1.f / sqrtf(q / d + eps);
 }
 
+// A lane's chunks of a row, as fetch8 leaves them, and their values.
 template <bool F32, int C, int NT, bool GENERAL>
-__device__ __forceinline__ void load_vec(const void* p, int64_t off, const int (&n)[C], float fill, float (&v)[C][8]) {
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = (c * NT + threadIdx.x) * 8;
-    if (p && n[c] > 0) {
-      load8<F32>(p, off, col, GENERAL ? n[c] : 8, v[c]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = fill;
-    }
-  }
-}
-template <bool F32, int C, int NT, bool GENERAL>
-__device__ __forceinline__ void load_raw(const void* p, int64_t off, const int (&n)[C], Raw8<F32> (&v)[C]) {
+__device__ __forceinline__ void fetch(const void* p, int64_t off, const int (&n)[C], Raw8<F32> (&v)[C]) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = (c * NT + threadIdx.x) * 8;
     if (GENERAL)
-      v[c] = load_raw8<F32>(p, off, col, n[c]);
+      v[c] = fetch8<F32>(p, off, col, n[c]);
     else if (n[c] > 0)
-      v[c] = load_raw8<F32>(p, off, col, 8);
+      v[c] = fetch8<F32>(p, off, col, 8);
     else
       v[c] = Raw8<F32>{};
   }
 }
-template <bool F32, int C>
-__device__ __forceinline__ void unpack(const Raw8<F32> (&w)[C], float (&v)[C][8]) {
+template <bool F32, int C, int NT, bool GENERAL>
+__device__ __forceinline__ void unpack(const Raw8<F32> (&w)[C], const int (&n)[C], float (&v)[C][8]) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) unpack8<F32>(w[c], v[c]);
+  for (int c = 0; c < C; ++c)
+    unpack8<F32>(GENERAL ? settle8<F32>(w[c], (c * NT + static_cast<int>(threadIdx.x)) * 8, n[c]) : w[c], v[c]);
+}
+// The same of a vector that may not be there (`none` stands for its elements).
+template <bool F32, int C, int NT, bool GENERAL>
+__device__ __forceinline__ void fetch_vec(const void* p, int64_t off, const int (&n)[C], Raw8<F32> (&v)[C]) {
+  if (p) fetch<F32, C, NT, GENERAL>(p, off, n, v);
+}
+template <bool F32, int C, int NT, bool GENERAL>
+__device__ __forceinline__ void unpack_vec(const void* p, const Raw8<F32> (&w)[C], const int (&n)[C], float none, float (&v)[C][8]) {
+  if (p) {
+    unpack<F32, C, NT, GENERAL>(w, n, v);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = none;
+  }
+}
+template <bool F32, int C, int NT, bool GENERAL>
+__device__ __forceinline__ void load_vec(const void* p, int64_t off, const int (&n)[C], float none, float (&v)[C][8]) {
+  Raw8<F32> w[C];
+  fetch_vec<F32, C, NT, GENERAL>(p, off, n, w);
+  unpack_vec<F32, C, NT, GENERAL>(p, w, n, none, v);
 }
 template <int C>
 __device__ __forceinline__ void fill(float (&v)[C][8], float x) {
@@ -203,28 +227,39 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
   int n[C];
   chunk_sizes<C, NT>(a.d, n);
   Raw8<F32> xr[C], zr[C];
-  load_raw<F32, C, NT, GENERAL>(a.x, first * a.ldx, n, xr);
-  if (a.z) load_raw<F32, C, NT, GENERAL>(a.z, first * a.ldz, n, zr);
+  fetch<F32, C, NT, GENERAL>(a.x, first * a.ldx, n, xr);
+  if (a.z) fetch<F32, C, NT, GENERAL>(a.z, first * a.ldz, n, zr);
   float wp[C][8], bp[C][8], gate[C][8], wn[C][8], bn[C][8];
-  load_vec<F32, C, NT, GENERAL>(a.w_post, 0, n, 1.f, wp);
-  load_vec<F32, C, NT, GENERAL>(a.w_next, 0, n, 1.f, wn);
-  if (GENERAL) {
-    load_vec<F32, C, NT, GENERAL>(a.b_post, 0, n, 0.f, bp);
-    load_vec<F32, C, NT, GENERAL>(a.b_next, 0, n, 0.f, bn);
+  // the first gate row is loaded with the weights, not when a row waits for it
+  int64_t group = first / a.rows_per_gate;
+  {
+    Raw8<F32> v[5][C];
+    fetch_vec<F32, C, NT, GENERAL>(a.w_post, 0, n, v[0]);
+    fetch_vec<F32, C, NT, GENERAL>(a.w_next, 0, n, v[1]);
+    if (GENERAL) {
+      fetch_vec<F32, C, NT, GENERAL>(a.b_post, 0, n, v[2]);
+      fetch_vec<F32, C, NT, GENERAL>(a.b_next, 0, n, v[3]);
+    }
+    fetch_vec<F32, C, NT, GENERAL>(a.gate, group * a.ld_gate, n, v[4]);
+    unpack_vec<F32, C, NT, GENERAL>(a.w_post, v[0], n, 1.f, wp);
+    unpack_vec<F32, C, NT, GENERAL>(a.w_next, v[1], n, 1.f, wn);
+    if (GENERAL) {
+      unpack_vec<F32, C, NT, GENERAL>(a.b_post, v[2], n, 0.f, bp);
+      unpack_vec<F32, C, NT, GENERAL>(a.b_next, v[3], n, 0.f, bn);
+    }
+    unpack_vec<F32, C, NT, GENERAL>(a.gate, v[4], n, 1.f, gate);
   }
-  fill<C>(gate, 1.f);
-  int64_t group = -1;
   for (int64_t row = first; row < last; ++row) {
     float z[C][8], r[C][8];
-    unpack<F32, C>(xr, r);
-    unpack<F32, C>(zr, z);
+    unpack<F32, C, NT, GENERAL>(xr, n, r);
+    unpack<F32, C, NT, GENERAL>(zr, n, z);
     if (row + 1 < last) {  // the next row's loads go ahead of this row's stores
-      load_raw<F32, C, NT, GENERAL>(a.x, (row + 1) * a.ldx, n, xr);
-      if (a.z) load_raw<F32, C, NT, GENERAL>(a.z, (row + 1) * a.ldz, n, zr);
+      fetch<F32, C, NT, GENERAL>(a.x, (row + 1) * a.ldx, n, xr);
+      if (a.z) fetch<F32, C, NT, GENERAL>(a.z, (row + 1) * a.ldz, n, zr);
     }
     float mz = 0.f, rz = 1.f, mr = 0.f, rr = 1.f;
     if (a.z) {
-      if (a.gate && (group < 0 || row >= (group + 1) * a.rows_per_gate)) {
+      if (a.gate && row >= (group + 1) * a.rows_per_gate) {
         group = row / a.rows_per_gate;
         load_vec<F32, C, NT, GENERAL>(a.gate, group * a.ld_gate, n, 1.f, gate);
       }
@@ -287,11 +322,11 @@ __global__ __launch_bounds__(NT, NT == 512 || GENERAL ? 2 : 3) void norm_backwar
   auto load = [&](int64_t row) {
     st = *reinterpret_cast<const floatx4*>(a.stats + row * 4);
     if (has_next) {
-      load_raw<F32, C, NT, GENERAL>(a.r, row * a.ldr, n, rw);
-      load_raw<F32, C, NT, GENERAL>(a.dn, row * a.lddn, n, dnw);
+      fetch<F32, C, NT, GENERAL>(a.r, row * a.ldr, n, rw);
+      fetch<F32, C, NT, GENERAL>(a.dn, row * a.lddn, n, dnw);
     }
-    if (a.dr) load_raw<F32, C, NT, GENERAL>(a.dr, row * a.lddr, n, drw);
-    if (a.z) load_raw<F32, C, NT, GENERAL>(a.z, row * a.ldz, n, zw);
+    if (a.dr) fetch<F32, C, NT, GENERAL>(a.dr, row * a.lddr, n, drw);
+    if (a.z) fetch<F32, C, NT, GENERAL>(a.z, row * a.ldz, n, zw);
   };
   if (first < last) load(first);
   // Rows over 4096 wide read weights and gate anew for each row (from the
@@ -304,11 +339,19 @@ __global__ __launch_bounds__(NT, NT == 512 || GENERAL ? 2 : 3) void norm_backwar
     load_vec<F32, C, NT, GENERAL>(a.w_post, 0, n, 1.f, wp);
     if (GENERAL) load_vec<F32, C, NT, GENERAL>(a.b_post, 0, n, 0.f, bp);
   };
-  if (HOLD) {
-    load_next();
-    load_post();
-  }
+  int64_t group = first / a.rows_per_gate;
   fill<C>(gate, 1.f);
+  if (HOLD && first < last) {  // the first gate row too
+    Raw8<F32> v[4][C];
+    fetch_vec<F32, C, NT, GENERAL>(a.w_next, 0, n, v[0]);
+    fetch_vec<F32, C, NT, GENERAL>(a.w_post, 0, n, v[1]);
+    if (GENERAL) fetch_vec<F32, C, NT, GENERAL>(a.b_post, 0, n, v[2]);
+    fetch_vec<F32, C, NT, GENERAL>(a.gate, group * a.ld_gate, n, v[3]);
+    unpack_vec<F32, C, NT, GENERAL>(a.w_next, v[0], n, 1.f, wn);
+    unpack_vec<F32, C, NT, GENERAL>(a.w_post, v[1], n, 1.f, wp);
+    if (GENERAL) unpack_vec<F32, C, NT, GENERAL>(a.b_post, v[2], n, 0.f, bp);
+    unpack_vec<F32, C, NT, GENERAL>(a.gate, v[3], n, 1.f, gate);
+  }
   float s_wn[C][8], s_bn[C][8], s_wp[C][8], s_bp[C][8], s_g[C][8];
   fill<C>(s_wn, 0.f);
   fill<C>(s_wp, 0.f);
@@ -321,7 +364,6 @@ __global__ __launch_bounds__(NT, NT == 512 || GENERAL ? 2 : 3) void norm_backwar
   auto put = [&](int what, const float (&v)[C][8]) {
     store_row<C, NT, GENERAL>(a.partial + what * plane, static_cast<int64_t>(blockIdx.x) * a.d, n, true, v);
   };
-  int64_t group = -1;
   auto put_gate = [&]() {
     const int64_t begin = group * a.rows_per_gate;
     const int64_t end = begin + a.rows_per_gate < a.rows ? begin + a.rows_per_gate : a.rows;
@@ -336,17 +378,17 @@ __global__ __launch_bounds__(NT, NT == 512 || GENERAL ? 2 : 3) void norm_backwar
     float r[C][8], dn[C][8], dr[C][8], z[C][8];
     const float m = st[2], rs = st[3], mz = st[0], rz = st[1];
     if (has_next) {
-      unpack<F32, C>(rw, r);
-      unpack<F32, C>(dnw, dn);
+      unpack<F32, C, NT, GENERAL>(rw, n, r);
+      unpack<F32, C, NT, GENERAL>(dnw, n, dn);
     }
     if (a.dr)
-      unpack<F32, C>(drw, dr);
+      unpack<F32, C, NT, GENERAL>(drw, n, dr);
     else
       fill<C>(dr, 0.f);
-    if (a.z) unpack<F32, C>(zw, z);
+    if (a.z) unpack<F32, C, NT, GENERAL>(zw, n, z);
     if (row + 1 < last) load(row + 1);  // ahead of this row's stores
-    if (a.gate && (group < 0 || row >= (group + 1) * a.rows_per_gate)) {
-      if (a.dgate && group >= 0) {
+    if (a.gate && row >= (group + 1) * a.rows_per_gate) {
+      if (a.dgate) {
         put_gate();
         fill<C>(s_g, 0.f);
       }
@@ -429,7 +471,7 @@ __global__ __launch_bounds__(NT, NT == 512 || GENERAL ? 2 : 3) void norm_backwar
     if (a.db_next) put(kSumBNext, s_bn);
     if (a.db_post) put(kSumBPost, s_bp);
   }
-  if (a.gate && a.dgate && group >= 0) put_gate();
+  if (a.gate && a.dgate && first < last) put_gate();
 }
 
 // Joins the workgroups' column sums: 32 columns a workgroup, its 32 half-waves
