@@ -596,20 +596,26 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
     const float* p = g.partial + static_cast<int64_t>(problem) * parts * plane;
     constexpr int U = 4;  // parts in flight
     for (int s = 0; s < g.splits; s += U, p += U * jump) {
-      float x[U][8], y[U][8];
+      Raw8<true> x[U], y[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int m = s + k < g.splits ? n : 0;
-        load8<true>(p + k * jump, row * g.N, col, m, x[k]);
-        if (EPI == kGate) load8<true>(p + k * jump + plane, row * g.N, col, m, y[k]);
+        x[k] = fetch8<true>(p + k * jump, row * g.N, col, m);
+        if (EPI == kGate) y[k] = fetch8<true>(p + k * jump + plane, row * g.N, col, m);
       }
 #pragma unroll
-      for (int k = 0; k < U; ++k)
+      for (int k = 0; k < U; ++k) {
+        const int m = s + k < g.splits ? n : 0;
+        float t[8];
+        unpack8<true>(settle8<true>(x[k], col, m), t);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] += x[k][q];
-          if (EPI == kGate) w[q] += y[k][q];
+        for (int q = 0; q < 8; ++q) v[q] += t[q];
+        if (EPI == kGate) {
+          unpack8<true>(settle8<true>(y[k], col, m), t);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) w[q] += t[q];
         }
+      }
     }
     if (F32 && g.max_a) {
       const int exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
@@ -648,19 +654,23 @@ __global__ __launch_bounds__(256) void max_kernel(PackList l) {
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, step = static_cast<int64_t>(gridDim.x) * 256;
   float m = 0.f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
-    float v[4][8];
+    Raw8<true> x[4];
+    int col[4], n[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t at = i + k * step;
       int64_t row;
-      int col;
-      group_place(at < total ? at : 0, c8, total, row, col);
-      load8<true>(p.src, row * p.ld, col, at < total ? static_cast<int>(min<int64_t>(8, p.cols - col)) : 0, v[k]);
+      group_place(at < total ? at : 0, c8, total, row, col[k]);
+      n[k] = at < total ? static_cast<int>(min<int64_t>(8, p.cols - col[k])) : 0;
+      x[k] = fetch8<true>(p.src, row * p.ld, col[k], n[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      float v[8];
+      unpack8<true>(settle8<true>(x[k], col[k], n[k]), v);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = fmaxf(m, finite_abs(v[k][q]));
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, finite_abs(v[q]));
+    }
   }
   m = block_max(m);
   if (threadIdx.x == 0) p.parts[blockIdx.x] = __float_as_uint(m);

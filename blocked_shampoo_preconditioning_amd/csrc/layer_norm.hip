@@ -212,11 +212,11 @@ __device__ __forceinline__ void chunk_sizes(int d, int (&n)[C]) {
 // p = norm(z) w + b, r = alpha x + drop(gate p), n = norm'(r) w' + b': reads x and
 // z, writes r, n and four statistics a row. GENERAL: there is a bias, or the
 // row's last group is short; without, the registers for them are saved. 16384 x
-// 2048 bf16, RMS, gate, dropout (268 MB): 62 us, 4.3 TB/s, bound by HBM and the
-// integer products of the generator; 3001 x 777 fp32, layer norms (37 MB): 18 us,
-// two rows of a workgroup one after the other (a row is two trips to memory and
-// four sums over its lanes; one row each 20 us, three 20, rows of one wave 18);
-// one row of 2048: 4.3 us, the launch.
+// 2048 bf16, RMS, gate, dropout (268 MB): 54 us, 5.0 TB/s, bound by HBM; 3001 x
+// 777 fp32, layer norms (37 MB): 17.5 us, bound by the launch, the first loads (4
+// us for all rows at once) and two rows of a workgroup one after the other (one
+// row each 18 us, three 20, rows of one wave 18); one row of 2048: 3.6 us, the
+// launch.
 template <bool F32, int NT, int C, bool GENERAL>
 __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
   __shared__ float buf[2][2][NT / 64 + 1];
@@ -304,8 +304,8 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
 // order. A gate row whose tokens all lie in this range is stored at once; one
 // that reaches over an end of the range goes to the partial sums (place 0: it
 // began before the range or fills it, place 1: it goes on after it). 16384 x
-// 2048 bf16 (403 MB): 98 us, 4.1 TB/s, bound by HBM and by what 168 registers
-// leave in flight; 3001 x 777 fp32 (56 MB): 27 us, as the forward pass.
+// 2048 bf16 (403 MB): 83 us, 4.9 TB/s, bound by HBM; 3001 x 777 fp32 (56 MB): 23
+// us, as the forward pass.
 enum { kSumWNext = 0, kSumBNext = 1, kSumWPost = 2, kSumBPost = 3, kSumGate = 4, kSums = 6 };
 
 template <bool F32, int NT, int C, bool GENERAL>
@@ -547,15 +547,16 @@ bool norm_general(const NormArgs& a, bool backward) {
   return a.d % 8 != 0 || a.b_post || (backward ? a.db_post || a.db_next : a.b_next != nullptr);
 }
 
-// Workgroups of the row kernels: as many as the card holds at once (twice that
-// in the forward pass; 16384 x 2048 backward: 95 us at three waves a SIMD, 116
-// at two and at four), and where there are rows enough at least two rows each
-// (forward) or four, which share the reads of weights and keep the backward
-// pass's column sums a small part of its traffic (3001 x 777 fp32 backward: 28
-// us at four rows, 32 at two).
+// Workgroups of the row kernels: as many as the card holds at once (four times
+// that in the forward pass: 16384 x 2048 54 us, 56 at twice and at once; backward
+// at three waves a SIMD 95, 116 at two and at four), and where there are rows
+// enough at least two rows each (forward) or four, which share the reads of
+// weights and keep the backward pass's column sums a small part of its traffic
+// (3001 x 777 fp32 backward with its sums: 29 us at four rows, 28 at three, 34 at
+// six; 4096 x 768 bf16 22 at four, 24 at three and at six).
 int64_t norm_grid(const NormArgs& a, bool backward, bool general) {
   const int lanes = norm_lanes(a.d);
-  const int64_t most = backward ? 256 * (lanes == 512 || general ? 8 : 12) * 64 / lanes : 2 * 256 * 16 * 64 / lanes;
+  const int64_t most = backward ? 256 * (lanes == 512 || general ? 8 : 12) * 64 / lanes : 4 * 256 * 16 * 64 / lanes;
   int64_t per = (a.rows + most - 1) / most;
   const int64_t wanted = backward ? 4 : 2;
   const int64_t least = (a.rows + 511) / 512;
