@@ -549,7 +549,9 @@ int norm_args(const shampoo_norm_t* a, bool backward, shl::NormArgs& k) {
   k.dx = a->dx, k.dz = a->dz, k.lddx = a->ld_dx, k.lddz = a->ld_dz;
   k.dw_post = a->d_post_weight, k.db_post = a->d_post_bias, k.dgate = a->d_gate, k.dw_next = a->d_next_weight;
   k.db_next = a->d_next_bias, k.ld_dgate = a->ld_d_gate;
-  k.rows = a->rows, k.rows_per_gate = a->gate ? a->rows_per_gate : 1;
+  // over the rows it is one gate row for all: the kernels and launches add rows
+  // to it, which must not pass 2^63
+  k.rows = a->rows, k.rows_per_gate = a->gate && a->rows > 0 ? (a->rows_per_gate < a->rows ? a->rows_per_gate : a->rows) : 1;
   k.d = static_cast<int32_t>(a->width), k.f32 = a->dtype == SHAMPOO_F32 ? 1 : 0;
   k.post_kind = a->post_kind, k.next_kind = a->next_kind;
   // without z nothing is scaled: the norm's input is x itself
