@@ -32,45 +32,53 @@ struct Activation {
   }
 };
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < __builtin_inff() ? a : 0.f;
-}
-
-// Raises a maximum word by a wave's largest finite |value|. The order of the
-// atomics does not change the result. They queue up at a word, so that every
-// workgroup has one of kMaxParts (1024 on one word: 42 us for a finish kernel
-// that now takes 12), and it does not look at the word first (16 us).
-__device__ __forceinline__ void raise_max(uint32_t* word, float m) {
+// An fp32 value as the sum of three bf16 values, each the nearest one to what the
+// ones before it leave: 24 bits in all, so the sum is exact, at every exponent
+// (below 2^-100 the last terms may lie under the type's smallest normal number).
+// The largest values, which would round up to infinity, are cut off instead.
+// Infinities and NaN go to the first term alone.
+__device__ __forceinline__ void split3(const float (&v)[8], uint4v (&t)[3]) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const uint32_t bits = __float_as_uint(m);
-  if ((threadIdx.x & 63) == 0 && bits) atomicMax(word, bits);
+  for (int i = 0; i < 4; ++i) {
+    float x[2] = {v[2 * i], v[2 * i + 1]};
+    bool finite[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) finite[k] = fabsf(x[k]) < __builtin_inff();
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t w = pack_bf16(x[0], x[1]);
+      if (p == 0) {
+        if (finite[0] && (w & 0x7fffu) == 0x7f80u) w = (w & 0xffff0000u) | __float_as_uint(x[0]) >> 16;
+        if (finite[1] && (w & 0x7fff0000u) == 0x7f800000u) w = (w & 0xffffu) | (__float_as_uint(x[1]) & 0xffff0000u);
+      }
+      t[p][i] = w;
+      x[0] = finite[0] ? x[0] - __uint_as_float(w << 16) : 0.f;
+      x[1] = finite[1] ? x[1] - __uint_as_float(w & 0xffff0000u) : 0.f;
+    }
+  }
 }
-
-// Power of two that an operand's planes are scaled by: its largest finite
-// |value| comes into [2^14, 2^15).
-__device__ __forceinline__ int scale_exp(uint32_t word) {
-  if (word == 0) return 0;
-  const int e = static_cast<int>(word >> 23);
-  return 14 - ((e ? e : 1) - 127);
+// Eight elements to a product's operand: fp32 to three planes.
+__device__ __forceinline__ void store_planes(void* p, int64_t off, int64_t plane, const float (&v)[8]) {
+  uint4v t[3];
+  split3(v, t);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4v*>(static_cast<uint16_t*>(p) + off + k * plane) = t[k];
 }
 
 // The epilogue on columns [col, col + 8) of one row: v (and for kGate also w,
 // the same columns of u; for kActBwd g and u as they lie in memory). oc, og: the
-// place in the results and in g and u. Columns from N to pad_to get zeros.
-// Returns the largest finite |value| of a result that a later product reads.
+// place in the results and in g and u. Columns from N to pad_to get zeros. fp32
+// results that a later product reads are written as its planes (e.plane).
 // bf16 g and u are rounded where they are kept (the activation takes them before
 // that): the kept state and this epilogue's traffic, which is as long as its
 // product at ordinary widths, would double without.
 template <bool F32, int EPI>
-__device__ __forceinline__ float finish8(const EpiArgs& e, const Activation& act, int problem, int64_t oc, int64_t og, int col, int N,
+__device__ __forceinline__ void finish8(const EpiArgs& e, const Activation& act, int problem, int64_t oc, int64_t og, int col, int N,
                                          float (&v)[8], float (&w)[8], const Raw8<F32>& gr, const Raw8<F32>& ur) {
   const int width = e.pad_to > N ? e.pad_to : N;
   // all but a kStore's rows are padded to whole groups of eight
   const int n = EPI == kStore ? min(8, width - col) : col < width ? 8 : 0;
-  float m = 0.f;
-  if (n <= 0) return m;
+  if (n <= 0) return;
   if (col + 8 > N) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -88,9 +96,11 @@ __device__ __forceinline__ float finish8(const EpiArgs& e, const Activation& act
       float a, da;
       act(v[i], a, da);
       v[i] = a * w[i];
-      if (F32) m = fmaxf(m, finite_abs(v[i]));
     }
-    store8(e.c[0], oc, 8, F32, v);
+    if (F32 && e.plane)
+      store_planes(e.c[0], oc, e.plane, v);
+    else
+      store8(e.c[0], oc, 8, F32, v);
   } else {
     float g[8], u[8];
     unpack8<F32>(gr, g);
@@ -101,12 +111,15 @@ __device__ __forceinline__ float finish8(const EpiArgs& e, const Activation& act
       act(g[i], a, da);
       g[i] = v[i] * u[i] * da;
       u[i] = v[i] * a;
-      if (F32) m = fmaxf(m, fmaxf(finite_abs(g[i]), finite_abs(u[i])));
     }
-    store8(e.c[0], oc, 8, F32, g);
-    store8(e.c[1], oc, 8, F32, u);
+    if (F32) {
+      store_planes(e.c[0], oc, e.plane, g);
+      store_planes(e.c[1], oc, e.plane, u);
+    } else {
+      store8(e.c[0], oc, 8, F32, g);
+      store8(e.c[1], oc, 8, F32, u);
+    }
   }
-  return m;
 }
 
 // What kActBwd reads of g and u for eight columns of a row.

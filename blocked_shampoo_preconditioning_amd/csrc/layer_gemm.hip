@@ -6,9 +6,13 @@
 // registers (buffer loads with an LDS destination, 16 bytes a lane), double
 // buffered over K steps of 64; fragments leave LDS as 16-byte rows (K
 // contiguous) or through the transposing 8-byte read (K the slow index), so no
-// operand is ever transposed in memory. fp32 operands come as two fp16 planes
-// each (pack_kernel): three products of them in a row, the small ones first,
-// give fp32 accuracy at three bf16 products' cost.
+// operand is ever transposed in memory. fp32 operands come as three bf16 planes
+// whose sum is the value exactly (split3), at every exponent: no element's digits
+// go by what the others hold, as one scale for an array would have it. A product
+// of two is six products of planes (the three left out are below 2^-25 of it
+// together); all six take their fragments from one K step's planes in
+// LDS, so a result costs six times the matrix instructions of bf16, but three
+// times the loads.
 //
 // What bounds it: large products run into the power limit (8192 x 2048 x 8192
 // bf16, all six: 2.09 ms, 1180 TFLOP/s, the matrix cores busy 62% of the time at
@@ -16,8 +20,13 @@
 // L2s, which feed a 128 tile 32 KiB a K step (0.46 us with every CU busy, half
 // the rate of the matrix cores), small ones what a launch costs besides its K
 // loop: about 9 us from the first load to the last store. Step of 4096 x 768 x
-// 2048 bf16 156 us (743 TFLOP/s), 1024 x 768 x 2048 75 us, 4096 x 768 x 2048 fp32
-// 469 us (247 TFLOP/s of fp32 results; the library's fp32 product alone: 154).
+// 2048 bf16 156 us (743 TFLOP/s), 1024 x 768 x 2048 75 us. fp32 4096 x 768 x 2048
+// 620 us (187 TFLOP/s of fp32 results; the library's fp32 product alone: 154), 2048
+// x 2048 x 8192 3.0 ms (205; 1230 of bf16 products, the power limit). Two fp16
+// planes under one power of two for an operand took 480 us, but rows 10^9 times
+// smaller than the largest kept three digits and at 10^12 none.
+#include <type_traits>
+
 #include "layer_epilogue.h"
 #include "layer_kernels.h"
 
@@ -27,11 +36,9 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) int int4v;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(8))) _Float16 halfx8;
 typedef __attribute__((ext_vector_type(4))) short short4v;
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kBK = 64;                 // K step
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // ------------------------------------------------------------------ the tile
@@ -40,25 +47,34 @@ constexpr uint32_t kOutOfRange = 0x80000000u;
 // sums are joined through LDS: four waves alone on a CU leave its matrix cores
 // idle between their phases (a 128 tile takes 0.6 us a K step with them, half of
 // 0.85 with eight; y of 4096 x 2048 x 768, 192 tiles: 26.5 against 22.8 us).
-template <int FM_, int FN_, int WM_, int WN_, int KG_ = 1>
+// P planes of an operand (planes(f32)); the K step BK is 32 for three, so that
+// two steps of 128 x 256 results fit in LDS.
+constexpr int k_step(bool f32) { return f32 ? 32 : 64; }
+template <int FM_, int FN_, int WM_, int WN_, int KG_, bool F32_>
 struct Tile {
   static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, KG = KG_;
+  static constexpr bool F32 = F32_;
+  static constexpr int P = planes(F32), BK = k_step(F32);
   static constexpr int NW = WM * WN, NT = NW * 64 * KG;
-  static_assert(KG == 1 || (KG == 2 && FM == 4), "");
+  static_assert(KG == 1 || (KG == 2 && FM == 4 && !F32), "");
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
-  static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;  // one plane's
+  static constexpr int STAGE = P * (A_BYTES + B_BYTES);
   static constexpr int PITCH = FN * 16 + 4;  // floats of a row of the epilogue's strips
   static constexpr int STRIPS = NT / 64 * 32 * PITCH * 4;
   static constexpr int LDS = KG * 2 * STAGE > STRIPS ? KG * 2 * STAGE : STRIPS;
+  static constexpr int WAVES = 160 * 1024 / LDS * NT / 256;  // of a SIMD at once
 };
 
-// LDS order of 16-byte chunks. A row operand's tile is [rows][64 k] (8 chunks
-// a row), a column operand's [64 k][width] (16 or 8 chunks a row). Chunk c of
-// row r sits at place c ^ swizzle(r), so that the rows that one read takes
+// LDS order of 16-byte chunks. A row operand's tile is [rows][BK k] (8 or 4
+// chunks a row), a column operand's [BK k][width] (16 or 8 chunks a row). Chunk c
+// of row r sits at place c ^ swizzle(r), so that the rows that one read takes
 // together fall on different banks, whether the LDS serves 128 or 256 bytes
 // at a time.
-__device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+template <int BK>
+__device__ __forceinline__ int swz_row(int r) {
+  return BK == 64 ? (r & 7) ^ ((r >> 3) & 1) : ((r >> 1) & 3) ^ ((r >> 3) & 1);
+}
 template <int WIDTH>
 __device__ __forceinline__ int swz_col(int k) {
   return WIDTH == 128 ? ((k & 3) << 1) ^ ((k & 3) << 2) ^ ((k >> 1) & 4) : ((k & 3) << 1) ^ ((k >> 2) & 2);
@@ -101,25 +117,21 @@ __device__ __forceinline__ bf16x8 lds_read_tr(uint32_t at, int second) {
   return x.v;
 }
 
-// The operands' 16 bits are bf16, or fp16 for the planes of fp32 values. The
-// 16 x 16 x 32 instruction takes less power than the 32 x 32 x 16 one (2090
+// The 16 x 16 x 32 instruction takes less power than the 32 x 32 x 16 one (2090
 // against 1860 TFLOP/s sustained from registers), and power is what limits the
 // large products.
-template <bool F16>
 __device__ __forceinline__ floatx4 mfma(const bf16x8& a, const bf16x8& b, const floatx4& c) {
-  if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // One workgroup's tile (or its part of K) of a product: `block` of `blocks`
 // workgroups, a multiple of 8. Forward of 8192 x 2048 x 8192 bf16: g, u and h in
 // 522 us (1053 TFLOP/s; 403 MB are written in it), y in 232 (1187); dh with dg and
 // du in 340 (808; 268 MB are read and 268 written by its epilogue).
-template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
+template <class T, bool ACOL, bool BCOL, int EPI>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uint32_t blocks, char* lds) {
-  constexpr bool GATE = EPI == kGate;
+  constexpr bool GATE = EPI == kGate, F32 = T::F32;
+  constexpr int BK = T::BK, P = T::P;
   constexpr int HN = GATE ? T::BN / 2 : T::BN;       // result columns of a tile
   constexpr int BW = GATE ? T::BN / 2 : 128;         // width of a B panel
   static_assert(BW == 128 || BW == 64, "");
@@ -153,7 +165,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   const int m0 = (4 * group + id - tcol * in_group) * T::BM, n0 = tcol * HN;
 
   // K steps of this split, cut as evenly as they go
-  const int ksteps = (g.K + kBK - 1) / kBK, steps = ksteps * g.nseg;
+  const int ksteps = (g.K + BK - 1) / BK, steps = ksteps * g.nseg;
   int first = 0, last = steps;
   if (g.splits > 1) {
     const int each = steps / g.splits, rest = steps - each * g.splits;
@@ -165,16 +177,19 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   first += kgroup * turns;
   int loads = min(turns, last - first);  // steps still to be loaded
 
-  // Loads: 1 KiB an instruction, NW instructions at a time. A row operand's
-  // buffer starts at the tile's first row and its offsets move along K; a
-  // column operand's starts at the step's first K row and its offsets stay.
-  constexpr int NA = T::A_BYTES / 1024 / T::NW, NB = T::B_BYTES / 1024 / T::NW;
-  constexpr int BPP = BW * kBK * 2 / 1024 / T::NW;  // instructions of one B panel
+  // Loads: 1 KiB an instruction, NW instructions at a time, plane after plane. A
+  // row operand's buffer starts at the tile's first row and its offsets move along
+  // K; a column operand's starts at the step's first K row and its offsets stay.
+  constexpr int NAP = T::A_BYTES / 1024 / T::NW, NBP = T::B_BYTES / 1024 / T::NW;  // of one plane
+  constexpr int NA = P * NAP, NB = P * NBP;
+  constexpr int APP = 128 * BK * 2 / 1024 / T::NW, BPP = BW * BK * 2 / 1024 / T::NW;  // of one panel
+  static_assert(APP > 0 && BPP > 0 && NAP > 0, "");
+  constexpr int CPR = BK / 8, RPI = 64 / CPR;  // row operand: chunks a row, rows an instruction
   const int64_t lda2 = g.lda * 2, ldb2 = g.ldb * 2;
-  // row operand: row (instruction * NW + wave) * 8 + lane / 8, chunk lane % 8 (swizzled)
-  const int rchunk = (lane & 7) ^ swz_row((lane >> 3) + 8 * wave);
+  // row operand: row (instruction * NW + wave) * RPI + lane / CPR, chunk lane % CPR (swizzled)
+  const int rchunk = (lane % CPR) ^ swz_row<BK>(lane / CPR + RPI * wave);
   auto row_off = [&](int64_t ld2, int j) {
-    return static_cast<uint32_t>(((j * T::NW + wave) * 8 + (lane >> 3)) * ld2 + rchunk * 16);
+    return static_cast<uint32_t>(((j * T::NW + wave) * RPI + lane / CPR) * ld2 + rchunk * 16);
   };
   // column operand of panels `width` wide: K row of the panel, chunk (swizzled)
   auto col_off = [&](int64_t ld2, int width, int j, int panel) {
@@ -183,11 +198,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     const int c = (lane % per_row) ^ (width == 128 ? swz_col<128>(k) : swz_col<64>(k));
     return static_cast<uint32_t>(k * ld2 + c * 16 + panel * width * 2);
   };
-  uint32_t va[NA], vb[NB];
+  uint32_t va[NAP], vb[NBP];
 #pragma unroll
-  for (int j = 0; j < NA; ++j) va[j] = ACOL ? col_off(lda2, 128, j % (16 / T::NW), j / (16 / T::NW)) : row_off(lda2, j);
+  for (int j = 0; j < NAP; ++j) va[j] = ACOL ? col_off(lda2, 128, j % APP, j / APP) : row_off(lda2, j);
 #pragma unroll
-  for (int j = 0; j < NB; ++j) vb[j] = BCOL ? col_off(ldb2, BW, j % BPP, GATE ? 0 : j / BPP) : row_off(ldb2, j);
+  for (int j = 0; j < NBP; ++j) vb[j] = BCOL ? col_off(ldb2, BW, j % BPP, GATE ? 0 : j / BPP) : row_off(ldb2, j);
   const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds)) + kgroup * (2 * T::STAGE);
   const uint32_t lds0 = lds_base + wave * 1024;
   const int64_t a_start = ACOL ? 2 * static_cast<int64_t>(m0) : m0 * lda2;
@@ -201,27 +216,28 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   // instruction here is paid for in every K step, so a step moves the buffers by
   // a few scalar additions; a row operand's chunks past K, which only a
   // segment's last step can have, get an offset out of range once.
-  const int64_t a_step = ACOL ? kBK * lda2 : kBK * 2, b_step = BCOL ? kBK * ldb2 : kBK * 2;
+  const int64_t a_step = ACOL ? BK * lda2 : BK * 2, b_step = BCOL ? BK * ldb2 : BK * 2;
+  const int64_t plane_a2 = g.plane_a * 2, plane_b2 = g.plane_b * 2;
   int seg = 0;
   if (first) seg = min(first, steps - 1) / ksteps;
-  int k0 = (first - seg * ksteps) * kBK;
+  int k0 = (first - seg * ksteps) * BK;
   uint64_t pa = 0, pb = 0, pb1 = 0;
   int64_t left_a = 0, left_b = 0;
   bool cut = false;
   auto cut_chunks = [&]() {
-    const bool now = (!ACOL || !BCOL) && k0 + kBK > g.K;
+    const bool now = (!ACOL || !BCOL) && k0 + BK > g.K;
     if (now == cut) return;
     cut = now;
     const uint32_t bit = now && k0 + rchunk * 8 >= g.K ? kOutOfRange : 0u;
 #pragma unroll
-    for (int j = 0; j < NA; ++j)
+    for (int j = 0; j < NAP; ++j)
       if (!ACOL) va[j] = (va[j] & ~kOutOfRange) | bit;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < NBP; ++j)
       if (!BCOL) vb[j] = (vb[j] & ~kOutOfRange) | bit;
   };
   auto enter = [&]() {
-    const int64_t ka = k0 / kBK * a_step, kb = k0 / kBK * b_step;
+    const int64_t ka = k0 / BK * a_step, kb = k0 / BK * b_step;
     pa = reinterpret_cast<uint64_t>(g.a[seg]) + a_start + ka;
     pb = reinterpret_cast<uint64_t>(GATE ? g.b[0][seg] : g.b[problem][seg]) + b_start + kb;
     if (GATE) pb1 = reinterpret_cast<uint64_t>(g.b[1][seg]) + b_start + kb;
@@ -229,28 +245,35 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     left_b = b_size - kb;
     cut_chunks();
   };
-  int4v ra, rb, rb1;
+  int4v ra[P], rb[P], rb1[P];
   uint32_t at = 0;
   auto aim = [&](int buf) {
     at = lds0 + buf * T::STAGE;
     // past the last step nothing is read: the buffer gets zeros
-    ra = make_rsrc(pa, loads > 0 ? left_a : 0);
-    rb = make_rsrc(pb, loads > 0 ? left_b : 0);
-    if (GATE) rb1 = make_rsrc(pb1, loads > 0 ? left_b : 0);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      ra[p] = make_rsrc(pa + p * plane_a2, loads > 0 ? left_a : 0);
+      rb[p] = make_rsrc(pb + p * plane_b2, loads > 0 ? left_b : 0);
+      if (GATE) rb1[p] = make_rsrc(pb1 + p * plane_b2, loads > 0 ? left_b : 0);
+    }
   };
   auto load = [&](int q) {
-    const int j = q < NA ? q : q - NA;
-    load_lds(q < NA ? ra : (GATE && j >= BPP ? rb1 : rb), q < NA ? va[j] : vb[j], at,
-             (q < NA ? 0 : T::A_BYTES) + j * T::NW * 1024);
+    if (q < NA) {
+      const int p = q / NAP, j = q % NAP;
+      load_lds(ra[p], va[j], at, p * T::A_BYTES + j * T::NW * 1024);
+    } else {
+      const int p = (q - NA) / NBP, j = (q - NA) % NBP;
+      load_lds(GATE && j >= BPP ? rb1[p] : rb[p], vb[j], at, P * T::A_BYTES + p * T::B_BYTES + j * T::NW * 1024);
+    }
   };
   auto advance = [&]() {
     if (--loads <= 0) return;
-    k0 += kBK;
+    k0 += BK;
     if (k0 < g.K) {
       pa += a_step, pb += b_step;
       if (GATE) pb1 += b_step;
       left_a -= a_step, left_b -= b_step;
-      if (k0 + kBK > g.K) cut_chunks();
+      if (k0 + BK > g.K) cut_chunks();
     } else {
       ++seg;
       k0 = 0;
@@ -261,9 +284,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   // A lane's places in the fragment reads (16 rows or columns x 32 k, eight k of
   // one row a lane), as LDS addresses of the buffer that is read.
   const int r16 = lane & 15, q4 = lane >> 4;
-  // row operand: row r16 of a fragment, chunk 4 ks + q4; fragments 2 KiB apart
+  // row operand: row r16 of a fragment, chunk 4 ks + q4
   auto row_at = [&](uint32_t tile, int row0, int ks) {
-    return static_cast<uint32_t>(tile + (row0 + r16) * 128 + (((4 * ks + q4) ^ swz_row(r16)) << 4));
+    return static_cast<uint32_t>(tile + (row0 + r16) * (2 * BK) + (((4 * ks + q4) ^ swz_row<BK>(r16)) << 4));
   };
   // column operand: k = 32 ks + 8 q4 + (lane % 16) / 4 (+ 4 in the second
   // read), columns 4 (lane % 4) on
@@ -273,16 +296,18 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     const int s = width == 128 ? swz_col<128>(kk) : swz_col<64>(kk);
     return static_cast<uint32_t>(tile + kk * (width * 2) + ((c ^ s) << 4) + (lane & 1) * 8);
   };
-  uint32_t fa[ACOL ? T::FM : 2], fb[BCOL ? T::FN : 2];
+  constexpr int KS = BK / 32;
+  constexpr uint32_t b_base = P * T::A_BYTES;
+  uint32_t fa[ACOL ? T::FM : KS], fb[BCOL ? T::FN : KS];
   if (ACOL) {
 #pragma unroll
     for (int i = 0; i < T::FM; ++i) {
       const int row = (wm * T::FM + i) * 16;
-      fa[ACOL ? i : 0] = col_at(lds_base + (row >> 7) * 16384, 128, row & 127);
+      fa[ACOL ? i : 0] = col_at(lds_base + (row >> 7) * (256 * BK), 128, row & 127);
     }
   } else {
-    fa[0] = row_at(lds_base, wm * T::FM * 16, 0);
-    fa[1] = row_at(lds_base, wm * T::FM * 16, 1);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) fa[ACOL ? 0 : ks] = row_at(lds_base, wm * T::FM * 16, ks);
   }
   if (BCOL) {
 #pragma unroll
@@ -291,19 +316,20 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
       constexpr int H2 = T::FN / 2;
       const int col = GATE ? (wn * H2 + j % H2) * 16 : (wn * T::FN + j) * 16;
       const int panel = GATE ? j / H2 : col >> 7;
-      fb[BCOL ? j : 0] = col_at(lds_base + T::A_BYTES + panel * (BW * kBK * 2), BW, GATE ? col : col & 127);
+      fb[BCOL ? j : 0] = col_at(lds_base + b_base + panel * (BW * BK * 2), BW, GATE ? col : col & 127);
     }
   } else {
-    fb[0] = row_at(lds_base + T::A_BYTES, wn * T::FN * 16, 0);
-    fb[1] = row_at(lds_base + T::A_BYTES, wn * T::FN * 16, 1);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) fb[BCOL ? 0 : ks] = row_at(lds_base + b_base, wn * T::FN * 16, ks);
   }
-  auto frag_a = [&](int i, int ks) {
-    if (ACOL) return lds_read_tr(fa[ACOL ? i : 0] + ks * (32 * 256), 4 * 256);
-    return lds_read16(fa[ks] + i * 2048);
+  // fragment i of slice ks (32 k) of plane p
+  auto frag_a = [&](int i, int ks, int p = 0) {
+    if (ACOL) return lds_read_tr(fa[ACOL ? i : 0] + (ks * (32 * 256) + p * T::A_BYTES), 4 * 256);
+    return lds_read16(fa[ACOL ? 0 : ks] + (i * (32 * BK) + p * T::A_BYTES));
   };
-  auto frag_b = [&](int j, int ks) {
-    if (BCOL) return lds_read_tr(fb[BCOL ? j : 0] + ks * (32 * BW * 2), 4 * BW * 2);
-    return lds_read16(fb[ks] + j * 2048);
+  auto frag_b = [&](int j, int ks, int p = 0) {
+    if (BCOL) return lds_read_tr(fb[BCOL ? j : 0] + (ks * (32 * BW * 2) + p * T::B_BYTES), 4 * BW * 2);
+    return lds_read16(fb[BCOL ? 0 : ks] + (j * (32 * BK) + p * T::B_BYTES));
   };
   uint32_t flip = T::STAGE;
   auto other_buffer = [&]() {
@@ -329,104 +355,178 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   // barrier a wave's loads of the next step have landed and its reads of this
   // step are done, so after it the next step can be read and this step's buffer
   // be filled again, which the last phase does with its loads between the
-  // products.
-  constexpr bool HALVE_A = T::FM >= T::FN, TWO = T::FM * T::FN > 16;
-  constexpr int H = (HALVE_A ? T::FM : T::FN) / (TWO ? 2 : 1), F = HALVE_A ? T::FN : T::FM;
-  bf16x8 lo[H], hi[H], full0[F], full1[F];
-  auto read_half = [&](int ks, int half, bf16x8(&x)[H]) {
-#pragma unroll
-    for (int i = 0; i < H; ++i) x[i] = HALVE_A ? frag_a(half * H + i, ks) : frag_b(half * H + i, ks);
-  };
-  auto read_full = [&](int ks, bf16x8(&x)[F]) {
-#pragma unroll
-    for (int i = 0; i < F; ++i) x[i] = HALVE_A ? frag_b(i, ks) : frag_a(i, ks);
-  };
-  constexpr int kMma = H * F;
-  auto product = [&](int half, int q, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
-    const int h = q / F, f = q % F;
-    if (HALVE_A) {
-      floatx4& c = acc[half * H + h][f];
-      c = mfma<F32>(y[f], x[h], c);
-    } else {
-      floatx4& c = acc[f][half * H + h];
-      c = mfma<F32>(x[h], y[f], c);
+  // products. With three planes a K step is one slice and six phases, the
+  // products of two planes; the last of them are the middle planes', whose
+  // fragments' registers the next step's first do not need.
+  auto prologue = [&](auto first_reads) {
+    if (turns > 0) {
+      enter();
+  #pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        aim(i);
+  #pragma unroll
+        for (int q = 0; q < NA + NB; ++q) load(q);
+        advance();
+      }
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NA + NB) : "memory");
+      first_reads();
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // one phase's products, with the LDS reads before them in the program spread
-  // between them (a read of a row operand is one instruction, of a column
-  // operand two)
-  constexpr int kHalfReads = H * ((HALVE_A ? ACOL : BCOL) ? 2 : 1), kFullReads = F * ((HALVE_A ? BCOL : ACOL) ? 2 : 1);
-  auto mma = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F], int reads) {
+  if constexpr (F32) {
+    bf16x8 a[P][T::FM], b[P][T::FN];
+    auto read_a = [&](int p) {
 #pragma unroll
-    for (int q = 0; q < kMma; ++q) product(half, q, x, y);
-    if (reads == kHalfReads) {
+      for (int i = 0; i < T::FM; ++i) a[p][i] = frag_a(i, 0, p);
+    };
+    auto read_b = [&](int p) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) b[p][j] = frag_b(j, 0, p);
+    };
+    constexpr int kMma = T::FM * T::FN, kReadsA = T::FM * (ACOL ? 2 : 1), kReadsB = T::FN * (BCOL ? 2 : 1);
+    auto product = [&](int q, int pa_, int pb_) {
+      floatx4& c = acc[q / T::FN][q % T::FN];
+      c = mfma(b[pb_][q % T::FN], a[pa_][q / T::FN], c);
+    };
+    // a phase's products, the LDS reads before them in the program between them
+    auto mma = [&](int pa_, int pb_, auto reads) {
+      constexpr int kEach = (decltype(reads)::value + kMma / 2 - 1) / (kMma / 2);
+#pragma unroll
+      for (int q = 0; q < kMma; ++q) product(q, pa_, pb_);
+      if constexpr (kEach > 0) {
+#pragma unroll
+        for (int q = 0; q < kMma; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    prologue([&]() {
+      read_a(0);
+      read_b(0);
+    });
+    int buf = 0;
+    for (int turn = 0; turn < turns; ++turn) {
+      aim(buf);
+      buf ^= 1;
+      read_b(1);
+      read_a(1);
+      mma(0, 0, std::integral_constant<int, kReadsA + kReadsB>{});
+      read_b(2);
+      mma(0, 1, std::integral_constant<int, kReadsB>{});
+      read_a(2);
+      mma(1, 0, std::integral_constant<int, kReadsA>{});
+      mma(0, 2, std::integral_constant<int, 0>{});
+      mma(2, 0, std::integral_constant<int, 0>{});
+      other_buffer();
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      read_a(0);
+      read_b(0);
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int kEach = (NA + NB + kMma - 1) / kMma;
 #pragma unroll
       for (int q = 0; q < kMma; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kMma / 2 - 1) / (kMma / 2), 0);
+        product(q, 1, 1);
+        if (q * kEach < NA + NB) {
+#pragma unroll
+          for (int e = 0; e < kEach; ++e)
+            if (q * kEach + e < NA + NB) load(q * kEach + e);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < kMma; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kFullReads + kMma / 2 - 1) / (kMma / 2), 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // the same with a step's loads between them
-  auto mma_load = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
-    constexpr int kEach = (NA + NB + kMma - 1) / kMma;
-#pragma unroll
-    for (int q = 0; q < kMma; ++q) {
-      product(half, q, x, y);
-      if (q * kEach < NA + NB) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e)
-          if (q * kEach + e < NA + NB) load(q * kEach + e);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  if (turns > 0) {
-    enter();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      aim(i);
-#pragma unroll
-      for (int q = 0; q < NA + NB; ++q) load(q);
+      __builtin_amdgcn_sched_barrier(0);
       advance();
     }
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NA + NB) : "memory");
-    read_half(0, 0, lo);
-    read_full(0, full0);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  int buf = 0;
-  for (int turn = 0; turn < turns; ++turn) {
-    aim(buf);
-    buf ^= 1;
-    if (TWO) {
-      read_half(0, 1, hi);
-      mma(0, lo, full0, kHalfReads);
-      read_half(1, 0, lo);
-      read_full(1, full1);
-      mma(1, hi, full0, kHalfReads + kFullReads);
-      read_half(1, 1, hi);
-      mma(0, lo, full1, kHalfReads);
-    } else {
-      read_half(1, 0, hi);
-      read_full(1, full1);
-      mma(0, lo, full0, kHalfReads + kFullReads);
+  } else {
+    constexpr bool HALVE_A = T::FM >= T::FN, TWO = T::FM * T::FN > 16;
+    constexpr int H = (HALVE_A ? T::FM : T::FN) / (TWO ? 2 : 1), F = HALVE_A ? T::FN : T::FM;
+    bf16x8 lo[H], hi[H], full0[F], full1[F];
+    auto read_half = [&](int ks, int half, bf16x8(&x)[H]) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) x[i] = HALVE_A ? frag_a(half * H + i, ks) : frag_b(half * H + i, ks);
+    };
+    auto read_full = [&](int ks, bf16x8(&x)[F]) {
+#pragma unroll
+      for (int i = 0; i < F; ++i) x[i] = HALVE_A ? frag_b(i, ks) : frag_a(i, ks);
+    };
+    constexpr int kMma = H * F;
+    auto product = [&](int half, int q, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
+      const int h = q / F, f = q % F;
+      if (HALVE_A) {
+        floatx4& c = acc[half * H + h][f];
+        c = mfma(y[f], x[h], c);
+      } else {
+        floatx4& c = acc[f][half * H + h];
+        c = mfma(x[h], y[f], c);
+      }
+    };
+    // one phase's products, with the LDS reads before them in the program spread
+    // between them (a read of a row operand is one instruction, of a column
+    // operand two)
+    constexpr int kHalfReads = H * ((HALVE_A ? ACOL : BCOL) ? 2 : 1), kFullReads = F * ((HALVE_A ? BCOL : ACOL) ? 2 : 1);
+    auto mma = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F], int reads) {
+#pragma unroll
+      for (int q = 0; q < kMma; ++q) product(half, q, x, y);
+      if (reads == kHalfReads) {
+#pragma unroll
+        for (int q = 0; q < kMma; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kMma / 2 - 1) / (kMma / 2), 0);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < kMma; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, (kHalfReads + kFullReads + kMma / 2 - 1) / (kMma / 2), 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // the same with a step's loads between them
+    auto mma_load = [&](int half, const bf16x8(&x)[H], const bf16x8(&y)[F]) {
+      constexpr int kEach = (NA + NB + kMma - 1) / kMma;
+#pragma unroll
+      for (int q = 0; q < kMma; ++q) {
+        product(half, q, x, y);
+        if (q * kEach < NA + NB) {
+#pragma unroll
+          for (int e = 0; e < kEach; ++e)
+            if (q * kEach + e < NA + NB) load(q * kEach + e);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    prologue([&]() {
+      read_half(0, 0, lo);
+      read_full(0, full0);
+    });
+    int buf = 0;
+    for (int turn = 0; turn < turns; ++turn) {
+      aim(buf);
+      buf ^= 1;
+      if (TWO) {
+        read_half(0, 1, hi);
+        mma(0, lo, full0, kHalfReads);
+        read_half(1, 0, lo);
+        read_full(1, full1);
+        mma(1, hi, full0, kHalfReads + kFullReads);
+        read_half(1, 1, hi);
+        mma(0, lo, full1, kHalfReads);
+      } else {
+        read_half(1, 0, hi);
+        read_full(1, full1);
+        mma(0, lo, full0, kHalfReads + kFullReads);
+      }
+      other_buffer();
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      read_half(0, 0, lo);
+      read_full(0, full0);
+      __builtin_amdgcn_sched_barrier(0);
+      mma_load(TWO ? 1 : 0, hi, full1);
+      advance();
     }
-    other_buffer();
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read_half(0, 0, lo);
-    read_full(0, full0);
-    __builtin_amdgcn_sched_barrier(0);
-    mma_load(TWO ? 1 : 0, hi, full1);
-    advance();
   }
 
   // Epilogue. A lane's accumulators are column r16 (row m of the result) and
@@ -472,9 +572,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     __syncthreads();
   }
   float* strip = reinterpret_cast<float*>(lds) + any_wave * (32 * PITCH);
-  int exponent = 0;
-  if (F32) exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
-  float largest = 0.f;
 #pragma unroll
   for (int i = 0; i < STRIPS; ++i) {
     if (act_bwd && i + AHEAD < STRIPS) {
@@ -515,12 +612,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
         float v[8], w[8];
         strip8(p, v, w);
         if (row0 + down >= g.M) return;
-        if (F32) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = ldexpf(v[q], exponent), w[q] = ldexpf(w[q], exponent);
-        }
-        largest = fmaxf(largest, finish8<F32, EPI>(g.e, act, problem, oc + down * ldc, og + down * g.e.ldg, col, g.N, v, w,
-                                                   gr[i & AHEAD][p], ur[i & AHEAD][p]));
+        finish8<F32, EPI>(g.e, act, problem, oc + down * ldc, og + down * g.e.ldg, col, g.N, v, w, gr[i & AHEAD][p], ur[i & AHEAD][p]);
       };
       if (EPI == kActBwd) {
 #pragma unroll
@@ -533,13 +625,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  if (F32 && EPI != kStore && g.splits == 1) raise_max(g.max_parts + blockIdx.x % kMaxParts, largest);
 }
 
-template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
+template <class T, bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(T::NT, T::WAVES) void gemm_kernel(GemmArgs g) {
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
-  gemm_tile<T, F32, ACOL, BCOL, EPI>(g, blockIdx.x, gridDim.x, lds);
+  gemm_tile<T, ACOL, BCOL, EPI>(g, blockIdx.x, gridDim.x, lds);
 }
 
 // The backward pass's last three products in one launch: dx (operands by rows),
@@ -548,26 +639,16 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_kernel(GemmArgs g) {
 // together nearly do, with fewer splits and no gaps between launches (backward
 // pass of 1024 tokens 71 -> 47 us, of 4096 142 -> 105). 8192 x 2048 x 8192 bf16:
 // 1077 us (1276 TFLOP/s); 4096 x 768 x 2048: 68 us (945).
-template <class T, bool F32>
-__global__ __launch_bounds__(T::NT, 2) void gemm_group_kernel(GroupArgs a) {
+template <class T>
+__global__ __launch_bounds__(T::NT, T::WAVES) void gemm_group_kernel(GroupArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
   const uint32_t b = blockIdx.x;
   if (b < a.start[1])
-    gemm_tile<T, F32, false, false, kStore>(a.g[0], b, a.start[1], lds);
+    gemm_tile<T, false, false, kStore>(a.g[0], b, a.start[1], lds);
   else if (b < a.start[2])
-    gemm_tile<T, F32, true, true, kStore>(a.g[1], b - a.start[1], a.start[2] - a.start[1], lds);
+    gemm_tile<T, true, true, kStore>(a.g[1], b - a.start[1], a.start[2] - a.start[1], lds);
   else
-    gemm_tile<T, F32, true, true, kStore>(a.g[2], b - a.start[2], a.start[3] - a.start[2], lds);
-}
-
-// The largest of a workgroup's values (256 threads), in every thread.
-__device__ __forceinline__ float block_max(float m) {
-  __shared__ float waves[4];
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = m;
-  __syncthreads();
-  return fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
+    gemm_tile<T, true, true, kStore>(a.g[2], b - a.start[2], a.start[3] - a.start[2], lds);
 }
 
 // Joins the parts of a split product in their order and runs the epilogue. A
@@ -585,7 +666,6 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
   constexpr int parts = EPI == kGate ? 2 : 1;
   const int64_t plane = static_cast<int64_t>(g.M) * g.N;
   const int n = max(0, min(8, g.N - col));
-  float largest = 0.f;
   if (i < static_cast<int64_t>(c8) * g.M) {
     Raw8<F32> gr, ur;
     if (EPI == kActBwd) load_gu<F32>(g.e, true, og, col, g.N, gr, ur);
@@ -617,16 +697,7 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
         }
       }
     }
-    if (F32 && g.max_a) {
-      const int exponent = -(scale_exp(*g.max_a) + scale_exp(*g.max_b));
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = ldexpf(v[q], exponent), w[q] = ldexpf(w[q], exponent);
-    }
-    largest = finish8<F32, EPI>(g.e, Activation(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
-  }
-  if (F32 && EPI != kStore && g.max_parts) {
-    largest = block_max(largest);
-    if (threadIdx.x < 64) raise_max(g.max_parts + blockIdx.x % kMaxParts, largest);
+    finish8<F32, EPI>(g.e, Activation(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
   }
 }
 
@@ -644,90 +715,41 @@ __device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total
   }
 }
 
-// Largest finite |value| of what each workgroup reads of an operand
-// (blockIdx.y), to the operand's kMaxParts places: 1024 atomics on three words
-// took longer than the reads. Clears the words that products will raise. Bound
-// by HBM and the launch: x and the weights of 4096 x 768 x 2048 (31 MB) in 10 us.
-__global__ __launch_bounds__(256) void max_kernel(PackList l) {
-  const PackArgs& p = l.t[blockIdx.y];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kMaxParts) l.clear[threadIdx.x] = 0;
-  const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, step = static_cast<int64_t>(gridDim.x) * 256;
-  float m = 0.f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
-    Raw8<true> x[4];
-    int col[4], n[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t at = i + k * step;
-      int64_t row;
-      group_place(at < total ? at : 0, c8, total, row, col[k]);
-      n[k] = at < total ? static_cast<int>(min<int64_t>(8, p.cols - col[k])) : 0;
-      x[k] = fetch8<true>(p.src, row * p.ld, col[k], n[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float v[8];
-      unpack8<true>(settle8<true>(x[k], col[k], n[k]), v);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) m = fmaxf(m, finite_abs(v[q]));
-    }
-  }
-  m = block_max(m);
-  if (threadIdx.x == 0) p.parts[blockIdx.x] = __float_as_uint(m);
-}
-
 // Copies operands into rows that loads can take (16-byte aligned, padded with
-// zeros to whole 16 bytes). fp32 values become two fp16 planes: x 2^e = h + l
-// + d with e from the operand's largest finite |value| (scale_exp), |d| <=
-// 2^-22 |x 2^e| (or 2^-25 for the smallest). Infinities and NaN go to h alone,
-// so a product they enter is not finite and no other is touched. Bound by HBM: x
-// and the weights of 4096 x 768 x 2048 fp32 (63 MB both ways) in 12.6 us, bf16 of
-// odd strides (1537 x 1001 x 2730, 39 MB) in 8.
+// zeros to whole 16 bytes); fp32 values become three bf16 planes (split3). Bound
+// by HBM.
 template <bool F32>
 __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
   const PackArgs& p = list.t[blockIdx.y];
   const int64_t c8 = p.ld_out / 8, total = c8 * p.rows, plane = p.rows * p.ld_out;
-  int e = 0;
-  if (F32 && p.n_parts > 0) {  // the word comes from the parts of all operands that share it
-    float m = 0.f;
-    for (int i = threadIdx.x; i < p.n_parts; i += 256) m = fmaxf(m, __uint_as_float(p.parts[p.first_part + i]));
-    const uint32_t word = __float_as_uint(block_max(m));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.word = word;
-    e = scale_exp(word);
-  } else if (F32) {
-    e = scale_exp(*p.word);
-  }
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
     int64_t row;
     int col;
     group_place(i, c8, total, row, col);
     const int n = static_cast<int>(min<int64_t>(8, p.cols - col));
     const Raw8<F32> raw = load_raw8<F32>(p.src, row * p.ld, col, n);
-    uint16_t* out = p.out + row * p.ld_out + col;
-    if (!F32) {
-      *reinterpret_cast<uint4v*>(out) = raw.w[0];
-      continue;
+    if constexpr (F32) {
+      float v[8];
+      unpack8<F32>(raw, v);
+      store_planes(p.out, row * p.ld_out + col, plane, v);
+    } else {
+      *reinterpret_cast<uint4v*>(p.out + row * p.ld_out + col) = raw.w[0];
     }
-    float v[8];
-    unpack8<F32>(raw, v);
-    halfx8 h, l;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float x = ldexpf(v[q], e);
-      h[q] = static_cast<_Float16>(x);
-      l[q] = fabsf(v[q]) < __builtin_inff() ? static_cast<_Float16>(x - static_cast<float>(h[q])) : static_cast<_Float16>(0.f);
-    }
-    *reinterpret_cast<halfx8*>(out) = h;
-    *reinterpret_cast<halfx8*>(out + plane) = l;
   }
 }
 
 // 256 tiles run as eight waves of 128 x 64 (kGate: 64 x 128, so that a wave's
-// rows of h are whole 128-byte segments).
+// rows of h are whole 128-byte segments). fp32 tiles too run as eight: of 64 x 64
+// in the wide one, of 64 x 32 in the other, but for the gate's, whose panels of 64
+// columns are loads for four waves (step of 8192 x 256 x 512 with four everywhere
+// 223 us, with eight 190; 300 x 512 x 1024 87 and 79).
 template <int EPI>
-using Tile256 = Tile<EPI == kGate ? 4 : 8, EPI == kGate ? 8 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4>;
-using Tile128 = Tile<4, 4, 2, 2>;
-using Tile128x2 = Tile<4, 4, 2, 2, 2>;
+using Tile256 = Tile<EPI == kGate ? 4 : 8, EPI == kGate ? 8 : 4, EPI == kGate ? 4 : 2, EPI == kGate ? 2 : 4, 1, false>;
+using Tile128 = Tile<4, 4, 2, 2, 1, false>;
+template <int EPI>
+using TileF32 = Tile<4, EPI == kGate ? 4 : 2, 2, EPI == kGate ? 2 : 4, 1, true>;
+using Tile128x2 = Tile<4, 4, 2, 2, 2, false>;
+using TileWide = Tile<4, 4, 2, 4, 1, true>;
 
 // Workgroups of a product, a multiple of 8 (one for each XCD).
 int64_t gemm_blocks(const GemmArgs& g, TileKind tile, bool gate) {
@@ -735,45 +757,40 @@ int64_t gemm_blocks(const GemmArgs& g, TileKind tile, bool gate) {
   return (gemm_tiles(g.M, g.N, g.problems, tile, gate) * g.splits + 7) / 8 * 8;
 }
 
-template <class T, bool F32, bool ACOL, bool BCOL, int EPI>
+template <class T, bool ACOL, bool BCOL, int EPI>
 hipError_t launch_one(const GemmArgs& g, TileKind tile, hipStream_t s) {
   const int64_t grid = gemm_blocks(g, tile, EPI == kGate);
-  if (grid > 0x7fffffff || gemm_steps(g.K, g.nseg) > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_kernel<T, F32, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
+  if (grid > 0x7fffffff || gemm_steps(g.K, g.nseg, T::F32) > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_kernel<T, ACOL, BCOL, EPI>), dim3(static_cast<uint32_t>(grid)), dim3(T::NT), 0, s, g);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || g.splits == 1) return err;
   return launch_finish(g, static_cast<Epi>(EPI), s);
 }
 
-template <class T, bool F32>
+template <class T>
 hipError_t launch_group_tiles(GroupArgs& a, TileKind tile, hipStream_t s) {
   int64_t at = 0;
   for (int i = 0; i < 3; ++i) {
     a.start[i] = static_cast<uint32_t>(at);
     at += gemm_blocks(a.g[i], tile, false);
-    if (at > 0x7fffffff || gemm_steps(a.g[i].K, a.g[i].nseg) > 0x7fffffff) return hipErrorInvalidValue;
+    if (at > 0x7fffffff || gemm_steps(a.g[i].K, a.g[i].nseg, T::F32) > 0x7fffffff) return hipErrorInvalidValue;
   }
   a.start[3] = static_cast<uint32_t>(at);
   if (at == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm_group_kernel<T, F32>), dim3(static_cast<uint32_t>(at)), dim3(T::NT), 0, s, a);
+  hipLaunchKernelGGL((gemm_group_kernel<T>), dim3(static_cast<uint32_t>(at)), dim3(T::NT), 0, s, a);
   hipError_t e = hipGetLastError();
   for (int i = 0; i < 3 && e == hipSuccess; ++i)
     if (a.g[i].splits > 1 && a.g[i].M > 0) e = launch_finish(a.g[i], kStore, s);
   return e;
 }
 
-template <bool F32>
-hipError_t launch_typed(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
-#define SHL_CASE(AC, BC, E)                                                                           \
-  if (a_cols == AC && b_cols == BC && epi == E)                                                       \
-    return tile == kTile256 ? launch_one<Tile256<E>, F32, AC, BC, E>(g, tile, s)                      \
-                            : tile == kTile128 ? launch_one<Tile128, F32, AC, BC, E>(g, tile, s)      \
-                                               : launch_one<Tile128x2, F32, AC, BC, E>(g, tile, s);
-  SHL_CASE(false, true, kGate)
-  SHL_CASE(false, true, kStore)
-  SHL_CASE(false, false, kActBwd)
-#undef SHL_CASE
-  return hipErrorInvalidValue;
+template <bool ACOL, bool BCOL, int EPI>
+hipError_t launch_tile(const GemmArgs& g, TileKind tile, hipStream_t s) {
+  if (g.f32)
+    return tile == kTileWide ? launch_one<TileWide, ACOL, BCOL, EPI>(g, tile, s) : launch_one<TileF32<EPI>, ACOL, BCOL, EPI>(g, tile, s);
+  return tile == kTile256   ? launch_one<Tile256<EPI>, ACOL, BCOL, EPI>(g, tile, s)
+         : tile == kTile128 ? launch_one<Tile128, ACOL, BCOL, EPI>(g, tile, s)
+                            : launch_one<Tile128x2, ACOL, BCOL, EPI>(g, tile, s);
 }
 
 uint32_t pack_grid(const PackList& l) {
@@ -788,26 +805,27 @@ uint32_t pack_grid(const PackList& l) {
 }  // namespace
 
 int64_t gemm_tiles(int64_t M, int64_t N, int problems, TileKind tile, bool gate) {
-  const int64_t w = tile == kTile256 ? 256 : 128, hn = gate ? w / 2 : w;
-  return ((M + w - 1) / w) * ((N + hn - 1) / hn) * problems;
+  const int64_t h = tile == kTile256 ? 256 : 128, w = tile == kTile256 || tile == kTileWide ? 256 : 128, hn = gate ? w / 2 : w;
+  return ((M + h - 1) / h) * ((N + hn - 1) / hn) * problems;
 }
 
-int64_t gemm_steps(int64_t K, int nseg) { return (K + kBK - 1) / kBK * nseg; }
+int64_t gemm_steps(int64_t K, int nseg, bool f32) { return (K + k_step(f32) - 1) / k_step(f32) * nseg; }
 
 hipError_t launch_gemm(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
-  return g.f32 ? launch_typed<true>(g, tile, a_cols, b_cols, epi, s) : launch_typed<false>(g, tile, a_cols, b_cols, epi, s);
-}
-
-template <class T>
-static hipError_t launch_group_typed(GroupArgs& a, TileKind tile, bool f32, hipStream_t s) {
-  return f32 ? launch_group_tiles<T, true>(a, tile, s) : launch_group_tiles<T, false>(a, tile, s);
+  if (!is_tile(tile, g.f32)) return hipErrorInvalidValue;
+  if (!a_cols && b_cols && epi == kGate) return launch_tile<false, true, kGate>(g, tile, s);
+  if (!a_cols && b_cols && epi == kStore) return launch_tile<false, true, kStore>(g, tile, s);
+  if (!a_cols && !b_cols && epi == kActBwd) return launch_tile<false, false, kActBwd>(g, tile, s);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_group(GroupArgs& a, TileKind tile, bool f32, hipStream_t s) {
-  return tile == kTile256   ? launch_group_typed<Tile256<kStore>>(a, tile, f32, s)
-         : tile == kTile128 ? launch_group_typed<Tile128>(a, tile, f32, s)
-                            : launch_group_typed<Tile128x2>(a, tile, f32, s);
+  if (!is_tile(tile, f32)) return hipErrorInvalidValue;
+  if (f32) return tile == kTileWide ? launch_group_tiles<TileWide>(a, tile, s) : launch_group_tiles<TileF32<kStore>>(a, tile, s);
+  return tile == kTile256   ? launch_group_tiles<Tile256<kStore>>(a, tile, s)
+         : tile == kTile128 ? launch_group_tiles<Tile128>(a, tile, s)
+                            : launch_group_tiles<Tile128x2>(a, tile, s);
 }
 
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s) {
@@ -826,12 +844,6 @@ hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s) {
   SHL_FINISH(kActBwd)
 #undef SHL_FINISH
   return hipErrorInvalidValue;
-}
-
-hipError_t launch_max(const PackList& l, hipStream_t s) {
-  if (l.n == 0) return hipSuccess;
-  hipLaunchKernelGGL(max_kernel, dim3(kMaxParts, l.n), dim3(256), 0, s, l);
-  return hipGetLastError();
 }
 
 hipError_t launch_pack(const PackList& l, hipStream_t s) {

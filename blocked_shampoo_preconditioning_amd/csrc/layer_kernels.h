@@ -7,7 +7,9 @@
 
 namespace shl {
 
-constexpr int kMaxSeg = 6;  // two products of three plane pairs (gradient of x, fp32)
+constexpr int kMaxSeg = 2;  // the gradient of x is the sum of two products
+// bf16 terms of an operand: fp32 values are the sum of three (split3)
+constexpr int planes(bool f32) { return f32 ? 3 : 1; }
 
 enum Act { kSilu = 0, kGelu = 1, kRelu = 2 };
 
@@ -26,21 +28,18 @@ struct EpiArgs {
   int64_t ldg;
   int32_t act;
   int32_t pad_to;      // columns [N, pad_to) are written as zeros (rows padded for a later product)
+  int64_t plane;       // f32, kGate and kActBwd: c are planes, `plane` elements apart; 0: fp32 arrays
 };
 
-// Partial maxima that an operand's largest |value| is put together from.
-constexpr int kMaxParts = 256;
-
-// sum over segments s of A_s B_s, A_s [M][K], B_s [K][N], 16-bit operands with
+// sum over segments s of A_s B_s, A_s [M][K], B_s [K][N], bf16 operands with
 // fp32 accumulation. An operand is read by rows (K contiguous) or by columns (K
 // is the slow index). f32 = 0: bf16 operands and bf16 arrays in the epilogue; 1:
-// fp16 planes of scaled fp32 values and fp32 arrays.
+// operands are three bf16 planes whose sum is the fp32 value, arrays fp32.
 struct GemmArgs {
   const uint16_t* a[kMaxSeg];
   const uint16_t* b[2][kMaxSeg];  // [1]: u's weights (kGate) or problem 1's operand
-  const uint32_t *max_a, *max_b;  // f32: the operands' maximum words (PackArgs)
-  uint32_t* max_parts;            // f32: kMaxParts words raised by h (kGate), dg and du (kActBwd)
   int64_t lda, ldb;
+  int64_t plane_a, plane_b;       // f32: elements from one plane to the next
   int32_t f32;
   int32_t nseg;
   int32_t M, N;        // N: columns of one result
@@ -52,14 +51,16 @@ struct GemmArgs {
   EpiArgs e;
 };
 
-// Results of a workgroup: 256 x 256 or 128 x 128 (kGate: 128 or 64 columns of
-// h); x2: by two sets of waves with half of K each.
-enum TileKind { kTile256, kTile128, kTile128x2 };
+// Results of a workgroup: 256 x 256, 128 x 128 or 128 x 256 (kGate: 128 or 64
+// columns of h); x2: by two sets of waves with half of K each. bf16 takes the
+// first three, f32 kTile128 and kTileWide.
+enum TileKind { kTile256, kTile128, kTile128x2, kTileWide };
+constexpr bool is_tile(TileKind t, bool f32) { return f32 ? t == kTile128 || t == kTileWide : t != kTileWide; }
 hipError_t launch_gemm(const GemmArgs& g, TileKind tile, bool a_cols, bool b_cols, Epi epi, hipStream_t s);
 // Tiles of one launch before splitting.
 int64_t gemm_tiles(int64_t M, int64_t N, int problems, TileKind tile, bool gate);
-// K steps of one launch (all segments).
-int64_t gemm_steps(int64_t K, int nseg);
+// K steps of one launch (all segments): of 64, f32 of 32 (which has six products).
+int64_t gemm_steps(int64_t K, int nseg, bool f32);
 
 // Three products of one launch: g[0] reads both operands by rows, g[1] and g[2]
 // by columns; all store (M = 0: left out). start is filled by the launch.
@@ -88,26 +89,17 @@ int64_t decode_batches(int64_t K);  // the smallest parts K is cut into
 hipError_t launch_decode(const DecodeArgs& a, bool f32, Epi epi, hipStream_t s);
 
 // A copy of an operand: out[rows][ld_out], columns zero-padded to ld_out (a
-// multiple of 8). fp32 sources give two fp16 planes, out[2][rows][ld_out],
-// scaled by the power of two that brings the value in `word` (the bits of the
-// largest finite |value| of all that share the scale) into [2^14, 2^15).
+// multiple of 8); fp32 sources give three bf16 planes, out[3][rows][ld_out].
 struct PackArgs {
   const void* src;
   uint16_t* out;
-  uint32_t* word;
   int64_t rows, cols, ld, ld_out;
-  // launch_max writes the operand's kMaxParts partial maxima to parts; with
-  // n_parts > 0 launch_pack takes the word from parts[first_part..] and stores it
-  uint32_t* parts;
-  int32_t first_part, n_parts;
 };
 constexpr int kMaxPack = 6;
 struct PackList {
   PackArgs t[kMaxPack];
-  uint32_t* clear;  // launch_max: kMaxParts words to be cleared
   int32_t n, f32;
 };
-hipError_t launch_max(const PackList& l, hipStream_t s);
 hipError_t launch_pack(const PackList& l, hipStream_t s);
 
 enum NormKind { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };

@@ -54,18 +54,22 @@ int guarded(F&& f) {
 
 // ------------------------------------------------- gated feed-forward block
 // Tile and K splits of the products of one launch, by an estimate of its time in
-// microseconds. A K step of 64 takes 1.6 for a 256 tile alone on its CU, 0.92
-// for two 128 tiles on one and 0.72 for one alone, with two sets of waves 0.43
-// on a part of the card and 0.55 on the whole (the L2s' rate), which is what is
-// reckoned with. Workgroups of unequal length fill the card about as well as equal ones of the same total,
-// but the launch takes at least its longest one's time. Filling and emptying
-// costs 5, 3 or 4, a split another launch and its sums' way through memory.
-// Measured with the choices left open (a whole step, us): dx of 2048 x 2048 x
-// 8192 as 256 tiles in 4 parts 656, as 128 tiles unsplit 709; dWg and dWu of
-// 1024 x 768 x 2048 as unsplit 128 tiles 114, in two parts 122, y of that size
+// microseconds. bf16: a K step of 64 takes 1.6 for a 256 tile alone on its CU,
+// 0.92 for two 128 tiles on one and 0.72 for one alone, with two sets of waves
+// 0.43 on a part of the card and 0.55 on the whole (the L2s' rate), which is what
+// is reckoned with. fp32: a K step of 32, six products, takes 2.5 for a 128 x 256
+// tile and 1.35 for a 128 tile (2.0 for the gate's, whose four waves are alone on
+// the CU). Workgroups of unequal length fill the card about as well as equal ones
+// of the same total, but the launch takes at least its longest one's time. Filling
+// and emptying costs 5, 3 or 4, a split another launch and its sums' way through
+// memory. Measured with the choices left open (a whole step, us): dx of 2048 x
+// 2048 x 8192 as 256 tiles in 4 parts 656, as 128 tiles unsplit 709; dWg and dWu
+// of 1024 x 768 x 2048 as unsplit 128 tiles 114, in two parts 122, y of that size
 // unsplit 124, in 4 parts 118; y of 4096 x 768 x 2048 with one set of waves 159,
-// with two 156, its g, u and h as 256 tiles 155, as 128 tiles 161; f32 of 1536 x
-// 1000 x 2728 with 0.55 388, with 0.46 425.
+// with two 156, its g, u and h as 256 tiles 155, as 128 tiles 161. fp32, first the
+// choice, then the other tile's best: 4096 x 768 x 2048 g, u and h 625 as 128 x
+// 256 tiles (734), dx with the weights' gradients 639 (665); 300 x 512 x 1024
+// those 80 as 128 tiles in 8 parts (90), y 79 (84).
 struct Shape {
   int64_t M, N;
   int problems;
@@ -74,7 +78,7 @@ struct Shape {
   int32_t splits;
 };
 
-double estimate(const Shape* p, int n, shl::TileKind tile) {
+double estimate(const Shape* p, int n, shl::TileKind tile, bool f32) {
   double work = 0, longest = 0, extra = 0;
   int64_t groups = 0;
   for (int i = 0; i < n; ++i) {
@@ -87,8 +91,9 @@ double estimate(const Shape* p, int n, shl::TileKind tile) {
     if (p[i].splits > 1)
       extra += 4 + static_cast<double>(p[i].M) * static_cast<double>(p[i].N) * p[i].problems * (p[i].gate ? 2 : 1) * 6 / 4e6 * p[i].splits;
   }
-  const bool big = tile == shl::kTile256, alone = tile != shl::kTile128 || groups <= 256;
-  const double step = big ? 1.6 : tile == shl::kTile128x2 ? 0.55 : alone ? 0.72 : 0.92, slots = alone ? 256 : 512;
+  const bool big = tile == shl::kTile256 || tile == shl::kTileWide, alone = f32 || tile != shl::kTile128 || groups <= 256;
+  const double step = f32 ? big ? 2.5 : p[0].gate ? 2.0 : 1.35 : big ? 1.6 : tile == shl::kTile128x2 ? 0.55 : alone ? 0.72 : 0.92;
+  const double slots = alone ? 256 : 512;
   // equal workgroups go in whole rounds; unequal ones about half a round apart
   const double mean = work / static_cast<double>(groups > 0 ? groups : 1);
   double rounds = static_cast<double>(groups) / slots;
@@ -99,51 +104,53 @@ double estimate(const Shape* p, int n, shl::TileKind tile) {
 }
 
 // One product.
-shl::TileKind choose_tile(Shape p, int32_t& splits) {
-  shl::TileKind tile = shl::kTile256;
+constexpr shl::TileKind kTiles[] = {shl::kTile256, shl::kTile128, shl::kTile128x2, shl::kTileWide};
+
+shl::TileKind choose_tile(Shape p, int32_t& splits, bool f32) {
+  shl::TileKind tile = shl::kTile128;
   double best = -1;
-  for (shl::TileKind t : {shl::kTile256, shl::kTile128, shl::kTile128x2})
+  for (shl::TileKind t : kTiles) {
+    if (!shl::is_tile(t, f32)) continue;
     for (int32_t s = 1; s <= 32 && (s == 1 || s * 4 <= p.steps); ++s) {
       p.splits = s;
-      const double us = estimate(&p, 1, t);
+      const double us = estimate(&p, 1, t, f32);
       if (best < 0 || us < best) best = us, tile = t, splits = s;
     }
+  }
   return tile;
 }
 
 // dx (p[0]) with dWd and dWg, dWu (p[1], p[2], whose sums are equally long).
-shl::TileKind choose_group(Shape (&p)[3]) {
+shl::TileKind choose_group(Shape (&p)[3], bool f32) {
   static const int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-  shl::TileKind tile = shl::kTile256;
+  shl::TileKind tile = shl::kTile128;
   double best = -1;
   int32_t a = 1, b = 1;
-  for (shl::TileKind t : {shl::kTile256, shl::kTile128, shl::kTile128x2})
+  for (shl::TileKind t : kTiles) {
+    if (!shl::is_tile(t, f32)) continue;
     for (int32_t sa : kSplits) {
       if (sa > 1 && (p[0].M == 0 || sa * 4 > p[0].steps)) break;
       for (int32_t sb : kSplits) {
         if (sb > 1 && (p[1].M + p[2].M == 0 || sb * 4 > p[2].steps)) break;
         p[0].splits = sa, p[1].splits = p[2].splits = sb;
-        const double us = estimate(p, 3, t);
+        const double us = estimate(p, 3, t, f32);
         if (best < 0 || us < best) best = us, tile = t, a = sa, b = sb;
       }
     }
+  }
   p[0].splits = a, p[1].splits = p[2].splits = b;
   return tile;
 }
 
+// A product's operand: its first plane, elements from one plane to the next.
 struct Planes {
-  const uint16_t* p[2] = {};
-  int64_t ld = 0;
-  const uint32_t* word = nullptr;
+  const uint16_t* p = nullptr;
+  int64_t ld = 0, plane = 0;
 };
 
 // One pass over the block's launches: with run = false only the workspace is
 // laid out.
 struct Ffn {
-  // Maximum words of the fp32 operands. The forward pass keeps its own (up to kH)
-  // behind h in `saved`, and h as the planes that its second product read.
-  enum Word { kX, kWIn, kWDown, kH, kDy, kDgu, kWords };
-
   const shampoo_ffn_t& a;
   char* ws;
   hipStream_t stream;
@@ -152,7 +159,6 @@ struct Ffn {
   hipError_t err = hipSuccess;
   int64_t N, d, f, fp, e;
   bool f32;
-  uint32_t *words = nullptr, *kept = nullptr, *raised = nullptr;
   shl::PackList list{};
 
   Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
@@ -165,88 +171,53 @@ struct Ffn {
   void ok(hipError_t x) {
     if (err == hipSuccess) err = x;
   }
+  // `saved`: g, u, and h, which fp32 keeps as the planes that its second product
+  // reads (as an fp32 array where the forward pass took the few-token kernels).
   int64_t act_bytes() const { return shp_rt::align_up(N * fp * e); }
+  int64_t saved_bytes() const { return 2 * act_bytes() + shp_rt::align_up(N * fp * 2 * shl::planes(f32)); }
+  char* saved_h() const { return static_cast<char*>(a.saved) + 2 * act_bytes(); }
 
   // A bf16 operand that loads can take where it is; sums_over_cols: its
   // columns are the product's summation index.
   bool usable(const void* p, int64_t cols, int64_t ld, bool sums_over_cols) const {
     return !f32 && aligned(p, 16) && ld % 8 == 0 && (!sums_over_cols || cols % 8 == 0);
   }
-  Planes operand(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld, bool sums_over_cols) {
-    if (!usable(p, cols, ld, sums_over_cols)) return copied(w, p, rows, cols, ld);
-    Planes o;
-    o.p[0] = static_cast<const uint16_t*>(p);
-    o.ld = ld;
-    return o;
+  Planes operand(const void* p, int64_t rows, int64_t cols, int64_t ld, bool sums_over_cols) {
+    if (!usable(p, cols, ld, sums_over_cols)) return copied(p, rows, cols, ld);
+    return {static_cast<const uint16_t*>(p), ld, 0};
   }
+  // h, dg and du as the epilogues write them: what the next products read.
+  Planes written(const void* p) const { return {static_cast<const uint16_t*>(p), fp, f32 ? N * fp : 0}; }
   // Puts a copy on the list; flush() makes it.
-  Planes copied(Word w, const void* p, int64_t rows, int64_t cols, int64_t ld, void* to = nullptr) {
-    Planes o;
-    o.ld = round8(cols);
-    uint16_t* out = static_cast<uint16_t*>(to ? to : take((f32 ? 2 : 1) * rows * o.ld * 2));
-    o.p[0] = out;
-    if (f32) o.p[1] = out + rows * o.ld, o.word = word(w);
-    if (rows) list.t[list.n++] = shl::PackArgs{p, out, word(w), rows, cols, ld, o.ld, nullptr, 0, 0};
-    return o;
+  Planes copied(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    const int64_t ld_out = round8(cols);
+    uint16_t* out = static_cast<uint16_t*>(take(shl::planes(f32) * rows * ld_out * 2));
+    if (rows) list.t[list.n++] = shl::PackArgs{p, out, rows, cols, ld, ld_out};
+    return {out, ld_out, rows * ld_out};
   }
-  // Both weights of the fused products share one leading dimension (and scale).
+  // Both weights of the fused products share one leading dimension.
   void operands(const void* p, const void* q, int64_t rows, int64_t cols, int64_t ldp, int64_t ldq, bool sums_over_cols, Planes& x,
                 Planes& y) {
     const bool in_place = ldp == ldq && usable(p, cols, ldp, sums_over_cols) && usable(q, cols, ldq, sums_over_cols);
-    x = in_place ? operand(kWIn, p, rows, cols, ldp, sums_over_cols) : copied(kWIn, p, rows, cols, ldp);
-    y = in_place ? operand(kWIn, q, rows, cols, ldq, sums_over_cols) : copied(kWIn, q, rows, cols, ldq);
+    x = in_place ? operand(p, rows, cols, ldp, sums_over_cols) : copied(p, rows, cols, ldp);
+    y = in_place ? operand(q, rows, cols, ldq, sums_over_cols) : copied(q, rows, cols, ldq);
   }
-  uint32_t* saved_words() const { return reinterpret_cast<uint32_t*>(static_cast<char*>(a.saved) + 3 * act_bytes()); }
-  void start_words(bool backward) {
-    if (!f32) return;
-    words = !backward && a.saved ? saved_words() : static_cast<uint32_t*>(take(kWords * 4));
-    kept = backward && !few() ? saved_words() : nullptr;
-    raised = static_cast<uint32_t*>(take(4 * shl::kMaxParts));
-  }
-  uint32_t* word(Word w) const { return kept && w <= kH ? kept + w : words + w; }
-  bool is_kept(const uint32_t* w) const { return kept && w >= kept && w <= kept + kH; }
-  // Makes the listed copies. maxima: those of fp32 operands are found first (the
-  // backward pass has the forward pass's) and `raised` is cleared for the
-  // product that follows; else they are in `raised`, from the product that
-  // wrote the operands.
-  void flush(bool maxima) {
-    if (f32 && maxima) {
-      shl::PackList scan{};
-      scan.f32 = 1;
-      scan.clear = raised;
-      for (int i = 0; i < list.n; ++i)
-        if (!is_kept(list.t[i].word)) scan.t[scan.n++] = list.t[i];
-      uint32_t* parts = static_cast<uint32_t*>(take(int64_t(4) * shl::kMaxParts * shl::kMaxPack));
-      // operands that share a word are next to each other
-      for (int i = 0; i < scan.n; ++i) scan.t[i].parts = parts + i * shl::kMaxParts;
-      for (int i = 0; i < list.n; ++i) {
-        shl::PackArgs& p = list.t[i];
-        p.parts = parts, p.n_parts = 0;
-        for (int k = scan.n - 1; k >= 0; --k)
-          if (scan.t[k].word == p.word) p.first_part = k * shl::kMaxParts, p.n_parts += shl::kMaxParts;
-      }
-      if (run) ok(shl::launch_max(scan, stream));
-    } else if (f32) {
-      for (int i = 0; i < list.n; ++i) list.t[i].parts = raised, list.t[i].first_part = 0, list.t[i].n_parts = shl::kMaxParts;
-    }
+  // Makes the listed copies.
+  void flush() {
     if (run) ok(shl::launch_pack(list, stream));
     list.n = 0;
   }
 
-  // Adds one product's plane pairs to the segments, the smaller terms first.
-  void segments(shl::GemmArgs& g, const Planes& A, const Planes& B, const Planes* B1 = nullptr) {
-    static const int kPairs[3][2] = {{0, 1}, {1, 0}, {0, 0}};
-    for (int i = f32 ? 0 : 2; i < 3; ++i) {
-      g.a[g.nseg] = A.p[kPairs[i][0]];
-      g.b[0][g.nseg] = B.p[kPairs[i][1]];
-      if (B1) g.b[1][g.nseg] = B1->p[kPairs[i][1]];
-      ++g.nseg;
-    }
-    g.lda = A.ld, g.ldb = B.ld, g.max_a = A.word, g.max_b = B.word;
+  // Adds a product to the segments of one sum.
+  void segment(shl::GemmArgs& g, const Planes& A, const Planes& B, const Planes* B1 = nullptr) {
+    g.a[g.nseg] = A.p, g.b[0][g.nseg] = B.p;
+    if (B1) g.b[1][g.nseg] = B1->p;
+    ++g.nseg;
+    g.lda = A.ld, g.ldb = B.ld, g.plane_a = A.plane, g.plane_b = B.plane;
   }
 
   Shape shape(const shl::GemmArgs& g, bool gate) const {
-    return {g.M, g.M ? g.N : 0, g.problems, gate, shl::gemm_steps(g.K, g.nseg), 1};
+    return {g.M, g.M ? g.N : 0, g.problems, gate, shl::gemm_steps(g.K, g.nseg, f32), 1};
   }
   void settle(shl::GemmArgs& g, bool gate) {
     g.f32 = f32 ? 1 : 0;
@@ -256,13 +227,13 @@ struct Ffn {
   }
   void product(shl::GemmArgs& g, bool a_cols, bool b_cols, shl::Epi epi) {
     const bool gate = epi == shl::kGate;
-    const shl::TileKind tile = choose_tile(shape(g, gate), g.splits);
+    const shl::TileKind tile = choose_tile(shape(g, gate), g.splits, f32);
     settle(g, gate);
     if (run) ok(shl::launch_gemm(g, tile, a_cols, b_cols, epi, stream));
   }
   void group(shl::GroupArgs& q) {
     Shape p[3] = {shape(q.g[0], false), shape(q.g[1], false), shape(q.g[2], false)};
-    const shl::TileKind tile = choose_group(p);
+    const shl::TileKind tile = choose_group(p, f32);
     for (int i = 0; i < 3; ++i) {
       q.g[i].splits = p[i].splits;
       settle(q.g[i], false);
@@ -296,7 +267,7 @@ struct Ffn {
   }
   void forward_few() {
     char* saved = static_cast<char*>(a.saved);
-    void* h = saved ? saved + 2 * act_bytes() : take(N * fp * e);
+    void* h = saved ? saved_h() : take(N * fp * e);
     shl::DecodeArgs g{};
     g.x = a.x, g.ldx = a.ld_x, g.w[0] = a.w_gate, g.w[1] = a.w_up, g.ldw[0] = a.ld_gate, g.ldw[1] = a.ld_up;
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(d);
@@ -312,29 +283,24 @@ struct Ffn {
 
   void forward() {
     if (few()) return forward_few();
-    start_words(false);
-    const Planes x = operand(kX, a.x, N, d, a.ld_x, true);
+    const Planes x = operand(a.x, N, d, a.ld_x, true);
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
-    const Planes wd = operand(kWDown, a.w_down, f, d, a.ld_down, false);
-    flush(true);
+    const Planes wd = operand(a.w_down, f, d, a.ld_down, false);
+    flush();
     char* saved = static_cast<char*>(a.saved);
-    // bf16 h is kept as it is, fp32 h as its planes, which take as much
-    void* h = saved && !f32 ? saved + 2 * act_bytes() : take(N * fp * e);
+    const Planes h = written(saved ? saved_h() : take(N * fp * 2 * shl::planes(f32)));
     {
       shl::GemmArgs g{};
-      segments(g, x, wg, &wu);
+      segment(g, x, wg, &wu);
       g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
-      g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
+      g.e.c[0] = const_cast<uint16_t*>(h.p), g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp), g.e.plane = h.plane;
       if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
-      g.max_parts = raised;
       product(g, false, true, shl::kGate);
     }
-    const Planes hp = f32 && saved ? copied(kH, h, N, fp, fp, saved + 2 * act_bytes()) : operand(kH, h, N, fp, fp, true);
-    flush(false);
     shl::GemmArgs g{};
-    segments(g, hp, wd);
+    segment(g, h, wd);
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
     g.k_real = static_cast<int32_t>(f), g.problems = 1;
     g.e.c[0] = a.y, g.e.ldc = a.ld_y;
@@ -342,59 +308,47 @@ struct Ffn {
   }
 
   void backward() {
-    start_words(true);
     char* saved = static_cast<char*>(a.saved);
     const bool want_gate = a.dx || a.dw_gate;
     // dy is read by rows for dh and by columns for dWd: one copy serves both
-    const Planes dy = operand(kDy, a.dy, N, d, a.ld_dy, true);
+    const Planes dy = operand(a.dy, N, d, a.ld_dy, true);
     Planes wd, h, wg, wu, x;
-    if (want_gate) wd = operand(kWDown, a.w_down, f, d, a.ld_down, true);
-    if (a.dw_down && kept) {
-      h.ld = fp, h.word = word(kH);
-      h.p[0] = reinterpret_cast<const uint16_t*>(saved + 2 * act_bytes());
-      h.p[1] = h.p[0] + N * fp;
-    } else if (a.dw_down) {
-      h = operand(kH, saved + 2 * act_bytes(), N, fp, fp, false);
-    }
+    if (want_gate) wd = operand(a.w_down, f, d, a.ld_down, true);
+    if (a.dw_down) h = f32 && few() ? copied(saved_h(), N, fp, fp) : written(saved_h());
     if (a.dx) operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, true, wg, wu);
-    if (a.dw_gate) x = operand(kX, a.x, N, d, a.ld_x, false);
-    flush(true);
-    void *dg = nullptr, *du = nullptr;
-    if (want_gate) {
-      dg = take(N * fp * e);
-      du = take(N * fp * e);
-      shl::GemmArgs g{};
-      segments(g, dy, wd);
-      g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
-      g.k_real = static_cast<int32_t>(d), g.problems = 1;
-      g.e.c[0] = dg, g.e.c[1] = du, g.e.ldc = fp, g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
-      g.e.pad_to = static_cast<int32_t>(fp);
-      g.max_parts = raised;
-      product(g, false, false, shl::kActBwd);
-    }
+    if (a.dw_gate) x = operand(a.x, N, d, a.ld_x, false);
+    flush();
     Planes pg, pu;
     if (want_gate) {
-      pg = operand(kDgu, dg, N, fp, fp, true), pu = operand(kDgu, du, N, fp, fp, true);
-      flush(false);
+      pg = written(take(N * fp * 2 * shl::planes(f32)));
+      pu = written(take(N * fp * 2 * shl::planes(f32)));
+      shl::GemmArgs g{};
+      segment(g, dy, wd);
+      g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
+      g.k_real = static_cast<int32_t>(d), g.problems = 1;
+      g.e.c[0] = const_cast<uint16_t*>(pg.p), g.e.c[1] = const_cast<uint16_t*>(pu.p), g.e.ldc = fp, g.e.plane = pg.plane;
+      g.e.g = saved, g.e.u = saved + act_bytes(), g.e.ldg = fp;
+      g.e.pad_to = static_cast<int32_t>(fp);
+      product(g, false, false, shl::kActBwd);
     }
     shl::GroupArgs q{};
     if (a.dx) {
       shl::GemmArgs& g = q.g[0];
-      segments(g, pg, wg);
-      segments(g, pu, wu);
+      segment(g, pg, wg);
+      segment(g, pu, wu);
       g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(d), g.K = static_cast<int32_t>(fp);
       g.k_real = static_cast<int32_t>(f), g.problems = 1;
       g.e.c[0] = a.dx, g.e.ldc = a.ld_dx;
     }
     if (a.dw_down) {
       shl::GemmArgs& g = q.g[1];
-      segments(g, h, dy);
+      segment(g, h, dy);
       g.M = static_cast<int32_t>(f), g.N = static_cast<int32_t>(d), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 1;
       g.e.c[0] = a.dw_down, g.e.ldc = a.ld_dw_down;
     }
     if (a.dw_gate) {
       shl::GemmArgs& g = q.g[2];
-      segments(g, x, pg, &pu);
+      segment(g, x, pg, &pu);
       g.M = static_cast<int32_t>(d), g.N = static_cast<int32_t>(f), g.K = g.k_real = static_cast<int32_t>(N), g.problems = 2;
       g.e.c[0] = a.dw_gate, g.e.c[1] = a.dw_up, g.e.ldc = a.ld_dw_gate, g.e.ldc1 = a.ld_dw_up;
     }
@@ -567,7 +521,7 @@ int shampoo_ffn_saved_size(const shampoo_ffn_t* a, size_t* bytes_out) {
   RC(check_sizes(a));
   if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
   const Ffn p(*a, nullptr, nullptr, false);
-  *bytes_out = static_cast<size_t>(3 * p.act_bytes() + 256);
+  *bytes_out = static_cast<size_t>(p.saved_bytes());
   return SHAMPOO_OK;
 }
 

@@ -190,7 +190,7 @@ _NO_GRADIENTS = (0,) * 10
 def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
     """y = (act(x w_gate) * (x w_up)) w_down for x [tokens, d], w_gate and w_up
     [d, f], w_down [f, d]. With `save` returns (y, saved), `saved` being what
-    `ffn_backward` needs (an opaque tensor of three f-wide rows a token).
+    `ffn_backward` needs (an opaque tensor: g, u and h of every token).
     activation: "silu", "gelu" (tanh form) or "relu"."""
     fields = _ffn_inputs(x, w_gate, w_up, w_down, activation)
     n, d, f = fields[:3]

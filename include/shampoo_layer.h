@@ -38,11 +38,12 @@ extern "C" {
  *     dWg = x^T dg,  dWu = x^T du,  dWd = h^T dy.
  * x, y, dy, dx: tokens x d_model; Wg, Wu: d_model x d_hidden; Wd: d_hidden x
  * d_model. All of one dtype. bf16 products run on the bf16 matrix cores; fp32
- * operands are scaled by a power of two that brings their largest finite
- * |value| into [2^14, 2^15) and split into two fp16 terms (as
- * SHAMPOO_GEMM_SPLIT_F16), three products of which accumulate in fp32. An
- * infinite or NaN operand makes every result it enters non-finite, and leaves
- * the others as they are. In bf16, g, u, h, dg and du are rounded when they are
+ * operands are split exactly into three bf16 terms (as SHAMPOO_GEMM_SPLIT_BF16),
+ * six products of which accumulate in fp32: every product of two elements keeps
+ * an fp32 product's accuracy, whatever the sizes of the other elements (elements
+ * under 2^-100 to 2^-126 absolute). Up to 64 tokens the forward pass takes the fp32
+ * matrix instruction instead. An infinite or NaN operand makes every result it
+ * enters non-finite, and leaves the others as they are. In bf16, g, u, h, dg and du are rounded when they are
  * stored between the products (h from unrounded g and u): the matrix cores
  * take no more of h, dg and du, and g and u are what a step keeps. dx, dWg and
  * dWu then differ from fp32 intermediates' by 0.003 in relative norm, where
@@ -63,7 +64,7 @@ typedef struct {
   void* y;
   int64_t ld_y;
   void* saved; /* shampoo_ffn_saved_size bytes for the backward pass: g, u and
-                  h; NULL: not kept (inference)                            */
+                  h (fp32: its three terms); NULL: not kept (inference)    */
   /* backward (reads saved as the forward pass wrote it, with the same sizes,
      dtype and activation); a NULL result is not computed, dw_gate and dw_up
      together */

@@ -42,3 +42,85 @@ def test_one_gate_row_for_any_number_of_rows(rows_per_gate):
     del held
     for a, b in zip(run(rows_per_gate), want):
         assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
+def by_rows(a, b, terms):
+    """The largest over the rows of `rel` of that row."""
+    a, b = a.double().cpu(), b.double()
+    size = torch.maximum(torch.linalg.vector_norm(b, dim=1), torch.linalg.vector_norm(terms, dim=1))
+    return float((torch.linalg.vector_norm(a - b, dim=1) / size).max())
+
+
+def relu_terms(x, wg, wu, wd, dy):
+    """Root sums of squares of the five results' terms, each term of the size that its own sums' terms give it: g, u and dh that
+    cancel keep their terms' roundings, and a row of dw_down that one such token fills has them too (as in plain fp32)."""
+    x, wg, wu, wd, dy = (t.double().cpu() for t in (x, wg, wu, wd, dy))
+
+    def rss(a, b):
+        return (a.square() @ b.square()).sqrt()
+    g, u, dh = x @ wg, x @ wu, dy @ wd.T
+    gs, us, dhs = rss(x, wg), rss(x, wu), rss(dy, wd.T)
+    on, a = (g > 0).double(), torch.relu(g)
+    h, dg, du = on * (gs * u.abs() + a * us), on * (dhs * u.abs() + dh.abs() * us), on * (dhs * a + dh.abs() * gs)
+    return rss(h, wd), (rss(dg, wg.T).square() + rss(du, wu.T).square()).sqrt(), rss(x.T, dg), rss(x.T, du), rss(h.T, dy)
+
+
+def check_fp32_rows(x, wg, wu, wd, dy):
+    """Every row of every result is as exact as fp32 sums of its terms are, whatever the other rows and the other operands hold."""
+    y, s = layer.ffn_forward(x, wg, wu, wd, activation="relu", save=True)
+    got = (y, *layer.ffn_backward(dy, x, wg, wu, wd, s, activation="relu"))
+    want_y, want, _ = ref.ffn(x, wg, wu, wd, "relu", dy)
+    terms = relu_terms(x, wg, wu, wd, dy)
+    errs = [by_rows(a, b, t) for a, b, t in zip(got, (want_y, *want), terms)]
+    # columns of the weight gradients too
+    errs += [by_rows(a.t(), b.T, t.T) for a, b, t in zip(got[2:], want[1:], terms[2:])]
+    log("   errors " + " ".join(f"{e:.2e}" for e in errs))
+    assert max(errs) <= f32_tol(max(*x.shape, wg.shape[1]))
+
+
+FP32_SIZES = [(64, 96, 160), (65, 96, 160), (300, 257, 391), (1100, 128, 264)]
+
+
+@pytest.mark.parametrize("n,d,f", FP32_SIZES)
+def test_fp32_rows_of_uneven_size(n, d, f):
+    """Tokens between 2^-15 and 2^15 in size; their gradients the other way round, so that every token has the same share in the
+    weights' gradients."""
+    g = torch.Generator().manual_seed(2)
+    log(f"ffn {n} x {d} x {f} fp32, uneven rows")
+    size = torch.exp2(torch.randint(-15, 16, (n, 1), generator=g).float()).cuda()
+    check_fp32_rows(normal(g, n, d) * size, normal(g, d, f, std=d ** -0.5), normal(g, d, f, std=d ** -0.5), normal(g, f, d, std=f ** -0.5),
+                    normal(g, n, d) / size ** 2)
+
+
+@pytest.mark.parametrize("n,d,f", FP32_SIZES)
+def test_fp32_one_large_token(n, d, f):
+    g = torch.Generator().manual_seed(3)
+    log(f"ffn {n} x {d} x {f} fp32, one large token")
+    x, dy = normal(g, n, d), normal(g, n, d)
+    x[n // 2] *= 1e10
+    dy[n // 3] *= 1e12
+    check_fp32_rows(x, normal(g, d, f, std=d ** -0.5), normal(g, d, f, std=d ** -0.5), normal(g, f, d, std=f ** -0.5), dy)
+
+
+@pytest.mark.parametrize("n,d,f", FP32_SIZES)
+def test_fp32_features_and_weights_of_uneven_size(n, d, f):
+    """Features between 2^-15 and 2^15 in size with weights that even them out; a gate weight far smaller than the up weight."""
+    g = torch.Generator().manual_seed(4)
+    log(f"ffn {n} x {d} x {f} fp32, uneven features, small gate weight")
+    size = torch.exp2(torch.randint(-15, 16, (1, d), generator=g).float()).cuda()
+    hidden = torch.exp2(torch.randint(-15, 16, (1, f), generator=g).float()).cuda()
+    check_fp32_rows(normal(g, n, d) * size, normal(g, d, f, std=d ** -0.5) / size.t() * 2.0 ** -30, normal(g, d, f, std=d ** -0.5) / size.t() * hidden,
+                    normal(g, f, d, std=f ** -0.5) / hidden.t(), normal(g, n, d, std=1e-2))
+
+
+def test_fp32_whole_range():
+    """Values up to the type's largest and down to 2^-100 keep 24 bits; the largest does not become infinite."""
+    g = torch.Generator().manual_seed(5)
+    one = torch.eye(64).cuda()
+    for size, weight in ((torch.finfo(torch.float32).max, 2.0 ** -100), (2.0 ** -100, 2.0 ** 50)):
+        x = (torch.rand(130, 64, generator=g) * 0.5 + 0.5).cuda() * size
+        x[0, 0] = size
+        y = layer.ffn_forward(x, one * weight, one * weight, one, activation="relu")
+        want = (x.double().cpu() * weight).square()
+        log(f"   size {size:.1e}: {rel(y, want):.2e}")
+        assert rel(y, want) <= 8 * F32_STEP
