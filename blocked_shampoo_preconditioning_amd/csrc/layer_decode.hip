@@ -7,7 +7,9 @@
 // matrix cores take them as they come: the weights are the "A" operand (16 rows
 // of one 16 x 16 product are columns 2 j + i, j the lane of a row), x the "B"
 // operand (16 tokens). fp32 uses the fp32 matrix instruction, so it is exact to
-// fp32 accumulation.
+// fp32 accumulation. bf16 h comes as two bf16 terms: its rounding would save no
+// weight byte, and y is off by 0.0024 in norm with one term, by its own rounding,
+// 0.0017, with two (16 tokens of 2048 x 8192 35.7 and 39.1 us, 32 43 and 46).
 //
 // One token of 2048 x 8192 bf16: g, u and h (67 MB) in 20 us, y (34 MB) in 10 and
 // 4 to join its 8 parts of K (16 and 8 for the products when the last-level
@@ -58,16 +60,20 @@ __device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K,
 // kBatch rows of K from k0 for MATS matrices and 16 T tokens. Rows from K on lie
 // past the weights' end and read as zeros; what a lane reads past a row's last
 // column belongs to columns that are not stored.
-template <bool F32, int MATS, int T>
+template <bool F32, int MATS, int T, int TERMS>
 struct Batch {
-  uint32_t w[MATS][kRun][F32 ? 2 : 1], x[T][kWords<F32>];
+  uint32_t w[MATS][kRun][F32 ? 2 : 1], x[TERMS][T][kWords<F32>];
 };
-template <bool F32, int MATS, int T>
-__device__ __forceinline__ void load(const DecodeArgs& a, const int64_t (&xrow)[T], int k0, const uint32_t (&off)[MATS], Batch<F32, MATS, T>& b) {
+template <bool F32, int MATS, int T, int TERMS>
+__device__ __forceinline__ void load(const DecodeArgs& a, const int64_t (&xrow)[T], int k0, const uint32_t (&off)[MATS],
+                                     Batch<F32, MATS, T, TERMS>& b) {
   constexpr int E = F32 ? 4 : 2;
   const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int t = 0; t < T; ++t) load_x<F32>(a.x, xrow[t], k0 + kRun * q, a.K, b.x[t]);
+  for (int t = 0; t < T; ++t) {
+    load_x<F32>(a.x, xrow[t], k0 + kRun * q, a.K, b.x[0][t]);
+    if constexpr (TERMS == 2) load_x<F32>(a.x_rest, xrow[t], k0 + kRun * q, a.K, b.x[1][t]);
+  }
 #pragma unroll
   for (int m = 0; m < MATS; ++m) {
     const int64_t at = k0 * a.ldw[m] * E, end = ((a.K - 1) * a.ldw[m] + a.N) * E;
@@ -88,8 +94,8 @@ __device__ __forceinline__ void load(const DecodeArgs& a, const int64_t (&xrow)[
 }
 
 // Their products.
-template <bool F32, int MATS, int T>
-__device__ __forceinline__ void use(const Batch<F32, MATS, T>& b, floatx4 (&acc)[MATS][2][T]) {
+template <bool F32, int MATS, int T, int TERMS>
+__device__ __forceinline__ void use(const Batch<F32, MATS, T, TERMS>& b, floatx4 (&acc)[MATS][2][T]) {
   if constexpr (F32) {
 #pragma unroll
     for (int s = 0; s < kRun; ++s)
@@ -100,7 +106,7 @@ __device__ __forceinline__ void use(const Batch<F32, MATS, T>& b, floatx4 (&acc)
 #pragma unroll
           for (int t = 0; t < T; ++t)
             acc[m][i][t] =
-                __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b.w[m][s][i]), __uint_as_float(b.x[t][s]), acc[m][i][t], 0, 0, 0);
+                __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b.w[m][s][i]), __uint_as_float(b.x[0][t][s]), acc[m][i][t], 0, 0, 0);
   } else {
     typedef __attribute__((ext_vector_type(2))) uint32_t uint2v;
 #pragma unroll
@@ -113,10 +119,13 @@ __device__ __forceinline__ void use(const Batch<F32, MATS, T>& b, floatx4 (&acc)
         const uint2v c1 = {__builtin_amdgcn_perm(w1, w0, 0x07060302u), __builtin_amdgcn_perm(w3, w2, 0x07060302u)};
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          const uint2v xx = {b.x[t][2 * s], b.x[t][2 * s + 1]};
-          const short4v x4 = __builtin_bit_cast(short4v, xx);
-          acc[m][0][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c0), x4, acc[m][0][t], 0, 0, 0);
-          acc[m][1][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c1), x4, acc[m][1][t], 0, 0, 0);
+#pragma unroll
+          for (int e = TERMS - 1; e >= 0; --e) {
+            const uint2v xx = {b.x[e][t][2 * s], b.x[e][t][2 * s + 1]};
+            const short4v x4 = __builtin_bit_cast(short4v, xx);
+            acc[m][0][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c0), x4, acc[m][0][t], 0, 0, 0);
+            acc[m][1][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, c1), x4, acc[m][1][t], 0, 0, 0);
+          }
         }
       }
   }
@@ -126,9 +135,17 @@ __device__ __forceinline__ void use(const Batch<F32, MATS, T>& b, floatx4 (&acc)
 // of K, cut again over the waves; the waves' sums are added in order through
 // LDS. One part: the epilogue follows; more: the sums go to a.partial in
 // GemmArgs' layout and the finish kernel joins them.
-template <bool F32, int EPI, int T, int W>
+//
+// The second term of x (TERMS = 2, or FOLD: at most eight tokens, whose second
+// terms take the place of tokens 8 to 15) has its sums added to the first's.
+// Folded, one token of 2048 x 8192 takes 32.5 us, with one term 32.3; with twice the
+// registers for x 34.1, since they leave room for one workgroup of 16 waves on a
+// CU in place of two.
+template <bool F32, int EPI, int T, int W, int TERMS>
 __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
   constexpr int MATS = EPI == kGate ? 2 : 1;
+  constexpr bool FOLD = !F32 && EPI == kStore && TERMS == 1;
+  static_assert(!FOLD || T == 1, "");
   constexpr int PITCH = kCols + 4;
   __shared__ float sums[W][MATS * 16][PITCH];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -150,7 +167,10 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
   const int first = each * part + min(part, rest), last = first + each + (part < rest ? 1 : 0);
   int64_t xrow[T];
 #pragma unroll
-  for (int t = 0; t < T; ++t) xrow[t] = static_cast<int64_t>(min(16 * t + (lane & 15), a.M - 1)) * a.ldx;
+  for (int t = 0; t < T; ++t) {
+    xrow[t] = static_cast<int64_t>(min(16 * t + (lane & (FOLD ? 7 : 15)), a.M - 1)) * a.ldx;
+    if (FOLD && (lane & 8)) xrow[t] += static_cast<const uint16_t*>(a.x_rest) - static_cast<const uint16_t*>(a.x);
+  }
   floatx4 acc[MATS][2][T];
 #pragma unroll
   for (int m = 0; m < MATS; ++m)
@@ -159,19 +179,19 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int t = 0; t < T; ++t) acc[m][i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
   // one batch is loaded while the one before it is multiplied
-  Batch<F32, MATS, T> even, odd;
+  Batch<F32, MATS, T, TERMS> even, odd;
   int b = first;
-  if (b < last) load<F32, MATS, T>(a, xrow, b * kBatch, off, even);
+  if (b < last) load<F32, MATS, T, TERMS>(a, xrow, b * kBatch, off, even);
 #pragma unroll 1
   for (; b + 2 < last; b += 2) {
-    load<F32, MATS, T>(a, xrow, (b + 1) * kBatch, off, odd);
-    use<F32, MATS, T>(even, acc);
-    load<F32, MATS, T>(a, xrow, (b + 2) * kBatch, off, even);
-    use<F32, MATS, T>(odd, acc);
+    load<F32, MATS, T, TERMS>(a, xrow, (b + 1) * kBatch, off, odd);
+    use<F32, MATS, T, TERMS>(even, acc);
+    load<F32, MATS, T, TERMS>(a, xrow, (b + 2) * kBatch, off, even);
+    use<F32, MATS, T, TERMS>(odd, acc);
   }
-  if (b + 1 < last) load<F32, MATS, T>(a, xrow, (b + 1) * kBatch, off, odd);
-  if (b < last) use<F32, MATS, T>(even, acc);
-  if (b + 1 < last) use<F32, MATS, T>(odd, acc);
+  if (b + 1 < last) load<F32, MATS, T, TERMS>(a, xrow, (b + 1) * kBatch, off, odd);
+  if (b < last) use<F32, MATS, T, TERMS>(even, acc);
+  if (b + 1 < last) use<F32, MATS, T, TERMS>(odd, acc);
   const Activation act(a.e.act);
 #pragma unroll
   for (int t = 0; t < T; ++t) {
@@ -196,7 +216,7 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
       const int c = u % kCols, y = u / kCols, row = y < rows ? y : y - rows + 16;
       float x = 0.f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) x += sums[k][row][c];
+      for (int k = 0; k < W; ++k) x += FOLD ? sums[k][row][c] + sums[k][row + 8][c] : sums[k][row][c];
       sums[0][row][c] = x;
     }
     __syncthreads();
@@ -227,13 +247,16 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
 
 template <bool F32, int EPI>
 hipError_t launch_decode_tokens(const DecodeArgs& a, dim3 grid, hipStream_t s) {
+  constexpr int TERMS = !F32 && EPI == kStore ? 2 : 1;
   // more tokens take more registers a wave, so fewer waves
-  if (a.M <= 16)
-    hipLaunchKernelGGL((decode_kernel<F32, EPI, 1, F32 ? 8 : 16>), grid, dim3(F32 ? 512 : 1024), 0, s, a);
+  if (a.M <= 8)
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 1, F32 ? 8 : 16, 1>), grid, dim3(F32 ? 512 : 1024), 0, s, a);
+  else if (a.M <= 16)
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 1, F32 ? 8 : 16, TERMS>), grid, dim3(F32 ? 512 : 1024), 0, s, a);
   else if (a.M <= 32)
-    hipLaunchKernelGGL((decode_kernel<F32, EPI, 2, 8>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 2, 8, TERMS>), grid, dim3(512), 0, s, a);
   else if constexpr (F32)
-    hipLaunchKernelGGL((decode_kernel<F32, EPI, 4, 8>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decode_kernel<F32, EPI, 4, 8, TERMS>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

@@ -101,6 +101,14 @@ __device__ __forceinline__ void finish8(const EpiArgs& e, const Activation& act,
       store_planes(e.c[0], oc, e.plane, v);
     else
       store8(e.c[0], oc, 8, F32, v);
+    if (!F32 && e.c[1]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = bf16_to_f32(f32_to_bf16(v[i]));
+        v[i] = fabsf(h) < __builtin_inff() ? v[i] - h : 0.f;
+      }
+      store8(e.c[1], oc, 8, F32, v);
+    }
   } else {
     float g[8], u[8];
     unpack8<F32>(gr, g);

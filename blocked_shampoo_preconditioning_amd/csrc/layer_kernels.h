@@ -21,7 +21,8 @@ enum Epi {
 };
 
 struct EpiArgs {
-  void* c[2];          // kStore: results of problems 0, 1; kGate: [0] = h; kActBwd: dg, du
+  void* c[2];          // kStore: results of problems 0, 1; kGate: h, and in bf16 (may be NULL)
+                       // what its rounding leaves; kActBwd: dg, du
   void* g;             // kGate: stores of g, u (NULL: not kept); kActBwd: loads
   void* u;
   int64_t ldc, ldc1;   // elements; ldc1: problem 1's (kStore)
@@ -72,12 +73,12 @@ hipError_t launch_group(GroupArgs& a, TileKind tile, bool f32, hipStream_t s);
 // Joins a split product's parts and runs the epilogue.
 hipError_t launch_finish(const GemmArgs& g, Epi epi, hipStream_t s);
 
-// A forward product for at most decode_tokens rows of x, operands as the caller
-// has them: x [M][K], w [K][N] (kGate: both weights), bf16 weights with 4-byte
+// A forward product for at most decode_tokens rows of x: x [M][K], w [K][N] (kGate: both weights), bf16 weights with 4-byte
 // aligned rows; K, N >= 2.
 constexpr int decode_tokens(bool f32) { return f32 ? 64 : 32; }
 struct DecodeArgs {
   const void* x;
+  const void* x_rest;  // bf16, kStore: the second term of x (same layout)
   const void* w[2];
   int64_t ldx, ldw[2];
   int32_t M, N, K, splits;

@@ -241,15 +241,17 @@ struct Ffn {
     if (run) ok(shl::launch_group(q, tile, f32, stream));
   }
 
-  // Whether the forward pass takes the few-token kernels: they read two columns
-  // of a row in one aligned access. For fp32 the sizes alone decide, so that the
-  // backward pass knows in which form h was kept.
-  bool few() const {
-    auto pairs = [&](const void* p, int64_t ld) { return f32 || (aligned(p, 4) && ld % 2 == 0); };
-    return N <= shl::decode_tokens(f32) && d >= 2 && f >= 2 && pairs(a.w_gate, a.ld_gate) && pairs(a.w_up, a.ld_up) &&
-           pairs(a.w_down, a.ld_down);
+  // Whether the forward pass takes the few-token kernels. The sizes alone decide,
+  // so that results do not go by strides and the backward pass knows in which
+  // form fp32 h was kept.
+  bool few() const { return N <= shl::decode_tokens(f32) && d >= 2 && f >= 2; }
+  // A weight as they read it: bf16 in pairs of columns, so rows that are not 4-byte
+  // aligned are copied.
+  Planes few_weight(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    if (f32 || (aligned(p, 4) && ld % 2 == 0)) return {static_cast<const uint16_t*>(p), ld, 0};
+    return copied(p, rows, cols, ld);
   }
-  // The forward products of a few tokens, weights as the caller has them.
+  // The forward products of a few tokens.
   void few_product(shl::DecodeArgs& g, shl::Epi epi) {
     const int64_t groups = shl::decode_groups(g.N), batches = shl::decode_batches(g.K);
     int64_t s = 1;
@@ -268,14 +270,18 @@ struct Ffn {
   void forward_few() {
     char* saved = static_cast<char*>(a.saved);
     void* h = saved ? saved_h() : take(N * fp * e);
+    void* rest = f32 ? nullptr : take(N * fp * e);  // the second term of bf16 h
+    const Planes wg = few_weight(a.w_gate, d, f, a.ld_gate), wu = few_weight(a.w_up, d, f, a.ld_up);
+    const Planes wd = few_weight(a.w_down, f, d, a.ld_down);
+    flush();
     shl::DecodeArgs g{};
-    g.x = a.x, g.ldx = a.ld_x, g.w[0] = a.w_gate, g.w[1] = a.w_up, g.ldw[0] = a.ld_gate, g.ldw[1] = a.ld_up;
+    g.x = a.x, g.ldx = a.ld_x, g.w[0] = wg.p, g.w[1] = wu.p, g.ldw[0] = wg.ld, g.ldw[1] = wu.ld;
     g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(d);
-    g.e.c[0] = h, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
+    g.e.c[0] = h, g.e.c[1] = rest, g.e.ldc = fp, g.e.ldg = fp, g.e.pad_to = static_cast<int32_t>(fp);
     if (saved) g.e.g = saved, g.e.u = saved + act_bytes();
     few_product(g, shl::kGate);
     shl::DecodeArgs y{};
-    y.x = h, y.ldx = fp, y.w[0] = a.w_down, y.ldw[0] = a.ld_down;
+    y.x = h, y.x_rest = rest, y.ldx = fp, y.w[0] = wd.p, y.ldw[0] = wd.ld;
     y.M = static_cast<int32_t>(N), y.N = static_cast<int32_t>(d), y.K = static_cast<int32_t>(f);
     y.e.c[0] = a.y, y.e.ldc = a.ld_y;
     few_product(y, shl::kStore);

@@ -43,11 +43,13 @@ extern "C" {
  * an fp32 product's accuracy, whatever the sizes of the other elements (elements
  * under 2^-100 to 2^-126 absolute). Up to 64 tokens the forward pass takes the fp32
  * matrix instruction instead. An infinite or NaN operand makes every result it
- * enters non-finite, and leaves the others as they are. In bf16, g, u, h, dg and du are rounded when they are
- * stored between the products (h from unrounded g and u): the matrix cores
- * take no more of h, dg and du, and g and u are what a step keeps. dx, dWg and
- * dWu then differ from fp32 intermediates' by 0.003 in relative norm, where
- * rounding the results alone gives 0.0017. */
+ * enters non-finite, and leaves the others as they are. In bf16, g, u, h, dg
+ * and du are rounded when they are stored between the products (h from unrounded
+ * g and u): the matrix cores take no more of h, dg and du, and g and u are what a
+ * step keeps. dx, dWg and dWu then differ from fp32 intermediates' by 0.003 in
+ * relative norm, where rounding the results alone gives 0.0017. Up to 32 tokens
+ * (d_model and d_hidden over 1) y is rounded alone: there h goes on as two bf16
+ * terms; `saved` has the first. */
 typedef enum {
   SHAMPOO_ACT_SILU = 0, /* g / (1 + exp(-g))                               */
   SHAMPOO_ACT_GELU = 1, /* tanh form                                       */

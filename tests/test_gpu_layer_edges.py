@@ -124,3 +124,17 @@ def test_fp32_whole_range():
         want = (x.double().cpu() * weight).square()
         log(f"   size {size:.1e}: {rel(y, want):.2e}")
         assert rel(y, want) <= 8 * F32_STEP
+
+
+@pytest.mark.parametrize("n", [1, 16, 17, 32])
+@pytest.mark.parametrize("d,f", [(256, 512), (768, 513), (2048, 4096)])
+def test_few_tokens_round_the_result_alone(n, d, f):
+    """bf16 results of the few-token kernels are rounded once: h goes into the second product as two bf16 terms (2^-17), sums are
+    fp32."""
+    g = torch.Generator().manual_seed(6)
+    x, wg, wu, wd = (normal(g, *s, std=k, dtype="bf16") for s, k in (((n, d), 1), ((d, f), d ** -0.5), ((d, f), d ** -0.5), ((f, d), f ** -0.5)))
+    want = ref.ffn(x, wg, wu, wd, "silu")
+    y = layer.ffn_forward(x, wg, wu, wd)
+    log(f"ffn {n} x {d} x {f} bf16: {rel(y, want):.2e}")
+    assert rel(y, want) <= BF16_STEP + 2.0 ** -15 + f32_tol(max(d, f))
+    assert torch.equal(y, layer.ffn_forward(x, wg, wu, wd, save=True)[0])
