@@ -192,7 +192,7 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
   if (b + 1 < last) load<F32, MATS, T, TERMS>(a, xrow, (b + 1) * kBatch, off, odd);
   if (b < last) use<F32, MATS, T, TERMS>(even, acc);
   if (b + 1 < last) use<F32, MATS, T, TERMS>(odd, acc);
-  const Activation act(a.e.act);
+  const Activation<F32> act(a.e.act);
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     const int rows = min(16, a.M - 16 * t);

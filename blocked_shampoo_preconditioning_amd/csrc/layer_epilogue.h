@@ -11,6 +11,10 @@ namespace shl {
 // Value a and derivative da at g. SiLU is g s(g), s the logistic function; the
 // tanh form of GELU is g s(t), t = 2 k (g + c g^3), k = sqrt(2 / pi), c =
 // 0.044715, since (1 + tanh(x)) / 2 = s(2 x). So both are g s(g (p + q g^2)).
+// bf16 takes the hardware's exponential and reciprocal, whose errors (the first's
+// grows with its argument: 62 steps of fp32 at -80) its own rounding covers; fp32
+// the exact ones, which an epilogue has time for (step of 4096 x 768 x 2048 the same).
+template <bool F32>
 struct Activation {
   float p, q;
   bool relu;
@@ -22,7 +26,8 @@ struct Activation {
   }
   __device__ __forceinline__ void operator()(float g, float& a, float& da) const {
     const float g2 = fminf(g * g, 1e30f);  // q g^2 stays a number where q = 0
-    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-g * (p + q * g2)));
+    const float t = -g * (p + q * g2);
+    const float s = F32 ? 1.f / (1.f + expf(t)) : __builtin_amdgcn_rcpf(1.f + __expf(t));
     a = g * s;
     da = s + a * (1.f - s) * (p + 3.f * q * g2);
     if (relu) {
@@ -73,7 +78,7 @@ __device__ __forceinline__ void store_planes(void* p, int64_t off, int64_t plane
 // that): the kept state and this epilogue's traffic, which is as long as its
 // product at ordinary widths, would double without.
 template <bool F32, int EPI>
-__device__ __forceinline__ void finish8(const EpiArgs& e, const Activation& act, int problem, int64_t oc, int64_t og, int col, int N,
+__device__ __forceinline__ void finish8(const EpiArgs& e, const Activation<F32>& act, int problem, int64_t oc, int64_t og, int col, int N,
                                          float (&v)[8], float (&w)[8], const Raw8<F32>& gr, const Raw8<F32>& ur) {
   const int width = e.pad_to > N ? e.pad_to : N;
   // all but a kStore's rows are padded to whole groups of eight

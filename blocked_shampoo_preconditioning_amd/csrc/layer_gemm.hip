@@ -544,7 +544,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint32_t block, uin
   const int c8 = (lane % LR) * 8, col = n0 + wn * COLS + c8;
   const int64_t ldc = EPI == kStore && problem ? g.e.ldc1 : g.e.ldc;
   const int64_t oc = row0 * ldc + col, og = row0 * g.e.ldg + col;
-  const Activation act(g.e.act);
+  const Activation<F32> act(g.e.act);
   Raw8<F32> gr[1 + AHEAD][NP], ur[1 + AHEAD][NP];
   const bool act_bwd = EPI == kActBwd && g.splits == 1;
   if (act_bwd && AHEAD) {
@@ -697,7 +697,7 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
         }
       }
     }
-    finish8<F32, EPI>(g.e, Activation(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
+    finish8<F32, EPI>(g.e, Activation<F32>(g.e.act), problem, oc, og, col, g.N, v, w, gr, ur);
   }
 }
 

@@ -138,3 +138,21 @@ def test_few_tokens_round_the_result_alone(n, d, f):
     log(f"ffn {n} x {d} x {f} bf16: {rel(y, want):.2e}")
     assert rel(y, want) <= BF16_STEP + 2.0 ** -15 + f32_tol(max(d, f))
     assert torch.equal(y, layer.ffn_forward(x, wg, wu, wd, save=True)[0])
+
+
+@pytest.mark.parametrize("n", [40, 300])
+def test_fp32_silu_keeps_its_digits(n):
+    """SiLU and its derivative element by element over g in [-80, 80]: identity weights make y = act(x) x and dx = dy' (x act'(x) +
+    act(x)). Each of a few operations (exponential, sum, quotient, products) is off by at most one or two steps of its own value."""
+    d = 64
+    x = torch.linspace(-80, 80, n * d).view(n, d).cuda()
+    one = torch.eye(d).cuda()
+    y, s = layer.ffn_forward(x, one, one, one, save=True)
+    dx = layer.ffn_backward(torch.ones_like(x), x, one, one, one, s, need_dw=False)[0]
+    v = x.double().cpu()
+    sg = torch.sigmoid(v)
+    want = v * sg * v
+    assert float(((y.double().cpu() - want).abs() / want.abs()).max()) <= 12 * F32_STEP
+    terms = (v * sg).abs() * 2 + (v * v * sg * (1 - sg)).abs()
+    err = (dx.double().cpu() - (v * sg * (1 + v * (1 - sg)) + v * sg)).abs() / terms
+    assert float(err.max()) <= 16 * F32_STEP
