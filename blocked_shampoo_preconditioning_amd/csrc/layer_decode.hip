@@ -57,6 +57,15 @@ __device__ __forceinline__ void load_x(const void* x, int64_t row, int k, int K,
   }
 }
 
+// A lane's first column, at most that of the last pair. bf16 pairs are aligned
+// words, so of an odd N the last one has the next row's element, or a pad, in its
+// second place (the buffer's length is rounded up to a word for the last row's);
+// fp32 pairs end with the last column.
+template <bool F32>
+__device__ __forceinline__ int pair_col(int n, int N) {
+  return min(n, F32 ? N - 2 : (N - 1) & ~1);
+}
+
 // kBatch rows of K from k0 for MATS matrices and 16 T tokens. Rows from K on lie
 // past the weights' end and read as zeros; what a lane reads past a row's last
 // column belongs to columns that are not stored.
@@ -76,7 +85,7 @@ __device__ __forceinline__ void load(const DecodeArgs& a, const int64_t (&xrow)[
   }
 #pragma unroll
   for (int m = 0; m < MATS; ++m) {
-    const int64_t at = k0 * a.ldw[m] * E, end = ((a.K - 1) * a.ldw[m] + a.N) * E;
+    const int64_t at = k0 * a.ldw[m] * E, end = (((a.K - 1) * a.ldw[m] + a.N) * E + 3) & ~int64_t(3);
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(static_cast<const char*>(a.w[m]) + at), 0, static_cast<int>(max<int64_t>(0, min<int64_t>(end - at, 0x7ffffff0))), 0x00020000);
     const uint32_t step = static_cast<uint32_t>(a.ldw[m]) * E;
@@ -155,8 +164,8 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
   const uint32_t groups = (a.N + kCols - 1) / kCols;
   if (id >= groups * a.splits) return;
   const uint32_t group = id / a.splits, split = id - group * a.splits;
-  // a lane's two columns; the last lanes repeat the last two of the matrix
-  const int n0 = group * kCols, col = min(n0 + 2 * (lane & 15), a.N - 2);
+  // a lane's two columns; the last lanes repeat the matrix's last pair
+  const int n0 = group * kCols, col = pair_col<F32>(n0 + 2 * (lane & 15), a.N);
   uint32_t off[MATS];
 #pragma unroll
   for (int m = 0; m < MATS; ++m)
@@ -203,7 +212,7 @@ __global__ __launch_bounds__(W * 64) void decode_kernel(DecodeArgs a) {
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = min(n0 + 2 * (4 * (lane >> 4) + r), a.N - 2) + i - n0;
+        const int c = pair_col<F32>(n0 + 2 * (4 * (lane >> 4) + r), a.N) + i - n0;
         if (c >= 0) {
 #pragma unroll
           for (int m = 0; m < MATS; ++m) sums[wave][m * 16 + (lane & 15)][c] = acc[m][i][t][r];
