@@ -97,12 +97,17 @@ __device__ __forceinline__ int4v make_rsrc(uint64_t base, int64_t left) {
 // lane. Written as asm because the compiler would wait for every such load
 // before any transposing LDS read; it has no register results, and its arrival
 // is waited for at the barrier of the next K step.
+// The compiler allots m0 itself and warns of any mention of it; what it knows of
+// its changes it needs all the same.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(const int4v& rsrc, uint32_t voff, uint32_t lds, int plus) {
   asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(rsrc), "i"(plus)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 
 typedef __attribute__((address_space(3))) const bf16x8* lds_frag;
 typedef __attribute__((address_space(3))) short4v* lds_quad;
