@@ -153,6 +153,21 @@ def _workspace(nbytes, like):
     return ws.data_ptr(), ws
 
 
+_sizes = {}  # what a call's byte count goes by -> the count
+_MAX_SIZES = 4096
+
+
+def _known_size(key, name, args, *more):
+    """A byte count of the library, asked once for each key; the table is emptied when it is full."""
+    size = _sizes.get(key)
+    if size is None:
+        size = _size(name, args, *more)
+        if len(_sizes) >= _MAX_SIZES:
+            _sizes.clear()
+        _sizes[key] = size
+    return size
+
+
 # ------------------------------------------------------ gated feed-forward block
 def _ffn_inputs(x, w_gate, w_up, w_down, activation):
     """The leading fields of the C struct, tokens to ld_down."""
@@ -170,18 +185,10 @@ def _ffn_inputs(x, w_gate, w_up, w_down, activation):
     return n, d, f, dt, act, px, pg, pu, pd, lx, lg, lu, ld
 
 
-_sizes = {}  # (sizes and dtype, direction, leading dimensions, alignments) -> bytes of workspace
-
-
 def _ffn_workspace(fields, args, backward, more):
-    """Workspace bytes of a call: asked once for each combination of what they go by."""
+    """Workspace bytes of a call, which go by sizes, direction, leading dimensions and alignments."""
     key = (fields[:4], backward, fields[9:], fields[5] & 15, fields[6] & 15, fields[7] & 15, fields[8] & 15, more)
-    size = _sizes.get(key)
-    if size is None:
-        if len(_sizes) >= 4096:
-            _sizes.clear()
-        size = _sizes[key] = _size("shampoo_ffn_workspace_size", args, backward)
-    return size
+    return _known_size(key, "shampoo_ffn_workspace_size", args, backward)
 
 
 _NO_GRADIENTS = (0,) * 10
@@ -206,11 +213,7 @@ def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
 
 
 def _saved_size(fields):
-    key = fields[:4]
-    size = _sizes.get(key)
-    if size is None:
-        size = _sizes[key] = _size("shampoo_ffn_saved_size", _FFN.pack(*fields, *(0,) * 13))
-    return size
+    return _sizes.get(fields[:4]) or _known_size(fields[:4], "shampoo_ffn_saved_size", _FFN.pack(*fields, *(0,) * 13))
 
 
 def ffn_backward(dy, x, w_gate, w_up, w_down, saved, activation="silu", need_dx=True, need_dw=True):
@@ -299,6 +302,11 @@ def norm_forward(x, kind="rms", weight=None, bias=None, eps=1e-6):
     return out, stats
 
 
+def _norm_workspace(head, args):
+    """Workspace bytes of a backward call, which go by rows, width and dtype alone."""
+    return _known_size(head[:3], "shampoo_norm_workspace_size", args)
+
+
 def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
     """x: the forward pass's r (or its input, where there is no z)."""
     n, d = head[:2]
@@ -326,10 +334,7 @@ def _norm_backward(head, x, z, px, lx, vectors, dr, dn, stats):
     pointers = [g.data_ptr() if g is not None else 0 for g in grads]  # an empty one: 0, nothing to write
     args = _NORM.pack(*head, pz, px, lz, lx, px if z is not None else 0, 0, lx, 0, *vectors, stats.data_ptr(), pdr, pdn, ldr,
                       ldn, dx.data_ptr(), dz.data_ptr() if z is not None else 0, d, d, *pointers, d)
-    key = (head[:3], vectors[2] != 0)
-    size = _sizes.get(key)
-    if size is None:
-        size = _sizes[key] = _size("shampoo_norm_workspace_size", args)
+    size = _norm_workspace(head, args)
     ws, keep = _workspace(size, x)
     _call("shampoo_norm_backward", args, x.get_device(), ws, size)
     return dx, dz, grads
