@@ -104,10 +104,6 @@ __device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&v)[8]) {
       v[i] = __uint_as_float(i % 2 ? r.w[0][i / 2] & 0xffff0000u : r.w[0][i / 2] << 16);
   }
 }
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t row, int col, int n, float (&v)[8]) {
-  unpack8<F32>(load_raw8<F32>(p, row, col, n), v);
-}
 
 // Eight elements to a row, or its last n < 8: one by one in a rolled loop over
 // a shifting register file, since these lines are in every kernel many times and

@@ -365,7 +365,7 @@ struct Ffn {
 int check_sizes(const shampoo_ffn_t* a) {
   if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
   if (a->tokens < 0 || a->d_model < 1 || a->d_hidden < 1 || a->tokens > kMaxDim || a->d_model > kMaxLd || a->d_hidden > kMaxLd)
-    return fail(SHAMPOO_ERR_INVALID_ARG, "tokens must be in [0, 2^31), d_model and d_hidden in [1, 2^21]");
+    return fail(SHAMPOO_ERR_INVALID_ARG, "tokens must be in [0, 2^31 - 1024], d_model and d_hidden in [1, 2^21]");
   RC(check_dtype(a->dtype));
   if (a->activation < SHAMPOO_ACT_SILU || a->activation > SHAMPOO_ACT_RELU)
     return fail(SHAMPOO_ERR_UNSUPPORTED, "activation must be one of shampoo_activation_t");
@@ -590,7 +590,7 @@ int shampoo_dropout(const shampoo_dropout_t* a, void* hip_stream) {
   return guarded([&]() -> int {
     if (!a) return fail(SHAMPOO_ERR_INVALID_ARG, "arguments are NULL");
     if (a->rows < 0 || a->cols < 0 || a->cols > kMaxDim || a->rows > (int64_t(1) << 40))
-      return fail(SHAMPOO_ERR_INVALID_ARG, "rows must be in [0, 2^40], cols in [0, 2^31)");
+      return fail(SHAMPOO_ERR_INVALID_ARG, "rows must be in [0, 2^40], cols in [0, 2^31 - 1024]");
     RC(check_dtype(a->dtype));
     const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
     RC(check_matrix("x", a->x, a->rows, a->cols, a->ld_x, e, kAnyLd));

@@ -8,7 +8,8 @@ weight gradients go to its `step` as they are. Tensors are 2-D CUDA tensors of
 float32 or bfloat16 with contiguous rows (any row stride); a call's tensors
 share one dtype. Every call runs on torch's current stream, returns before it
 has run, and takes its scratch memory from torch's allocator on that stream.
-Results are deterministic.
+Results are deterministic. The calls record no autograd graph, also where an
+input requires a gradient: a program calls the backward functions itself.
 """
 from __future__ import annotations
 

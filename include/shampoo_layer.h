@@ -57,7 +57,8 @@ typedef enum {
 } shampoo_activation_t;
 
 typedef struct {
-  int64_t tokens, d_model, d_hidden; /* tokens >= 0, the others >= 1; < 2^31 */
+  int64_t tokens, d_model, d_hidden; /* 0 <= tokens <= 2^31 - 1024; the others
+                                        in [1, 2^21]                      */
   int32_t dtype;                     /* shampoo_dtype_t                      */
   int32_t activation;                /* shampoo_activation_t                 */
   const void *x, *w_gate, *w_up, *w_down;
@@ -107,7 +108,7 @@ int shampoo_ffn_backward(const shampoo_ffn_t* a, void* workspace, size_t workspa
 typedef enum { SHAMPOO_NORM_NONE = 0, SHAMPOO_NORM_RMS = 1, SHAMPOO_NORM_LAYER = 2 } shampoo_norm_kind_t;
 
 typedef struct {
-  int64_t rows, width; /* rows >= 0, 1 <= width <= 8192               */
+  int64_t rows, width; /* 0 <= rows <= 2^40, 1 <= width <= 8192        */
   int32_t dtype;       /* shampoo_dtype_t of every array but stats     */
   int32_t post_kind, next_kind;
   float eps;            /* > 0                                         */
@@ -144,7 +145,7 @@ int shampoo_norm_backward(const shampoo_norm_t* a, void* workspace, size_t works
  * y = x where kept (times the scale above), else 0; y may be x itself. Its
  * gradient is the same call on dy. */
 typedef struct {
-  int64_t rows, cols; /* cols <= 2^31 */
+  int64_t rows, cols; /* 0 <= rows <= 2^40, 0 <= cols <= 2^31 - 1024 */
   int32_t dtype;
   uint32_t offset;
   double dropout;
