@@ -135,6 +135,10 @@ struct NormArgs {
 };
 constexpr int kMaxNormWidth = 8192;
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s);
+// What the rounding of bf16 n = norm(x) left, made again from x and the kept
+// statistics (a.x, a.stats, a.w_next, a.b_next; a.n is read): out[rows][ld_out],
+// columns zero-padded to ld_out (a multiple of 8).
+hipError_t launch_norm_rest(const NormArgs& a, uint16_t* out, int64_t ld_out, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s);
 int64_t norm_partial_floats(const NormArgs& a);
 

@@ -297,6 +297,43 @@ __global__ __launch_bounds__(NT) void norm_forward_kernel(NormArgs a) {
   }
 }
 
+// The second term of bf16 n: what its rounding left. An element counts only where
+// the rounding of what is made again here is n's element itself, so that n may
+// have been changed since, and every other input too: the term is then 0. Bound by
+// HBM: 4096 x 768 (19 MB) in 6 us.
+__global__ __launch_bounds__(256) void norm_rest_kernel(NormArgs a, uint16_t* out, int64_t ld_out) {
+  const int64_t c8 = ld_out / 8, total = c8 * a.rows;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / c8;
+    const int col = static_cast<int>(i - row * c8) * 8, m = max(0, min(8, a.d - col));
+    const floatx4 st = *reinterpret_cast<const floatx4*>(a.stats + row * 4);
+    Raw8<false> xr = fetch8<false>(a.x, row * a.ldx, col, m), nr = fetch8<false>(a.n, row * a.ldn, col, m), wr, br;
+    if (a.w_next) wr = fetch8<false>(a.w_next, 0, col, m);
+    if (a.b_next) br = fetch8<false>(a.b_next, 0, col, m);
+    float x[8], n[8], w[8], b[8];
+    unpack8<false>(settle8<false>(xr, col, m), x);
+    unpack8<false>(settle8<false>(nr, col, m), n);
+    if (a.w_next) unpack8<false>(settle8<false>(wr, col, m), w);
+    if (a.b_next) unpack8<false>(settle8<false>(br, col, m), b);
+    uint4v t;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float d[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = 2 * k + h;
+        float v = (x[e] - st[2]) * st[3];
+        if (a.w_next) v *= w[e];
+        if (a.b_next) v += b[e];
+        const float rounded = bf16_to_f32(f32_to_bf16(v));
+        d[h] = e < m && rounded == n[e] && fabsf(v) < __builtin_inff() ? v - rounded : 0.f;
+      }
+      t[k] = pack_bf16(d[0], d[1]);
+    }
+    *reinterpret_cast<uint4v*>(out + row * ld_out + col) = t;
+  }
+}
+
 // Backward. With c = dn w', dR = dr + rstd (c - [mean c] - r^ mean(c r^));
 // dx = alpha dR; db = drop(dR); dgate = sum db p; dp = db gate; dz likewise
 // from dp w. The four vectors' sums stay in registers over the workgroup's
@@ -607,6 +644,14 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   return a.f32 ? dispatch_norm<true>(a, false, norm_grid(a, false, norm_general(a, false)), s)
                : dispatch_norm<false>(a, false, norm_grid(a, false, norm_general(a, false)), s);
+}
+
+hipError_t launch_norm_rest(const NormArgs& a, uint16_t* out, int64_t ld_out, hipStream_t s) {
+  const int64_t blocks = (a.rows * (ld_out / 8) + 255) / 256;
+  if (blocks == 0) return hipSuccess;
+  if (a.f32) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(norm_rest_kernel, dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a, out, ld_out);
+  return hipGetLastError();
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {

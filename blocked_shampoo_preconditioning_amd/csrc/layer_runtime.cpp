@@ -152,6 +152,7 @@ struct Planes {
 // laid out.
 struct Ffn {
   const shampoo_ffn_t& a;
+  const shl::NormArgs* norm;  // of bf16 x, where g and u are to be taken from it unrounded
   char* ws;
   hipStream_t stream;
   bool run;
@@ -161,7 +162,8 @@ struct Ffn {
   bool f32;
   shl::PackList list{};
 
-  Ffn(const shampoo_ffn_t& a_, char* ws_, hipStream_t s, bool run_) : a(a_), ws(ws_), stream(s), run(run_) {
+  Ffn(const shampoo_ffn_t& a_, const shl::NormArgs* norm_, char* ws_, hipStream_t s, bool run_)
+      : a(a_), norm(norm_), ws(ws_), stream(s), run(run_) {
     N = a.tokens, d = a.d_model, f = a.d_hidden, fp = round8(f);
     f32 = a.dtype == SHAMPOO_F32;
     e = f32 ? 4 : 2;
@@ -288,8 +290,17 @@ struct Ffn {
   }
 
   void forward() {
-    if (few()) return forward_few();
-    const Planes x = operand(a.x, N, d, a.ld_x, true);
+    if (few() && !norm) return forward_few();
+    // With a second term both have the same leading dimension, of whole groups. It
+    // doubles the first product (forward of 4096 x 768 x 2048 56 -> 80 us) where one
+    // term leaves dx and dWg 2 to 4% wrong; SiLU and GELU are 0.5% off either way.
+    const Planes x = !norm || a.ld_x == round8(d) ? operand(a.x, N, d, a.ld_x, true) : copied(a.x, N, d, a.ld_x);
+    Planes rest = x;
+    if (norm) {
+      uint16_t* out = static_cast<uint16_t*>(take(N * x.ld * 2));
+      rest.p = out;
+      if (run) ok(shl::launch_norm_rest(*norm, out, x.ld, stream));
+    }
     Planes wg, wu;
     operands(a.w_gate, a.w_up, d, f, a.ld_gate, a.ld_up, false, wg, wu);
     const Planes wd = operand(a.w_down, f, d, a.ld_down, false);
@@ -298,6 +309,7 @@ struct Ffn {
     const Planes h = written(saved ? saved_h() : take(N * fp * 2 * shl::planes(f32)));
     {
       shl::GemmArgs g{};
+      if (norm) segment(g, rest, wg, &wu);
       segment(g, x, wg, &wu);
       g.M = static_cast<int32_t>(N), g.N = static_cast<int32_t>(f), g.K = static_cast<int32_t>(round8(d));
       g.k_real = static_cast<int32_t>(d), g.problems = 1;
@@ -393,25 +405,23 @@ int check_ffn(const shampoo_ffn_t* a, bool backward) {
   return SHAMPOO_OK;
 }
 
-int64_t ffn_workspace(const shampoo_ffn_t* a, bool backward) {
-  Ffn p(*a, nullptr, nullptr, false);
+int64_t ffn_workspace(const shampoo_ffn_t* a, const shl::NormArgs* norm, bool backward) {
+  Ffn p(*a, norm, nullptr, nullptr, false);
   backward ? p.backward() : p.forward();
   return p.carve.o;
 }
 
-int run_ffn(const shampoo_ffn_t* a, void* workspace, size_t bytes, void* stream, bool backward) {
-  return guarded([&]() -> int {
-    RC(check_ffn(a, backward));
-    const int64_t need = ffn_workspace(a, backward);
-    if (need > 0 && !workspace) return fail(SHAMPOO_ERR_INVALID_ARG, "workspace is NULL");
-    if (!aligned(workspace, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "workspace is not aligned to 256 bytes");
-    if (bytes < static_cast<size_t>(need))
-      return fail(SHAMPOO_ERR_WORKSPACE_TOO_SMALL,
-                  "workspace has " + std::to_string(bytes) + " bytes, the call needs " + std::to_string(need));
-    Ffn p(*a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream), true);
-    backward ? p.backward() : p.forward();
-    return p.err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(p.err, backward ? "shampoo_ffn_backward" : "shampoo_ffn_forward");
-  });
+// The launches of a checked call.
+int run_ffn(const shampoo_ffn_t* a, const shl::NormArgs* norm, void* workspace, size_t bytes, void* stream, bool backward) {
+  const int64_t need = ffn_workspace(a, norm, backward);
+  if (need > 0 && !workspace) return fail(SHAMPOO_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned(workspace, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "workspace is not aligned to 256 bytes");
+  if (bytes < static_cast<size_t>(need))
+    return fail(SHAMPOO_ERR_WORKSPACE_TOO_SMALL,
+                "workspace has " + std::to_string(bytes) + " bytes, the call needs " + std::to_string(need));
+  Ffn p(*a, norm, static_cast<char*>(workspace), static_cast<hipStream_t>(stream), true);
+  backward ? p.backward() : p.forward();
+  return p.err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(p.err, backward ? "shampoo_ffn_backward" : "shampoo_ffn_forward");
 }
 
 // --------------------------------------------------------- norms and dropout
@@ -519,6 +529,23 @@ int norm_args(const shampoo_norm_t* a, bool backward, shl::NormArgs& k) {
   return make_drop(a->dropout, a->seed, a->offset, k.drop);
 }
 
+// The norm that made a block's x; `used`: whether the block takes x unrounded (bf16
+// with ReLU, whose derivative jumps).
+int check_normed(const shampoo_ffn_t* a, const shampoo_norm_t* norm, shl::NormArgs& k, bool& used) {
+  RC(check_ffn(a, false));
+  if (!norm) return fail(SHAMPOO_ERR_INVALID_ARG, "norm is NULL");
+  if (norm->z) return fail(SHAMPOO_ERR_INVALID_ARG, "norm has a z: only a norm alone can be made again");
+  RC(check_norm(norm, false));
+  if (norm->rows != a->tokens || norm->width != a->d_model || norm->dtype != a->dtype)
+    return fail(SHAMPOO_ERR_INVALID_ARG, "norm has another size or dtype than x");
+  if (!norm->stats && norm->rows) return fail(SHAMPOO_ERR_INVALID_ARG, "norm's stats are NULL: the norm has to keep them");
+  RC(norm_args(norm, false, k));
+  // n is x itself, wherever the norm's call left it
+  k.n = const_cast<void*>(a->x), k.ldn = a->ld_x;
+  used = a->dtype == SHAMPOO_BF16 && a->activation == SHAMPOO_ACT_RELU;
+  return SHAMPOO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -526,7 +553,7 @@ extern "C" {
 int shampoo_ffn_saved_size(const shampoo_ffn_t* a, size_t* bytes_out) {
   RC(check_sizes(a));
   if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
-  const Ffn p(*a, nullptr, nullptr, false);
+  const Ffn p(*a, nullptr, nullptr, nullptr, false);
   *bytes_out = static_cast<size_t>(p.saved_bytes());
   return SHAMPOO_OK;
 }
@@ -535,17 +562,44 @@ int shampoo_ffn_workspace_size(const shampoo_ffn_t* a, int32_t backward, size_t*
   return guarded([&]() -> int {
     RC(check_ffn(a, backward != 0));
     if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
-    *bytes_out = static_cast<size_t>(ffn_workspace(a, backward != 0));
+    *bytes_out = static_cast<size_t>(ffn_workspace(a, nullptr, backward != 0));
     return SHAMPOO_OK;
   });
 }
 
 int shampoo_ffn_forward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
-  return run_ffn(a, workspace, workspace_bytes, hip_stream, false);
+  return guarded([&]() -> int {
+    RC(check_ffn(a, false));
+    return run_ffn(a, nullptr, workspace, workspace_bytes, hip_stream, false);
+  });
 }
 
 int shampoo_ffn_backward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
-  return run_ffn(a, workspace, workspace_bytes, hip_stream, true);
+  return guarded([&]() -> int {
+    RC(check_ffn(a, true));
+    return run_ffn(a, nullptr, workspace, workspace_bytes, hip_stream, true);
+  });
+}
+
+int shampoo_ffn_normed_workspace_size(const shampoo_ffn_t* a, const shampoo_norm_t* norm, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    shl::NormArgs k;
+    bool used;
+    RC(check_normed(a, norm, k, used));
+    if (!bytes_out) return fail(SHAMPOO_ERR_INVALID_ARG, "bytes_out is NULL");
+    *bytes_out = static_cast<size_t>(ffn_workspace(a, used ? &k : nullptr, false));
+    return SHAMPOO_OK;
+  });
+}
+
+int shampoo_ffn_forward_normed(const shampoo_ffn_t* a, const shampoo_norm_t* norm, void* workspace, size_t workspace_bytes,
+                               void* hip_stream) {
+  return guarded([&]() -> int {
+    shl::NormArgs k;
+    bool used;
+    RC(check_normed(a, norm, k, used));
+    return run_ffn(a, used ? &k : nullptr, workspace, workspace_bytes, hip_stream, false);
+  });
 }
 
 int shampoo_norm_workspace_size(const shampoo_norm_t* a, size_t* bytes_out) {

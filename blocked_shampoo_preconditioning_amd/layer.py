@@ -41,6 +41,8 @@ _SIGNATURES = {
     "shampoo_ffn_workspace_size": [_A, ctypes.c_int32, _SIZE],
     "shampoo_ffn_forward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
     "shampoo_ffn_backward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "shampoo_ffn_normed_workspace_size": [_A, _A, _SIZE],
+    "shampoo_ffn_forward_normed": [_A, _A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
     "shampoo_norm_workspace_size": [_A, _SIZE],
     "shampoo_norm_forward": [_A, ctypes.c_void_p],
     "shampoo_norm_backward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
@@ -186,9 +188,11 @@ def _ffn_inputs(x, w_gate, w_up, w_down, activation):
     return n, d, f, dt, act, px, pg, pu, pd, lx, lg, lu, ld
 
 
-def _ffn_workspace(fields, args, backward, more):
+def _ffn_workspace(fields, args, backward, more, norm=None):
     """Workspace bytes of a call, which go by sizes, direction, leading dimensions and alignments."""
     key = (fields[:4], backward, fields[9:], fields[5] & 15, fields[6] & 15, fields[7] & 15, fields[8] & 15, more)
+    if norm:
+        return _known_size(key, "shampoo_ffn_normed_workspace_size", args, norm)
     return _known_size(key, "shampoo_ffn_workspace_size", args, backward)
 
 
@@ -199,7 +203,10 @@ def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
     """y = (act(x w_gate) * (x w_up)) w_down for x [tokens, d], w_gate and w_up
     [d, f], w_down [f, d]. With `save` returns (y, saved), `saved` being what
     `ffn_backward` needs (an opaque tensor: g, u and h of every token).
-    activation: "silu", "gelu" (tanh form) or "relu"."""
+    activation: "silu", "gelu" (tanh form) or "relu". Where bf16 x is the result
+    of `norm_forward` itself, a saved ReLU block takes g and u from it as it was
+    before its rounding, which would move g over 0 in one element of 2000 (an
+    element of x that was changed since is taken as it is)."""
     fields = _ffn_inputs(x, w_gate, w_up, w_down, activation)
     n, d, f = fields[:3]
     y = _new_like(x)
@@ -207,10 +214,33 @@ def ffn_forward(x, w_gate, w_up, w_down, activation="silu", save=False):
     if save:
         saved = torch.empty(_saved_size(fields), dtype=torch.uint8, device=x.device)
     args = _FFN.pack(*fields, y.data_ptr() or 256, d, saved.data_ptr() if save else 0, *_NO_GRADIENTS)
+    norm = _norm_of(x) if save and activation == "relu" and fields[3] == SHAMPOO_BF16 else None
+    if norm:
+        size = _ffn_workspace(fields, args, 0, "normed", norm)
+        ws, keep = _workspace(size, x)
+        _call("shampoo_ffn_forward_normed", args, x.get_device(), norm, ws, size)
+        return y, saved
     size = _ffn_workspace(fields, args, 0, save)
     ws, keep = _workspace(size, x)
     _call("shampoo_ffn_forward", args, x.get_device(), ws, size)
     return (y, saved) if save else y
+
+
+def _norm_of(x):
+    """The C struct of the `norm_forward` call that returned x; None if no such call did, or its tensors are others by now."""
+    made = getattr(x, "_norm_call", None)
+    if made is None:
+        return None
+    head, source, weight, bias, stats = made
+    n, d = head[:2]
+    try:
+        px, lx = _matrix("n", x, n, d, x)
+        ps, ls = _matrix("x", source, n, d, x)
+        pw, pb = _vector("weight", weight, d, x), _vector("bias", bias, d, x)
+        _matrix("stats", stats, n, 4, stats)
+    except ValueError:
+        return None
+    return _NORM.pack(*head, 0, ps, 0, ls, 0, px, 0, lx, 0, 0, 0, pw, pb, 0, stats.data_ptr(), *_NO_NORM_GRADIENTS)
 
 
 def _saved_size(fields):
@@ -289,7 +319,9 @@ def residual_forward(x, z, *, post="rms", post_weight=None, post_bias=None, gate
 
 
 def norm_forward(x, kind="rms", weight=None, bias=None, eps=1e-6):
-    """n = norm(x), [rows, width]; returns (n, stats for `norm_backward`)."""
+    """n = norm(x), [rows, width]; returns (n, stats for `norm_backward`). bf16 n
+    knows this call's inputs (and keeps them in memory as long as it is there), for
+    a ReLU block that takes it: see `ffn_forward`."""
     if kind in ("none", None):
         raise ValueError("kind must be 'rms' or 'layer'")
     dt, n, d = _first("x", x)
@@ -300,6 +332,8 @@ def norm_forward(x, kind="rms", weight=None, bias=None, eps=1e-6):
     stats = torch.empty((n, 4), dtype=torch.float32, device=x.device)
     args = _NORM.pack(*head, 0, px, 0, lx, 0, out.data_ptr(), d, d, *vectors, stats.data_ptr(), *_NO_NORM_GRADIENTS)
     _call("shampoo_norm_forward", args, x.get_device())
+    if dt == SHAMPOO_BF16:
+        out._norm_call = (head, x, weight, bias, stats)
     return out, stats
 
 

@@ -86,6 +86,17 @@ int shampoo_ffn_workspace_size(const shampoo_ffn_t* a, int32_t backward, size_t*
 int shampoo_ffn_forward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream);
 int shampoo_ffn_backward(const shampoo_ffn_t* a, void* workspace, size_t workspace_bytes, void* hip_stream);
 
+/* A block behind a norm, shampoo_ffn_forward_normed (declared with the norms):
+ * shampoo_ffn_forward for x = n of a shampoo_norm_forward call `norm` with z =
+ * NULL, whose x, stats, weight and bias are still there. ReLU's derivative jumps
+ * at 0, and the rounding of bf16 n moves g over it in one element of 2000, which
+ * would make dx and dWg 2 to 4% wrong in norm. So for bf16 and ReLU g and u are
+ * taken from n as it was before its rounding: what that left is made again as a
+ * second term of x, for every element whose rounding is still x's own (else it
+ * is 0). Its products run as those of over 32 tokens, and those of g and u take
+ * twice as long. For other activations, whose results this would change by less
+ * than their own roundings do, and for fp32 it is shampoo_ffn_forward itself. */
+
 /* -------------------------- norms before and after a block, with dropout
  *     p = norm_post(z),  r = residual_scale x + drop(gate * p),
  *     n = norm_next(r)
@@ -140,6 +151,11 @@ typedef struct {
 int shampoo_norm_workspace_size(const shampoo_norm_t* a, size_t* bytes_out);
 int shampoo_norm_forward(const shampoo_norm_t* a, void* hip_stream);
 int shampoo_norm_backward(const shampoo_norm_t* a, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* The block behind the norm (above). Host only: its bytes of workspace. */
+int shampoo_ffn_normed_workspace_size(const shampoo_ffn_t* a, const shampoo_norm_t* norm, size_t* bytes_out);
+int shampoo_ffn_forward_normed(const shampoo_ffn_t* a, const shampoo_norm_t* norm, void* workspace, size_t workspace_bytes,
+                               void* hip_stream);
 
 /* ------------------------------------------------------------- dropout
  * y = x where kept (times the scale above), else 0; y may be x itself. Its

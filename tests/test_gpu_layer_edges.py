@@ -156,3 +156,58 @@ def test_fp32_silu_keeps_its_digits(n):
     terms = (v * sg).abs() * 2 + (v * v * sg * (1 - sg)).abs()
     err = (dx.double().cpu() - (v * sg * (1 + v * (1 - sg)) + v * sg)).abs() / terms
     assert float(err.max()) <= 16 * F32_STEP
+
+
+def norm_then_relu(n, d, f, kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    x, dy = normal(g, n, d, dtype="bf16"), normal(g, n, d, std=1e-2, dtype="bf16")
+    w, b = normal(g, d, std=0.1, mean=1.0, dtype="bf16"), normal(g, d, std=0.1, dtype="bf16") if kind == "layer" else None
+    ws = [normal(g, *s, std=s[0] ** -0.5, dtype="bf16") for s in ((d, f), (d, f), (f, d))]
+    return x, w, b, ws, dy
+
+
+@pytest.mark.parametrize("n,d,f,kind", [(1, 64, 4000, "rms"), (20, 64, 896, "layer"), (300, 100, 391, "rms"), (150, 131, 264, "layer"),
+                                        (1100, 256, 520, "layer"), (3000, 96, 384, "rms")])
+def test_relu_block_behind_a_norm(n, d, f, kind):
+    """The rounding of the norm's bf16 result does not decide on which side of 0 the block's g lies. Tolerance: what the block alone
+    has (6 BF16_STEP), one for the rounding of its input, and the elements of g that the two terms' error, 2^-18 of g's size, may
+    still move over 0: a share of 2^-18 of them, half of all being on, is sqrt(2^-17) in norm."""
+    x, w, b, ws, dy = norm_then_relu(n, d, f, kind, 21)
+    log(f"norm and ffn {n} x {d} x {f} bf16 relu")
+    a, _ = layer.norm_forward(x, kind, w, b)
+    y, s = layer.ffn_forward(a, *ws, activation="relu", save=True)
+    got = (y, *layer.ffn_backward(dy, a, *ws, s, activation="relu"))
+    exact = ref.norm(x.double().cpu(), kind, w.double().cpu(), b.double().cpu() if b is not None else None, 1e-6)[0]
+    want_y, want, terms = ref.ffn(exact, *ws, "relu", dy)
+    errs = [rel(p, q, t) for p, q, t in zip(got, (want_y, *want), terms)]
+    log("   errors " + " ".join(f"{e:.2e}" for e in errs))
+    assert max(errs) <= 7 * BF16_STEP + 2.0 ** -8.5
+
+
+@pytest.mark.parametrize("n", [20, 300])
+def test_relu_block_takes_a_changed_input_as_it_is(n):
+    """An input that was changed after its norm, or whose norm's own inputs were, counts as it is."""
+    d, f = 96, 200
+    x, w, b, ws, dy = norm_then_relu(n, d, f, "layer", 22)
+    tol = 6 * BF16_STEP
+
+    def check(a):
+        y, s = layer.ffn_forward(a, *ws, activation="relu", save=True)
+        got = (y, *layer.ffn_backward(dy, a, *ws, s, activation="relu"))
+        want_y, want, terms = ref.ffn(a, *ws, "relu", dy)
+        assert max(rel(p, q, t) for p, q, t in zip(got, (want_y, *want), terms)) <= tol
+    # every element a step or more away from its norm's result; dropped or scaled; of another tensor
+    for change in (lambda a: a.view(torch.int16).add_(1), lambda a: a.mul_(-1.5), lambda a: layer.dropout(a, 0.5, 3, out=a).neg_(),
+                   lambda a: a.copy_(torch.flip(a, (0,)).neg())):
+        a, _ = layer.norm_forward(x, "layer", w, b)
+        change(a)
+        check(a)
+    for change in (lambda v, st: v.zero_(), lambda v, st: st.fill_(float("nan")), lambda v, st: v.mul_(1.25), lambda v, st: v.resize_(1, d)):
+        v = x.clone()
+        a, st = layer.norm_forward(v, "layer", w, b)
+        change(v, st)
+        check(a)
+    # a tensor that came from no norm, and one with other strides
+    a, _ = layer.norm_forward(x, "layer", w, b)
+    check(a.clone())
+    check(torch.cat([a, a], 1)[:, :d])

@@ -6,7 +6,7 @@ import pytest
 
 from blocked_shampoo_preconditioning_amd import layer as L
 from blocked_shampoo_preconditioning_amd import shampoo as S
-from tests.test_layer_host import DROP, FAKE, FFN, INVALID, NORM
+from tests.test_layer_host import DROP, FAKE, FFN, INVALID, MISALIGNED, NORM, SMALL, UNSUPPORTED
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -54,3 +54,41 @@ def test_largest_sizes_of_dropout(lib):
     assert lib.shampoo_dropout(L._DROP.pack(*{**DROP, "rows": 0, "cols": LARGEST + 1}.values()), None) == INVALID
     assert "[0, 2^31 - 1024]" in lib.shampoo_last_error().decode()
     assert "0 <= cols <= 2^31 - 1024" in open(L.LAYER_HEADER_PATH).read()
+
+
+# the norm alone that made a block's x
+BEFORE = {**NORM, **dict(z=0, post_kind=0, post_weight=0, gate=0, r=0, dtype=1, dr=0, dn=0, dx=0, dz=0, d_post_weight=0, d_gate=0, d_next_weight=0)}
+
+
+@pytest.mark.parametrize("over,norm,code", [
+    ({}, {}, 0), (dict(activation=2), {}, 0), ({}, dict(z=FAKE), INVALID), ({}, dict(rows=5), INVALID), ({}, dict(width=8), INVALID),
+    ({}, dict(dtype=0), INVALID), ({}, dict(next_kind=0, next_weight=0), INVALID), ({}, dict(stats=0), INVALID), ({}, dict(stats=FAKE + 8), MISALIGNED),
+    ({}, dict(x=0), INVALID), ({}, dict(ld_x=15), INVALID), ({}, dict(next_kind=3), UNSUPPORTED), (dict(x=0), {}, INVALID),
+    (dict(activation=3), {}, UNSUPPORTED)])
+def test_refusals_of_the_block_behind_a_norm(lib, over, norm, code):
+    out = ctypes.c_size_t()
+    args = L._FFN.pack(*{**FFN, "activation": 2, **over}.values()), L._NORM.pack(*{**BEFORE, **norm}.values())
+    assert lib.shampoo_ffn_normed_workspace_size(*args, ctypes.byref(out)) == code
+    if code:
+        assert lib.shampoo_last_error().decode()
+        assert lib.shampoo_ffn_forward_normed(*args, FAKE, 1 << 30, None) == code
+
+
+def test_workspace_of_the_block_behind_a_norm(lib):
+    """The second term costs workspace with ReLU and bf16 alone; a NULL norm and a small workspace are refused."""
+    def size(name, *args):
+        out = ctypes.c_size_t()
+        assert getattr(lib, name)(*args, ctypes.byref(out)) == 0
+        return out.value
+    for activation, dtype in ((2, 1), (0, 1), (2, 0)):
+        ffn = L._FFN.pack(*{**FFN, "tokens": 100, "activation": activation, "dtype": dtype}.values())
+        norm = L._NORM.pack(*{**BEFORE, "rows": 100, "dtype": dtype}.values())
+        with_norm, without = size("shampoo_ffn_normed_workspace_size", ffn, norm), size("shampoo_ffn_workspace_size", ffn, 0)
+        assert (with_norm > without) == (activation == 2 and dtype == 1)
+    ffn, norm = L._FFN.pack(*{**FFN, "tokens": 100, "activation": 2}.values()), L._NORM.pack(*{**BEFORE, "rows": 100}.values())
+    need = size("shampoo_ffn_normed_workspace_size", ffn, norm)
+    assert lib.shampoo_ffn_normed_workspace_size(ffn, norm, None) == INVALID
+    assert lib.shampoo_ffn_normed_workspace_size(ffn, None, ctypes.byref(ctypes.c_size_t())) == INVALID
+    assert lib.shampoo_ffn_forward_normed(ffn, norm, None, need, None) == INVALID
+    assert lib.shampoo_ffn_forward_normed(ffn, norm, FAKE + 8, need, None) == MISALIGNED
+    assert lib.shampoo_ffn_forward_normed(ffn, norm, FAKE, need - 1, None) == SMALL
