@@ -15,11 +15,12 @@
 // times the loads.
 //
 // What bounds it: large products run into the power limit (8192 x 2048 x 8192
-// bf16, all six: 2.09 ms, 1180 TFLOP/s, the matrix cores busy 62% of the time at
-// 2 GHz; other schedules of the loop change nothing there), ordinary ones the
-// L2s, which feed a 128 tile 32 KiB a K step (0.46 us with every CU busy, half
-// the rate of the matrix cores), small ones what a launch costs besides its K
-// loop: about 9 us from the first load to the last store. Step of 4096 x 768 x
+// bf16, all six: 2.09 ms, 1180 TFLOP/s; the clock falls to 1.9 GHz and the matrix
+// cores are busy 62% of the time in the last three products, 38% in dh with its
+// epilogue; other schedules of the loop change nothing there), ordinary ones the
+// L2s, which feed a 128 tile 32 KiB a K step (0.46 us with every CU busy, 14 TB/s,
+// half the rate of the matrix cores), small ones what a launch costs besides its
+// K loop: about 9 us from the first load to the last store. Step of 4096 x 768 x
 // 2048 bf16 156 us (743 TFLOP/s), 1024 x 768 x 2048 75 us. fp32 4096 x 768 x 2048
 // 620 us (187 TFLOP/s of fp32 results; the library's fp32 product alone: 154), 2048
 // x 2048 x 8192 3.0 ms (205; 1230 of bf16 products, the power limit). Two fp16
@@ -658,7 +659,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void gemm_group_kernel(GroupArgs a
 
 // Joins the parts of a split product in their order and runs the epilogue. A
 // launch and one trip to the caches, which still hold the parts: 1024 x 768 from
-// 4 parts 4.1 us, dg and du of 1024 x 2048 fp32 from 2 parts 12 us (50 MB).
+// 4 parts 4.1 us, dg and du of 1024 x 2048 fp32 from 2 parts 12.6 us (59 MB).
 template <bool F32, int EPI>
 __global__ __launch_bounds__(256) void gemm_finish_kernel(GemmArgs g) {
   const int width = max(g.N, g.e.pad_to);
@@ -722,7 +723,8 @@ __device__ __forceinline__ void group_place(int64_t i, int64_t c8, int64_t total
 
 // Copies operands into rows that loads can take (16-byte aligned, padded with
 // zeros to whole 16 bytes); fp32 values become three bf16 planes (split3). Bound
-// by HBM.
+// by HBM: x and the weights of 4096 x 768 x 2048 fp32 (31 MB in, 47 out) in 16.5
+// us, bf16 of odd strides (1537 x 1001 x 2730, 39 MB) in 8.
 template <bool F32>
 __global__ __launch_bounds__(256) void pack_kernel(PackList list) {
   const PackArgs& p = list.t[blockIdx.y];

@@ -8,16 +8,16 @@
  * Conventions are shampoo.h's: status codes, shampoo_last_error, device
  * memory owned by the caller, every call asynchronous on the given stream,
  * row-major matrices with a leading dimension in elements. In addition:
- *  - Results are deterministic: every sum is taken in a fixed order, and
- *    atomics only take maxima.
+ *  - Results are deterministic: every sum is taken in a fixed order.
  *  - Sums, statistics and products accumulate in fp32; an element is rounded
  *    (to nearest even) when it is stored in bf16.
  *  - A workspace is scratch: nothing is kept in it after the call's work on
  *    the stream. It must not be shared by calls that may run at once.
  *  - Pointers are aligned to their element size; workspace and saved to 256
- *    bytes. 16-byte aligned matrices with ld a multiple of 8 (and, where a
- *    row is a product's summation index, cols a multiple of 8) are read in
- *    place; others are first copied to the workspace.
+ *    bytes. The block's products read 16-byte aligned bf16 matrices with ld a
+ *    multiple of 8 (and, where a row is a product's summation index, cols a
+ *    multiple of 8) in place; others, and fp32 ones as their three terms, are
+ *    first copied to the workspace. Norms and dropout read any in place.
  *  - An output must not overlap an input or another output, except where
  *    said.
  */
