@@ -1,4 +1,5 @@
-// Launchers of the experts' kernels (experts_route.hip), called by the host side
+// Launchers of the experts' kernels (experts_route.hip, experts_quantize.hip,
+// experts_product.hip), called by the host side
 // of the C ABI (experts_runtime.cpp). Not public.
 #pragma once
 
@@ -36,5 +37,89 @@ struct RouteArgs {
 hipError_t launch_dispatch(const RouteArgs& a, hipStream_t s);
 hipError_t launch_combine(const RouteArgs& a, hipStream_t s);
 hipError_t launch_combine_backward(const RouteArgs& a, hipStream_t s);
+
+// ------------------------------------------------------ 8-bit products
+// Values in 8 bits are e4m3, their scales exponents with a bias of 127. An
+// operand of a product has its rows along its summation index, K: bytes
+// [rows][K rounded up to 128], zero behind K. Rows of tokens come in blocks of
+// 128 that begin with each expert's first row ("padded rows"), so that a block is
+// one expert's and the scales of a token block are one expert's too.
+constexpr int kBlock = 128;
+
+// Where row (or column) i of a block of 128 has its scale: the matrix
+// instruction's operand i / 16 of a lane takes rows that make a lane's results
+// 16 consecutive columns, and a lane reads the scales of its eight rows at once.
+__host__ __device__ constexpr int scale_place(int i) { return (((i >> 4) & 3) * 4 + (i & 3)) * 8 + (i >> 6) * 4 + ((i >> 2) & 3); }
+// The row of operand f of 16 rows, row r of it.
+__host__ __device__ constexpr int operand_row(int f, int r) { return 64 * (f >> 2) + 16 * (r >> 2) + 4 * (f & 3) + (r & 3); }
+
+// The experts' rows: expert e has offsets[e] .. offsets[e + 1] of n (offsets
+// NULL: one expert has all).
+struct Groups {
+  const int32_t* offsets;
+  int32_t n, experts;
+  int32_t blocks;  // at least as many as all experts' rows take
+};
+
+// A row tile of a product: `count` rows of the result from `row`, padded rows
+// from 128 * block; expert < 0: rows behind the last expert's, whose results are 0.
+struct RowTile {
+  int32_t expert, block, row, count;
+};
+
+// 128 x 128 tiles of x in 8 bits: by rows (a scale for each row of the tile), by
+// columns (a scale for each column, values transposed), either or both.
+struct QuantizeArgs {
+  const void* x;
+  int64_t ld;
+  int32_t f32, cols, col_blocks;
+  Groups g;
+  const int32_t* source;  // padded row r of x is row source[r] / slots; NULL: r
+  uint32_t slots;
+  int32_t rows_in;        // rows of x
+  uint8_t *by_rows, *row_scales;  // [128 blocks][128 col_blocks], [col_blocks][blocks][128]
+  uint8_t *by_cols, *col_scales;  // [128 col_blocks][128 blocks], [blocks][col_blocks][128]
+  // written for the products that follow, where offsets are given
+  int32_t* first_block;   // [experts + 1]: each expert's first block
+  RowTile* tiles;         // [max_tiles]
+  int32_t* tile_count;
+  int32_t tile_blocks, max_tiles;  // blocks of a row tile
+};
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
+
+// Weights w [in][out], one scale for each tile: transposed ("forward": [out][in])
+// and as they lie ("backward": [in][out]), rows padded to 128, scale rows to 4.
+struct WeightArgs {
+  const void* w;
+  int64_t ld, expert_stride;
+  int32_t f32, experts, in, out;
+  uint8_t *forward, *forward_scales, *backward, *backward_scales;
+};
+hipError_t launch_quantize_weight(const WeightArgs& a, hipStream_t s);
+
+// C = sum over k of A[m][k] B[n][k] with their scales, on the matrix cores.
+// by_expert 0: rows of tokens against one matrix an expert (y, dx). 1: for each
+// expert, over its blocks of padded rows (dW).
+struct ProductArgs {
+  const uint8_t *a, *a_scales, *b, *b_scales;
+  int64_t pitch_a, pitch_b;        // bytes of a row
+  int64_t size_a, size_b;          // bytes; of b, one expert's
+  int64_t b_stride, b_scale_stride;  // from an expert to the next
+  int32_t a_blocks, b_blocks;      // of 128 rows: the scales' [K block][blocks][128], or b's [blocks][b_scale_pitch]
+  int32_t b_scale_pitch;
+  int32_t M, N, k_blocks;
+  int32_t by_expert, experts;
+  const int32_t* first_block;      // by_expert: K blocks of an expert; NULL: k_blocks
+  const RowTile* tiles;            // NULL: one expert, rows in order
+  const int32_t* tile_count;
+  int32_t row_tiles;               // at most
+  void* c;
+  int64_t ldc, c_stride;
+  int32_t f32;
+};
+// Rows and columns of a result tile.
+enum ProductTile { kProduct256, kProduct128 };
+constexpr int product_tile(ProductTile t) { return t == kProduct256 ? 256 : 128; }
+hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s);
 
 }  // namespace she

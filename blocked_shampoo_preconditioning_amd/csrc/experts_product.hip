@@ -1,0 +1,421 @@
+// The 8-bit products on the matrix cores: y and dx by rows of tokens against one
+// matrix an expert, dW over an expert's rows.
+//
+// Both operands lie along K, 128 values with one scale, which is what one
+// instruction of 16 x 16 x 128 takes: it multiplies by the two scales itself, so
+// the sums stay in its accumulators from the first K block to the last and no
+// other instruction touches them. bf16 results come from there. Inside, it adds
+// the products of eight k with what lies 14 bits and more below the largest of
+// them cut off, and the groups' sums in fp32 (measured on single products; 1.5e-5
+// of the terms' root sum of squares for terms of one size, whatever K). That is a
+// hundredth of what rounding to bf16 leaves, and where one term stands out, less
+// than a seventieth of what its own rounding to 8 bits does. It is too much for
+// fp32 results: those come from the bf16 instruction with both operands widened,
+// scales included, which is exact, at a quarter of the rate.
+//
+// Operands go from HBM to LDS by direct loads of 16 bytes a lane, double buffered,
+// a K block a step; the scales of a step go the same way, 256 bytes an operand. A
+// step's products are four phases (halves of A by halves of B), and each phase's
+// fragments are read while the one before multiplies, also across the barrier,
+// which sits in the middle: before it the step's last reads are done and the next
+// step has landed.
+#include <type_traits>
+#include <utility>
+
+#include "experts_kernels.h"
+#include "layer_device.h"
+
+namespace she {
+
+using shl::floatx4;
+using shl::store8;
+
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) int int4v;
+typedef __attribute__((ext_vector_type(8))) int int8v;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) const int4v* lds_int4;
+typedef __attribute__((address_space(3))) const uint32_t* lds_word;
+
+template <int N, class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0) .. f(N - 1) with constants: the instruction's scale selectors are part of it.
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+// FM x FN operands of 16 rows a wave, 2 x 2 waves.
+template <int FM_, int FN_, bool F32_, bool BBLOCK_, int WAVES_>
+struct Tile {
+  static constexpr int FM = FM_, FN = FN_, WM = 2, WN = 2, NW = 4, NT = 256;
+  static constexpr bool F32 = F32_, BBLOCK = BBLOCK_;  // BBLOCK: B's scales are those of 128 x 128 tiles
+  static constexpr int WAVES = WAVES_;                 // of a SIMD at once
+  static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  static constexpr int A_SCALES = A_BYTES + B_BYTES, B_SCALES = A_SCALES + 256;
+  static constexpr int STAGE = B_SCALES + 256;
+};
+
+// A buffer of `left` bytes from base; loads past it give zeros. 2 GiB of them are
+// enough, since a tile's offsets stay under that. Lengths are multiples of 4.
+__device__ __forceinline__ int4v make_rsrc(uint64_t base, int64_t left) {
+  int4v r;
+  r[0] = static_cast<int>(base);
+  r[1] = static_cast<int>(base >> 32);
+  r[2] = left <= 0 ? 0 : left > 0x7ffffff0 ? 0x7ffffff0 : static_cast<int>(left);
+  r[3] = 0x00020000;
+  return r;
+}
+
+// 64 x 16 or 4 bytes from rsrc + voff (a lane's own) to LDS at `lds` + plus + 16 or
+// 4 * lane; waited for at the next step's barrier. As asm because the compiler
+// would wait for every such load before any LDS read; it has no register results.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds16(const int4v& rsrc, uint32_t voff, uint32_t lds, int plus) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc), "i"(plus)
+               : "memory", "scc", "m0");
+}
+__device__ __forceinline__ void load_lds4(const int4v& rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// An operand of 16 rows: 32 of a row's 128 values a lane.
+template <bool F32>
+struct Fragment {
+  int4v lo, hi;
+};
+template <>
+struct Fragment<true> {
+  bf16x8 k[4];
+};
+
+// Four bytes in 8 bits times a scale (its exponent), exactly.
+__device__ __forceinline__ void widen(int w, float scale, bf16x8& out, int at) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+  out[at] = a[0];
+  out[at + 1] = a[1];
+  out[at + 2] = b[0];
+  out[at + 3] = b[1];
+}
+
+template <class T>
+__device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
+  constexpr bool F32 = T::F32;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::WM, wn = wave / T::WM;
+
+  // Workgroups go round the 8 XCDs; each takes a contiguous range of the tiles, in
+  // groups of four row tiles, so that those in flight on one XCD share their
+  // operands in its L2.
+  const uint32_t tn = (g.N + T::BN - 1) / T::BN;
+  const uint32_t tm = g.by_expert ? (g.M + T::BM - 1) / T::BM : g.tiles ? static_cast<uint32_t>(*g.tile_count) : static_cast<uint32_t>(g.row_tiles);
+  const uint32_t tiles = tm * tn, all = g.by_expert ? tiles * g.experts : tiles;
+  const uint32_t per = (all + 7) / 8;
+  if (blockIdx.x / 8 >= per) return;
+  uint32_t id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (id >= all) return;
+  int expert = 0;
+  if (g.by_expert) {
+    expert = static_cast<int>(id / tiles);
+    id -= expert * tiles;
+  }
+  const uint32_t group = id / (4 * tn);
+  const uint32_t in_group = min(4u, tm - 4 * group);
+  id -= group * 4 * tn;
+  const uint32_t tcol = id / in_group;
+  const int trow = static_cast<int>(4 * group + id - tcol * in_group);
+  const int n0 = static_cast<int>(tcol) * T::BN;
+
+  // the tile's rows of A and C, and its K blocks
+  int a_block, count, k0 = 0, turns = g.k_blocks;
+  int64_t c_row;
+  if (g.by_expert) {
+    a_block = trow * (T::BM / kBlock);
+    c_row = trow * T::BM;
+    count = min(T::BM, g.M - trow * T::BM);
+    if (g.first_block) {
+      k0 = g.first_block[expert];
+      turns = g.first_block[expert + 1] - k0;
+    }
+  } else if (g.tiles) {
+    const RowTile t = g.tiles[trow];
+    expert = t.expert;
+    a_block = t.block;
+    c_row = t.row;
+    count = t.count;
+    if (expert < 0) expert = 0, turns = 0;
+  } else {
+    a_block = trow * (T::BM / kBlock);
+    c_row = trow * T::BM;
+    count = min(T::BM, g.M - trow * T::BM);
+  }
+
+  // A load instruction covers eight rows of 128 bytes: row (instruction * 4 + wave)
+  // * 8 + lane / 8, place lane % 8. A row's chunk c of 16 bytes sits at place c ^
+  // swizzle, so that the rows that one read takes together (row r of an operand,
+  // which operand_row sends to row (r & 3) + 16 (r >> 2) + ..) fall on different
+  // banks.
+  auto swizzle = [](int r16) { return (r16 & 7) ^ ((r16 >> 3) & 1); };
+  constexpr int NA = T::BM / 32, NB = T::BN / 32;
+  uint32_t va[NA], vb[NB];
+  auto row_off = [&](int j, int64_t pitch) {
+    const int row = (j * 4 + wave) * 8 + (lane >> 3);
+    const int r16 = (row & 3) | ((row >> 4) & 3) << 2;
+    return static_cast<uint32_t>(row * pitch + (((lane & 7) ^ swizzle(r16)) << 4));
+  };
+#pragma unroll
+  for (int j = 0; j < NA; ++j) va[j] = row_off(j, g.pitch_a);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) vb[j] = row_off(j, g.pitch_b);
+  const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
+
+  const int64_t a_at = static_cast<int64_t>(a_block) * kBlock * g.pitch_a + static_cast<int64_t>(k0) * kBlock;
+  const int64_t b_at = n0 * g.pitch_b + static_cast<int64_t>(k0) * kBlock;
+  uint64_t pa = reinterpret_cast<uint64_t>(g.a) + a_at;
+  uint64_t pb = reinterpret_cast<uint64_t>(g.b) + (g.by_expert ? 0 : expert * g.b_stride) + b_at;
+  int64_t left_a = g.size_a - a_at, left_b = g.size_b - b_at;
+  // scales: a wave takes A's (even) or B's, by 4 bytes a lane
+  const bool b_scales = wave & 1;
+  const int sa_row = a_block * kBlock;
+  int kb = k0;  // K block of the next step to load
+  const int64_t scale_step = static_cast<int64_t>(b_scales ? g.b_blocks : g.a_blocks) * kBlock;
+  const uint64_t scales = reinterpret_cast<uint64_t>(b_scales ? g.b_scales + (T::BBLOCK ? expert * g.b_scale_stride : n0) : g.a_scales + sa_row);
+  const int64_t scales_size = b_scales ? (T::BBLOCK ? static_cast<int64_t>(g.b_blocks) * g.b_scale_pitch : g.k_blocks * scale_step - n0)
+                                       : g.k_blocks * scale_step - sa_row;
+  const uint32_t block_row = min(n0 / kBlock + (lane >> 5), g.b_blocks - 1);  // BBLOCK: each half of a wave its 128 columns
+  const uint32_t vs = T::BBLOCK && b_scales ? block_row * g.b_scale_pitch : lane * 4;
+
+  int loads = turns;  // steps still to be loaded
+  int4v ra, rb, rs;
+  uint32_t at = 0;
+  auto aim = [&](int buf) {
+    at = lds_base + buf * T::STAGE;
+    // past the last step nothing is read: the buffer gets zeros
+    ra = make_rsrc(pa, loads > 0 ? left_a : 0);
+    rb = make_rsrc(pb, loads > 0 ? left_b : 0);
+    const int64_t down = T::BBLOCK && b_scales ? kb & ~3 : kb * scale_step;
+    rs = make_rsrc(scales + down, loads > 0 ? scales_size - down : 0);
+  };
+  auto load = [&](int q) {
+    if (q < NA)
+      load_lds16(ra, va[q], at + wave * 1024, q * 4096);
+    else if (q < NA + NB)
+      load_lds16(rb, vb[q - NA], at + wave * 1024, T::A_BYTES + (q - NA) * 4096);
+    else
+      load_lds4(rs, vs, at + (b_scales ? T::B_SCALES : T::A_SCALES));
+  };
+  constexpr int kLoads = NA + NB + 1;
+  auto advance = [&]() {
+    --loads;
+    ++kb;
+    pa += kBlock, pb += kBlock;
+    left_a -= kBlock, left_b -= kBlock;
+  };
+
+  // A lane's places in the reads: row r16 of an operand, chunks q4 and q4 + 4.
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const uint32_t chunk = (q4 ^ swizzle(r16)) << 4;
+  const int lane_row = 16 * (r16 >> 2) + (r16 & 3);
+  uint32_t fa = lds_base + (wm * T::FM * 16 + lane_row) * 128 + chunk;
+  uint32_t fb = lds_base + T::A_BYTES + (wn * T::FN * 16 + lane_row) * 128 + chunk;
+  uint32_t fsa = lds_base + T::A_SCALES + (wm * T::FM * 16 & ~127) + r16 * 8 + (T::FM == 4 ? (wm & 1) * 4 : 0);
+  uint32_t fsb = lds_base + T::B_SCALES + (T::BBLOCK ? (wn * T::FN * 16 & ~127) : (wn * T::FN * 16 & ~127) + r16 * 8 + (T::FN == 4 ? (wn & 1) * 4 : 0));
+  uint32_t flip = T::STAGE;
+  auto other_buffer = [&]() {
+    fa += flip, fb += flip, fsa += flip, fsb += flip;
+    flip = 0u - flip;
+  };
+
+  // scales of the step that is multiplied: operand f's in byte f % 4 of word f / 4
+  constexpr int SA = T::FM / 4, SB = T::BBLOCK ? 1 : T::FN / 4;
+  uint32_t sa[SA], sb[SB], sa2[SA], sb2[SB];
+  int kc = k0;  // its K block
+  auto read_scales = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < SA; ++i) sa2[i] = *reinterpret_cast<lds_word>(fsa + 4 * i);
+#pragma unroll
+    for (int i = 0; i < SB; ++i) sb2[i] = *reinterpret_cast<lds_word>(fsb + 4 * i);
+    if (T::BBLOCK) sb2[0] >>= (k & 3) * 8;
+  };
+  auto use_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < SA; ++i) sa[i] = sa2[i];
+#pragma unroll
+    for (int i = 0; i < SB; ++i) sb[i] = sb2[i];
+  };
+  auto scale_a = [&](int i) { return __uint_as_float((sa2[i >> 2] >> (8 * (i & 3)) & 255u) << 23); };
+  auto scale_b = [&](int j) { return __uint_as_float((T::BBLOCK ? sb2[0] & 255u : sb2[T::BBLOCK ? 0 : j >> 2] >> (8 * (j & 3)) & 255u) << 23); };
+  auto fetch = [&](uint32_t base, int f, float scale) {
+    const uint32_t from = base + (64 * (f >> 2) + 4 * (f & 3)) * 128;
+    const int4v lo = *reinterpret_cast<lds_int4>(from), hi = *reinterpret_cast<lds_int4>(from ^ 64u);
+    Fragment<F32> x;
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        widen(i < 2 ? lo[2 * i] : hi[2 * i - 4], scale, x.k[i], 0);
+        widen(i < 2 ? lo[2 * i + 1] : hi[2 * i - 3], scale, x.k[i], 4);
+      }
+    } else {
+      x.lo = lo;
+      x.hi = hi;
+    }
+    return x;
+  };
+
+  floatx4 acc[T::FM][T::FN];
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  constexpr int HA = T::FM / 2, HB = T::FN / 2, kMma = HA * HB;
+  Fragment<F32> a0[HA], a1[HA], b0[HB], b1[HB];
+  auto product = [&](auto i_, auto j_, const Fragment<F32>& x, const Fragment<F32>& y) {
+    constexpr int i = decltype(i_)::value, j = decltype(j_)::value;
+    if constexpr (F32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.k[k], x.k[k], acc[i][j], 0, 0, 0);
+    } else {
+      const int8v av = __builtin_shufflevector(x.lo, x.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const int8v bv = __builtin_shufflevector(y.lo, y.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[i][j], 0, 0, T::BBLOCK ? 0 : j & 3,
+                                                                   static_cast<int>(sb[T::BBLOCK ? 0 : j >> 2]), i & 3, static_cast<int>(sa[i >> 2]));
+    }
+  };
+  // One phase: products of half IH of A and half JH of B, with more(q) behind the q-th.
+  auto phase = [&](auto ih, auto jh, const Fragment<F32>(&x)[HA], const Fragment<F32>(&y)[HB], auto&& more) {
+    each<kMma>([&](auto q) {
+      constexpr int Q = decltype(q)::value, i = Q / HB, j = Q % HB;
+      product(std::integral_constant<int, decltype(ih)::value * HA + i>{}, std::integral_constant<int, decltype(jh)::value * HB + j>{}, x[i], y[j]);
+      more(Q);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  const std::integral_constant<int, 0> first{};
+  const std::integral_constant<int, 1> second{};
+
+  if (turns > 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      aim(i);
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) load(q);
+      advance();
+    }
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    read_scales(kc);
+#pragma unroll
+    for (int i = 0; i < HA; ++i) a0[i] = fetch(fa, i, F32 ? scale_a(i) : 0.f);
+#pragma unroll
+    for (int j = 0; j < HB; ++j) b0[j] = fetch(fb, j, F32 ? scale_b(j) : 0.f);
+    use_scales();
+    __builtin_amdgcn_sched_barrier(0);
+    int buf = 0;
+    for (int turn = 0; turn < turns; ++turn) {
+      aim(buf);
+      buf ^= 1;
+      phase(first, first, a0, b0, [&](int q) {
+        if (q < HB) b1[q] = fetch(fb, HB + q, F32 ? scale_b(HB + q) : 0.f);
+      });
+      phase(first, second, a0, b1, [&](int q) {
+        if (q < HA) a1[q] = fetch(fa, HA + q, F32 ? scale_a(HA + q) : 0.f);
+      });
+      other_buffer();
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // the next step's first fragments, and the loads of the one after it
+      constexpr int kEach = (kLoads + 2 * kMma - 1) / (2 * kMma);
+      auto loads_at = [&](int q) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+          if (q * kEach + e < kLoads) load(q * kEach + e);
+      };
+      ++kc;
+      read_scales(kc);
+      phase(second, first, a1, b0, [&](int q) {
+        if (q < HA) a0[q] = fetch(fa, q, F32 ? scale_a(q) : 0.f);
+        loads_at(q);
+      });
+      phase(second, second, a1, b1, [&](int q) {
+        if (q < HB) b0[q] = fetch(fb, q, F32 ? scale_b(q) : 0.f);
+        loads_at(kMma + q);
+      });
+      use_scales();
+      advance();
+    }
+    // the last loads (zeros) have landed: LDS is free
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  // A lane's accumulators of four operands of B are 16 consecutive columns of a row.
+  char* c = static_cast<char*>(g.c) + (g.by_expert ? expert * g.c_stride * (F32 ? 4 : 2) : 0);
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int row = wm * T::FM * 16 + 64 * (i >> 2) + 4 * (i & 3) + lane_row;
+    if (row >= count) continue;
+#pragma unroll
+    for (int J = 0; J < T::FN / 4; ++J) {
+      const int col = n0 + wn * T::FN * 16 + 64 * J + 16 * q4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = acc[i][4 * J + 2 * h + q / 4][q % 4];
+        const int n = min(8, g.N - col - 8 * h);
+        if (n > 0) store8(c, (c_row + row) * g.ldc + col + 8 * h, n, F32, v);
+      }
+    }
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(ProductArgs g) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
+  product_tile<T>(g, lds);
+}
+
+template <class T>
+void start(const ProductArgs& a, hipStream_t s) {
+  const int64_t tn = (a.N + T::BN - 1) / T::BN;
+  const int64_t tm = a.by_expert ? static_cast<int64_t>((a.M + T::BM - 1) / T::BM) * a.experts : a.row_tiles;
+  const uint32_t grid = static_cast<uint32_t>((tm * tn + 7) / 8 * 8);
+  if (grid) product_kernel<T><<<grid, T::NT, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s) {
+  if (a.f32) {
+    if (a.by_expert)
+      start<Tile<4, 4, true, false, 2>>(a, s);
+    else
+      start<Tile<4, 4, true, true, 2>>(a, s);
+  } else if (tile == kProduct256) {
+    if (a.by_expert)
+      start<Tile<8, 8, false, false, 1>>(a, s);
+    else
+      start<Tile<8, 8, false, true, 1>>(a, s);
+  } else {
+    if (a.by_expert)
+      start<Tile<4, 4, false, false, 2>>(a, s);
+    else
+      start<Tile<4, 4, false, true, 2>>(a, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace she

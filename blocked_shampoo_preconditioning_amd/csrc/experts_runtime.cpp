@@ -112,6 +112,239 @@ int route(const shampoo_route_t* a, Route what, const char* name, void* hip_stre
   return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, name);
 }
 
+// -------------------------------------------------------- products in 8 bits
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 18);  // padded rows of 1024 experts stay in 32 bits
+
+int64_t blocks_of(int64_t n) { return (n + she::kBlock - 1) / she::kBlock; }
+
+int check_sizes(int64_t in, int64_t out, int32_t experts, int32_t dtype) {
+  if (in < 1 || in > kMaxWidth || out < 1 || out > kMaxWidth) return invalid("in and out must be in [1, 2^21]");
+  if (experts < 1 || experts > 1024) return invalid("experts must be in [1, 1024]");
+  return check_dtype(dtype);
+}
+
+int check_aligned(const char* name, const void* p, int64_t a) {
+  if (!p) return invalid(std::string(name) + " is NULL");
+  if (!aligned(p, a)) return fail(SHAMPOO_ERR_MISALIGNED, std::string(name) + " is not aligned to " + std::to_string(a) + " bytes");
+  return SHAMPOO_OK;
+}
+
+int check_matrices(const char* name, const void* p, int64_t experts, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int64_t esize) {
+  RC(check_array(name, p, rows, cols, ld, esize));
+  if (experts > 1 && (stride < (rows - 1) * ld + cols || stride > kAnyLd))
+    return invalid(std::string(name) + ": matrices overlap, or lie over 2^40 elements apart");
+  return SHAMPOO_OK;
+}
+
+int check_product(const shampoo_product8_t* a) {
+  if (!a) return invalid("arguments are NULL");
+  if (a->rows < 0 || a->rows > kMaxRows) return invalid("rows must be in [0, 2^31 - 2^18]");
+  RC(check_sizes(a->in, a->out, a->experts, a->dtype));
+  if (!a->offsets && a->experts > 1) return invalid("offsets is NULL: with several experts it says which rows are whose");
+  if (a->offsets) RC(check_aligned("offsets", a->offsets, 4));
+  if (a->source) {
+    if (!a->offsets) return invalid("source is given without offsets");
+    RC(check_aligned("source", a->source, 4));
+    if (a->slots < 1 || a->slots > 1024) return invalid("slots must be in [1, 1024]");
+    if (a->x_rows < (a->rows > 0 ? 1 : 0) || a->x_rows > kMaxTotal) return invalid("x_rows must be in [1, 2^31 - 1024]");
+  }
+  return SHAMPOO_OK;
+}
+
+// Blocks of 128 padded rows that all experts' rows can take.
+int64_t row_blocks(const shampoo_product8_t* a) {
+  if (!a->offsets) return blocks_of(a->rows);
+  const int64_t e = a->experts < a->rows ? a->experts : a->rows;
+  return (a->rows + (she::kBlock - 1) * e) / she::kBlock;
+}
+
+// The most row tiles there can be, rows behind the last expert's among them.
+int64_t row_tiles(const shampoo_product8_t* a, int64_t height) {
+  if (!a->offsets) return (a->rows + height - 1) / height;
+  const int64_t e = a->experts < a->rows ? a->experts : a->rows;
+  return (a->rows + (height - 1) * (e + 1)) / height;
+}
+
+// Tiles of 256 where they fill most of the card.
+she::ProductTile choose_tile(const shampoo_product8_t* a, bool by_expert, int64_t m, int64_t n) {
+  if (a->dtype == SHAMPOO_F32) return she::kProduct128;
+  const int64_t tm = by_expert ? (m + 255) / 256 * a->experts : row_tiles(a, 256);
+  return tm * ((n + 255) / 256) >= 200 ? she::kProduct256 : she::kProduct128;
+}
+
+// Quantized operands by rows and by columns, and the tables beside them.
+struct ProductPlan {
+  int64_t blocks = 0;
+  shp_rt::Carver ws;
+  int64_t by_rows = -1, row_scales = -1, by_cols = -1, col_scales = -1, first_block = -1, tiles = -1, tile_count = -1;
+  she::ProductTile tile = she::kProduct128;
+  int64_t max_tiles = 0;
+};
+
+size_t saved_size(const shampoo_product8_t* a) {
+  shp_rt::Carver c;
+  const int64_t nb = row_blocks(a), ib = blocks_of(a->in);
+  if (nb == 0) return 0;
+  c.take(nb * ib * she::kBlock * she::kBlock);
+  c.take(nb * ib * she::kBlock);
+  return static_cast<size_t>(c.o);
+}
+
+ProductPlan plan_product(const shampoo_product8_t* a, bool backward) {
+  ProductPlan p;
+  p.blocks = row_blocks(a);
+  if (p.blocks == 0) return p;
+  const int64_t k = backward ? a->out : a->in, n = backward ? a->in : a->out;
+  const int64_t kb = blocks_of(k), bytes = p.blocks * kb * she::kBlock * she::kBlock;
+  const bool rows = !backward || a->dx, cols = backward && a->dw;
+  if (rows) {
+    p.by_rows = p.ws.take(bytes);
+    p.row_scales = p.ws.take(bytes / she::kBlock);
+    p.tile = choose_tile(a, false, a->rows, n);
+    p.max_tiles = row_tiles(a, she::product_tile(p.tile));
+  }
+  if (cols) {
+    p.by_cols = p.ws.take(bytes);
+    p.col_scales = p.ws.take(bytes / she::kBlock);
+  }
+  if (a->offsets) {
+    p.first_block = p.ws.take(4 * (a->experts + 1));
+    if (rows) {
+      p.tiles = p.ws.take(p.max_tiles * static_cast<int64_t>(sizeof(she::RowTile)));
+      p.tile_count = p.ws.take(4);
+    }
+  }
+  return p;
+}
+
+template <class T>
+T* in_ws(void* ws, int64_t off) {
+  return off < 0 ? nullptr : reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+she::QuantizeArgs quantize_args(const shampoo_product8_t* a, const ProductPlan& p, void* ws, const void* x, int64_t ld, int64_t cols) {
+  she::QuantizeArgs q{};
+  q.x = x;
+  q.ld = ld;
+  q.f32 = a->dtype == SHAMPOO_F32;
+  q.cols = static_cast<int32_t>(cols);
+  q.col_blocks = static_cast<int32_t>(blocks_of(cols));
+  q.g = she::Groups{a->offsets, static_cast<int32_t>(a->rows), a->experts, static_cast<int32_t>(p.blocks)};
+  q.by_rows = in_ws<uint8_t>(ws, p.by_rows);
+  q.row_scales = in_ws<uint8_t>(ws, p.row_scales);
+  q.by_cols = in_ws<uint8_t>(ws, p.by_cols);
+  q.col_scales = in_ws<uint8_t>(ws, p.col_scales);
+  q.first_block = in_ws<int32_t>(ws, p.first_block);
+  q.tiles = in_ws<she::RowTile>(ws, p.tiles);
+  q.tile_count = in_ws<int32_t>(ws, p.tile_count);
+  q.tile_blocks = she::product_tile(p.tile) / she::kBlock;
+  q.max_tiles = static_cast<int32_t>(p.max_tiles);
+  return q;
+}
+
+// y or dx: rows of tokens, quantized by rows into the workspace, against the weights.
+she::ProductArgs row_product(const shampoo_product8_t* a, const ProductPlan& p, void* ws, const void* values, const void* scales, int64_t k,
+                             int64_t n, void* c, int64_t ldc) {
+  const int64_t kb = blocks_of(k), nb = blocks_of(n), pitch = kb * she::kBlock, scale_pitch = (kb + 3) / 4 * 4;
+  she::ProductArgs g{};
+  g.a = in_ws<uint8_t>(ws, p.by_rows);
+  g.a_scales = in_ws<uint8_t>(ws, p.row_scales);
+  g.b = static_cast<const uint8_t*>(values);
+  g.b_scales = static_cast<const uint8_t*>(scales);
+  g.pitch_a = g.pitch_b = pitch;
+  g.size_a = p.blocks * she::kBlock * pitch;
+  g.size_b = g.b_stride = n * pitch;
+  g.b_scale_stride = nb * scale_pitch;
+  g.a_blocks = static_cast<int32_t>(p.blocks);
+  g.b_blocks = static_cast<int32_t>(nb);
+  g.b_scale_pitch = static_cast<int32_t>(scale_pitch);
+  g.M = static_cast<int32_t>(a->rows);
+  g.N = static_cast<int32_t>(n);
+  g.k_blocks = static_cast<int32_t>(kb);
+  g.experts = a->experts;
+  g.tiles = in_ws<she::RowTile>(ws, p.tiles);
+  g.tile_count = in_ws<int32_t>(ws, p.tile_count);
+  g.row_tiles = static_cast<int32_t>(p.max_tiles);
+  g.c = c;
+  g.ldc = ldc;
+  g.f32 = a->dtype == SHAMPOO_F32;
+  return g;
+}
+
+int forward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t s) {
+  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+  RC(check_aligned("values", a->values, 16));
+  RC(check_aligned("scales", a->scales, 4));
+  RC(check_array("x", a->x, a->source ? a->x_rows : a->rows, a->in, a->ld_x, e));
+  RC(check_array("y", a->y, a->rows, a->out, a->ld_y, e));
+  if (a->saved && !aligned(a->saved, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "saved is not aligned to 256 bytes");
+  const ProductPlan p = plan_product(a, false);
+  RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
+  if (a->rows == 0) return SHAMPOO_OK;
+  she::QuantizeArgs q = quantize_args(a, p, ws, a->x, a->ld_x, a->in);
+  q.source = a->source;
+  q.slots = static_cast<uint32_t>(a->source ? a->slots : 1);
+  q.rows_in = static_cast<int32_t>(a->source ? a->x_rows : a->rows);
+  if (a->saved) {
+    q.by_cols = static_cast<uint8_t*>(a->saved);
+    q.col_scales = q.by_cols + shp_rt::align_up(p.blocks * q.col_blocks * she::kBlock * she::kBlock);
+  }
+  hipError_t err = she::launch_quantize(q, s);
+  if (err == hipSuccess) err = she::launch_product(row_product(a, p, ws, a->values, a->scales, a->in, a->out, a->y, a->ld_y), p.tile, s);
+  return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, "shampoo_product8_forward");
+}
+
+int backward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t s) {
+  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+  if (!a->dx && !a->dw) return SHAMPOO_OK;
+  RC(check_array("dy", a->dy, a->rows, a->out, a->ld_dy, e));
+  if (a->dx) {
+    RC(check_aligned("back_values", a->back_values, 16));
+    RC(check_aligned("back_scales", a->back_scales, 4));
+    RC(check_array("dx", a->dx, a->rows, a->in, a->ld_dx, e));
+  }
+  if (a->dw) {
+    if (a->rows > 0) RC(check_aligned("saved", a->saved, 256));
+    RC(check_matrices("dw", a->dw, a->experts, a->in, a->out, a->ld_dw, a->stride_dw, e));
+  }
+  const ProductPlan p = plan_product(a, true);
+  RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
+  hipError_t err = hipSuccess;
+  if (p.blocks > 0) {
+    she::QuantizeArgs q = quantize_args(a, p, ws, a->dy, a->ld_dy, a->out);
+    q.slots = 1;
+    q.rows_in = static_cast<int32_t>(a->rows);
+    err = she::launch_quantize(q, s);
+    if (err == hipSuccess && a->dx)
+      err = she::launch_product(row_product(a, p, ws, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx), p.tile, s);
+  }
+  if (err == hipSuccess && a->dw) {
+    const int64_t ib = blocks_of(a->in), ob = blocks_of(a->out), pitch = p.blocks * she::kBlock;
+    she::ProductArgs g{};
+    g.a = static_cast<const uint8_t*>(a->saved);
+    g.a_scales = g.a + shp_rt::align_up(ib * she::kBlock * pitch);
+    g.b = in_ws<uint8_t>(ws, p.by_cols);
+    g.b_scales = in_ws<uint8_t>(ws, p.col_scales);
+    g.pitch_a = g.pitch_b = pitch;
+    g.size_a = ib * she::kBlock * pitch;
+    g.size_b = ob * she::kBlock * pitch;
+    g.a_blocks = static_cast<int32_t>(ib);
+    g.b_blocks = static_cast<int32_t>(ob);
+    g.M = static_cast<int32_t>(a->in);
+    g.N = static_cast<int32_t>(a->out);
+    g.k_blocks = static_cast<int32_t>(p.blocks);
+    g.by_expert = 1;
+    g.experts = a->experts;
+    g.first_block = p.blocks > 0 ? in_ws<int32_t>(ws, p.first_block) : nullptr;
+    g.c = a->dw;
+    g.ldc = a->ld_dw;
+    g.c_stride = a->stride_dw;
+    g.f32 = a->dtype == SHAMPOO_F32;
+    err = she::launch_product(g, choose_tile(a, true, a->in, a->out), s);
+  }
+  return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, "shampoo_product8_backward");
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,6 +385,57 @@ int shampoo_combine(const shampoo_route_t* a, void* hip_stream) {
 
 int shampoo_combine_backward(const shampoo_route_t* a, void* hip_stream) {
   return guarded([&] { return route(a, kCombineBackward, "shampoo_combine_backward", hip_stream); });
+}
+
+int shampoo_quantize_weight(const shampoo_weight8_t* a, void* hip_stream) {
+  return guarded([&]() -> int {
+    if (!a) return invalid("arguments are NULL");
+    RC(check_sizes(a->in, a->out, a->experts, a->dtype));
+    RC(check_matrices("w", a->w, a->experts, a->in, a->out, a->ld_w, a->stride_w, a->dtype == SHAMPOO_F32 ? 4 : 2));
+    RC(check_aligned("values", a->values, 16));
+    RC(check_aligned("scales", a->scales, 4));
+    if (a->back_values || a->back_scales) {
+      RC(check_aligned("back_values", a->back_values, 16));
+      RC(check_aligned("back_scales", a->back_scales, 4));
+    }
+    const she::WeightArgs k{a->w, a->ld_w, a->stride_w, a->dtype == SHAMPOO_F32 ? 1 : 0, a->experts, static_cast<int32_t>(a->in),
+                            static_cast<int32_t>(a->out), static_cast<uint8_t*>(a->values), static_cast<uint8_t*>(a->scales),
+                            static_cast<uint8_t*>(a->back_values), static_cast<uint8_t*>(a->back_scales)};
+    const hipError_t e = she::launch_quantize_weight(k, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_quantize_weight");
+  });
+}
+
+int shampoo_product8_saved_size(const shampoo_product8_t* a, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    RC(check_product(a));
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    *bytes_out = saved_size(a);
+    return SHAMPOO_OK;
+  });
+}
+
+int shampoo_product8_workspace_size(const shampoo_product8_t* a, int32_t backward, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    RC(check_product(a));
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    *bytes_out = static_cast<size_t>(plan_product(a, backward != 0).ws.o);
+    return SHAMPOO_OK;
+  });
+}
+
+int shampoo_product8_forward(const shampoo_product8_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    RC(check_product(a));
+    return forward(a, workspace, workspace_bytes, static_cast<hipStream_t>(hip_stream));
+  });
+}
+
+int shampoo_product8_backward(const shampoo_product8_t* a, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    RC(check_product(a));
+    return backward(a, workspace, workspace_bytes, static_cast<hipStream_t>(hip_stream));
+  });
 }
 
 }  // extern "C"

@@ -1,11 +1,12 @@
 """The experts' path of a feed-forward block, forward and backward, on the
-library's own kernels: tokens sorted by expert and back, with weights applied
-(the C ABI in include/shampoo_experts.h).
+library's own kernels: tokens sorted by expert and back, with weights applied,
+and matrix products in 8-bit floating point with a scale for each block of 128,
+dense or one matrix an expert (the C ABI in include/shampoo_experts.h).
 
-    plan = experts.sort_tokens(ids, n_experts)       # ids [tokens, slots]: each token's experts
-    xs = experts.dispatch(x, plan)                   # rows by expert
-    ...                                              # each expert's matrices on its rows of xs: ys
-    y = experts.combine(ys, plan, weights)           # back, with the router's weights
+    w8 = experts.quantize_weight(w)                                # w [n_experts, in, out], once
+    plan = experts.sort_tokens(ids, n_experts)                     # ids [tokens, slots]: each token's experts
+    ys = experts.product8_forward(x, w8, plan, gather=True)        # each expert's matrix on its tokens
+    y = experts.combine(ys, plan, weights)                         # back, with the router's weights
 
 Tensors are as `layer` takes them: 2-D CUDA tensors of float32 or bfloat16 with
 contiguous rows (any row stride). Every call runs on torch's current stream,
@@ -23,9 +24,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import layer as _layer
 from . import shampoo as _s
-from .layer import _first, _matrix, _raw_stream, _unlike, _workspace
+from .layer import _first, _matrix, _raw_stream, _workspace
 from .shampoo import HEADER_PATH as _CORE_HEADER
 
 EXPERTS_HEADER_PATH = os.path.join(os.path.dirname(_CORE_HEADER), "shampoo_experts.h")
@@ -34,6 +34,8 @@ MAX_EXPERTS = 1024
 # The C argument structs, field by field (native sizes and alignment), as in `layer`.
 _SORT = struct.Struct("@q iii P q PPP")
 _ROUTE = struct.Struct("@qq ii PP PP qq PP qq P")
+_WEIGHT = struct.Struct("@qq ii P qq PPPP")
+_PRODUCT = struct.Struct("@qqq ii PP q i PPPP P q P q P P q P q P qq")
 
 _A, _SIZE = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
 _SIGNATURES = {
@@ -42,6 +44,11 @@ _SIGNATURES = {
     "shampoo_dispatch": [_A, ctypes.c_void_p],
     "shampoo_combine": [_A, ctypes.c_void_p],
     "shampoo_combine_backward": [_A, ctypes.c_void_p],
+    "shampoo_quantize_weight": [_A, ctypes.c_void_p],
+    "shampoo_product8_saved_size": [_A, _SIZE],
+    "shampoo_product8_workspace_size": [_A, ctypes.c_int32, _SIZE],
+    "shampoo_product8_forward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "shampoo_product8_backward": [_A, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
 }
 _lib = None
 
@@ -189,3 +196,165 @@ def combine_backward(dy, ys, plan, weights=None):
     _call("shampoo_combine_backward", _ROUTE.pack(tokens, d, slots, dt, rows, pw, pdy, pys, ldy, lys, 0, dys.data_ptr(), 0, d, dweights.data_ptr()),
           dy.get_device())
     return dys, dweights
+
+
+# --------------------------------------------------------- products in 8 bits
+class Weight8(NamedTuple):
+    """8-bit weights of one [n_in, n_out] matrix, or of one for each expert (a leading dimension more), as
+    `quantize_weight` returns them; a program may make them itself from values and scales that it has.
+    values float8_e4m3fn [n_out, n_in rounded up to 128]: the transposed matrix over its scales, 0 behind n_in.
+    scales float8_e8m0fnu [n_out / 128, n_in / 128], both rounded up, then the latter up to a multiple of 4: a
+    power of two (2^-126 .. 2^127) for each block of 128 x 128.
+    back_values, back_scales: the same with in and out exchanged, for `product8_backward`'s dx (or None)."""
+    values: torch.Tensor
+    scales: torch.Tensor
+    n_in: int
+    n_out: int
+    back_values: torch.Tensor | None = None
+    back_scales: torch.Tensor | None = None
+
+
+_MAX_DIM = 1 << 21
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _weight_shapes(lead, n_in, n_out):
+    return (*lead, n_out, _blocks(n_in) * 128), (*lead, _blocks(n_out), (_blocks(n_in) + 3) // 4 * 4)
+
+
+def quantize_weight(w, backward=False):
+    """`Weight8` of w [in, out], or [n_experts, in, out] (contiguous rows; rows and matrices any distance apart):
+    every block of 128 x 128 over the smallest power of two that brings it to 448 at most, rounded to e4m3.
+    backward: also as dx needs it."""
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise ValueError("w must be a CUDA tensor")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [in, out] or [experts, in, out], got shape {tuple(w.shape)}")
+    flat = w if w.dim() == 3 else w[None]
+    n_experts, n_in, n_out = flat.shape
+    if not (1 <= n_experts <= MAX_EXPERTS and 1 <= n_in <= _MAX_DIM and 1 <= n_out <= _MAX_DIM):
+        raise ValueError(f"w has shape {tuple(w.shape)}: up to {MAX_EXPERTS} matrices of 1 to 2^21 rows and columns are supported")
+    dt, _, _ = _first("w", flat[0])
+    ptr, ld = _matrix("w", flat[0], n_in, n_out, w)
+    stride = flat.stride(0) if n_experts > 1 else n_in * ld
+    lead = w.shape[:-2]
+    made = []
+    for rows, cols in ((n_in, n_out), (n_out, n_in)) if backward else ((n_in, n_out),):
+        values, scales = _weight_shapes(lead, rows, cols)
+        made.append(torch.empty(values, dtype=torch.float8_e4m3fn, device=w.device))
+        made.append(torch.empty(scales, dtype=torch.float8_e8m0fnu, device=w.device))
+    pointers = [t.data_ptr() for t in made] + [0, 0] * (not backward)
+    _call("shampoo_quantize_weight", _WEIGHT.pack(n_in, n_out, n_experts, dt, ptr, ld, stride, *pointers), w.get_device())
+    return Weight8(made[0], made[1], n_in, n_out, *made[2:])
+
+
+def _weight_pointers(name, values, scales, lead, n_in, n_out, like):
+    for t, dtype, shape, what in zip((values, scales), (torch.float8_e4m3fn, torch.float8_e8m0fnu), _weight_shapes(lead, n_in, n_out),
+                                     ("values", "scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != like.get_device():
+            raise ValueError(f"{name}{what} must be a {dtype} tensor on {like.device}")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}{what} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return values.data_ptr(), scales.data_ptr()
+
+
+def _product_head(t, name, w8, plan):
+    """(leading dimensions of the weights, experts, dtype code, pointer of offsets)."""
+    lead = w8.values.shape[:-2]
+    n_experts = lead[0] if lead else 1
+    dt = _first(name, t)[0]
+    if plan is None:
+        if lead:
+            raise ValueError("plan is None: with a matrix for each expert it says which rows are whose")
+        return lead, n_experts, dt, 0
+    offsets = plan.offsets
+    if offsets.dtype is not torch.int32 or offsets.get_device() != t.get_device() or not offsets.is_contiguous():
+        raise ValueError("plan.offsets must be a contiguous int32 tensor on the call's device")
+    if offsets.shape != (n_experts + 1,):
+        raise ValueError(f"plan.offsets has shape {tuple(offsets.shape)}, expected ({n_experts + 1},)")
+    return lead, n_experts, dt, offsets.data_ptr()
+
+
+def product8_forward(x, w8, plan=None, gather=False, save=False):
+    """y = Q(x) W for x [rows, in] and the 8-bit weights W of `w8`, where Q rounds every 128 columns of a row to
+    e4m3 over their own power of two. With a plan, rows are those of `dispatch` and meet their expert's
+    matrix; with `gather` x has a row for each token, and the product takes them by plan.source itself. y [rows,
+    out]; rows behind the last expert's are 0. With `save` returns (y, saved), saved being what
+    `product8_backward` needs for dw (an opaque tensor: x in 8 bits by 128 rows of a column)."""
+    n_in, n_out = w8.n_in, w8.n_out
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D (rows, width), got shape {tuple(x.shape)}")
+    x_rows, source, slots, rows = x.shape[0], 0, 1, x.shape[0]
+    if gather:
+        if plan is None:
+            raise ValueError("gather needs a plan")
+        _, x_rows, slots = _plan_rows(plan, x)
+        rows = x_rows * slots
+        if plan.source.dtype is not torch.int32 or plan.source.get_device() != x.get_device() or plan.source.shape != (rows,) or \
+                not plan.source.is_contiguous():
+            raise ValueError(f"plan.source must be a contiguous int32 tensor of {rows} elements on the call's device")
+        source = plan.source.data_ptr()
+    elif plan is not None:
+        _, tokens, slots = _plan_rows(plan, x)
+        x_rows = rows = tokens * slots
+    lead, n_experts, dt, offsets = _product_head(x, "x", w8, plan)
+    px, lx = _matrix("x", x, x_rows, n_in, x)
+    values, scales = _weight_pointers("w8.", w8.values, w8.scales, lead, n_in, n_out, x)
+    y = x.new_empty((rows, n_out))
+    head = (rows, n_in, n_out, n_experts, dt, offsets, source, x_rows, slots or 1)
+    key = (rows, n_in, n_out, n_experts, dt, plan is None)
+    saved = None
+    if save:
+        size = _known_size(("saved", key), "shampoo_product8_saved_size", _PRODUCT.pack(*head, *_NO_PRODUCT))
+        saved = torch.empty(size, dtype=torch.uint8, device=x.device)
+    args = _PRODUCT.pack(*head, values, scales, 0, 0, px, lx, y.data_ptr(), n_out, saved.data_ptr() if save else 0, 0, 0, 0, 0, 0, 0, 0)
+    size = _known_size(("forward", key), "shampoo_product8_workspace_size", args, 0)
+    ws, keep = _workspace(size, x)
+    _call("shampoo_product8_forward", args, x.get_device(), ws, size)
+    return (y, saved) if save else y
+
+
+_NO_PRODUCT = (0,) * 16
+
+
+def product8_backward(dy, w8, saved, plan=None, need_dx=True, need_dw=True):
+    """(dx, dw) from dy [rows, out], the forward pass's w8 and plan and what it saved: dx = Q(dy) W^T by rows, [rows,
+    in] (with a plan in sorted order: `dispatch_backward` takes it to the tokens), and dw = Q(x)^T Q(dy) with both by
+    128 rows of a column, in w's shape and dy's dtype. The roundings of x, W and dy themselves have gradient 1.
+    need_dx (needs w8.back_values) / need_dw (needs saved): None is returned for what is not needed."""
+    n_in, n_out = w8.n_in, w8.n_out
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be 2-D (rows, width), got shape {tuple(dy.shape)}")
+    rows = dy.shape[0]
+    if plan is not None:
+        _, tokens, slots = _plan_rows(plan, dy)
+        rows = tokens * slots
+    lead, n_experts, dt, offsets = _product_head(dy, "dy", w8, plan)
+    pdy, ldy = _matrix("dy", dy, rows, n_out, dy)
+    back = (0, 0)
+    if need_dx:
+        if w8.back_values is None:
+            raise ValueError("w8 has no backward values: quantize_weight(w, backward=True)")
+        back = _weight_pointers("w8.back_", w8.back_values, w8.back_scales, lead, n_out, n_in, dy)
+    head = (rows, n_in, n_out, n_experts, dt, offsets, 0, rows, 1)
+    key = (rows, n_in, n_out, n_experts, dt, plan is None)
+    dx = dw = None
+    if need_dx:
+        dx = dy.new_empty((rows, n_in))
+    psaved = 0
+    if need_dw:
+        size = _known_size(("saved", key), "shampoo_product8_saved_size", _PRODUCT.pack(*head, *_NO_PRODUCT))
+        if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or saved.numel() != size or saved.get_device() != dy.get_device():
+            raise ValueError("saved is not what product8_forward kept for these sizes")
+        psaved = saved.data_ptr()
+        dw = dy.new_empty((*lead, n_in, n_out))
+    if need_dx or need_dw:
+        args = _PRODUCT.pack(*head, 0, 0, *back, 0, 0, 0, 0, psaved, pdy, ldy, (dx.data_ptr() or 256) if need_dx else 0, n_in,
+                             dw.data_ptr() if need_dw else 0, n_out, n_in * n_out)
+        size = _known_size(("backward", key, need_dx, need_dw), "shampoo_product8_workspace_size", args, 1)
+        ws, keep = _workspace(size, dy)
+        _call("shampoo_product8_backward", args, dy.get_device(), ws, size)
+    return dx, dw

@@ -52,6 +52,11 @@ def test_struct_layouts(tmp_path):
         v[i] = 0x1122334455667788
         return fmt.pack(*v).index(mark)
     assert got[:2] == [X._SORT.size, X._ROUTE.size]
+    more = c_sizes(tmp_path, "sizeof(shampoo_weight8_t)", "sizeof(shampoo_product8_t)", "offsetof(shampoo_weight8_t, back_scales)",
+                   "offsetof(shampoo_product8_t, x_rows)", "offsetof(shampoo_product8_t, values)", "offsetof(shampoo_product8_t, saved)",
+                   "offsetof(shampoo_product8_t, stride_dw)")
+    assert more == [X._WEIGHT.size, X._PRODUCT.size, place(X._WEIGHT, 11, 10), place(X._PRODUCT, 25, 7), place(X._PRODUCT, 25, 9),
+                    place(X._PRODUCT, 25, 17), place(X._PRODUCT, 25, 24)]
     assert got[2:] == [place(X._SORT, 9, 8), place(X._ROUTE, 15, 9), place(X._ROUTE, 15, 14)]
 
 
@@ -96,9 +101,70 @@ def test_route_refusals_by_entry(lib, name, over, code):
     assert getattr(lib, name)(X._ROUTE.pack(*{**ROUTE, **over}.values()), None) == code
 
 
+WEIGHT = dict(n_in=200, n_out=300, experts=2, dtype=1, w=FAKE, ld_w=300, stride_w=60000, values=FAKE, scales=FAKE, back_values=FAKE,
+              back_scales=FAKE)
+PRODUCT = dict(rows=100, n_in=200, n_out=300, experts=2, dtype=1, offsets=FAKE, source=FAKE, x_rows=50, slots=2, values=FAKE, scales=FAKE,
+               back_values=FAKE, back_scales=FAKE, x=FAKE, ld_x=200, y=FAKE, ld_y=300, saved=FAKE, dy=FAKE, ld_dy=300, dx=FAKE, ld_dx=200,
+               dw=FAKE, ld_dw=300, stride_dw=60000)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n_in=0), INVALID), (dict(n_out=(1 << 21) + 1), INVALID), (dict(experts=0), INVALID), (dict(experts=1025), INVALID),
+    (dict(dtype=3), UNSUPPORTED), (dict(w=0), INVALID), (dict(w=FAKE + 1), MISALIGNED), (dict(ld_w=299), INVALID),
+    (dict(stride_w=59999), INVALID), (dict(values=0), INVALID), (dict(values=FAKE + 8), MISALIGNED), (dict(scales=FAKE + 2), MISALIGNED),
+    (dict(back_scales=0), INVALID), (dict(back_values=FAKE + 4), MISALIGNED)])
+def test_weight_refusals(lib, over, code):
+    assert lib.shampoo_quantize_weight(X._WEIGHT.pack(*{**WEIGHT, **over}.values()), None) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    ({}, 0), (dict(rows=0, x_rows=0), 0), (dict(rows=-1), INVALID), (dict(rows=1 << 31), INVALID), (dict(n_in=0), INVALID), (dict(experts=0), INVALID),
+    (dict(offsets=0), INVALID), (dict(offsets=0, experts=1), INVALID), (dict(offsets=FAKE + 2), MISALIGNED), (dict(x_rows=0), INVALID),
+    (dict(slots=0), INVALID), (dict(source=FAKE + 1), MISALIGNED), (dict(dtype=-1), UNSUPPORTED)])
+def test_product_sizes(lib, over, code):
+    out = ctypes.c_size_t()
+    args = X._PRODUCT.pack(*{**PRODUCT, **over}.values())
+    assert lib.shampoo_product8_workspace_size(args, 0, ctypes.byref(out)) == code
+    assert lib.shampoo_product8_workspace_size(args, 1, ctypes.byref(out)) == code
+    assert lib.shampoo_product8_saved_size(args, ctypes.byref(out)) == code
+
+
+@pytest.mark.parametrize("over,ws,size,code", [
+    (dict(values=0), FAKE, 1 << 30, INVALID), (dict(values=FAKE + 8), FAKE, 1 << 30, MISALIGNED), (dict(scales=0), FAKE, 1 << 30, INVALID),
+    (dict(x=0), FAKE, 1 << 30, INVALID), (dict(ld_x=199), FAKE, 1 << 30, INVALID), (dict(x=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
+    (dict(y=0), FAKE, 1 << 30, INVALID), (dict(ld_y=1), FAKE, 1 << 30, INVALID), (dict(saved=FAKE + 16), FAKE, 1 << 30, MISALIGNED),
+    ({}, 0, 1 << 30, INVALID), ({}, FAKE + 16, 1 << 30, MISALIGNED), ({}, FAKE, 1000, SMALL)])
+def test_product_forward_refusals(lib, over, ws, size, code):
+    assert lib.shampoo_product8_forward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
+
+
+@pytest.mark.parametrize("over,ws,size,code", [
+    (dict(back_values=0), FAKE, 1 << 30, INVALID), (dict(back_scales=FAKE + 1), FAKE, 1 << 30, MISALIGNED), (dict(dy=0), FAKE, 1 << 30, INVALID),
+    (dict(ld_dy=299), FAKE, 1 << 30, INVALID), (dict(ld_dx=199), FAKE, 1 << 30, INVALID), (dict(dx=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
+    (dict(saved=0), FAKE, 1 << 30, INVALID), (dict(ld_dw=299), FAKE, 1 << 30, INVALID), (dict(stride_dw=59999), FAKE, 1 << 30, INVALID),
+    ({}, 0, 0, INVALID), ({}, FAKE, 1000, SMALL)])
+def test_product_backward_refusals(lib, over, ws, size, code):
+    assert lib.shampoo_product8_backward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
+
+
+def test_workspace_holds_every_spread_of_rows(lib):
+    """The bound on blocks of 128 over the experts, for every way to share rows between a few of them."""
+    for rows in (1, 2, 127, 128, 129, 300):
+        for a in range(rows + 1):
+            for b in range(0, rows - a + 1, 7):
+                sizes = [a, b, rows - a - b]
+                need = sum(-(-s // 128) for s in sizes)
+                out = ctypes.c_size_t()
+                args = X._PRODUCT.pack(*{**PRODUCT, "rows": rows, "experts": 3, "n_in": 128}.values())
+                assert lib.shampoo_product8_saved_size(args, ctypes.byref(out)) == 0
+                assert out.value >= need * 128 * 128 + need * 128
+
+
 def test_null_arguments(lib):
     for name, more in (("shampoo_sort_workspace_size", (None,)), ("shampoo_sort_tokens", (None, 0, None)), ("shampoo_dispatch", (None,)),
-                       ("shampoo_combine", (None,)), ("shampoo_combine_backward", (None,))):
+                       ("shampoo_combine", (None,)), ("shampoo_combine_backward", (None,)), ("shampoo_quantize_weight", (None,)),
+                       ("shampoo_product8_saved_size", (None,)), ("shampoo_product8_workspace_size", (0, None)),
+                       ("shampoo_product8_forward", (None, 0, None)), ("shampoo_product8_backward", (None, 0, None))):
         assert getattr(lib, name)(None, *more) == INVALID
 
 
@@ -132,3 +198,31 @@ def test_reference_gradients():
     dxs = torch.randn(8, 5, generator=g, dtype=torch.float64)
     dx, = torch.autograd.grad(ref.dispatch(x, rows), [x], dxs)
     assert torch.allclose(ref.combine(dxs, rows)[0], dx)
+
+
+def test_reference_quantized():
+    """Against torch's own conversion to e4m3 where the scale is plain to see."""
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(64, 300, generator=g)
+    x[:, ::128] = 448.0 * torch.exp2(torch.randint(-20, 20, (64, 1), generator=g).float())
+    q, e = ref.quantized(x, (1,))
+    for b in range(3):
+        part = slice(128 * b, min(300, 128 * b + 128))
+        scale = torch.exp2(e[:, 128 * b:128 * b + 1].float())
+        top = x[:, part].abs().amax(1, keepdim=True)
+        assert ((top <= 448 * scale) & (top > 224 * scale)).all()
+        assert torch.equal((x[:, part] / scale).to(torch.float8_e4m3fn).double(), q[:, part])
+
+
+def test_reference_product_gradients():
+    """Of whole numbers, which 8 bits hold: against autograd of the plain product."""
+    g = torch.Generator().manual_seed(1)
+    x, w, dy = (torch.randint(-8, 9, s, generator=g).double() for s in ((10, 130), (2, 130, 20), (10, 20)))
+    offsets = np.array([0, 4, 9])
+    x.requires_grad_()
+    w.requires_grad_()
+    y = torch.cat([x[:4] @ w[0], x[4:9] @ w[1], torch.zeros(1, 20, dtype=torch.float64)])
+    assert torch.equal(ref.product(x.detach(), w.detach(), offsets)[0], y)
+    dx, dw = torch.autograd.grad(y, [x, w], dy)
+    assert torch.equal(ref.product(dy, w.detach().transpose(1, 2), offsets)[0], dx)
+    assert torch.equal(ref.product_dw(x.detach(), dy, offsets, 2)[0], dw)

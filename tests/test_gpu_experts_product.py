@@ -1,0 +1,327 @@
+"""Products in 8 bits on the GPU against plain 64-bit forms of the same definition (tests/experts_reference.py).
+
+The 8 bits and their scales are compared exactly. Tolerances of results, set before the first run, for each element:
+ - bf16: one rounding (2^-8 of the value) and what the 8-bit matrix instruction leaves of a sum. It keeps some 16 bits below
+   the largest of a block's products: 2^-16 of the terms' root sum of squares in the mean, of which 16 times as much is
+   allowed for a single element.
+   That holds for terms of about one size. The instruction adds the products of eight k with what lies 14 bits and more
+   below the largest of them cut off each (measured on single products of powers of two: 2^-13 of the largest is kept,
+   2^-14 is not), and the groups' sums in fp32. So where single terms stand out, a result is off by up to 7 * 2^-13 of
+   the sum over groups of their largest product, whatever the signs; the test of uneven rows and columns allows that.
+ - fp32: one rounding, and for fp32 sums of k exact products in any order (k + 16) * 2^-24 of the sum of their magnitudes.
+Results under 2^-126 absolute are not compared further."""
+import numpy as np
+import pytest
+import torch
+
+from blocked_shampoo_preconditioning_amd import experts
+from tests import experts_reference as ref
+from tests.experts_reference import HALF_STEP
+from tests.gpu_common import log
+from tests.test_gpu_experts_route import DT, make_ids, padded
+
+pytestmark = pytest.mark.gpu
+
+
+def close(name, got, want, k, groups=None):
+    """groups: the sum over groups of eight k of their largest product, where single terms stand out."""
+    dtype = got.dtype
+    value, rss, total = (t.cuda() for t in want)
+    bound = value.abs() * HALF_STEP[dtype] + 2.0 ** -126 + (2.0 ** -12 * rss if dtype is torch.bfloat16 else (k + 16) * 2.0 ** -24 * total)
+    if groups is not None and dtype is torch.bfloat16:
+        bound = bound + 7 * 2.0 ** -13 * groups.cuda()
+    assert torch.equal(torch.isnan(got), torch.isnan(value)), name
+    assert got.shape == value.shape, name
+    worst = torch.nan_to_num((got.double() - value).abs() / bound).max().item() if value.numel() else 0.0
+    log(f"  {name}: {worst:.3f} of the bound")
+    assert worst <= 1.0, (name, worst)
+
+
+def normal(gen, *shape, std=1.0, dtype="bf16"):
+    return (torch.randn(*shape, generator=gen) * std).to(DT[dtype])
+
+
+def check_weight(w8, w):
+    """Bytes and scales of a Weight8 against the definition."""
+    lead, (n_in, n_out) = w.shape[:-2], w.shape[-2:]
+    q, e = ref.quantized(w, (-2, -1))
+    for values, scales, q, e in ((w8.values, w8.scales, q.transpose(-1, -2), e.transpose(-1, -2)), (w8.back_values, w8.back_scales, q, e)):
+        if values is None:
+            continue
+        cols = q.shape[-1]
+        got = values.float().double().cpu()
+        assert torch.equal(torch.isnan(got[..., :cols]), torch.isnan(q)) and torch.equal(torch.nan_to_num(got[..., :cols]), torch.nan_to_num(q))
+        assert not got[..., cols:].any()
+        power = scales.view(torch.uint8).cpu().int() - 127
+        kb = (cols + 127) // 128
+        assert torch.equal(power[..., :kb], e[..., ::128, ::128].int()) and not power[..., kb:].any()
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (128, 128), (127, 129), (130, 7), (300, 1000), (3, 64, 200), (5, 129, 385), (1, 40, 40)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["normal", "wide", "special"])
+def test_quantize_weight(shape, dtype, kind):
+    g = torch.Generator().manual_seed(sum(shape))
+    w = torch.randn(*shape, generator=g)
+    if kind == "wide":
+        w = torch.ldexp(w, torch.randint(-100, 100, shape, generator=g))
+    if kind == "special":  # ties, the block's largest on each side of 448, zeros, subnormals, what is not finite
+        pool = torch.tensor([448.0, 449.0, 447.0, 1.0625, 1.1875, 17.0, 19.0, 0.0, -0.0, 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -10, 1e-40, float("inf"),
+                             float("-inf"), float("nan"), 3.3e38])
+        w = pool[torch.randint(0, len(pool) - (0 if w.numel() % 2 else 4), shape, generator=g)]
+    w = w.to(DT[dtype])
+    log(f"quantize {shape} {dtype} {kind}")
+    wide = torch.full((*shape[:-1], shape[-1] + 3), float("nan"), dtype=w.dtype)
+    wide[..., :shape[-1]] = w
+    for dev in (w.cuda(), wide.cuda()[..., :shape[-1]]):
+        check_weight(experts.quantize_weight(dev, backward=True), w)
+        check_weight(experts.quantize_weight(dev), w)
+
+
+def test_quantize_small_and_zero_blocks():
+    w = torch.zeros(256, 256)
+    w[:128, :128] = 1e-39  # under what a scale of 2^-126 shows
+    w[:128, 128:] = 2.0 ** -130
+    w[128:, 128:] = 2.0 ** -126 * 448
+    check_weight(experts.quantize_weight(w.cuda(), backward=True), w)
+
+
+def check_product(rows, n_in, n_out, dtype, n_experts=0, ids=None, slots=1, gather=False, pad=0, seed=0, change=None, uneven=False):
+    """Forward and backward of one shape. ids [tokens, slots]: the experts of a grouped product."""
+    log(f"product {rows} x {n_in} x {n_out} {dtype} experts {n_experts} gather {gather} pad {pad}")
+    g = torch.Generator().manual_seed(seed + rows + n_in)
+    x = normal(g, rows // slots if gather else rows, n_in, dtype=dtype)
+    w = normal(g, max(1, n_experts), n_in, n_out, std=n_in ** -0.5, dtype=dtype)
+    dy = normal(g, rows, n_out, std=1e-2, dtype=dtype)
+    if change:
+        change(x, w, dy)
+    plan = offsets = None
+    kept = rows
+    if n_experts:
+        plan = experts.sort_tokens(torch.from_numpy(ids).cuda(), n_experts)
+        offsets, plan_rows, source = ref.plan(ids, n_experts)
+        kept = int(offsets[-1])
+        dy[kept:] = float("nan")  # not read
+    xs = x
+    if gather:
+        xs = torch.zeros(rows, n_in, dtype=x.dtype)
+        xs[:kept] = x[torch.from_numpy(source[:kept] // slots)]
+    elif n_experts:
+        x[kept:] = float("nan")
+        xs = x.clone()
+        xs[kept:] = 0
+    dev_w = w.cuda() if n_experts else w[0].cuda()
+    w8 = experts.quantize_weight(dev_w, backward=True)
+    y, saved = experts.product8_forward(padded(x, pad), w8, plan, gather=gather, save=True)
+    want = ref.product(xs, w, offsets)
+    want[:, kept:] = 0
+    assert not uneven or not n_experts
+    w_bits = ref.rounded(w[0], (0, 1)) if uneven else None
+    close("y", y, want, n_in, ref.largest_of_groups(ref.rounded(xs, (1,)), w_bits) if uneven else None)
+    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(experts.product8_forward(padded(x, pad), w8, plan, gather=gather)))
+    dx, dw = experts.product8_backward(padded(dy, pad), w8, saved, plan)
+    clean = torch.where(torch.arange(rows)[:, None] < kept, dy, torch.zeros((), dtype=dy.dtype))
+    want = ref.product(clean, w.transpose(1, 2), offsets)
+    want[:, kept:] = 0
+    close("dx", dx, want, n_out, ref.largest_of_groups(ref.rounded(clean, (1,)), w_bits.t()) if uneven else None)
+    assert dw.shape == dev_w.shape
+    close("dw", dw if n_experts else dw[None], ref.product_dw(xs, clean, offsets, max(1, n_experts)), rows,
+          ref.largest_of_groups(ref.rounded(xs, (0,)).t(), ref.rounded(clean, (0,))) if uneven else None)
+    only_dx, none = experts.product8_backward(dy.cuda(), w8, None, plan, need_dw=False)
+    assert none is None and torch.equal(torch.nan_to_num(only_dx), torch.nan_to_num(dx))
+    none, only_dw = experts.product8_backward(dy.cuda(), w8, saved, plan, need_dx=False)
+    assert none is None and torch.equal(torch.nan_to_num(only_dw), torch.nan_to_num(dw))
+
+
+@pytest.mark.parametrize("rows,n_in,n_out,pad", [
+    (1, 1, 1, 0), (1, 128, 128, 0), (1, 2048, 512, 0), (2, 129, 130, 1), (5, 127, 129, 3), (16, 300, 64, 0), (17, 64, 1000, 8), (33, 257, 48, 0),
+    (64, 256, 2100, 0), (65, 100, 100, 4), (128, 128, 256, 0), (130, 300, 77, 5), (300, 1000, 520, 0), (257, 2048, 640, 0), (1000, 130, 1031, 7)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dense(rows, n_in, n_out, pad, dtype):
+    check_product(rows, n_in, n_out, dtype, pad=pad)
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(3700, 200, 3500), (130, 3590, 3601), (3585, 3600, 136)])
+def test_dense_large_tiles(rows, n_in, n_out):
+    check_product(rows, n_in, n_out, "bf16")
+
+
+def spread(kind, tokens, slots, n_experts):
+    """ids of a case of uneven experts."""
+    g = np.random.default_rng(tokens + n_experts)
+    ids = g.integers(0, n_experts, size=(tokens, slots))
+    if kind == "one":
+        ids[:] = n_experts - 1
+    if kind == "gaps":  # every second expert has none, the first among them
+        ids = ids // 2 * 2 + 1 if n_experts > 1 else ids
+        ids = np.minimum(ids, n_experts - 1)
+    if kind == "whole":  # whole blocks of 128 for each
+        ids = np.repeat(np.arange(n_experts), -(-tokens * slots // n_experts // 128) * 128)[:tokens * slots].reshape(tokens, slots)
+    if kind == "left":
+        ids = np.where(g.random(ids.shape) < 0.3, -1, ids)
+    if kind == "none":
+        ids[:] = -1
+    return ids
+
+
+@pytest.mark.parametrize("tokens,slots,n_experts,n_in,n_out", [
+    (1, 1, 1, 64, 64), (1, 2, 8, 300, 200), (7, 2, 64, 128, 130), (16, 2, 8, 520, 384), (60, 1, 3, 100, 260), (300, 2, 5, 257, 129),
+    (500, 3, 16, 130, 200), (200, 8, 33, 64, 136), (1000, 1, 1, 200, 72)])
+@pytest.mark.parametrize("kind", ["even", "one", "gaps", "whole", "left", "none"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts(tokens, slots, n_experts, n_in, n_out, kind, gather):
+    ids = spread(kind, tokens, slots, n_experts)
+    check_product(tokens * slots, n_in, n_out, "f32" if tokens in (16, 300) else "bf16", n_experts, ids, slots, gather, pad=3 if gather else 0)
+
+
+@pytest.mark.parametrize("kind", ["even", "gaps", "left"])
+def test_experts_large_tiles(kind):
+    check_product(1500, 90, 4000, "bf16", 16, spread(kind, 750, 2, 16), 2, True)
+    check_product(1500, 1000, 1025, "bf16", 16, spread(kind, 750, 2, 16), 2, False)
+
+
+def test_many_experts():
+    check_product(3000, 40, 72, "bf16", 1024, spread("even", 1500, 2, 1024), 2, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_uneven_rows_and_columns(dtype):
+    """Rows, columns and blocks from 2^-40 to 2^40 of each other, rows and blocks of zeros."""
+    def change(x, w, dy):
+        g = torch.Generator().manual_seed(4)
+        for t in (x, dy, w[0]):
+            t.mul_(torch.exp2(torch.randint(-40, 40, (t.shape[0], 1), generator=g).float()).to(t.dtype))
+            t.mul_(torch.exp2(torch.randint(-20, 20, (1, t.shape[1]), generator=g).float()).to(t.dtype))
+            t[3] = 0
+            t[:, 5] = 0
+        x[:, 128:256] = 0
+        w[0, :128, :128] = 0
+    check_product(200, 300, 260, dtype, change=change, uneven=True)
+    check_product(9, 300, 260, dtype, change=change, uneven=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [200, 12])
+def test_non_finite_values(dtype, rows):
+    """Each reaches the results it enters as NaN (close compares where) and leaves the scales of its block alone."""
+    def change(x, w, dy):
+        x[4, 10], x[7, 200], dy[2, 3], dy[9, 130] = float("inf"), float("nan"), float("-inf"), float("nan")
+        w[0, 17, 40], w[0, 150, 3] = float("inf"), float("nan")
+    check_product(rows, 260, 200, dtype, change=change)
+    ids = spread("even", rows, 1, 3)
+
+    def change_experts(x, w, dy):
+        x[4, 10], w[1, 17, 40] = float("inf"), float("nan")
+    check_product(rows, 260, 200, dtype, 3, ids, 1, True, change=change_experts)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_against_differences(dtype):
+    """With whole numbers up to 16 the 8 bits hold every element, so y is linear in x and in w, the central difference of
+    <dy, y> is exact in fp32 (sums of whole numbers under 2^24), and the gradients are those numbers."""
+    g = torch.Generator().manual_seed(2)
+    rows, n_in, n_out = 70, 140, 100
+
+    def whole(top, *shape):
+        return torch.randint(-top, top + 1, shape, generator=g).float()
+    x, u, w, v, dy = whole(8, rows, n_in), whole(8, rows, n_in), whole(8, n_in, n_out), whole(8, n_in, n_out), whole(2, rows, n_out)
+    dt = torch.float32  # results of whole numbers up to 2^24; bf16 operands hold the same numbers
+
+    def loss(x, w):
+        y = experts.product8_forward(x.to(dt).cuda(), experts.quantize_weight(w.to(dt).cuda()))
+        return (y.double().cpu() * dy.double()).sum()
+    w8 = experts.quantize_weight(w.to(DT[dtype]).cuda(), backward=True)
+    y, saved = experts.product8_forward(x.to(DT[dtype]).cuda(), w8, save=True)
+    dx, dw = experts.product8_backward(dy.to(DT[dtype]).cuda(), w8, saved)
+    for got, d, size, want in ((dx, u, dy.abs() @ w.abs().t(), (loss(x + u, w) - loss(x - u, w)) / 2),
+                               (dw, v, x.abs().t() @ dy.abs(), (loss(x, w + v) - loss(x, w - v)) / 2)):
+        slack = (size.double() * d.double().abs()).sum() * (2.0 ** -8 + 2.0 ** -12) if dtype == "bf16" else 0.0  # bf16 rounds the gradients
+        assert abs((got.double().cpu() * d.double()).sum() - want) <= slack
+
+
+def test_offsets_past_32_bits():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for rows, n_in, n_out in ((300000, 128, 8192), (300000, 8192, 128)):  # y, and x in 8 bits, of 2.4e9 elements
+        log(f"far {rows} x {n_in} x {n_out}")
+        x = torch.randn(rows, n_in, generator=g, device="cuda").bfloat16()
+        w = (torch.randn(n_in, n_out, generator=g, device="cuda") * n_in ** -0.5).bfloat16()
+        y = experts.product8_forward(x, experts.quantize_weight(w))
+        at = torch.tensor([0, 1, 131071, 262143, 262144, 299000, 299998, 299999])
+        want = ref.product(x[at.cuda()].cpu(), w.cpu()[None])
+        close("y", y[at.cuda()], want, n_in)
+        del x, y
+
+
+def test_streams_graphs_and_repeats():
+    ids, dev = make_ids(8, 400, 2, 4, 0.1)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, w, dy = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((400, 192), (4, 192, 320), (800, 320)))
+
+    def run():
+        w8 = experts.quantize_weight(w, backward=True)
+        plan = experts.sort_tokens(dev, 4)
+        y, saved = experts.product8_forward(x, w8, plan, gather=True, save=True)
+        return y, *experts.product8_backward(dy, w8, saved, plan), experts.product8_forward(x[:3], experts.Weight8(w8.values[0], w8.scales[0], 192, 320))
+    want = [t.clone() for t in run()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = run()
+    for turn in range(3):
+        x.copy_(torch.randn(400, 192, device="cuda").bfloat16())
+        w.copy_(torch.randn(4, 192, 320, device="cuda").bfloat16())
+        dev.copy_(torch.from_numpy(make_ids(20 + turn, 400, 2, 4, 0.1)[0]).cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, run())), turn
+
+
+def test_there_and_back():
+    """A run of the operators together: sorted, through two matrices an expert, back with weights, and all gradients. bf16
+    results between the calls are part of the path, so each call is held to its own inputs."""
+    tokens, slots, n_experts, d, f = 500, 2, 6, 256, 384
+    ids, dev = make_ids(1, tokens, slots, n_experts, 0.1)
+    g = torch.Generator().manual_seed(11)
+    x, dy = normal(g, tokens, d), normal(g, tokens, d, std=1e-2)
+    w1, w2 = normal(g, n_experts, d, f, std=d ** -0.5), normal(g, n_experts, f, d, std=f ** -0.5)
+    weights = torch.rand(tokens, slots, generator=g)
+    offsets, rows, source = ref.plan(ids, n_experts)
+    kept = int(offsets[-1])
+    plan = experts.sort_tokens(dev, n_experts)
+    a, b = experts.quantize_weight(w1.cuda(), backward=True), experts.quantize_weight(w2.cuda(), backward=True)
+    h, saved1 = experts.product8_forward(x.cuda(), a, plan, gather=True, save=True)
+    r = torch.nn.functional.silu(h)
+    ys, saved2 = experts.product8_forward(r, b, plan, save=True)
+    y = experts.combine(ys, plan, weights.cuda())
+    dys, dweights = experts.combine_backward(dy.cuda(), ys, plan, weights.cuda())
+    dr, dw2 = experts.product8_backward(dys, b, saved2, plan)
+    sg = torch.sigmoid(h.float())
+    dh = (dr.float() * sg * (1 + h.float() * (1 - sg))).bfloat16()
+    dxs, dw1 = experts.product8_backward(dh, a, saved1, plan)
+    dx = experts.dispatch_backward(dxs, plan)
+    xs = ref.dispatch(x, rows)
+    close("h", h, ref.product(xs, w1, offsets), d)
+    close("ys", ys, ref.product(r.cpu(), w2, offsets), f)
+    close("dr", dr, ref.product(dys.cpu(), w2.transpose(1, 2), offsets), d)
+    close("dw2", dw2, ref.product_dw(r.cpu(), dys.cpu(), offsets, n_experts), 1000)
+    close("dxs", dxs, ref.product(dh.cpu(), w1.transpose(1, 2), offsets), f)
+    close("dw1", dw1, ref.product_dw(xs, dh.cpu(), offsets, n_experts), 1000)
+    # and all of it against the path without any rounding to 8 bits: one is off by 2^-4 of a value at most, evenly spread, so by
+    # 2^-4 / sqrt(3) in the mean square; up to six of them, of independent values, enter a result
+    xg, w1g, w2g, wg = (t.double().requires_grad_() for t in (x, w1, w2, weights))
+    t, j, rr = ref.kept_pairs(rows)
+    full = torch.zeros(kept, d, dtype=torch.float64).index_add(0, rr, xg[t])
+    hid = torch.nn.functional.silu(torch.cat([full[p] @ w1g[e] for e, p in ref.expert_rows(offsets, kept)]))
+    out = torch.cat([hid[p] @ w2g[e] for e, p in ref.expert_rows(offsets, kept)])
+    yy = torch.zeros(tokens, d, dtype=torch.float64).index_add(0, t, out[rr] * wg[t, j][:, None])
+    grads = torch.autograd.grad(yy, [xg, w1g, w2g, wg], dy.double())
+    for name, got, want in (("y", y, yy.detach()), ("dx", dx, grads[0]), ("dw1", dw1, grads[1]), ("dw2", dw2, grads[2]), ("dweights", dweights, grads[3])):
+        off = ((got.double().cpu() - want).norm() / want.norm()).item()
+        log(f"  whole path, {name}: {off:.4f}")
+        assert off <= 2.0 ** -4 / 3 ** 0.5 * 6 ** 0.5, name
