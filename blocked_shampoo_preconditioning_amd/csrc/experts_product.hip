@@ -50,10 +50,10 @@ __device__ __forceinline__ void each(F&& f) {
   each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-// FM x FN operands of 16 rows a wave, 2 x 2 waves.
-template <int FM_, int FN_, bool F32_, bool BBLOCK_, int WAVES_>
+// FM x FN operands of 16 rows a wave, WM x WN waves.
+template <int FM_, int FN_, int WM_, int WN_, bool F32_, bool BBLOCK_, int WAVES_>
 struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WM = 2, WN = 2, NW = 4, NT = 256;
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, NW = WM * WN, NT = 64 * NW;
   static constexpr bool F32 = F32_, BBLOCK = BBLOCK_;  // BBLOCK: B's scales are those of 128 x 128 tiles
   static constexpr int WAVES = WAVES_;                 // of a SIMD at once
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
@@ -62,32 +62,35 @@ struct Tile {
   static constexpr int STAGE = B_SCALES + 256;
 };
 
-// A buffer of `left` bytes from base; loads past it give zeros. 2 GiB of them are
+// A buffer of `left` bytes from base; loads past it give zeros. 4 GiB of them are
 // enough, since a tile's offsets stay under that. Lengths are multiples of 4.
-__device__ __forceinline__ int4v make_rsrc(uint64_t base, int64_t left) {
+__device__ __forceinline__ uint32_t buffer_size(int64_t left) {
+  return left <= 0 ? 0u : left > 0xfffffff0ll ? 0xfffffff0u : static_cast<uint32_t>(left);
+}
+__device__ __forceinline__ int4v make_rsrc(uint64_t base) {
   int4v r;
   r[0] = static_cast<int>(base);
   r[1] = static_cast<int>(base >> 32);
-  r[2] = left <= 0 ? 0 : left > 0x7ffffff0 ? 0x7ffffff0 : static_cast<int>(left);
+  r[2] = 0;
   r[3] = 0x00020000;
   return r;
 }
 
-// 64 x 16 or 4 bytes from rsrc + voff (a lane's own) to LDS at `lds` + plus + 16 or
+// 64 x 16 or 4 bytes from rsrc + soff + voff (a lane's own) to LDS at `lds` + plus + 16 or
 // 4 * lane; waited for at the next step's barrier. As asm because the compiler
 // would wait for every such load before any LDS read; it has no register results.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void load_lds16(const int4v& rsrc, uint32_t voff, uint32_t lds, int plus) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+__device__ __forceinline__ void load_lds16(const int4v& rsrc, uint32_t voff, uint32_t soff, uint32_t lds, int plus) {
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(lds), "v"(voff), "s"(rsrc), "i"(plus)
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff), "i"(plus)
                : "memory", "scc", "m0");
 }
-__device__ __forceinline__ void load_lds4(const int4v& rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+__device__ __forceinline__ void load_lds4(const int4v& rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                :
-               : "s"(lds), "v"(voff), "s"(rsrc)
+               : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -165,16 +168,16 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
     count = min(T::BM, g.M - trow * T::BM);
   }
 
-  // A load instruction covers eight rows of 128 bytes: row (instruction * 4 + wave)
+  // A load instruction covers eight rows of 128 bytes: row (instruction * NW + wave)
   // * 8 + lane / 8, place lane % 8. A row's chunk c of 16 bytes sits at place c ^
   // swizzle, so that the rows that one read takes together (row r of an operand,
   // which operand_row sends to row (r & 3) + 16 (r >> 2) + ..) fall on different
-  // banks.
-  auto swizzle = [](int r16) { return (r16 & 7) ^ ((r16 >> 3) & 1); };
-  constexpr int NA = T::BM / 32, NB = T::BN / 32;
+  // banks: 6.1 cycles a read where (r & 7) ^ (r >> 3) takes 8.4 and none 16.3.
+  auto swizzle = [](int r16) { return r16 & 6; };
+  constexpr int NA = T::BM / 8 / T::NW, NB = T::BN / 8 / T::NW;
   uint32_t va[NA], vb[NB];
   auto row_off = [&](int j, int64_t pitch) {
-    const int row = (j * 4 + wave) * 8 + (lane >> 3);
+    const int row = (j * T::NW + wave) * 8 + (lane >> 3);
     const int r16 = (row & 3) | ((row >> 4) & 3) << 2;
     return static_cast<uint32_t>(row * pitch + (((lane & 7) ^ swizzle(r16)) << 4));
   };
@@ -184,48 +187,45 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   for (int j = 0; j < NB; ++j) vb[j] = row_off(j, g.pitch_b);
   const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
 
+  // The buffers begin at the tile's first row and K block, and a step adds to the
+  // loads' scalar offset: every instruction here is paid for in every K step.
   const int64_t a_at = static_cast<int64_t>(a_block) * kBlock * g.pitch_a + static_cast<int64_t>(k0) * kBlock;
   const int64_t b_at = n0 * g.pitch_b + static_cast<int64_t>(k0) * kBlock;
-  uint64_t pa = reinterpret_cast<uint64_t>(g.a) + a_at;
-  uint64_t pb = reinterpret_cast<uint64_t>(g.b) + (g.by_expert ? 0 : expert * g.b_stride) + b_at;
-  int64_t left_a = g.size_a - a_at, left_b = g.size_b - b_at;
+  int4v ra = make_rsrc(reinterpret_cast<uint64_t>(g.a) + a_at);
+  int4v rb = make_rsrc(reinterpret_cast<uint64_t>(g.b) + (g.by_expert ? 0 : expert * g.b_stride) + b_at);
+  const uint32_t na = buffer_size(g.size_a - a_at), nb = buffer_size(g.size_b - b_at);
   // scales: a wave takes A's (even) or B's, by 4 bytes a lane
-  const bool b_scales = wave & 1;
-  const int sa_row = a_block * kBlock;
-  int kb = k0;  // K block of the next step to load
+  const bool b_scales = wave & 1, of_blocks = T::BBLOCK && b_scales;
   const int64_t scale_step = static_cast<int64_t>(b_scales ? g.b_blocks : g.a_blocks) * kBlock;
-  const uint64_t scales = reinterpret_cast<uint64_t>(b_scales ? g.b_scales + (T::BBLOCK ? expert * g.b_scale_stride : n0) : g.a_scales + sa_row);
-  const int64_t scales_size = b_scales ? (T::BBLOCK ? static_cast<int64_t>(g.b_blocks) * g.b_scale_pitch : g.k_blocks * scale_step - n0)
-                                       : g.k_blocks * scale_step - sa_row;
-  const uint32_t block_row = min(n0 / kBlock + (lane >> 5), g.b_blocks - 1);  // BBLOCK: each half of a wave its 128 columns
-  const uint32_t vs = T::BBLOCK && b_scales ? block_row * g.b_scale_pitch : lane * 4;
+  const int64_t s_at = of_blocks ? 0 : k0 * scale_step + (b_scales ? n0 : a_block * kBlock);
+  const int64_t s_size = of_blocks ? static_cast<int64_t>(g.b_blocks) * g.b_scale_pitch : g.k_blocks * scale_step;
+  int4v rs = make_rsrc(reinterpret_cast<uint64_t>(b_scales ? g.b_scales : g.a_scales) + (of_blocks ? expert * g.b_scale_stride : 0) + s_at);
+  const uint32_t ns = buffer_size(s_size - s_at);
+  const uint32_t block_row = min(n0 / kBlock + (lane >> 5), g.b_blocks - 1);  // of_blocks: each half of a wave its 128 columns
+  const uint32_t vs = of_blocks ? block_row * g.b_scale_pitch : lane * 4;
 
-  int loads = turns;  // steps still to be loaded
-  int4v ra, rb, rs;
-  uint32_t at = 0;
+  int step = 0;  // the next to be loaded
+  uint32_t at = 0, ks = 0, ss = 0;
   auto aim = [&](int buf) {
     at = lds_base + buf * T::STAGE;
     // past the last step nothing is read: the buffer gets zeros
-    ra = make_rsrc(pa, loads > 0 ? left_a : 0);
-    rb = make_rsrc(pb, loads > 0 ? left_b : 0);
-    const int64_t down = T::BBLOCK && b_scales ? kb & ~3 : kb * scale_step;
-    rs = make_rsrc(scales + down, loads > 0 ? scales_size - down : 0);
+    const bool on = step < turns;
+    ra[2] = static_cast<int>(on ? na : 0u);
+    rb[2] = static_cast<int>(on ? nb : 0u);
+    rs[2] = static_cast<int>(on ? ns : 0u);
+    ks = static_cast<uint32_t>(step) * kBlock;
+    ss = of_blocks ? static_cast<uint32_t>(step) & ~3u : static_cast<uint32_t>(step) * static_cast<uint32_t>(scale_step);
+    ++step;
   };
   auto load = [&](int q) {
     if (q < NA)
-      load_lds16(ra, va[q], at + wave * 1024, q * 4096);
+      load_lds16(ra, va[q], ks, at + wave * 1024, q * T::NW * 1024);
     else if (q < NA + NB)
-      load_lds16(rb, vb[q - NA], at + wave * 1024, T::A_BYTES + (q - NA) * 4096);
+      load_lds16(rb, vb[q - NA], ks, at + wave * 1024, T::A_BYTES + (q - NA) * T::NW * 1024);
     else
-      load_lds4(rs, vs, at + (b_scales ? T::B_SCALES : T::A_SCALES));
+      load_lds4(rs, vs, ss, at + (b_scales ? T::B_SCALES : T::A_SCALES));
   };
   constexpr int kLoads = NA + NB + 1;
-  auto advance = [&]() {
-    --loads;
-    ++kb;
-    pa += kBlock, pb += kBlock;
-    left_a -= kBlock, left_b -= kBlock;
-  };
 
   // A lane's places in the reads: row r16 of an operand, chunks q4 and q4 + 4.
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -241,40 +241,41 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
     flip = 0u - flip;
   };
 
-  // scales of the step that is multiplied: operand f's in byte f % 4 of word f / 4
+  // scales: operand f's in byte f % 4 of word f / 4; those of the step that is
+  // multiplied, and those of the step that is read
   constexpr int SA = T::FM / 4, SB = T::BBLOCK ? 1 : T::FN / 4;
   uint32_t sa[SA], sb[SB], sa2[SA], sb2[SB];
-  int kc = k0;  // its K block
-  auto read_scales = [&](int k) {
+  int kc = 0;  // the step that is read
+  auto read_scales = [&]() {
 #pragma unroll
     for (int i = 0; i < SA; ++i) sa2[i] = *reinterpret_cast<lds_word>(fsa + 4 * i);
 #pragma unroll
     for (int i = 0; i < SB; ++i) sb2[i] = *reinterpret_cast<lds_word>(fsb + 4 * i);
-    if (T::BBLOCK) sb2[0] >>= (k & 3) * 8;
   };
   auto use_scales = [&]() {
 #pragma unroll
     for (int i = 0; i < SA; ++i) sa[i] = sa2[i];
 #pragma unroll
-    for (int i = 0; i < SB; ++i) sb[i] = sb2[i];
+    for (int i = 0; i < SB; ++i) sb[i] = T::BBLOCK ? sb2[i] >> (kc & 3) * 8 : sb2[i];
   };
   auto scale_a = [&](int i) { return __uint_as_float((sa2[i >> 2] >> (8 * (i & 3)) & 255u) << 23); };
-  auto scale_b = [&](int j) { return __uint_as_float((T::BBLOCK ? sb2[0] & 255u : sb2[T::BBLOCK ? 0 : j >> 2] >> (8 * (j & 3)) & 255u) << 23); };
-  auto fetch = [&](uint32_t base, int f, float scale) {
+  auto scale_b = [&](int j) {
+    const uint32_t s = T::BBLOCK ? sb2[0] >> (kc & 3) * 8 : sb2[T::BBLOCK ? 0 : j >> 2] >> (8 * (j & 3));
+    return __uint_as_float((s & 255u) << 23);
+  };
+  // half of operand f: chunk q4 or q4 + 4 of its row
+  auto fetch = [&](Fragment<F32>& x, uint32_t base, int f, int half, float scale) {
     const uint32_t from = base + (64 * (f >> 2) + 4 * (f & 3)) * 128;
-    const int4v lo = *reinterpret_cast<lds_int4>(from), hi = *reinterpret_cast<lds_int4>(from ^ 64u);
-    Fragment<F32> x;
+    const int4v v = *reinterpret_cast<lds_int4>(half ? from ^ 64u : from);
     if constexpr (F32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        widen(i < 2 ? lo[2 * i] : hi[2 * i - 4], scale, x.k[i], 0);
-        widen(i < 2 ? lo[2 * i + 1] : hi[2 * i - 3], scale, x.k[i], 4);
+      for (int i = 0; i < 2; ++i) {
+        widen(v[2 * i], scale, x.k[2 * half + i], 0);
+        widen(v[2 * i + 1], scale, x.k[2 * half + i], 4);
       }
     } else {
-      x.lo = lo;
-      x.hi = hi;
+      (half ? x.hi : x.lo) = v;
     }
-    return x;
   };
 
   floatx4 acc[T::FM][T::FN];
@@ -306,6 +307,20 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
       __builtin_amdgcn_sched_barrier(0);
     });
   };
+  // A phase's reads of a half of A or B, spread over the first three quarters of
+  // its products: four waves that read two at a time would wait for the LDS.
+  auto reads = [&](auto count, int q, auto&& read) {
+    constexpr int N = 2 * decltype(count)::value, SPAN = kMma * 3 / 4 > 0 ? kMma * 3 / 4 : 1;
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+      if (r * SPAN / N == q) read(r >> 1, r & 1);
+  };
+  auto read_a = [&](Fragment<F32>(&x)[HA], int first, int q) {
+    reads(std::integral_constant<int, HA>{}, q, [&](int i, int half) { fetch(x[i], fa, first + i, half, F32 ? scale_a(first + i) : 0.f); });
+  };
+  auto read_b = [&](Fragment<F32>(&x)[HB], int first, int q) {
+    reads(std::integral_constant<int, HB>{}, q, [&](int j, int half) { fetch(x[j], fb, first + j, half, F32 ? scale_b(first + j) : 0.f); });
+  };
   const std::integral_constant<int, 0> first{};
   const std::integral_constant<int, 1> second{};
 
@@ -315,49 +330,46 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
       aim(i);
 #pragma unroll
       for (int q = 0; q < kLoads; ++q) load(q);
-      advance();
     }
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-    read_scales(kc);
+    kc = k0;
+    read_scales();
 #pragma unroll
-    for (int i = 0; i < HA; ++i) a0[i] = fetch(fa, i, F32 ? scale_a(i) : 0.f);
-#pragma unroll
-    for (int j = 0; j < HB; ++j) b0[j] = fetch(fb, j, F32 ? scale_b(j) : 0.f);
+    for (int q = 0; q < kMma; ++q) {
+      read_a(a0, 0, q);
+      read_b(b0, 0, q);
+    }
     use_scales();
     __builtin_amdgcn_sched_barrier(0);
     int buf = 0;
     for (int turn = 0; turn < turns; ++turn) {
-      aim(buf);
-      buf ^= 1;
       phase(first, first, a0, b0, [&](int q) {
-        if (q < HB) b1[q] = fetch(fb, HB + q, F32 ? scale_b(HB + q) : 0.f);
+        if (q == 0) aim(buf);
+        read_b(b1, HB, q);
       });
-      phase(first, second, a0, b1, [&](int q) {
-        if (q < HA) a1[q] = fetch(fa, HA + q, F32 ? scale_a(HA + q) : 0.f);
-      });
+      phase(first, second, a0, b1, [&](int q) { read_a(a1, HA, q); });
       other_buffer();
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
       // the next step's first fragments, and the loads of the one after it
-      constexpr int kEach = (kLoads + 2 * kMma - 1) / (2 * kMma);
       auto loads_at = [&](int q) {
 #pragma unroll
-        for (int e = 0; e < kEach; ++e)
-          if (q * kEach + e < kLoads) load(q * kEach + e);
+        for (int e = 0; e < kLoads; ++e)
+          if (e * 2 * kMma / kLoads == q) load(e);
       };
       ++kc;
-      read_scales(kc);
+      buf ^= 1;
       phase(second, first, a1, b0, [&](int q) {
-        if (q < HA) a0[q] = fetch(fa, q, F32 ? scale_a(q) : 0.f);
+        if (q == 0) read_scales();
+        read_a(a0, 0, q);
         loads_at(q);
       });
       phase(second, second, a1, b1, [&](int q) {
-        if (q < HB) b0[q] = fetch(fb, q, F32 ? scale_b(q) : 0.f);
+        read_b(b0, 0, q);
         loads_at(kMma + q);
       });
       use_scales();
-      advance();
     }
-    // the last loads (zeros) have landed: LDS is free
+    // the last loads (zeros) have landed
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
@@ -401,19 +413,19 @@ void start(const ProductArgs& a, hipStream_t s) {
 hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s) {
   if (a.f32) {
     if (a.by_expert)
-      start<Tile<4, 4, true, false, 2>>(a, s);
+      start<Tile<4, 4, 2, 2, true, false, 2>>(a, s);
     else
-      start<Tile<4, 4, true, true, 2>>(a, s);
+      start<Tile<4, 4, 2, 2, true, true, 2>>(a, s);
   } else if (tile == kProduct256) {
     if (a.by_expert)
-      start<Tile<8, 8, false, false, 1>>(a, s);
+      start<Tile<8, 8, 2, 2, false, false, 1>>(a, s);
     else
-      start<Tile<8, 8, false, true, 1>>(a, s);
+      start<Tile<8, 8, 2, 2, false, true, 1>>(a, s);
   } else {
     if (a.by_expert)
-      start<Tile<4, 4, false, false, 2>>(a, s);
+      start<Tile<4, 4, 2, 2, false, false, 2>>(a, s);
     else
-      start<Tile<4, 4, false, true, 2>>(a, s);
+      start<Tile<4, 4, 2, 2, false, true, 2>>(a, s);
   }
   return hipGetLastError();
 }

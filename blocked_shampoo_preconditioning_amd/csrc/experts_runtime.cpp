@@ -115,6 +115,8 @@ int route(const shampoo_route_t* a, Route what, const char* name, void* hip_stre
 // -------------------------------------------------------- products in 8 bits
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 18);  // padded rows of 1024 experts stay in 32 bits
 
+constexpr int64_t kMaxSavedRows = (int64_t(1) << 23) - (int64_t(1) << 18);  // 256 columns of them stay within 32-bit byte offsets
+
 int64_t blocks_of(int64_t n) { return (n + she::kBlock - 1) / she::kBlock; }
 
 int check_sizes(int64_t in, int64_t out, int32_t experts, int32_t dtype) {
@@ -278,6 +280,7 @@ int forward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t 
   RC(check_array("x", a->x, a->source ? a->x_rows : a->rows, a->in, a->ld_x, e));
   RC(check_array("y", a->y, a->rows, a->out, a->ld_y, e));
   if (a->saved && !aligned(a->saved, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "saved is not aligned to 256 bytes");
+  if (a->saved && a->rows > kMaxSavedRows) return invalid("rows must be at most 2^23 - 2^18 where they are saved for dw");
   const ProductPlan p = plan_product(a, false);
   RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
   if (a->rows == 0) return SHAMPOO_OK;
@@ -304,6 +307,7 @@ int backward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t
     RC(check_array("dx", a->dx, a->rows, a->in, a->ld_dx, e));
   }
   if (a->dw) {
+    if (a->rows > kMaxSavedRows) return invalid("rows must be at most 2^23 - 2^18 where dw is wanted");
     if (a->rows > 0) RC(check_aligned("saved", a->saved, 256));
     RC(check_matrices("dw", a->dw, a->experts, a->in, a->out, a->ld_dw, a->stride_dw, e));
   }

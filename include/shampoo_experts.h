@@ -104,7 +104,8 @@ typedef struct {
 int shampoo_quantize_weight(const shampoo_weight8_t* a, void* hip_stream);
 
 typedef struct {
-  int64_t rows;           /* 0 .. 2^31 - 2^18: of y, dy, dx and of x       */
+  int64_t rows;           /* 0 .. 2^31 - 2^18: of y, dy, dx and of x; with saved
+                             or dw at most 2^23 - 2^18                     */
   int64_t in, out;        /* 1 .. 2^21                                     */
   int32_t experts, dtype; /* matrices, 1 .. 1024; dtype of x, y, dy, dx, dw */
   const int32_t* offsets; /* experts + 1, or NULL: one matrix, all rows    */

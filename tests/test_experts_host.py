@@ -133,6 +133,7 @@ def test_product_sizes(lib, over, code):
     (dict(values=0), FAKE, 1 << 30, INVALID), (dict(values=FAKE + 8), FAKE, 1 << 30, MISALIGNED), (dict(scales=0), FAKE, 1 << 30, INVALID),
     (dict(x=0), FAKE, 1 << 30, INVALID), (dict(ld_x=199), FAKE, 1 << 30, INVALID), (dict(x=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
     (dict(y=0), FAKE, 1 << 30, INVALID), (dict(ld_y=1), FAKE, 1 << 30, INVALID), (dict(saved=FAKE + 16), FAKE, 1 << 30, MISALIGNED),
+    (dict(rows=1 << 23), FAKE, 1 << 50, INVALID),
     ({}, 0, 1 << 30, INVALID), ({}, FAKE + 16, 1 << 30, MISALIGNED), ({}, FAKE, 1000, SMALL)])
 def test_product_forward_refusals(lib, over, ws, size, code):
     assert lib.shampoo_product8_forward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
@@ -141,7 +142,7 @@ def test_product_forward_refusals(lib, over, ws, size, code):
 @pytest.mark.parametrize("over,ws,size,code", [
     (dict(back_values=0), FAKE, 1 << 30, INVALID), (dict(back_scales=FAKE + 1), FAKE, 1 << 30, MISALIGNED), (dict(dy=0), FAKE, 1 << 30, INVALID),
     (dict(ld_dy=299), FAKE, 1 << 30, INVALID), (dict(ld_dx=199), FAKE, 1 << 30, INVALID), (dict(dx=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
-    (dict(saved=0), FAKE, 1 << 30, INVALID), (dict(ld_dw=299), FAKE, 1 << 30, INVALID), (dict(stride_dw=59999), FAKE, 1 << 30, INVALID),
+    (dict(rows=1 << 23), FAKE, 1 << 50, INVALID), (dict(saved=0), FAKE, 1 << 30, INVALID), (dict(ld_dw=299), FAKE, 1 << 30, INVALID), (dict(stride_dw=59999), FAKE, 1 << 30, INVALID),
     ({}, 0, 0, INVALID), ({}, FAKE, 1000, SMALL)])
 def test_product_backward_refusals(lib, over, ws, size, code):
     assert lib.shampoo_product8_backward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
