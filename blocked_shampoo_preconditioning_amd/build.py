@@ -4,7 +4,7 @@
 
 Compiles the HIP kernels (csrc/kernels.hip, csrc/tensor_kernels.hip and the
 layer operators' csrc/layer_gemm.hip, layer_decode.hip, layer_norm.hip,
-experts_route.hip, experts_quantize.hip, experts_product.hip) and the host runtime (csrc/runtime.cpp, roots.cpp,
+experts_route.hip, experts_quantize.hip, experts_product.hip, experts_few.hip) and the host runtime (csrc/runtime.cpp, roots.cpp,
 tensor_runtime.cpp, layer_runtime.cpp, experts_runtime.cpp) with hipcc into one shared library next to this file. Packed fp32 instructions are disabled for the
 device code (-packed-fp32-ops); hipcc's host pass warns that it does not know
 that feature, which is harmless.
@@ -23,7 +23,7 @@ LIB_NAME = "libshampoo_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "tensor_kernels.hip", "layer_gemm.hip",
                                             "layer_decode.hip", "layer_norm.hip", "experts_route.hip", "experts_quantize.hip",
-                                            "experts_product.hip", "runtime.cpp", "roots.cpp", "tensor_runtime.cpp",
+                                            "experts_product.hip", "experts_few.hip", "runtime.cpp", "roots.cpp", "tensor_runtime.cpp",
                                             "layer_runtime.cpp", "experts_runtime.cpp")]
 ARCH = "gfx950"
 

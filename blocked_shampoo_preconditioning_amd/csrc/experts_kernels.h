@@ -1,5 +1,5 @@
 // Launchers of the experts' kernels (experts_route.hip, experts_quantize.hip,
-// experts_product.hip), called by the host side
+// experts_product.hip, experts_few.hip), called by the host side
 // of the C ABI (experts_runtime.cpp). Not public.
 #pragma once
 
@@ -121,5 +121,25 @@ struct ProductArgs {
 enum ProductTile { kProduct256, kProduct128 };
 constexpr int product_tile(ProductTile t) { return t == kProduct256 ? 256 : 128; }
 hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s);
+
+// Rows of tokens, 64 at most in all, against one matrix an expert, in one launch:
+// x is quantized as it is read.
+constexpr int kFewRows = 64;
+struct FewArgs {
+  const void* x;
+  int64_t ld_x;
+  Groups g;                // blocks is not read
+  const int32_t* source;
+  uint32_t slots;
+  int32_t rows_in;
+  const uint8_t *b, *b_scales;
+  int64_t pitch_b, b_stride, b_scale_stride;
+  int32_t b_scale_pitch;
+  int32_t K, N;
+  void* c;
+  int64_t ldc;
+  int32_t f32;
+};
+hipError_t launch_few(const FewArgs& a, hipStream_t s);
 
 }  // namespace she

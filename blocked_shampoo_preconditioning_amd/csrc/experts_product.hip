@@ -22,8 +22,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "experts_kernels.h"
-#include "layer_device.h"
+#include "experts_device.h"
 
 namespace she {
 
@@ -32,10 +31,6 @@ using shl::store8;
 
 namespace {
 
-typedef __attribute__((ext_vector_type(4))) int int4v;
-typedef __attribute__((ext_vector_type(8))) int int8v;
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) const int4v* lds_int4;
 typedef __attribute__((address_space(3))) const uint32_t* lds_word;
@@ -105,16 +100,6 @@ struct Fragment<true> {
   bf16x8 k[4];
 };
 
-// Four bytes in 8 bits times a scale (its exponent), exactly.
-__device__ __forceinline__ void widen(int w, float scale, bf16x8& out, int at) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
-  out[at] = a[0];
-  out[at + 1] = a[1];
-  out[at + 2] = b[0];
-  out[at + 3] = b[1];
-}
-
 template <class T>
 __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   constexpr bool F32 = T::F32;
@@ -127,16 +112,22 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   // operands in its L2.
   const uint32_t tn = (g.N + T::BN - 1) / T::BN;
   const uint32_t tm = g.by_expert ? (g.M + T::BM - 1) / T::BM : g.tiles ? static_cast<uint32_t>(*g.tile_count) : static_cast<uint32_t>(g.row_tiles);
-  const uint32_t tiles = tm * tn, all = g.by_expert ? tiles * g.experts : tiles;
-  const uint32_t per = (all + 7) / 8;
-  if (blockIdx.x / 8 >= per) return;
-  uint32_t id = blockIdx.x % 8 * per + blockIdx.x / 8;
-  if (id >= all) return;
+  const uint32_t tiles = tm * tn, xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
+  const uint32_t per = (tiles + 7) / 8;  // of an XCD, of each expert
   int expert = 0;
-  if (g.by_expert) {
-    expert = static_cast<int>(id / tiles);
-    id -= expert * tiles;
+  uint32_t id;
+  if (g.by_expert && tiles < 16) {
+    // fewer tiles of an expert than two an XCD: all experts' in turn
+    expert = static_cast<int>(blockIdx.x / tiles);
+    id = blockIdx.x - expert * tiles;
+  } else {
+    // experts have sums of different length: each XCD takes its part of every
+    // expert's tiles, another one for each (eight experts of 16384 x 2048 x 2048
+    // bf16: DW_SPLIT us; with an expert an XCD 126)
+    expert = static_cast<int>(nth / per);
+    id = (xcd + expert) % 8 * per + (nth - expert * per);
   }
+  if (expert >= (g.by_expert ? g.experts : 1) || id >= tiles) return;
   const uint32_t group = id / (4 * tn);
   const uint32_t in_group = min(4u, tm - 4 * group);
   id -= group * 4 * tn;
@@ -258,10 +249,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
 #pragma unroll
     for (int i = 0; i < SB; ++i) sb[i] = T::BBLOCK ? sb2[i] >> (kc & 3) * 8 : sb2[i];
   };
-  auto scale_a = [&](int i) { return __uint_as_float((sa2[i >> 2] >> (8 * (i & 3)) & 255u) << 23); };
+  auto scale_a = [&](int i) { return value_of(sa2[i >> 2] >> (8 * (i & 3)) & 255u); };
   auto scale_b = [&](int j) {
     const uint32_t s = T::BBLOCK ? sb2[0] >> (kc & 3) * 8 : sb2[T::BBLOCK ? 0 : j >> 2] >> (8 * (j & 3));
-    return __uint_as_float((s & 255u) << 23);
+    return value_of(s & 255u);
   };
   // half of operand f: chunk q4 or q4 + 4 of its row
   auto fetch = [&](Fragment<F32>& x, uint32_t base, int f, int half, float scale) {
@@ -403,8 +394,8 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(ProductArgs g)
 template <class T>
 void start(const ProductArgs& a, hipStream_t s) {
   const int64_t tn = (a.N + T::BN - 1) / T::BN;
-  const int64_t tm = a.by_expert ? static_cast<int64_t>((a.M + T::BM - 1) / T::BM) * a.experts : a.row_tiles;
-  const uint32_t grid = static_cast<uint32_t>((tm * tn + 7) / 8 * 8);
+  const int64_t tiles = (a.by_expert ? (a.M + T::BM - 1) / T::BM : a.row_tiles) * tn, experts = a.by_expert ? a.experts : 1;
+  const uint32_t grid = static_cast<uint32_t>(a.by_expert && tiles < 16 ? tiles * experts : (tiles + 7) / 8 * 8 * experts);
   if (grid) product_kernel<T><<<grid, T::NT, 0, s>>>(a);
 }
 

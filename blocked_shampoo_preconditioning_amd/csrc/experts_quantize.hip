@@ -10,8 +10,7 @@
 // columns each, loaded at once and kept in registers, so that one read of x gives
 // the values by rows, by columns or both. What comes by columns is transposed
 // through LDS. Memory bounds it: 2 or 4 bytes in, 1 or 2 out an element.
-#include "experts_kernels.h"
-#include "layer_device.h"
+#include "experts_device.h"
 
 namespace she {
 
@@ -23,24 +22,6 @@ using shl::unpack8;
 namespace {
 
 constexpr int kThreads = 256;
-
-// Magnitude bits that count for a scale: none of what is not finite.
-__device__ __forceinline__ uint32_t magnitude(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u > 0x7f7fffffu ? 0u : u;
-}
-// The scale's biased exponent: 448 = 1.75 * 2^8, so a magnitude 1.f * 2^x takes x - 8,
-// and one more where 1.f is over 1.75.
-__device__ __forceinline__ uint32_t scale_of(uint32_t amax) {
-  const int e = static_cast<int>((amax + 0x1fffffu) >> 23) - 8;
-  return static_cast<uint32_t>(max(e, 1));
-}
-__device__ __forceinline__ float inverse_of(uint32_t scale) { return __uint_as_float((254u - scale) << 23); }
-
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
-}
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
@@ -65,7 +46,7 @@ struct Found {
 __device__ __forceinline__ void find_group(const Groups& g, int p, int tile_blocks, int32_t* first_block, Found* out) {
   const int lane = threadIdx.x & 63, each = (g.experts + 63) / 64;
   const int from = min(lane * each, g.experts), to = min(from + each, g.experts);
-  auto row = [&](int e) { return min(max(g.offsets[e], 0), g.n); };
+  auto row = [&](int e) { return group_row(g, e); };
   auto blocks_of = [&](int lo, int hi) { return hi > lo ? (hi - lo + kBlock - 1) / kBlock : 0; };
   int blocks = 0, tiles = 0;
   for (int e = from; e < to; ++e) {

@@ -192,10 +192,15 @@ size_t saved_size(const shampoo_product8_t* a) {
   return static_cast<size_t>(c.o);
 }
 
+// Up to 64 rows that nothing is kept of go in one launch without a workspace.
+bool few_rows(const shampoo_product8_t* a, bool backward) {
+  return a->rows <= she::kFewRows && !(backward ? a->dw : a->saved);
+}
+
 ProductPlan plan_product(const shampoo_product8_t* a, bool backward) {
   ProductPlan p;
   p.blocks = row_blocks(a);
-  if (p.blocks == 0) return p;
+  if (p.blocks == 0 || few_rows(a, backward)) return p;
   const int64_t k = backward ? a->out : a->in, n = backward ? a->in : a->out;
   const int64_t kb = blocks_of(k), bytes = p.blocks * kb * she::kBlock * she::kBlock;
   const bool rows = !backward || a->dx, cols = backward && a->dw;
@@ -273,6 +278,34 @@ she::ProductArgs row_product(const shampoo_product8_t* a, const ProductPlan& p, 
   return g;
 }
 
+hipError_t few_product(const shampoo_product8_t* a, bool gather, const void* x, int64_t ld, const void* values, const void* scales, int64_t k, int64_t n,
+                       void* c, int64_t ldc, hipStream_t s) {
+  const int64_t kb = blocks_of(k), scale_pitch = (kb + 3) / 4 * 4;
+  she::FewArgs f{};
+  f.x = x;
+  f.ld_x = ld;
+  f.g = she::Groups{a->offsets, static_cast<int32_t>(a->rows), a->experts, 0};
+  f.slots = 1;
+  f.rows_in = static_cast<int32_t>(a->rows);
+  f.b = static_cast<const uint8_t*>(values);
+  f.b_scales = static_cast<const uint8_t*>(scales);
+  f.pitch_b = kb * she::kBlock;
+  f.b_stride = n * f.pitch_b;
+  f.b_scale_stride = blocks_of(n) * scale_pitch;
+  f.b_scale_pitch = static_cast<int32_t>(scale_pitch);
+  f.K = static_cast<int32_t>(k);
+  f.N = static_cast<int32_t>(n);
+  f.c = c;
+  f.ldc = ldc;
+  f.f32 = a->dtype == SHAMPOO_F32;
+  if (gather) {
+    f.source = a->source;
+    f.slots = static_cast<uint32_t>(a->slots);
+    f.rows_in = static_cast<int32_t>(a->x_rows);
+  }
+  return she::launch_few(f, s);
+}
+
 int forward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t s) {
   const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
   RC(check_aligned("values", a->values, 16));
@@ -284,6 +317,10 @@ int forward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t 
   const ProductPlan p = plan_product(a, false);
   RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
   if (a->rows == 0) return SHAMPOO_OK;
+  if (few_rows(a, false)) {
+    const hipError_t e = few_product(a, a->source != nullptr, a->x, a->ld_x, a->values, a->scales, a->in, a->out, a->y, a->ld_y, s);
+    return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_product8_forward");
+  }
   she::QuantizeArgs q = quantize_args(a, p, ws, a->x, a->ld_x, a->in);
   q.source = a->source;
   q.slots = static_cast<uint32_t>(a->source ? a->slots : 1);
@@ -314,7 +351,9 @@ int backward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t
   const ProductPlan p = plan_product(a, true);
   RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
   hipError_t err = hipSuccess;
-  if (p.blocks > 0) {
+  if (a->rows > 0 && few_rows(a, true)) {
+    err = few_product(a, false, a->dy, a->ld_dy, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx, s);
+  } else if (p.blocks > 0) {
     she::QuantizeArgs q = quantize_args(a, p, ws, a->dy, a->ld_dy, a->out);
     q.slots = 1;
     q.rows_in = static_cast<int32_t>(a->rows);

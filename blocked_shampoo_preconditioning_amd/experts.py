@@ -311,7 +311,7 @@ def product8_forward(x, w8, plan=None, gather=False, save=False):
         size = _known_size(("saved", key), "shampoo_product8_saved_size", _PRODUCT.pack(*head, *_NO_PRODUCT))
         saved = torch.empty(size, dtype=torch.uint8, device=x.device)
     args = _PRODUCT.pack(*head, values, scales, 0, 0, px, lx, y.data_ptr(), n_out, saved.data_ptr() if save else 0, 0, 0, 0, 0, 0, 0, 0)
-    size = _known_size(("forward", key), "shampoo_product8_workspace_size", args, 0)
+    size = _known_size(("forward", key, save), "shampoo_product8_workspace_size", args, 0)
     ws, keep = _workspace(size, x)
     _call("shampoo_product8_forward", args, x.get_device(), ws, size)
     return (y, saved) if save else y

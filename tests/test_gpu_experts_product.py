@@ -118,7 +118,13 @@ def check_product(rows, n_in, n_out, dtype, n_experts=0, ids=None, slots=1, gath
     assert not uneven or not n_experts
     w_bits = ref.rounded(w[0], (0, 1)) if uneven else None
     close("y", y, want, n_in, ref.largest_of_groups(ref.rounded(xs, (1,)), w_bits) if uneven else None)
-    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(experts.product8_forward(padded(x, pad), w8, plan, gather=gather)))
+    # up to 64 rows that nothing is kept of go another way, whose sums may differ by their order
+    plain = experts.product8_forward(padded(x, pad), w8, plan, gather=gather)
+    if rows <= 64:
+        close("y alone", plain, want, n_in, ref.largest_of_groups(ref.rounded(xs, (1,)), w_bits) if uneven else None)
+        assert torch.equal(torch.nan_to_num(plain), torch.nan_to_num(experts.product8_forward(padded(x, pad), w8, plan, gather=gather)))
+    else:
+        assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(plain))
     dx, dw = experts.product8_backward(padded(dy, pad), w8, saved, plan)
     clean = torch.where(torch.arange(rows)[:, None] < kept, dy, torch.zeros((), dtype=dy.dtype))
     want = ref.product(clean, w.transpose(1, 2), offsets)
@@ -128,7 +134,11 @@ def check_product(rows, n_in, n_out, dtype, n_experts=0, ids=None, slots=1, gath
     close("dw", dw if n_experts else dw[None], ref.product_dw(xs, clean, offsets, max(1, n_experts)), rows,
           ref.largest_of_groups(ref.rounded(xs, (0,)).t(), ref.rounded(clean, (0,))) if uneven else None)
     only_dx, none = experts.product8_backward(dy.cuda(), w8, None, plan, need_dw=False)
-    assert none is None and torch.equal(torch.nan_to_num(only_dx), torch.nan_to_num(dx))
+    assert none is None
+    if rows <= 64:
+        close("dx alone", only_dx, want, n_out, ref.largest_of_groups(ref.rounded(clean, (1,)), w_bits.t()) if uneven else None)
+    else:
+        assert torch.equal(torch.nan_to_num(only_dx), torch.nan_to_num(dx))
     none, only_dw = experts.product8_backward(dy.cuda(), w8, saved, plan, need_dx=False)
     assert none is None and torch.equal(torch.nan_to_num(only_dw), torch.nan_to_num(dw))
 
