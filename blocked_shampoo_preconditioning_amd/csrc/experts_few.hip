@@ -22,7 +22,6 @@ using shl::fetch8;
 using shl::floatx4;
 using shl::Raw8;
 using shl::settle8;
-using shl::unpack8;
 
 namespace {
 
@@ -120,23 +119,22 @@ __global__ __launch_bounds__(64 * NW, 2) void few_kernel(FewArgs a) {
     for (int c = 0; c < 4; ++c) row.x[c] = fetch8<F32>(a.x, at, column(kb, c), min(8, max(0, a.K - column(kb, c))));
   };
   auto quantize = [&](int kb, const Row& row) {
-    float v[4][8];
+    Eight<F32> v[4];
     uint32_t top = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      unpack8<F32>(settle8<F32>(row.x[c], column(kb, c), min(8, max(0, a.K - column(kb, c)))), v[c]);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) top = max(top, magnitude(v[c][q]));
+      v[c] = Eight<F32>(settle8<F32>(row.x[c], column(kb, c), min(8, max(0, a.K - column(kb, c)))));
+      top = max(top, v[c].magnitude());
     }
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
     Bytes r;
     r.scale = scale_of(top);
-    const float inv = inverse_of(r.scale);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      r.b[2 * c] = static_cast<int>(pack4(v[c][0] * inv, v[c][1] * inv, v[c][2] * inv, v[c][3] * inv));
-      r.b[2 * c + 1] = static_cast<int>(pack4(v[c][4] * inv, v[c][5] * inv, v[c][6] * inv, v[c][7] * inv));
+      const uint2 w = v[c].bytes(value_of(r.scale));
+      r.b[2 * c] = static_cast<int>(w.x);
+      r.b[2 * c + 1] = static_cast<int>(w.y);
     }
     return r;
   };
