@@ -61,14 +61,55 @@ struct Groups {
   int32_t blocks;  // at least as many as all experts' rows take
 };
 
-// A row tile of a product: `count` rows of the result from `row`, padded rows
-// from 128 * block; expert < 0: rows behind the last expert's, whose results are 0.
-struct RowTile {
-  int32_t expert, block, row, count;
+// C = sum over k of A[m][k] B[n][k] with their scales, on the matrix cores.
+// by_expert 0: rows of tokens against one matrix an expert (y, dx), rows behind the
+// last expert's get 0. 1: for each expert, over its blocks of padded rows (dW).
+struct ProductArgs {
+  const uint8_t *a, *a_scales, *b, *b_scales;
+  int64_t pitch;                     // bytes of a row of a and b
+  int64_t size_a, size_b;            // bytes; of b, one expert's
+  int64_t b_stride, b_scale_stride;  // from an expert to the next
+  int32_t a_blocks, b_blocks;        // of 128 rows: the scales' [K block][blocks][128], or b's [blocks][b_scale_pitch]
+  int32_t b_scale_pitch;
+  int32_t M, N, k_blocks;
+  int32_t by_expert;
+  void* c;
+  int64_t ldc, c_stride;
 };
+// Rows and columns of a result tile. kProduct128Deep: one workgroup a CU with four
+// steps' operands in LDS, for few tiles.
+enum ProductTile { kProduct256, kProduct128, kProduct128Deep };
+constexpr int product_tile(ProductTile t) { return t == kProduct256 ? 256 : 128; }
+// One or two products in one launch, of one type. Their work, a record for each
+// tile, is written by the launch that quantizes an operand: who has which rows is on
+// the GPU, and a workgroup that worked out its tile itself would wait for it in front
+// of its first loads (measured: 5 us of a launch).
+constexpr int kMaxProducts = 2;
+struct WorkRecord {
+  uint64_t a, b;              // addresses of the tile's first row and K block
+  uint32_t size_a, size_b;    // bytes from there on (at most 2^32 - 16)
+  uint64_t a_scales, b_scales;
+  uint32_t a_scales_size, b_scales_size;
+  uint64_t c;
+  int32_t turns;              // K blocks; < 0: no tile, see below
+  uint32_t shape;             // rows, columns << 10, words << 20, second << 21, product << 22
+};
+static_assert(sizeof(WorkRecord) == 64, "");
+constexpr int kNoTile = -1, kNoTileNorBehind = -2;
+struct Products {
+  ProductArgs p[kMaxProducts];
+  int32_t count, experts, f32;
+  WorkRecord* work;  // [8][per]: an XCD's tiles in order
+  int32_t per;
+  int32_t tile;      // ProductTile
+};
+// Tiles an XCD can have at most, for Products::per.
+int64_t work_length(const Products& a, int64_t rows, bool grouped);
+hipError_t launch_products(const Products& a, hipStream_t s);
 
 // 128 x 128 tiles of x in 8 bits: by rows (a scale for each row of the tile), by
-// columns (a scale for each column, values transposed), either or both.
+// columns (a scale for each column, values transposed), either or both; and the
+// records of the products' work.
 struct QuantizeArgs {
   const void* x;
   int64_t ld;
@@ -79,11 +120,7 @@ struct QuantizeArgs {
   int32_t rows_in;        // rows of x
   uint8_t *by_rows, *row_scales;  // [128 blocks][128 col_blocks], [col_blocks][blocks][128]
   uint8_t *by_cols, *col_scales;  // [128 col_blocks][128 blocks], [blocks][col_blocks][128]
-  // written for the products that follow, where offsets are given
-  int32_t* first_block;   // [experts + 1]: each expert's first block
-  RowTile* tiles;         // [max_tiles]
-  int32_t* tile_count;
-  int32_t tile_blocks, max_tiles;  // blocks of a row tile
+  Products products;
 };
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
 
@@ -96,31 +133,6 @@ struct WeightArgs {
   uint8_t *forward, *forward_scales, *backward, *backward_scales;
 };
 hipError_t launch_quantize_weight(const WeightArgs& a, hipStream_t s);
-
-// C = sum over k of A[m][k] B[n][k] with their scales, on the matrix cores.
-// by_expert 0: rows of tokens against one matrix an expert (y, dx). 1: for each
-// expert, over its blocks of padded rows (dW).
-struct ProductArgs {
-  const uint8_t *a, *a_scales, *b, *b_scales;
-  int64_t pitch_a, pitch_b;        // bytes of a row
-  int64_t size_a, size_b;          // bytes; of b, one expert's
-  int64_t b_stride, b_scale_stride;  // from an expert to the next
-  int32_t a_blocks, b_blocks;      // of 128 rows: the scales' [K block][blocks][128], or b's [blocks][b_scale_pitch]
-  int32_t b_scale_pitch;
-  int32_t M, N, k_blocks;
-  int32_t by_expert, experts;
-  const int32_t* first_block;      // by_expert: K blocks of an expert; NULL: k_blocks
-  const RowTile* tiles;            // NULL: one expert, rows in order
-  const int32_t* tile_count;
-  int32_t row_tiles;               // at most
-  void* c;
-  int64_t ldc, c_stride;
-  int32_t f32;
-};
-// Rows and columns of a result tile.
-enum ProductTile { kProduct256, kProduct128 };
-constexpr int product_tile(ProductTile t) { return t == kProduct256 ? 256 : 128; }
-hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s);
 
 // Rows of tokens, 64 at most in all, against one matrix an expert, in one launch:
 // x is quantized as it is read.

@@ -13,12 +13,17 @@
 // fp32 results: those come from the bf16 instruction with both operands widened,
 // scales included, which is exact, at a quarter of the rate.
 //
-// Operands go from HBM to LDS by direct loads of 16 bytes a lane, double buffered,
-// a K block a step; the scales of a step go the same way, 256 bytes an operand. A
-// step's products are four phases (halves of A by halves of B), and each phase's
-// fragments are read while the one before multiplies, also across the barrier,
-// which sits in the middle: before it the step's last reads are done and the next
-// step has landed.
+// Operands go from HBM to LDS by direct loads of 16 bytes a lane, a K block a step;
+// the scales of a step go the same way, 256 bytes an operand. A step's products are
+// four phases (halves of A by halves of B), and each phase's fragments are read
+// while the one before multiplies, also across the barrier, which sits in the
+// middle: before it the step's last reads are done and the next step has landed,
+// after it the step's place is loaded again.
+//
+// A workgroup stays on its CU and goes through tile after tile, of one product or
+// two, by records that the launch before has written. To the loads a tile's last
+// step is followed by the next tile's first, so that results are stored while the
+// next operands are on their way.
 #include <type_traits>
 #include <utility>
 
@@ -45,28 +50,27 @@ __device__ __forceinline__ void each(F&& f) {
   each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-// FM x FN operands of 16 rows a wave, WM x WN waves.
-template <int FM_, int FN_, int WM_, int WN_, bool F32_, bool BBLOCK_, int WAVES_>
+// FM x FN operands of 16 rows a wave, WM x WN waves; ST steps' operands in LDS.
+template <int FM_, int FN_, int WM_, int WN_, int ST_, bool F32_, int WAVES_>
 struct Tile {
   static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, NW = WM * WN, NT = 64 * NW;
-  static constexpr bool F32 = F32_, BBLOCK = BBLOCK_;  // BBLOCK: B's scales are those of 128 x 128 tiles
+  static constexpr int ST = ST_;
+  static constexpr bool F32 = F32_;
   static constexpr int WAVES = WAVES_;                 // of a SIMD at once
+  static constexpr int GROUPS = WAVES * 4 / NW;        // workgroups of a CU at once
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int A_SCALES = A_BYTES + B_BYTES, B_SCALES = A_SCALES + 256;
   static constexpr int STAGE = B_SCALES + 256;
+  static_assert(BM <= 256 && BN <= 256 && NW >= 2, "");
 };
 
-// A buffer of `left` bytes from base; loads past it give zeros. 4 GiB of them are
-// enough, since a tile's offsets stay under that. Lengths are multiples of 4.
-__device__ __forceinline__ uint32_t buffer_size(int64_t left) {
-  return left <= 0 ? 0u : left > 0xfffffff0ll ? 0xfffffff0u : static_cast<uint32_t>(left);
-}
-__device__ __forceinline__ int4v make_rsrc(uint64_t base) {
+// A buffer of `size` bytes from base; loads past it give zeros.
+__device__ __forceinline__ int4v make_rsrc(uint64_t base, uint32_t size) {
   int4v r;
   r[0] = static_cast<int>(base);
   r[1] = static_cast<int>(base >> 32);
-  r[2] = 0;
+  r[2] = static_cast<int>(size);
   r[3] = 0x00020000;
   return r;
 }
@@ -100,64 +104,25 @@ struct Fragment<true> {
   bf16x8 k[4];
 };
 
+// What this launch does not write, read by the scalar unit: a vector load would wait
+// for all operands that are on their way.
+typedef __attribute__((ext_vector_type(16))) int int16v;
+template <class V>
+__device__ __forceinline__ V scalar_load(const void* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) V*>(reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ uint64_t address(int low, int high) { return static_cast<uint64_t>(static_cast<uint32_t>(high)) << 32 | static_cast<uint32_t>(low); }
+
 template <class T>
-__device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) {
   constexpr bool F32 = T::F32;
+  __shared__ __attribute__((aligned(1024))) char lds[T::ST * T::STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM;
-
-  // Workgroups go round the 8 XCDs; each takes a contiguous range of the tiles, in
-  // groups of four row tiles, so that those in flight on one XCD share their
-  // operands in its L2.
-  const uint32_t tn = (g.N + T::BN - 1) / T::BN;
-  const uint32_t tm = g.by_expert ? (g.M + T::BM - 1) / T::BM : g.tiles ? static_cast<uint32_t>(*g.tile_count) : static_cast<uint32_t>(g.row_tiles);
-  const uint32_t tiles = tm * tn, xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
-  const uint32_t per = (tiles + 7) / 8;  // of an XCD, of each expert
-  int expert = 0;
-  uint32_t id;
-  if (g.by_expert && tiles < 16) {
-    // fewer tiles of an expert than two an XCD: all experts' in turn
-    expert = static_cast<int>(blockIdx.x / tiles);
-    id = blockIdx.x - expert * tiles;
-  } else {
-    // experts have sums of different length: each XCD takes its part of every
-    // expert's tiles, another one for each (eight experts of 16384 x 2048 x 2048
-    // bf16: DW_SPLIT us; with an expert an XCD 126)
-    expert = static_cast<int>(nth / per);
-    id = (xcd + expert) % 8 * per + (nth - expert * per);
-  }
-  if (expert >= (g.by_expert ? g.experts : 1) || id >= tiles) return;
-  const uint32_t group = id / (4 * tn);
-  const uint32_t in_group = min(4u, tm - 4 * group);
-  id -= group * 4 * tn;
-  const uint32_t tcol = id / in_group;
-  const int trow = static_cast<int>(4 * group + id - tcol * in_group);
-  const int n0 = static_cast<int>(tcol) * T::BN;
-
-  // the tile's rows of A and C, and its K blocks
-  int a_block, count, k0 = 0, turns = g.k_blocks;
-  int64_t c_row;
-  if (g.by_expert) {
-    a_block = trow * (T::BM / kBlock);
-    c_row = trow * T::BM;
-    count = min(T::BM, g.M - trow * T::BM);
-    if (g.first_block) {
-      k0 = g.first_block[expert];
-      turns = g.first_block[expert + 1] - k0;
-    }
-  } else if (g.tiles) {
-    const RowTile t = g.tiles[trow];
-    expert = t.expert;
-    a_block = t.block;
-    c_row = t.row;
-    count = t.count;
-    if (expert < 0) expert = 0, turns = 0;
-  } else {
-    a_block = trow * (T::BM / kBlock);
-    c_row = trow * T::BM;
-    count = min(T::BM, g.M - trow * T::BM);
-  }
+  // Workgroups go round the 8 XCDs; this one has every stride-th tile of its XCD's.
+  const int stride = static_cast<int>(gridDim.x / 8);
+  const WorkRecord* mine = all.work + static_cast<int64_t>(blockIdx.x % 8) * all.per;
 
   // A load instruction covers eight rows of 128 bytes: row (instruction * NW + wave)
   // * 8 + lane / 8, place lane % 8. A row's chunk c of 16 bytes sits at place c ^
@@ -170,43 +135,58 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   auto row_off = [&](int j, int64_t pitch) {
     const int row = (j * T::NW + wave) * 8 + (lane >> 3);
     const int r16 = (row & 3) | ((row >> 4) & 3) << 2;
-    return static_cast<uint32_t>(row * pitch + (((lane & 7) ^ swizzle(r16)) << 4));
+    return static_cast<uint32_t>(row * static_cast<uint32_t>(pitch) + (((lane & 7) ^ swizzle(r16)) << 4));
   };
-#pragma unroll
-  for (int j = 0; j < NA; ++j) va[j] = row_off(j, g.pitch_a);
-#pragma unroll
-  for (int j = 0; j < NB; ++j) vb[j] = row_off(j, g.pitch_b);
   const uint32_t lds_base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char*)lds));
 
-  // The buffers begin at the tile's first row and K block, and a step adds to the
-  // loads' scalar offset: every instruction here is paid for in every K step.
-  const int64_t a_at = static_cast<int64_t>(a_block) * kBlock * g.pitch_a + static_cast<int64_t>(k0) * kBlock;
-  const int64_t b_at = n0 * g.pitch_b + static_cast<int64_t>(k0) * kBlock;
-  int4v ra = make_rsrc(reinterpret_cast<uint64_t>(g.a) + a_at);
-  int4v rb = make_rsrc(reinterpret_cast<uint64_t>(g.b) + (g.by_expert ? 0 : expert * g.b_stride) + b_at);
-  const uint32_t na = buffer_size(g.size_a - a_at), nb = buffer_size(g.size_b - b_at);
-  // scales: a wave takes A's (even) or B's, by 4 bytes a lane
-  const bool b_scales = wave & 1, of_blocks = T::BBLOCK && b_scales;
-  const int64_t scale_step = static_cast<int64_t>(b_scales ? g.b_blocks : g.a_blocks) * kBlock;
-  const int64_t s_at = of_blocks ? 0 : k0 * scale_step + (b_scales ? n0 : a_block * kBlock);
-  const int64_t s_size = of_blocks ? static_cast<int64_t>(g.b_blocks) * g.b_scale_pitch : g.k_blocks * scale_step;
-  int4v rs = make_rsrc(reinterpret_cast<uint64_t>(b_scales ? g.b_scales : g.a_scales) + (of_blocks ? expert * g.b_scale_stride : 0) + s_at);
-  const uint32_t ns = buffer_size(s_size - s_at);
-  const uint32_t block_row = min(n0 / kBlock + (lane >> 5), g.b_blocks - 1);  // of_blocks: each half of a wave its 128 columns
-  const uint32_t vs = of_blocks ? block_row * g.b_scale_pitch : lane * 4;
-
-  int step = 0;  // the next to be loaded
+  // Where the loads are: a tile, its buffers, which begin at its first row and K
+  // block, and a step of it, which goes into the loads' scalar offset: every
+  // instruction here is paid for in every K step. Scales: a wave takes A's (even) or
+  // B's, by 4 bytes a lane; those of weights, one for 128 x 128, come as words of four
+  // K blocks, from which `pick` takes the step's for all four of a word's places.
+  const bool b_scales = wave & 1;
+  int4v ra = make_rsrc(0, 0), rb = ra, rs = ra;
+  uint32_t vs = 0, scale_step = 0;
+  int lnext = static_cast<int>(blockIdx.x / 8), lproduct = -1, lstep = 0, lturns = 0;
+  bool lwords = false, lwords_mine = false;
+  auto enter = [&]() __attribute__((always_inline)) {  // the next tile that has steps
+    int16v w = {};
+    int turns = kNoTileNorBehind;
+    do {
+      if (lnext < all.per) w = scalar_load<int16v>(mine + lnext);
+      turns = lnext < all.per ? w[14] : kNoTileNorBehind;
+      lnext += stride;
+    } while (turns == 0 || turns == kNoTile);
+    const bool more = turns > 0;
+    const int product = more ? w[15] >> 22 : 0;
+    const ProductArgs& g = all.p[product];
+    if (product != lproduct) {
+#pragma unroll
+      for (int j = 0; j < NA; ++j) va[j] = row_off(j, g.pitch);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) vb[j] = row_off(j, g.pitch);
+      lproduct = product;
+    }
+    // where nothing is left the loads give zeros
+    ra = make_rsrc(address(w[0], w[1]), more ? w[4] : 0);
+    rb = make_rsrc(address(w[2], w[3]), more ? w[5] : 0);
+    rs = make_rsrc(b_scales ? address(w[8], w[9]) : address(w[6], w[7]), !more ? 0 : b_scales ? w[11] : w[10]);
+    lwords = w[15] >> 20 & 1;
+    lwords_mine = lwords && b_scales;
+    // words: each half of a wave those of its 128 columns
+    vs = lwords_mine ? lane >> 5 && w[15] >> 21 & 1 ? static_cast<uint32_t>(g.b_scale_pitch) : 0u : lane * 4;
+    scale_step = static_cast<uint32_t>(b_scales ? g.b_blocks : g.a_blocks) * kBlock;
+    lturns = more ? turns : 0x7fffffff;
+    lstep = 0;
+  };
   uint32_t at = 0, ks = 0, ss = 0;
+  uint32_t picks[T::ST + 1];  // of the steps from the one that is read on
   auto aim = [&](int buf) {
     at = lds_base + buf * T::STAGE;
-    // past the last step nothing is read: the buffer gets zeros
-    const bool on = step < turns;
-    ra[2] = static_cast<int>(on ? na : 0u);
-    rb[2] = static_cast<int>(on ? nb : 0u);
-    rs[2] = static_cast<int>(on ? ns : 0u);
-    ks = static_cast<uint32_t>(step) * kBlock;
-    ss = of_blocks ? static_cast<uint32_t>(step) & ~3u : static_cast<uint32_t>(step) * static_cast<uint32_t>(scale_step);
-    ++step;
+    ks = static_cast<uint32_t>(lstep) * kBlock;
+    ss = lwords_mine ? static_cast<uint32_t>(lstep) & ~3u : static_cast<uint32_t>(lstep) * scale_step;
+    picks[T::ST] = lwords ? static_cast<uint32_t>(lstep & 3) * 0x01010101u : 0x03020100u;
+    ++lstep;
   };
   auto load = [&](int q) {
     if (q < NA)
@@ -217,6 +197,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
       load_lds4(rs, vs, ss, at + (b_scales ? T::B_SCALES : T::A_SCALES));
   };
   constexpr int kLoads = NA + NB + 1;
+  auto next_pick = [&]() {
+#pragma unroll
+    for (int i = 0; i < T::ST; ++i) picks[i] = picks[i + 1];
+  };
 
   // A lane's places in the reads: row r16 of an operand, chunks q4 and q4 + 4.
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -225,18 +209,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   uint32_t fa = lds_base + (wm * T::FM * 16 + lane_row) * 128 + chunk;
   uint32_t fb = lds_base + T::A_BYTES + (wn * T::FN * 16 + lane_row) * 128 + chunk;
   uint32_t fsa = lds_base + T::A_SCALES + (wm * T::FM * 16 & ~127) + r16 * 8 + (T::FM == 4 ? (wm & 1) * 4 : 0);
-  uint32_t fsb = lds_base + T::B_SCALES + (T::BBLOCK ? (wn * T::FN * 16 & ~127) : (wn * T::FN * 16 & ~127) + r16 * 8 + (T::FN == 4 ? (wn & 1) * 4 : 0));
-  uint32_t flip = T::STAGE;
+  uint32_t fsb = lds_base + T::B_SCALES + (wn * T::FN * 16 & ~127) + r16 * 8 + (T::FN == 4 ? (wn & 1) * 4 : 0);
+  int rbuf = 0;  // the buffer that is read
   auto other_buffer = [&]() {
-    fa += flip, fb += flip, fsa += flip, fsb += flip;
-    flip = 0u - flip;
+    const uint32_t by = ++rbuf == T::ST ? 0u - (T::ST - 1) * T::STAGE : static_cast<uint32_t>(T::STAGE);
+    if (rbuf == T::ST) rbuf = 0;
+    fa += by, fb += by, fsa += by, fsb += by;
   };
 
   // scales: operand f's in byte f % 4 of word f / 4; those of the step that is
   // multiplied, and those of the step that is read
-  constexpr int SA = T::FM / 4, SB = T::BBLOCK ? 1 : T::FN / 4;
+  constexpr int SA = T::FM / 4, SB = T::FN / 4;
   uint32_t sa[SA], sb[SB], sa2[SA], sb2[SB];
-  int kc = 0;  // the step that is read
   auto read_scales = [&]() {
 #pragma unroll
     for (int i = 0; i < SA; ++i) sa2[i] = *reinterpret_cast<lds_word>(fsa + 4 * i);
@@ -247,13 +231,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
 #pragma unroll
     for (int i = 0; i < SA; ++i) sa[i] = sa2[i];
 #pragma unroll
-    for (int i = 0; i < SB; ++i) sb[i] = T::BBLOCK ? sb2[i] >> (kc & 3) * 8 : sb2[i];
+    for (int i = 0; i < SB; ++i) sb[i] = __builtin_amdgcn_perm(sb2[i], sb2[i], picks[0]);
   };
   auto scale_a = [&](int i) { return value_of(sa2[i >> 2] >> (8 * (i & 3)) & 255u); };
-  auto scale_b = [&](int j) {
-    const uint32_t s = T::BBLOCK ? sb2[0] >> (kc & 3) * 8 : sb2[T::BBLOCK ? 0 : j >> 2] >> (8 * (j & 3));
-    return value_of(s & 255u);
-  };
+  auto scale_b = [&](int j) { return value_of(__builtin_amdgcn_perm(sb2[j >> 2], sb2[j >> 2], picks[0]) >> (8 * (j & 3)) & 255u); };
   // half of operand f: chunk q4 or q4 + 4 of its row
   auto fetch = [&](Fragment<F32>& x, uint32_t base, int f, int half, float scale) {
     const uint32_t from = base + (64 * (f >> 2) + 4 * (f & 3)) * 128;
@@ -270,10 +251,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   };
 
   floatx4 acc[T::FM][T::FN];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < T::FM; ++i)
+    for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < T::FN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  };
 
   constexpr int HA = T::FM / 2, HB = T::FN / 2, kMma = HA * HB;
   Fragment<F32> a0[HA], a1[HA], b0[HB], b1[HB];
@@ -285,8 +268,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
     } else {
       const int8v av = __builtin_shufflevector(x.lo, x.hi, 0, 1, 2, 3, 4, 5, 6, 7);
       const int8v bv = __builtin_shufflevector(y.lo, y.hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[i][j], 0, 0, T::BBLOCK ? 0 : j & 3,
-                                                                   static_cast<int>(sb[T::BBLOCK ? 0 : j >> 2]), i & 3, static_cast<int>(sa[i >> 2]));
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[i][j], 0, 0, j & 3, static_cast<int>(sb[j >> 2]), i & 3,
+                                                                   static_cast<int>(sa[i >> 2]));
     }
   };
   // One phase: products of half IH of A and half JH of B, with more(q) behind the q-th.
@@ -315,109 +298,132 @@ __device__ __forceinline__ void product_tile(const ProductArgs& g, char* lds) {
   const std::integral_constant<int, 0> first{};
   const std::integral_constant<int, 1> second{};
 
-  if (turns > 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      aim(i);
-#pragma unroll
-      for (int q = 0; q < kLoads; ++q) load(q);
-    }
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-    kc = k0;
-    read_scales();
-#pragma unroll
-    for (int q = 0; q < kMma; ++q) {
-      read_a(a0, 0, q);
-      read_b(b0, 0, q);
-    }
-    use_scales();
-    __builtin_amdgcn_sched_barrier(0);
-    int buf = 0;
-    for (int turn = 0; turn < turns; ++turn) {
-      phase(first, first, a0, b0, [&](int q) {
-        if (q == 0) aim(buf);
-        read_b(b1, HB, q);
-      });
-      phase(first, second, a0, b1, [&](int q) { read_a(a1, HA, q); });
-      other_buffer();
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      // the next step's first fragments, and the loads of the one after it
-      auto loads_at = [&](int q) {
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e)
-          if (e * 2 * kMma / kLoads == q) load(e);
-      };
-      ++kc;
-      buf ^= 1;
-      phase(second, first, a1, b0, [&](int q) {
-        if (q == 0) read_scales();
-        read_a(a0, 0, q);
-        loads_at(q);
-      });
-      phase(second, second, a1, b1, [&](int q) {
-        read_b(b0, 0, q);
-        loads_at(kMma + q);
-      });
-      use_scales();
-    }
-    // the last loads (zeros) have landed
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
+  // the tile that is multiplied: c, turns and shape of its record
+  int cnext = static_cast<int>(blockIdx.x / 8), turns = kNoTileNorBehind, turn = 0;
+  int4v c{};
+  auto next_tile = [&]() __attribute__((always_inline)) {
+    do {
+      if (cnext < all.per) c = scalar_load<int4v>(&mine[cnext].c);
+      turns = cnext < all.per ? c[2] : kNoTileNorBehind;
+      cnext += stride;
+    } while (turns == kNoTile);
+    turn = 0;
+  };
+  next_tile();
+  if (turns == kNoTileNorBehind) return;
 
-  // A lane's accumulators of four operands of B are 16 consecutive columns of a row.
-  char* c = static_cast<char*>(g.c) + (g.by_expert ? expert * g.c_stride * (F32 ? 4 : 2) : 0);
+  // the first tiles' first steps; their first fragments
+#pragma unroll 1
+  for (int i = 0; i < T::ST; ++i) {
+    if (lstep == lturns) enter();
+    aim(i);
+    next_pick();
 #pragma unroll
-  for (int i = 0; i < T::FM; ++i) {
-    const int row = wm * T::FM * 16 + 64 * (i >> 2) + 4 * (i & 3) + lane_row;
-    if (row >= count) continue;
+    for (int q = 0; q < kLoads; ++q) load(q);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((T::ST - 1) * kLoads) : "memory");
+  read_scales();
 #pragma unroll
-    for (int J = 0; J < T::FN / 4; ++J) {
-      const int col = n0 + wn * T::FN * 16 + 64 * J + 16 * q4;
+  for (int q = 0; q < kMma; ++q) {
+    read_a(a0, 0, q);
+    read_b(b0, 0, q);
+  }
+  use_scales();
+  __builtin_amdgcn_sched_barrier(0);
+  int buf = 0;
+  bool stores = false;  // whether some may be behind the loads that are out
+#pragma unroll 1
+  do {
+    clear();
+    // as many steps as neither the loads nor the products leave their tile
+#pragma unroll 1
+    while (turn < turns) {
+      if (lstep == lturns) enter();
+      const int until = turn + min(turns - turn, lturns - lstep);
+#pragma unroll 1
+      for (; turn < until; ++turn) {
+        phase(first, first, a0, b0, [&](int q) {
+          if (q == 0) aim(buf);
+          read_b(b1, HB, q);
+        });
+        phase(first, second, a0, b1, [&](int q) { read_a(a1, HA, q); });
+        other_buffer();
+        // the next step has landed: what is still out are the loads of those behind it
+        if (T::ST > 2 && !stores)
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((T::ST - 2) * kLoads) : "memory");
+        else
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        stores = false;
+        // the next step's first fragments, and the loads of the one that takes this one's place
+        auto loads_at = [&](int q) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = acc[i][4 * J + 2 * h + q / 4][q % 4];
-        const int n = min(8, g.N - col - 8 * h);
-        if (n > 0) store8(c, (c_row + row) * g.ldc + col + 8 * h, n, F32, v);
+          for (int e = 0; e < kLoads; ++e)
+            if (e * 2 * kMma / kLoads == q) load(e);
+        };
+        if (++buf == T::ST) buf = 0;
+        next_pick();
+        phase(second, first, a1, b0, [&](int q) {
+          if (q == 0) read_scales();
+          read_a(a0, 0, q);
+          loads_at(q);
+        });
+        phase(second, second, a1, b1, [&](int q) {
+          read_b(b0, 0, q);
+          loads_at(kMma + q);
+        });
+        use_scales();
       }
     }
-  }
+
+    // A lane's accumulators of four operands of B are 16 consecutive columns of a row.
+    char* out = reinterpret_cast<char*>(address(c[0], c[1]));
+    const int rows = c[3] & 1023, cols = c[3] >> 10 & 1023;
+    const int64_t ldc = all.p[c[3] >> 22].ldc;
+    // (not to be worked out ahead of the loop: registers are for its operands)
+    int row0 = wm * T::FM * 16 + lane_row, col0 = wn * T::FN * 16 + 16 * q4;
+    asm volatile("" : "+v"(row0), "+v"(col0));
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) {
+      const int row = row0 + 64 * (i >> 2) + 4 * (i & 3);
+      if (row >= rows) continue;
+#pragma unroll
+      for (int J = 0; J < T::FN / 4; ++J) {
+        const int col = col0 + 64 * J;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = acc[i][4 * J + 2 * h + q / 4][q % 4];
+          const int n = min(8, cols - col - 8 * h);
+          if (n > 0) store8(out, row * ldc + col + 8 * h, n, F32, v);
+        }
+      }
+    }
+    stores = true;
+    next_tile();
+  } while (turns != kNoTileNorBehind);
+  // the last loads (zeros) have landed
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <class T>
-__global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(ProductArgs g) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
-  product_tile<T>(g, lds);
-}
-
-template <class T>
-void start(const ProductArgs& a, hipStream_t s) {
-  const int64_t tn = (a.N + T::BN - 1) / T::BN;
-  const int64_t tiles = (a.by_expert ? (a.M + T::BM - 1) / T::BM : a.row_tiles) * tn, experts = a.by_expert ? a.experts : 1;
-  const uint32_t grid = static_cast<uint32_t>(a.by_expert && tiles < 16 ? tiles * experts : (tiles + 7) / 8 * 8 * experts);
+void start(const Products& a, hipStream_t s) {
+  // as many workgroups as the card takes at once
+  const int fit = 32 * T::GROUPS;
+  const uint32_t grid = static_cast<uint32_t>(8 * (a.per < fit ? a.per : fit));
   if (grid) product_kernel<T><<<grid, T::NT, 0, s>>>(a);
 }
 
 }  // namespace
 
-hipError_t launch_product(const ProductArgs& a, ProductTile tile, hipStream_t s) {
-  if (a.f32) {
-    if (a.by_expert)
-      start<Tile<4, 4, 2, 2, true, false, 2>>(a, s);
-    else
-      start<Tile<4, 4, 2, 2, true, true, 2>>(a, s);
-  } else if (tile == kProduct256) {
-    if (a.by_expert)
-      start<Tile<8, 8, 2, 2, false, false, 1>>(a, s);
-    else
-      start<Tile<8, 8, 2, 2, false, true, 1>>(a, s);
-  } else {
-    if (a.by_expert)
-      start<Tile<4, 4, 2, 2, false, false, 2>>(a, s);
-    else
-      start<Tile<4, 4, 2, 2, false, true, 2>>(a, s);
-  }
+hipError_t launch_products(const Products& a, hipStream_t s) {
+  const bool deep = a.tile == kProduct128Deep;
+  if (a.f32)
+    deep ? start<Tile<4, 4, 2, 2, 4, true, 1>>(a, s) : start<Tile<4, 4, 2, 2, 2, true, 2>>(a, s);
+  else if (a.tile == kProduct256)
+    start<Tile<8, 8, 2, 2, 2, false, 1>>(a, s);
+  else
+    deep ? start<Tile<4, 4, 2, 2, 4, false, 1>>(a, s) : start<Tile<4, 4, 2, 2, 2, false, 2>>(a, s);
   return hipGetLastError();
 }
 

@@ -57,48 +57,41 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 }
 
 // The expert whose rows block p holds (-1 where p is behind all blocks), its first
-// block, row tile and row, its rows, and the totals. Every wave finds it by itself.
+// block, its first row and its rows. Every wave finds it by itself.
 struct Found {
-  int expert, block0, tile0, row0, rows;
-  int all_tiles, all_rows;
+  int expert, block0, row0, rows;
 };
-__device__ __forceinline__ Found find_group(const Groups& g, int p, int tile_blocks, int32_t* first_block) {
+__device__ __forceinline__ int blocks_of(int rows) { return rows > 0 ? (rows + kBlock - 1) / kBlock : 0; }
+__device__ __forceinline__ Found find_group(const Groups& g, int p) {
   const int lane = threadIdx.x & 63, each = (g.experts + 63) / 64;
   const int from = min(lane * each, g.experts), to = min(from + each, g.experts);
-  auto blocks_of = [&](int lo, int hi) { return hi > lo ? (hi - lo + kBlock - 1) / kBlock : 0; };
   const int begin = group_row(g, from);
-  int blocks = 0, tiles = 0, lo = begin;
+  int blocks = 0, lo = begin;
   for (int e = from; e < to; ++e) {
-    const int hi = group_row(g, e + 1), b = blocks_of(lo, hi);
-    blocks += b;
-    tiles += (b + tile_blocks - 1) / tile_blocks;
+    const int hi = group_row(g, e + 1);
+    blocks += blocks_of(hi - lo);
     lo = hi;
   }
-  Found f{-1, 0, 0, 0, 0, 0, __shfl(lo, 63)};
-  int pb = blocks, pt = tiles;
+  int pb = blocks;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int ub = __shfl_up(pb, d), ut = __shfl_up(pt, d);
-    if (lane >= d) pb += ub, pt += ut;
+    const int up = __shfl_up(pb, d);
+    if (lane >= d) pb += up;
   }
-  f.all_tiles = __shfl(pt, 63);
-  if (first_block && lane == 63) first_block[g.experts] = min(pb, g.blocks);
   const bool here = p >= pb - blocks && p < pb;
-  pb -= blocks, pt -= tiles;
+  pb -= blocks;
   lo = begin;
+  Found f{-1, 0, 0, 0};
   for (int e = from; e < to; ++e) {
-    const int hi = group_row(g, e + 1), b = blocks_of(lo, hi);
-    if (first_block) first_block[e] = min(pb, g.blocks);
-    if (p >= pb && p < pb + b) f.expert = e, f.block0 = pb, f.tile0 = pt, f.row0 = lo, f.rows = hi - lo;
+    const int hi = group_row(g, e + 1), b = blocks_of(hi - lo);
+    if (p >= pb && p < pb + b) f = Found{e, pb, lo, hi - lo};
     pb += b;
-    pt += (b + tile_blocks - 1) / tile_blocks;
     lo = hi;
   }
   const uint64_t found = __ballot(here);
   const int who = found ? __ffsll(static_cast<unsigned long long>(found)) - 1 : 0;
   f.expert = found ? __builtin_amdgcn_readlane(f.expert, who) : -1;
   f.block0 = __builtin_amdgcn_readlane(f.block0, who);
-  f.tile0 = __builtin_amdgcn_readlane(f.tile0, who);
   f.row0 = __builtin_amdgcn_readlane(f.row0, who);
   f.rows = __builtin_amdgcn_readlane(f.rows, who);
   return f;
@@ -174,34 +167,169 @@ __device__ __forceinline__ void write_columns(const Tile<F32>& t, const uint32_t
   }
 }
 
+// ------------------------------------------------------------ the products' work
+__device__ __forceinline__ uint32_t buffer_size(int64_t left) {
+  return left <= 0 ? 0u : left > 0xfffffff0ll ? 0xfffffff0u : static_cast<uint32_t>(left);
+}
+
+// Records of the products' work, one a thread. An XCD takes a contiguous range of a
+// product's tiles, in groups of four row tiles, so that those in flight on one XCD
+// share their operands in its L2. Experts have sums of different length: each XCD
+// takes its part of every expert's tiles, another one for each (dW of eight experts of
+// 16384 x 2048 x 2048 bf16: 88 us; with an expert an XCD 126).
+__device__ __forceinline__ void write_work(const Products& all, const Groups& g, int which, int* first_tile, int* first_block) {
+  const int side = product_tile(static_cast<ProductTile>(all.tile)), per_tile = side / kBlock;
+  // each expert's first row tile and first block; [experts]: all
+  if (g.offsets) {
+    const int wave_lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) {
+      const int each = (g.experts + 63) / 64, from = min(wave_lane * each, g.experts), to = min(from + each, g.experts);
+      int tiles = 0, blocks = 0, lo = group_row(g, from);
+      const int begin = lo;
+      for (int e = from; e < to; ++e) {
+        const int hi = group_row(g, e + 1), b = blocks_of(hi - lo);
+        blocks += b;
+        tiles += (b + per_tile - 1) / per_tile;
+        lo = hi;
+      }
+      int pt = tiles, pb = blocks;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int ut = __shfl_up(pt, d), ub = __shfl_up(pb, d);
+        if (wave_lane >= d) pt += ut, pb += ub;
+      }
+      pt -= tiles, pb -= blocks;
+      lo = begin;
+      for (int e = from; e < to; ++e) {
+        const int hi = group_row(g, e + 1), b = blocks_of(hi - lo);
+        first_tile[e] = pt;
+        first_block[e] = min(pb, g.blocks);
+        pb += b;
+        pt += (b + per_tile - 1) / per_tile;
+        lo = hi;
+      }
+      if (wave_lane == 63) {
+        first_tile[g.experts] = pt;
+        first_block[g.experts] = min(pb, g.blocks);
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t record = static_cast<int64_t>(which) * kThreads + threadIdx.x;
+  if (record >= 8ll * all.per) return;
+  const uint32_t xcd = static_cast<uint32_t>(record / all.per);
+  uint32_t n = static_cast<uint32_t>(record - static_cast<int64_t>(xcd) * all.per);
+  WorkRecord w{};
+  w.turns = kNoTileNorBehind;
+  for (int q = 0; q < all.count; ++q) {
+    const ProductArgs& p = all.p[q];
+    const uint32_t tn = (p.N + side - 1) / side, experts = p.by_expert ? all.experts : 1;
+    uint32_t tm = (p.M + side - 1) / side;
+    int behind = 0;  // rows behind the last expert's
+    if (!p.by_expert && g.offsets) {
+      behind = g.n - group_row(g, g.experts);
+      tm = first_tile[g.experts] + (behind + side - 1) / side;
+    }
+    const uint32_t tiles = tm * tn, per = (tiles + 7) / 8;  // of an XCD, of each expert
+    const bool round = tiles < 16;                          // fewer than two of an expert an XCD: all experts' in turn
+    const uint32_t length = round ? (tiles * experts + 7) / 8 : per * experts;
+    if (n >= length) {
+      n -= length;
+      continue;
+    }
+    w.turns = kNoTile;
+    uint32_t expert, id;
+    if (round) {
+      const uint32_t at = n * 8 + xcd;
+      if (at >= tiles * experts) break;
+      expert = at / tiles;
+      id = at - expert * tiles;
+    } else {
+      expert = n / per;
+      id = (xcd + expert) % 8 * per + (n - expert * per);
+      if (id >= tiles) break;
+    }
+    const uint32_t group = id / (4 * tn), in_group = min(4u, tm - 4 * group);
+    id -= group * 4 * tn;
+    const int n0 = static_cast<int>(id / in_group) * side, trow = static_cast<int>(4 * group + id % in_group);
+    int a_block = trow * per_tile, rows = min(side, p.M - trow * side), k0 = 0;
+    int64_t c_row = static_cast<int64_t>(trow) * side;
+    w.turns = p.k_blocks;
+    if (p.by_expert) {
+      if (g.offsets) {
+        k0 = first_block[expert];
+        w.turns = first_block[expert + 1] - k0;
+      }
+    } else if (g.offsets) {
+      const int last = first_tile[g.experts];
+      if (trow >= last) {
+        const int down = (trow - last) * side;
+        c_row = group_row(g, g.experts) + down;
+        rows = min(side, behind - down);
+        a_block = 0;
+        w.turns = 0;
+      } else {
+        int lo = 0, hi = g.experts;  // the last expert whose first tile is not behind this one
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (first_tile[mid] <= trow) lo = mid;
+          else hi = mid;
+        }
+        expert = static_cast<uint32_t>(lo);
+        const int down = (trow - first_tile[lo]) * side, first_row = group_row(g, lo);
+        c_row = first_row + down;
+        rows = max(0, min(side, group_row(g, lo + 1) - first_row - down));
+        a_block = first_block[lo] + (trow - first_tile[lo]) * per_tile;
+      }
+    }
+    const int64_t a_at = static_cast<int64_t>(a_block) * kBlock * p.pitch + static_cast<int64_t>(k0) * kBlock;
+    const int64_t b_at = n0 * p.pitch + static_cast<int64_t>(k0) * kBlock;
+    const bool words = !p.by_expert;
+    w.a = reinterpret_cast<uint64_t>(p.a) + a_at;
+    w.b = reinterpret_cast<uint64_t>(p.b) + (words ? expert * p.b_stride : 0) + b_at;
+    w.size_a = buffer_size(p.size_a - a_at);
+    w.size_b = buffer_size(p.size_b - b_at);
+    const int64_t a_step = static_cast<int64_t>(p.a_blocks) * kBlock, b_step = static_cast<int64_t>(p.b_blocks) * kBlock;
+    const int64_t sa = k0 * a_step + static_cast<int64_t>(a_block) * kBlock;
+    const int64_t sb = words ? static_cast<int64_t>(n0 / kBlock) * p.b_scale_pitch : k0 * b_step + n0;
+    w.a_scales = reinterpret_cast<uint64_t>(p.a_scales) + sa;
+    w.b_scales = reinterpret_cast<uint64_t>(p.b_scales) + (words ? expert * p.b_scale_stride : 0) + sb;
+    w.a_scales_size = buffer_size(p.k_blocks * a_step - sa);
+    w.b_scales_size = buffer_size((words ? static_cast<int64_t>(p.b_blocks) * p.b_scale_pitch : p.k_blocks * b_step) - sb);
+    w.c = reinterpret_cast<uint64_t>(p.c) + ((p.by_expert ? expert * p.c_stride : 0) + c_row * p.ldc + n0) * (all.f32 ? 4 : 2);
+    const uint32_t second = n0 / kBlock + 1 < p.b_blocks;
+    w.shape = static_cast<uint32_t>(rows) | static_cast<uint32_t>(min(side, p.N - n0)) << 10 | static_cast<uint32_t>(words) << 20 | second << 21 |
+              static_cast<uint32_t>(q) << 22;
+    break;
+  }
+  all.work[record] = w;
+}
+
+constexpr int kMaxExperts = 1024;
+constexpr int kTileBytes = 128 * 128, kLds = kTileBytes > 8 * (kMaxExperts + 1) ? kTileBytes : 8 * (kMaxExperts + 1);
+
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a) {
   constexpr int W = Tile<F32>::W;
-  __shared__ __attribute__((aligned(16))) char lds[128 * 128];
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
   __shared__ uint32_t tops[4][128];
-  const int p = static_cast<int>(blockIdx.x / a.col_blocks), kt = static_cast<int>(blockIdx.x - static_cast<uint32_t>(p) * a.col_blocks);
+  // the first workgroups write the records
+  const uint32_t writers = (8 * static_cast<uint32_t>(a.products.per) + kThreads - 1) / kThreads;
+  if (blockIdx.x < writers) {
+    int* tables = reinterpret_cast<int*>(lds);
+    write_work(a.products, a.g, static_cast<int>(blockIdx.x), tables, tables + kMaxExperts + 1);
+    return;
+  }
+  const uint32_t block = blockIdx.x - writers;
+  const int p = static_cast<int>(block / a.col_blocks), kt = static_cast<int>(block - static_cast<uint32_t>(p) * a.col_blocks);
   const int cg = threadIdx.x & 15, rt = threadIdx.x >> 4;
   int row0 = p * kBlock, count = min(kBlock, a.g.n - row0);
   if (a.g.offsets) {
-    const bool lead = kt == 0 && p == 0;
-    const Found f = find_group(a.g, p, a.tile_blocks, lead && threadIdx.x < 64 ? a.first_block : nullptr);
-    if (lead && a.tiles) {
-      // tiles behind the experts': rows that get zeros
-      const int tile_rows = a.tile_blocks * kBlock, rest = a.g.n - f.all_rows;
-      const int more = (rest + tile_rows - 1) / tile_rows;
-      for (int i = threadIdx.x; i < more; i += kThreads)
-        if (f.all_tiles + i < a.max_tiles)
-          a.tiles[f.all_tiles + i] = RowTile{-1, 0, f.all_rows + i * tile_rows, min(tile_rows, rest - i * tile_rows)};
-      if (threadIdx.x == 0) *a.tile_count = min(f.all_tiles + more, a.max_tiles);
-    }
+    const Found f = find_group(a.g, p);
     if (f.expert < 0) return;
     const int local = p - f.block0;
     row0 = f.row0 + local * kBlock;
     count = min(kBlock, f.rows - local * kBlock);
-    if (kt == 0 && threadIdx.x == 0 && a.tiles && local % a.tile_blocks == 0) {
-      const int at = f.tile0 + local / a.tile_blocks;
-      if (at < a.max_tiles) a.tiles[at] = RowTile{f.expert, p, row0, min(a.tile_blocks * kBlock, f.rows - local * kBlock)};
-    }
   }
   const int col = kt * kBlock + cg * 8, n = min(8, max(0, a.cols - col));
   Raw8<F32> raw[8];
@@ -323,9 +451,25 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(WeightArgs a)
 
 }  // namespace
 
+int64_t work_length(const Products& a, int64_t rows, bool grouped) {
+  const int64_t side = product_tile(static_cast<ProductTile>(a.tile));
+  int64_t length = 0;
+  for (int q = 0; q < a.count; ++q) {
+    const ProductArgs& p = a.p[q];
+    const int64_t tn = (p.N + side - 1) / side, used = a.experts < rows ? a.experts : rows;
+    const int64_t tm = grouped && !p.by_expert ? (rows + (side - 1) * (used + 1)) / side : (p.M + side - 1) / side;
+    const int64_t experts = p.by_expert ? a.experts : 1, tiles = tm * tn;
+    // under 16 tiles all experts' go in turn; a grouped product may turn out to have so few
+    const int64_t round = ((tiles < 16 ? tiles : 15) * experts + 7) / 8, parts = tiles < 16 ? 0 : (tiles + 7) / 8 * experts;
+    length += round > parts ? round : parts;
+  }
+  return length;
+}
+
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
-  if (a.g.blocks == 0) return hipSuccess;
-  const uint32_t grid = static_cast<uint32_t>(a.col_blocks) * static_cast<uint32_t>(a.g.blocks);
+  const uint32_t writers = (8 * static_cast<uint32_t>(a.products.per) + kThreads - 1) / kThreads;
+  const uint32_t grid = static_cast<uint32_t>(a.col_blocks) * static_cast<uint32_t>(a.g.blocks) + writers;
+  if (grid == 0) return hipSuccess;
   if (a.f32)
     quantize_kernel<true><<<grid, kThreads, 0, s>>>(a);
   else

@@ -167,20 +167,25 @@ int64_t row_tiles(const shampoo_product8_t* a, int64_t height) {
   return (a->rows + (height - 1) * (e + 1)) / height;
 }
 
-// Tiles of 256 where they fill most of the card.
-she::ProductTile choose_tile(const shampoo_product8_t* a, bool by_expert, int64_t m, int64_t n) {
-  if (a->dtype == SHAMPOO_F32) return she::kProduct128;
-  const int64_t tm = by_expert ? (m + 255) / 256 * a->experts : row_tiles(a, 256);
-  return tm * ((n + 255) / 256) >= 200 ? she::kProduct256 : she::kProduct128;
+// Tiles of a launch's products: 256 where they fill most of the card; 128 one a CU
+// with more steps on their way where there are no more than CUs.
+she::ProductTile choose_tile(const shampoo_product8_t* a, bool backward) {
+  auto tiles = [&](int64_t side) {
+    const int64_t n = backward ? a->in : a->out;
+    int64_t t = !backward || a->dx ? row_tiles(a, side) * ((n + side - 1) / side) : 0;
+    if (backward && a->dw) t += (a->in + side - 1) / side * ((a->out + side - 1) / side) * a->experts;
+    return t;
+  };
+  if (a->dtype != SHAMPOO_F32 && tiles(256) >= 200) return she::kProduct256;
+  return tiles(128) <= 256 ? she::kProduct128Deep : she::kProduct128;
 }
 
-// Quantized operands by rows and by columns, and the tables beside them.
+// Quantized operands by rows and by columns in the workspace, and the products of a
+// call with their work, also in the workspace.
 struct ProductPlan {
   int64_t blocks = 0;
   shp_rt::Carver ws;
-  int64_t by_rows = -1, row_scales = -1, by_cols = -1, col_scales = -1, first_block = -1, tiles = -1, tile_count = -1;
-  she::ProductTile tile = she::kProduct128;
-  int64_t max_tiles = 0;
+  she::QuantizeArgs q{};
 };
 
 size_t saved_size(const shampoo_product8_t* a) {
@@ -197,85 +202,101 @@ bool few_rows(const shampoo_product8_t* a, bool backward) {
   return a->rows <= she::kFewRows && !(backward ? a->dw : a->saved);
 }
 
-ProductPlan plan_product(const shampoo_product8_t* a, bool backward) {
-  ProductPlan p;
-  p.blocks = row_blocks(a);
-  if (p.blocks == 0 || few_rows(a, backward)) return p;
-  const int64_t k = backward ? a->out : a->in, n = backward ? a->in : a->out;
-  const int64_t kb = blocks_of(k), bytes = p.blocks * kb * she::kBlock * she::kBlock;
-  const bool rows = !backward || a->dx, cols = backward && a->dw;
-  if (rows) {
-    p.by_rows = p.ws.take(bytes);
-    p.row_scales = p.ws.take(bytes / she::kBlock);
-    p.tile = choose_tile(a, false, a->rows, n);
-    p.max_tiles = row_tiles(a, she::product_tile(p.tile));
-  }
-  if (cols) {
-    p.by_cols = p.ws.take(bytes);
-    p.col_scales = p.ws.take(bytes / she::kBlock);
-  }
-  if (a->offsets) {
-    p.first_block = p.ws.take(4 * (a->experts + 1));
-    if (rows) {
-      p.tiles = p.ws.take(p.max_tiles * static_cast<int64_t>(sizeof(she::RowTile)));
-      p.tile_count = p.ws.take(4);
-    }
-  }
-  return p;
-}
-
-template <class T>
-T* in_ws(void* ws, int64_t off) {
-  return off < 0 ? nullptr : reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
-
-she::QuantizeArgs quantize_args(const shampoo_product8_t* a, const ProductPlan& p, void* ws, const void* x, int64_t ld, int64_t cols) {
-  she::QuantizeArgs q{};
-  q.x = x;
-  q.ld = ld;
-  q.f32 = a->dtype == SHAMPOO_F32;
-  q.cols = static_cast<int32_t>(cols);
-  q.col_blocks = static_cast<int32_t>(blocks_of(cols));
-  q.g = she::Groups{a->offsets, static_cast<int32_t>(a->rows), a->experts, static_cast<int32_t>(p.blocks)};
-  q.by_rows = in_ws<uint8_t>(ws, p.by_rows);
-  q.row_scales = in_ws<uint8_t>(ws, p.row_scales);
-  q.by_cols = in_ws<uint8_t>(ws, p.by_cols);
-  q.col_scales = in_ws<uint8_t>(ws, p.col_scales);
-  q.first_block = in_ws<int32_t>(ws, p.first_block);
-  q.tiles = in_ws<she::RowTile>(ws, p.tiles);
-  q.tile_count = in_ws<int32_t>(ws, p.tile_count);
-  q.tile_blocks = she::product_tile(p.tile) / she::kBlock;
-  q.max_tiles = static_cast<int32_t>(p.max_tiles);
-  return q;
-}
-
-// y or dx: rows of tokens, quantized by rows into the workspace, against the weights.
-she::ProductArgs row_product(const shampoo_product8_t* a, const ProductPlan& p, void* ws, const void* values, const void* scales, int64_t k,
-                             int64_t n, void* c, int64_t ldc) {
-  const int64_t kb = blocks_of(k), nb = blocks_of(n), pitch = kb * she::kBlock, scale_pitch = (kb + 3) / 4 * 4;
+// y or dx: rows of tokens, quantized by rows, against the weights.
+she::ProductArgs row_product(const shampoo_product8_t* a, int64_t blocks, const void* values, const void* scales, int64_t k, int64_t n, void* c,
+                             int64_t ldc) {
+  const int64_t kb = blocks_of(k), nb = blocks_of(n), scale_pitch = (kb + 3) / 4 * 4;
   she::ProductArgs g{};
-  g.a = in_ws<uint8_t>(ws, p.by_rows);
-  g.a_scales = in_ws<uint8_t>(ws, p.row_scales);
   g.b = static_cast<const uint8_t*>(values);
   g.b_scales = static_cast<const uint8_t*>(scales);
-  g.pitch_a = g.pitch_b = pitch;
-  g.size_a = p.blocks * she::kBlock * pitch;
-  g.size_b = g.b_stride = n * pitch;
+  g.pitch = kb * she::kBlock;
+  g.size_a = blocks * she::kBlock * g.pitch;
+  g.size_b = g.b_stride = n * g.pitch;
   g.b_scale_stride = nb * scale_pitch;
-  g.a_blocks = static_cast<int32_t>(p.blocks);
+  g.a_blocks = static_cast<int32_t>(blocks);
   g.b_blocks = static_cast<int32_t>(nb);
   g.b_scale_pitch = static_cast<int32_t>(scale_pitch);
   g.M = static_cast<int32_t>(a->rows);
   g.N = static_cast<int32_t>(n);
   g.k_blocks = static_cast<int32_t>(kb);
-  g.experts = a->experts;
-  g.tiles = in_ws<she::RowTile>(ws, p.tiles);
-  g.tile_count = in_ws<int32_t>(ws, p.tile_count);
-  g.row_tiles = static_cast<int32_t>(p.max_tiles);
   g.c = c;
   g.ldc = ldc;
-  g.f32 = a->dtype == SHAMPOO_F32;
   return g;
+}
+
+// dW: what was saved of x against dy, both by columns.
+she::ProductArgs column_product(const shampoo_product8_t* a, int64_t blocks) {
+  const int64_t ib = blocks_of(a->in), ob = blocks_of(a->out);
+  she::ProductArgs g{};
+  g.pitch = blocks * she::kBlock;
+  g.a = static_cast<const uint8_t*>(a->saved);
+  g.a_scales = g.a + shp_rt::align_up(ib * she::kBlock * g.pitch);
+  g.size_a = ib * she::kBlock * g.pitch;
+  g.size_b = ob * she::kBlock * g.pitch;
+  g.a_blocks = static_cast<int32_t>(ib);
+  g.b_blocks = static_cast<int32_t>(ob);
+  g.M = static_cast<int32_t>(a->in);
+  g.N = static_cast<int32_t>(a->out);
+  g.k_blocks = static_cast<int32_t>(blocks);
+  g.by_expert = 1;
+  g.c = a->dw;
+  g.ldc = a->ld_dw;
+  g.c_stride = a->stride_dw;
+  return g;
+}
+
+// A call's quantization and products, at `ws`; sizes are the same wherever that is.
+ProductPlan plan_product(const shampoo_product8_t* a, bool backward, void* ws) {
+  ProductPlan p;
+  p.blocks = row_blocks(a);
+  const bool dw = backward && a->dw;
+  if (few_rows(a, backward) || (p.blocks == 0 && !dw)) return p;
+  const int64_t k = backward ? a->out : a->in, kb = blocks_of(k), bytes = p.blocks * kb * she::kBlock * she::kBlock;
+  auto take = [&](int64_t n) { return static_cast<uint8_t*>(ws) + p.ws.take(n); };
+  she::QuantizeArgs& q = p.q;
+  q.x = backward ? a->dy : a->x;
+  q.ld = backward ? a->ld_dy : a->ld_x;
+  q.f32 = a->dtype == SHAMPOO_F32;
+  q.cols = static_cast<int32_t>(k);
+  q.col_blocks = static_cast<int32_t>(kb);
+  q.g = she::Groups{a->offsets, static_cast<int32_t>(a->rows), a->experts, static_cast<int32_t>(p.blocks)};
+  const bool gather = !backward && a->source;
+  q.source = gather ? a->source : nullptr;
+  q.slots = static_cast<uint32_t>(gather ? a->slots : 1);
+  q.rows_in = static_cast<int32_t>(gather ? a->x_rows : a->rows);
+  she::Products& g = q.products;
+  g.experts = a->experts;
+  g.f32 = q.f32;
+  g.tile = choose_tile(a, backward);
+  if (p.blocks > 0 && (!backward || a->dx)) {
+    q.by_rows = take(bytes);
+    q.row_scales = take(bytes / she::kBlock);
+    she::ProductArgs& r = g.p[g.count++];
+    r = backward ? row_product(a, p.blocks, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx)
+                 : row_product(a, p.blocks, a->values, a->scales, a->in, a->out, a->y, a->ld_y);
+    r.a = q.by_rows;
+    r.a_scales = q.row_scales;
+  }
+  if (dw) {
+    q.by_cols = take(bytes);
+    q.col_scales = take(bytes / she::kBlock);
+    she::ProductArgs& c = g.p[g.count++];
+    c = column_product(a, p.blocks);
+    c.b = q.by_cols;
+    c.b_scales = q.col_scales;
+  } else if (!backward && a->saved) {
+    q.by_cols = static_cast<uint8_t*>(a->saved);
+    q.col_scales = q.by_cols + shp_rt::align_up(bytes);
+  }
+  const int64_t per = she::work_length(g, a->rows, a->offsets != nullptr);
+  g.per = static_cast<int32_t>(per);
+  g.work = reinterpret_cast<she::WorkRecord*>(take(8 * per * static_cast<int64_t>(sizeof(she::WorkRecord))));
+  return p;
+}
+
+hipError_t run_products(const ProductPlan& p, hipStream_t s) {
+  const hipError_t e = she::launch_quantize(p.q, s);
+  return e == hipSuccess && p.q.products.count ? she::launch_products(p.q.products, s) : e;
 }
 
 hipError_t few_product(const shampoo_product8_t* a, bool gather, const void* x, int64_t ld, const void* values, const void* scales, int64_t k, int64_t n,
@@ -307,85 +328,43 @@ hipError_t few_product(const shampoo_product8_t* a, bool gather, const void* x, 
 }
 
 int forward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t s) {
-  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+  const int64_t esize = a->dtype == SHAMPOO_F32 ? 4 : 2;
   RC(check_aligned("values", a->values, 16));
   RC(check_aligned("scales", a->scales, 4));
-  RC(check_array("x", a->x, a->source ? a->x_rows : a->rows, a->in, a->ld_x, e));
-  RC(check_array("y", a->y, a->rows, a->out, a->ld_y, e));
+  RC(check_array("x", a->x, a->source ? a->x_rows : a->rows, a->in, a->ld_x, esize));
+  RC(check_array("y", a->y, a->rows, a->out, a->ld_y, esize));
   if (a->saved && !aligned(a->saved, 256)) return fail(SHAMPOO_ERR_MISALIGNED, "saved is not aligned to 256 bytes");
   if (a->saved && a->rows > kMaxSavedRows) return invalid("rows must be at most 2^23 - 2^18 where they are saved for dw");
-  const ProductPlan p = plan_product(a, false);
+  const ProductPlan p = plan_product(a, false, ws);
   RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
   if (a->rows == 0) return SHAMPOO_OK;
-  if (few_rows(a, false)) {
-    const hipError_t e = few_product(a, a->source != nullptr, a->x, a->ld_x, a->values, a->scales, a->in, a->out, a->y, a->ld_y, s);
-    return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_product8_forward");
-  }
-  she::QuantizeArgs q = quantize_args(a, p, ws, a->x, a->ld_x, a->in);
-  q.source = a->source;
-  q.slots = static_cast<uint32_t>(a->source ? a->slots : 1);
-  q.rows_in = static_cast<int32_t>(a->source ? a->x_rows : a->rows);
-  if (a->saved) {
-    q.by_cols = static_cast<uint8_t*>(a->saved);
-    q.col_scales = q.by_cols + shp_rt::align_up(p.blocks * q.col_blocks * she::kBlock * she::kBlock);
-  }
-  hipError_t err = she::launch_quantize(q, s);
-  if (err == hipSuccess) err = she::launch_product(row_product(a, p, ws, a->values, a->scales, a->in, a->out, a->y, a->ld_y), p.tile, s);
-  return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, "shampoo_product8_forward");
+  const hipError_t e = few_rows(a, false)
+                           ? few_product(a, a->source != nullptr, a->x, a->ld_x, a->values, a->scales, a->in, a->out, a->y, a->ld_y, s)
+                           : run_products(p, s);
+  return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_product8_forward");
 }
 
 int backward(const shampoo_product8_t* a, void* ws, size_t ws_bytes, hipStream_t s) {
-  const int64_t e = a->dtype == SHAMPOO_F32 ? 4 : 2;
+  const int64_t esize = a->dtype == SHAMPOO_F32 ? 4 : 2;
   if (!a->dx && !a->dw) return SHAMPOO_OK;
-  RC(check_array("dy", a->dy, a->rows, a->out, a->ld_dy, e));
+  RC(check_array("dy", a->dy, a->rows, a->out, a->ld_dy, esize));
   if (a->dx) {
     RC(check_aligned("back_values", a->back_values, 16));
     RC(check_aligned("back_scales", a->back_scales, 4));
-    RC(check_array("dx", a->dx, a->rows, a->in, a->ld_dx, e));
+    RC(check_array("dx", a->dx, a->rows, a->in, a->ld_dx, esize));
   }
   if (a->dw) {
     if (a->rows > kMaxSavedRows) return invalid("rows must be at most 2^23 - 2^18 where dw is wanted");
     if (a->rows > 0) RC(check_aligned("saved", a->saved, 256));
-    RC(check_matrices("dw", a->dw, a->experts, a->in, a->out, a->ld_dw, a->stride_dw, e));
+    RC(check_matrices("dw", a->dw, a->experts, a->in, a->out, a->ld_dw, a->stride_dw, esize));
   }
-  const ProductPlan p = plan_product(a, true);
+  const ProductPlan p = plan_product(a, true, ws);
   RC(check_workspace(ws, ws_bytes, static_cast<size_t>(p.ws.o)));
-  hipError_t err = hipSuccess;
-  if (a->rows > 0 && few_rows(a, true)) {
-    err = few_product(a, false, a->dy, a->ld_dy, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx, s);
-  } else if (p.blocks > 0) {
-    she::QuantizeArgs q = quantize_args(a, p, ws, a->dy, a->ld_dy, a->out);
-    q.slots = 1;
-    q.rows_in = static_cast<int32_t>(a->rows);
-    err = she::launch_quantize(q, s);
-    if (err == hipSuccess && a->dx)
-      err = she::launch_product(row_product(a, p, ws, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx), p.tile, s);
-  }
-  if (err == hipSuccess && a->dw) {
-    const int64_t ib = blocks_of(a->in), ob = blocks_of(a->out), pitch = p.blocks * she::kBlock;
-    she::ProductArgs g{};
-    g.a = static_cast<const uint8_t*>(a->saved);
-    g.a_scales = g.a + shp_rt::align_up(ib * she::kBlock * pitch);
-    g.b = in_ws<uint8_t>(ws, p.by_cols);
-    g.b_scales = in_ws<uint8_t>(ws, p.col_scales);
-    g.pitch_a = g.pitch_b = pitch;
-    g.size_a = ib * she::kBlock * pitch;
-    g.size_b = ob * she::kBlock * pitch;
-    g.a_blocks = static_cast<int32_t>(ib);
-    g.b_blocks = static_cast<int32_t>(ob);
-    g.M = static_cast<int32_t>(a->in);
-    g.N = static_cast<int32_t>(a->out);
-    g.k_blocks = static_cast<int32_t>(p.blocks);
-    g.by_expert = 1;
-    g.experts = a->experts;
-    g.first_block = p.blocks > 0 ? in_ws<int32_t>(ws, p.first_block) : nullptr;
-    g.c = a->dw;
-    g.ldc = a->ld_dw;
-    g.c_stride = a->stride_dw;
-    g.f32 = a->dtype == SHAMPOO_F32;
-    err = she::launch_product(g, choose_tile(a, true, a->in, a->out), s);
-  }
-  return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, "shampoo_product8_backward");
+  if (a->rows == 0 && !a->dw) return SHAMPOO_OK;
+  const hipError_t e = few_rows(a, true)
+                           ? few_product(a, false, a->dy, a->ld_dy, a->back_values, a->back_scales, a->out, a->in, a->dx, a->ld_dx, s)
+                           : run_products(p, s);
+  return e == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(e, "shampoo_product8_backward");
 }
 
 }  // namespace
@@ -462,7 +441,7 @@ int shampoo_product8_workspace_size(const shampoo_product8_t* a, int32_t backwar
   return guarded([&]() -> int {
     RC(check_product(a));
     if (!bytes_out) return invalid("bytes_out is NULL");
-    *bytes_out = static_cast<size_t>(plan_product(a, backward != 0).ws.o);
+    *bytes_out = static_cast<size_t>(plan_product(a, backward != 0, nullptr).ws.o);
     return SHAMPOO_OK;
   });
 }
