@@ -33,6 +33,7 @@ struct RouteArgs {
   void *y, *xs;
   int64_t ld_y, ld_xs;
   float* dweights;
+  bool past;  // xs is written past the caches
 };
 hipError_t launch_dispatch(const RouteArgs& a, hipStream_t s);
 hipError_t launch_combine(const RouteArgs& a, hipStream_t s);

@@ -51,22 +51,36 @@ __device__ __forceinline__ void wave_range(const SortArgs& a, uint32_t& first, u
   last = static_cast<uint32_t>(min(from + (wave + 1) * each, end));
 }
 
-// Counts of each expert (and of slots left out) by wave, into count[wave][e].
-__device__ __forceinline__ void count_waves(const SortArgs& a, uint32_t* count) {
+// Counts of each expert (and of slots left out) by wave, into count[wave][e]. Up to
+// 64 KEEP slots of a wave are read at once and kept.
+template <int KEEP>
+__device__ __forceinline__ void count_waves(const SortArgs& a, uint32_t* count, uint32_t (&kept)[KEEP > 0 ? KEEP : 1]) {
   const uint32_t n = a.experts + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint32_t i = threadIdx.x; i < n * kSortWaves; i += kSortThreads) count[i] = 0;
-  __syncthreads();
   uint32_t first, last;
   wave_range(a, first, last);
-  for (uint32_t i = first; i < last; i += 64)
-    if (i + lane < last) atomicAdd(&count[wave * n + slot_expert(a, i + lane)], 1u);
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const uint32_t slot = first + 64 * k + lane;
+    kept[k] = slot < last ? slot_expert(a, slot) : 0;
+  }
+  for (uint32_t i = threadIdx.x; i < n * kSortWaves; i += kSortThreads) count[i] = 0;
+  __syncthreads();
+  if (KEEP) {
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (first + 64 * k + lane < last) atomicAdd(&count[wave * n + kept[k]], 1u);
+  } else {
+    for (uint32_t i = first; i < last; i += 64)
+      if (i + lane < last) atomicAdd(&count[wave * n + slot_expert(a, i + lane)], 1u);
+  }
   __syncthreads();
 }
 
 // Sort, first of two launches: the counts of each workgroup.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ uint32_t count[kSortWaves * (kMaxExperts + 1)];
-  count_waves(a, count);
+  uint32_t none[1];
+  count_waves<0>(a, count, none);
   const uint32_t n = a.experts + 1;
   for (uint32_t e = threadIdx.x; e < n; e += kSortThreads) {
     uint32_t sum = 0;
@@ -77,6 +91,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 
 // Sort, second launch, or the only one where one workgroup does all: places.
 // 131072 slots of 64 experts: 64 workgroups; one token: what a launch costs.
+template <int KEEP>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ uint32_t count[kSortWaves * (kMaxExperts + 1)];
   __shared__ uint32_t before[kMaxExperts + 1], all[kMaxExperts + 1], wave_sum[kSortWaves];
@@ -84,7 +99,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   // counts of the workgroups before this one, and of all: several threads an
   // expert, each with every parts-th workgroup
   for (uint32_t e = threadIdx.x; e < n; e += kSortThreads) before[e] = all[e] = 0;
-  count_waves(a, count);
+  uint32_t kept[KEEP > 0 ? KEEP : 1];
+  count_waves<KEEP>(a, count, kept);
   if (a.blocks > 1) {
     const uint32_t parts = max(1u, kSortThreads / n);
     for (uint32_t i = threadIdx.x; i < n * parts; i += kSortThreads) {
@@ -142,10 +158,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   wave_range(a, first, last);
   const int bits = 32 - __clz(a.experts);
   uint32_t* next = count + wave * n;
-  for (uint32_t i = first; i < last; i += 64) {
-    const uint32_t slot = i + lane;
+  auto set_places = [&](uint32_t slot, uint32_t e) {
     const bool on = slot < last;
-    const uint32_t e = on ? slot_expert(a, slot) : 0;
     const uint64_t same = same_lanes(e, bits, on);
     const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
     uint32_t r = 0;
@@ -156,10 +170,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (on) {
-      const bool kept = e < a.experts;
-      a.rows[slot] = static_cast<int32_t>(kept ? r : ~r);
-      a.source[r] = static_cast<int32_t>(kept ? slot : ~slot);
+      const bool in = e < a.experts;
+      a.rows[slot] = static_cast<int32_t>(in ? r : ~r);
+      a.source[r] = static_cast<int32_t>(in ? slot : ~slot);
     }
+  };
+  if (KEEP) {
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (first + 64 * k < last) set_places(first + 64 * k + lane, kept[k]);
+  } else {
+    for (uint32_t i = first; i < last; i += 64) set_places(i + lane, i + lane < last ? slot_expert(a, i + lane) : 0);
   }
 }
 
@@ -176,13 +197,18 @@ __device__ __forceinline__ Raw8<F32> zeros8() {
 // the caches (non-temporal): kept there, they are written back while the next
 // kernel reads. All of a training pass of 8192 tokens x 2 x 2048 bf16 107 -> 89 us,
 // of 16384 x 8 x 2048 612 -> 590 (dispatch alone 90 -> 120, each combine 146 -> 118).
+// Only rows of whole cache lines are (`past`): 3001 x 3 x 777 fp32 10.2 us, so 12.3.
 template <bool F32>
-__device__ __forceinline__ void store_raw8(void* p, int64_t off, int n, const Raw8<F32>& r) {
-  typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t anywhere;
+__device__ __forceinline__ void store_raw8(void* p, int64_t off, int n, const Raw8<F32>& r, bool past) {
   if (n == 8) {
     char* q = static_cast<char*>(p) + off * (F32 ? 4 : 2);
-    __builtin_nontemporal_store(r.w[0], reinterpret_cast<anywhere*>(q));
-    if (F32) __builtin_nontemporal_store(r.w[F32 ? 1 : 0], reinterpret_cast<anywhere*>(q + 16));
+    if (past) {
+      __builtin_nontemporal_store(r.w[0], reinterpret_cast<uint4v*>(q));
+      if (F32) __builtin_nontemporal_store(r.w[F32 ? 1 : 0], reinterpret_cast<uint4v*>(q + 16));
+    } else {
+      __builtin_memcpy(q, &r.w[0], 16);
+      if (F32) __builtin_memcpy(q + 16, &r.w[F32 ? 1 : 0], 16);
+    }
   } else {
     constexpr int W = F32 ? 8 : 4;
     uint32_t w[W];
@@ -257,7 +283,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void dispatch_kernel(RouteArgs a)
     if (!s.any) continue;
     const int64_t at = static_cast<int64_t>(s.row) * a.ld_xs;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) store_raw8<F32>(a.xs, at + c.col[i], c.n[i], s.kept ? v[i] : zeros8<F32>());
+    for (int i = 0; i < NC; ++i) store_raw8<F32>(a.xs, at + c.col[i], c.n[i], s.kept ? v[i] : zeros8<F32>(), a.past);
   }
 }
 
@@ -365,7 +391,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void combine_backward_kernel(Rout
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) g[q] = at.kept ? g[q] * w : 0.f;
-        if (at.any) store_raw8<F32>(a.xs, static_cast<int64_t>(at.row) * a.ld_xs + c.col[i], c.n[i], pack8<F32>(g));
+        if (at.any) store_raw8<F32>(a.xs, static_cast<int64_t>(at.row) * a.ld_xs + c.col[i], c.n[i], pack8<F32>(g), a.past);
       }
     }
     dot = wave_sum(dot);
@@ -404,20 +430,23 @@ hipError_t by_columns(const RouteArgs& a, F&& f) {
 }  // namespace
 
 void sort_plan(int64_t total, uint32_t& blocks, uint32_t& per_block) {
-  // up to 4096 slots one workgroup is as fast as two launches; then at least 2048
-  // of them a workgroup, and at most 256 workgroups, whose counts each of them sums
-  per_block = 4096;
-  if (total > 4096) {
-    const int64_t each = (total + 255) / 256;
-    per_block = static_cast<uint32_t>(each > 2048 ? (each + 1023) / 1024 * 1024 : 2048);
-  }
+  // One workgroup up to 4096 slots (16384 of eight experts 22 us, two launches 10);
+  // then at least 1024 of them a workgroup, and at most 256 workgroups, whose counts
+  // each of them sums.
+  const int64_t each = total <= 4096 ? total : (total + 255) / 256;
+  per_block = static_cast<uint32_t>((each > 0 ? each + 1023 : 1024) / 1024 * 1024);
   blocks = static_cast<uint32_t>((total + per_block - 1) / per_block);
   if (blocks == 0) blocks = 1;
 }
 
 hipError_t launch_sort(const SortArgs& a, hipStream_t s) {
   if (a.blocks > 1) sort_count_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
-  sort_place_kernel<<<a.blocks, kSortThreads, 0, s>>>(a);
+  if (a.per_block <= 1024)
+    sort_place_kernel<1><<<a.blocks, kSortThreads, 0, s>>>(a);
+  else if (a.per_block <= 4096)
+    sort_place_kernel<4><<<a.blocks, kSortThreads, 0, s>>>(a);
+  else
+    sort_place_kernel<0><<<a.blocks, kSortThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

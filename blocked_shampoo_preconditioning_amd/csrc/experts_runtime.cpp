@@ -106,7 +106,7 @@ int route(const shampoo_route_t* a, Route what, const char* name, void* hip_stre
   }
   const she::RouteArgs k{a->tokens, static_cast<uint32_t>(a->slots), static_cast<uint32_t>(total), static_cast<int32_t>(a->width),
                          a->dtype == SHAMPOO_F32 ? 1 : 0, a->rows, a->weights, a->x, a->ys, a->ld_x, a->ld_ys, a->y, a->xs,
-                         a->ld_y, a->ld_xs, a->dweights};
+                         a->ld_y, a->ld_xs, a->dweights, aligned(a->xs, 128) && a->ld_xs * e % 128 == 0};
   const hipStream_t s = static_cast<hipStream_t>(hip_stream);
   const hipError_t err = what == kDispatch ? she::launch_dispatch(k, s) : what == kCombine ? she::launch_combine(k, s) : she::launch_combine_backward(k, s);
   return err == hipSuccess ? SHAMPOO_OK : shp_rt::hip_fail(err, name);
@@ -160,24 +160,34 @@ int64_t row_blocks(const shampoo_product8_t* a) {
   return (a->rows + (she::kBlock - 1) * e) / she::kBlock;
 }
 
-// The most row tiles there can be, rows behind the last expert's among them.
-int64_t row_tiles(const shampoo_product8_t* a, int64_t height) {
-  if (!a->offsets) return (a->rows + height - 1) / height;
-  const int64_t e = a->experts < a->rows ? a->experts : a->rows;
-  return (a->rows + (height - 1) * (e + 1)) / height;
-}
-
-// Tiles of a launch's products: 256 where they fill most of the card; 128 one a CU
-// with more steps on their way where there are no more than CUs.
+// The tile of a launch's products, by an estimate of its time in microseconds. A K
+// block takes a 256 tile alone on its CU 1.5, each of two 128 tiles on one 1.0; a tile
+// costs 2 besides, the launch 5. 256 tiles go in whole rounds over the CUs, while
+// 128 tiles that are left alone on a CU go faster. Of an expert's rows the last tile
+// is half empty in the mean. Measured, 256 and 128, us: y of 8192 x 2048 x 8192 118
+// and 145, dx and dW of it 212 and 260; y of 4096 x 8192 x 2048 - and 62, of 16384
+// rows of 64 experts x 2048 x 768 51 and 36, of eight x 2048 x 2048 81 and 74, dx and dW of
+// those 151 and 163. Where 128 tiles are no more than CUs, four steps of each are on
+// their way (dx and dW of 1024 x 768 x 2048: 15 us, with two 18).
 she::ProductTile choose_tile(const shampoo_product8_t* a, bool backward) {
-  auto tiles = [&](int64_t side) {
-    const int64_t n = backward ? a->in : a->out;
-    int64_t t = !backward || a->dx ? row_tiles(a, side) * ((n + side - 1) / side) : 0;
-    if (backward && a->dw) t += (a->in + side - 1) / side * ((a->out + side - 1) / side) * a->experts;
-    return t;
+  const bool dx = !backward || a->dx, dw = backward && a->dw;
+  const double experts = a->experts, rows = static_cast<double>(a->rows);
+  auto estimate = [&](int64_t side, double step, double slots, double& tiles) {
+    auto across = [&](int64_t n) { return static_cast<double>((n + side - 1) / side); };
+    const double used = a->offsets ? experts < rows ? experts : rows : 0;
+    const double n = dx ? (a->offsets ? rows / static_cast<double>(side) + used / 2 : across(a->rows)) * across(backward ? a->in : a->out) : 0;
+    const double c = dw ? across(a->in) * across(a->out) * experts : 0;
+    const double row_steps = static_cast<double>(blocks_of(backward ? a->out : a->in)), col_steps = rows / 128 / experts + 0.5;
+    tiles = n + c;
+    double rounds = tiles / slots;
+    if (side == 256) rounds = static_cast<double>(static_cast<int64_t>(rounds + 0.999));
+    if (rounds < 1) rounds = 1;
+    return tiles > 0 ? rounds * ((n * row_steps + c * col_steps) / tiles * step + 2) : 0;
   };
-  if (a->dtype != SHAMPOO_F32 && tiles(256) >= 200) return she::kProduct256;
-  return tiles(128) <= 256 ? she::kProduct128Deep : she::kProduct128;
+  double large, small;
+  const double us_large = estimate(256, 1.5, 256, large), us_small = estimate(128, 1.0, 512, small);
+  if (a->dtype != SHAMPOO_F32 && us_large < us_small) return she::kProduct256;
+  return small <= 256 ? she::kProduct128Deep : she::kProduct128;
 }
 
 // Quantized operands by rows and by columns in the workspace, and the products of a
