@@ -119,10 +119,14 @@ struct QuantizeArgs {
   const int32_t* source;  // padded row r of x is row source[r] / slots; NULL: r
   uint32_t slots;
   int32_t rows_in;        // rows of x
+  // not NULL, and by rows alone: tiles are of x, and each row's values go to the
+  // padded rows of its slots' rows [rows_in][slots]
+  const int32_t* slot_rows;
   uint8_t *by_rows, *row_scales;  // [128 blocks][128 col_blocks], [col_blocks][blocks][128]
   uint8_t *by_cols, *col_scales;  // [128 col_blocks][128 blocks], [blocks][col_blocks][128]
   Products products;
 };
+constexpr int kMaxScatter = 16;  // slots with slot_rows
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
 
 // Weights w [in][out], one scale for each tile: transposed ("forward": [out][in])

@@ -149,6 +149,10 @@ int check_product(const shampoo_product8_t* a) {
     RC(check_aligned("source", a->source, 4));
     if (a->slots < 1 || a->slots > 1024) return invalid("slots must be in [1, 1024]");
     if (a->x_rows < (a->rows > 0 ? 1 : 0) || a->x_rows > kMaxTotal) return invalid("x_rows must be in [1, 2^31 - 1024]");
+    if (a->slot_rows) {
+      RC(check_aligned("slot_rows", a->slot_rows, 4));
+      if (a->rows != a->x_rows * a->slots) return invalid("rows must be x_rows * slots with slot_rows");
+    }
   }
   return SHAMPOO_OK;
 }
@@ -274,6 +278,7 @@ ProductPlan plan_product(const shampoo_product8_t* a, bool backward, void* ws) {
   q.source = gather ? a->source : nullptr;
   q.slots = static_cast<uint32_t>(gather ? a->slots : 1);
   q.rows_in = static_cast<int32_t>(gather ? a->x_rows : a->rows);
+  if (gather && !a->saved && a->slot_rows && a->slots >= 2 && a->slots <= she::kMaxScatter) q.slot_rows = a->slot_rows;
   she::Products& g = q.products;
   g.experts = a->experts;
   g.f32 = q.f32;

@@ -35,7 +35,7 @@ MAX_EXPERTS = 1024
 _SORT = struct.Struct("@q iii P q PPP")
 _ROUTE = struct.Struct("@qq ii PP PP qq PP qq P")
 _WEIGHT = struct.Struct("@qq ii P qq PPPP")
-_PRODUCT = struct.Struct("@qqq ii PP q i PPPP P q P q P P q P q P qq")
+_PRODUCT = struct.Struct("@qqq ii PP q i P PPPP P q P q P P q P q P qq")
 
 _A, _SIZE = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
 _SIGNATURES = {
@@ -287,11 +287,11 @@ def product8_forward(x, w8, plan=None, gather=False, save=False):
     n_in, n_out = w8.n_in, w8.n_out
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D (rows, width), got shape {tuple(x.shape)}")
-    x_rows, source, slots, rows = x.shape[0], 0, 1, x.shape[0]
+    x_rows, source, slots, rows, slot_rows = x.shape[0], 0, 1, x.shape[0], 0
     if gather:
         if plan is None:
             raise ValueError("gather needs a plan")
-        _, x_rows, slots = _plan_rows(plan, x)
+        slot_rows, x_rows, slots = _plan_rows(plan, x)
         rows = x_rows * slots
         if plan.source.dtype is not torch.int32 or plan.source.get_device() != x.get_device() or plan.source.shape != (rows,) or \
                 not plan.source.is_contiguous():
@@ -304,7 +304,7 @@ def product8_forward(x, w8, plan=None, gather=False, save=False):
     px, lx = _matrix("x", x, x_rows, n_in, x)
     values, scales = _weight_pointers("w8.", w8.values, w8.scales, lead, n_in, n_out, x)
     y = x.new_empty((rows, n_out))
-    head = (rows, n_in, n_out, n_experts, dt, offsets, source, x_rows, slots or 1)
+    head = (rows, n_in, n_out, n_experts, dt, offsets, source, x_rows, slots or 1, slot_rows)
     key = (rows, n_in, n_out, n_experts, dt, plan is None)
     saved = None
     if save:
@@ -339,7 +339,7 @@ def product8_backward(dy, w8, saved, plan=None, need_dx=True, need_dw=True):
         if w8.back_values is None:
             raise ValueError("w8 has no backward values: quantize_weight(w, backward=True)")
         back = _weight_pointers("w8.back_", w8.back_values, w8.back_scales, lead, n_out, n_in, dy)
-    head = (rows, n_in, n_out, n_experts, dt, offsets, 0, rows, 1)
+    head = (rows, n_in, n_out, n_experts, dt, offsets, 0, rows, 1, 0)
     key = (rows, n_in, n_out, n_experts, dt, plan is None)
     dx = dw = None
     if need_dx:

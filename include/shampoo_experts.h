@@ -113,6 +113,8 @@ typedef struct {
                              source[r] / slots of x, which has x_rows      */
   int64_t x_rows;         /* >= 1 where rows >= 1; read with source        */
   int32_t slots;          /* 1 .. 1024; read with source                   */
+  const int32_t* slot_rows; /* shampoo_sort_tokens' rows of the same plan, or NULL; read
+                             with source, where rows is x_rows * slots     */
   /* as shampoo_quantize_weight wrote them (scales of 1 .. 254) */
   const void *values, *scales, *back_values, *back_scales;
   /* forward */

@@ -55,8 +55,8 @@ def test_struct_layouts(tmp_path):
     more = c_sizes(tmp_path, "sizeof(shampoo_weight8_t)", "sizeof(shampoo_product8_t)", "offsetof(shampoo_weight8_t, back_scales)",
                    "offsetof(shampoo_product8_t, x_rows)", "offsetof(shampoo_product8_t, values)", "offsetof(shampoo_product8_t, saved)",
                    "offsetof(shampoo_product8_t, stride_dw)")
-    assert more == [X._WEIGHT.size, X._PRODUCT.size, place(X._WEIGHT, 11, 10), place(X._PRODUCT, 25, 7), place(X._PRODUCT, 25, 9),
-                    place(X._PRODUCT, 25, 17), place(X._PRODUCT, 25, 24)]
+    assert more == [X._WEIGHT.size, X._PRODUCT.size, place(X._WEIGHT, 11, 10), place(X._PRODUCT, 26, 7), place(X._PRODUCT, 26, 10),
+                    place(X._PRODUCT, 26, 18), place(X._PRODUCT, 26, 25)]
     assert got[2:] == [place(X._SORT, 9, 8), place(X._ROUTE, 15, 9), place(X._ROUTE, 15, 14)]
 
 
@@ -103,7 +103,7 @@ def test_route_refusals_by_entry(lib, name, over, code):
 
 WEIGHT = dict(n_in=200, n_out=300, experts=2, dtype=1, w=FAKE, ld_w=300, stride_w=60000, values=FAKE, scales=FAKE, back_values=FAKE,
               back_scales=FAKE)
-PRODUCT = dict(rows=100, n_in=200, n_out=300, experts=2, dtype=1, offsets=FAKE, source=FAKE, x_rows=50, slots=2, values=FAKE, scales=FAKE,
+PRODUCT = dict(rows=100, n_in=200, n_out=300, experts=2, dtype=1, offsets=FAKE, source=FAKE, x_rows=50, slots=2, slot_rows=FAKE, values=FAKE, scales=FAKE,
                back_values=FAKE, back_scales=FAKE, x=FAKE, ld_x=200, y=FAKE, ld_y=300, saved=FAKE, dy=FAKE, ld_dy=300, dx=FAKE, ld_dx=200,
                dw=FAKE, ld_dw=300, stride_dw=60000)
 
@@ -120,7 +120,7 @@ def test_weight_refusals(lib, over, code):
 @pytest.mark.parametrize("over,code", [
     ({}, 0), (dict(rows=0, x_rows=0), 0), (dict(rows=-1), INVALID), (dict(rows=1 << 31), INVALID), (dict(n_in=0), INVALID), (dict(experts=0), INVALID),
     (dict(offsets=0), INVALID), (dict(offsets=0, experts=1), INVALID), (dict(offsets=FAKE + 2), MISALIGNED), (dict(x_rows=0), INVALID),
-    (dict(slots=0), INVALID), (dict(source=FAKE + 1), MISALIGNED), (dict(dtype=-1), UNSUPPORTED)])
+    (dict(slots=0), INVALID), (dict(slot_rows=FAKE + 2), MISALIGNED), (dict(rows=99), INVALID), (dict(source=FAKE + 1), MISALIGNED), (dict(dtype=-1), UNSUPPORTED)])
 def test_product_sizes(lib, over, code):
     out = ctypes.c_size_t()
     args = X._PRODUCT.pack(*{**PRODUCT, **over}.values())
@@ -133,7 +133,7 @@ def test_product_sizes(lib, over, code):
     (dict(values=0), FAKE, 1 << 30, INVALID), (dict(values=FAKE + 8), FAKE, 1 << 30, MISALIGNED), (dict(scales=0), FAKE, 1 << 30, INVALID),
     (dict(x=0), FAKE, 1 << 30, INVALID), (dict(ld_x=199), FAKE, 1 << 30, INVALID), (dict(x=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
     (dict(y=0), FAKE, 1 << 30, INVALID), (dict(ld_y=1), FAKE, 1 << 30, INVALID), (dict(saved=FAKE + 16), FAKE, 1 << 30, MISALIGNED),
-    (dict(rows=1 << 23), FAKE, 1 << 50, INVALID),
+    (dict(rows=1 << 23, x_rows=1 << 22), FAKE, 1 << 50, INVALID),
     ({}, 0, 1 << 30, INVALID), ({}, FAKE + 16, 1 << 30, MISALIGNED), ({}, FAKE, 1000, SMALL)])
 def test_product_forward_refusals(lib, over, ws, size, code):
     assert lib.shampoo_product8_forward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
@@ -142,7 +142,7 @@ def test_product_forward_refusals(lib, over, ws, size, code):
 @pytest.mark.parametrize("over,ws,size,code", [
     (dict(back_values=0), FAKE, 1 << 30, INVALID), (dict(back_scales=FAKE + 1), FAKE, 1 << 30, MISALIGNED), (dict(dy=0), FAKE, 1 << 30, INVALID),
     (dict(ld_dy=299), FAKE, 1 << 30, INVALID), (dict(ld_dx=199), FAKE, 1 << 30, INVALID), (dict(dx=FAKE + 1), FAKE, 1 << 30, MISALIGNED),
-    (dict(rows=1 << 23), FAKE, 1 << 50, INVALID), (dict(saved=0), FAKE, 1 << 30, INVALID), (dict(ld_dw=299), FAKE, 1 << 30, INVALID), (dict(stride_dw=59999), FAKE, 1 << 30, INVALID),
+    (dict(rows=1 << 23, source=0), FAKE, 1 << 50, INVALID), (dict(saved=0), FAKE, 1 << 30, INVALID), (dict(ld_dw=299), FAKE, 1 << 30, INVALID), (dict(stride_dw=59999), FAKE, 1 << 30, INVALID),
     ({}, 0, 0, INVALID), ({}, FAKE, 1000, SMALL)])
 def test_product_backward_refusals(lib, over, ws, size, code):
     assert lib.shampoo_product8_backward(X._PRODUCT.pack(*{**PRODUCT, **over}.values()), ws, size, None) == code
@@ -156,7 +156,7 @@ def test_workspace_holds_every_spread_of_rows(lib):
                 sizes = [a, b, rows - a - b]
                 need = sum(-(-s // 128) for s in sizes)
                 out = ctypes.c_size_t()
-                args = X._PRODUCT.pack(*{**PRODUCT, "rows": rows, "experts": 3, "n_in": 128}.values())
+                args = X._PRODUCT.pack(*{**PRODUCT, "rows": rows, "x_rows": rows, "slots": 1, "experts": 3, "n_in": 128}.values())
                 assert lib.shampoo_product8_saved_size(args, ctypes.byref(out)) == 0
                 assert out.value >= need * 128 * 128 + need * 128
 
