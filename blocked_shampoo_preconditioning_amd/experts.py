@@ -251,31 +251,43 @@ def quantize_weight(w, backward=False):
     return Weight8(made[0], made[1], n_in, n_out, *made[2:])
 
 
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
 def _weight_pointers(name, values, scales, lead, n_in, n_out, like):
-    for t, dtype, shape, what in zip((values, scales), (torch.float8_e4m3fn, torch.float8_e8m0fnu), _weight_shapes(lead, n_in, n_out),
-                                     ("values", "scales")):
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != like.get_device():
-            raise ValueError(f"{name}{what} must be a {dtype} tensor on {like.device}")
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}{what} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    return values.data_ptr(), scales.data_ptr()
+    """Pointers of 8-bit weights of these sizes, leading dimensions and device."""
+    dev = like.get_device()
+    shape, scale_shape = _weight_shapes(lead, n_in, n_out)
+    if values.dtype is _E4M3 and scales.dtype is _E8M0 and values.get_device() == dev and scales.get_device() == dev and \
+            values.shape == shape and scales.shape == scale_shape and values.is_contiguous() and scales.is_contiguous():
+        return values.data_ptr(), scales.data_ptr()
+    for t, dtype, want, what in ((values, _E4M3, shape, "values"), (scales, _E8M0, scale_shape, "scales")):
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise ValueError(f"{name}{what} must be a {dtype} tensor on {like.device}, got {t.dtype} on {t.device}")
+        if t.shape != want or not t.is_contiguous():
+            raise ValueError(f"{name}{what} must be contiguous with shape {tuple(want)}, got {tuple(t.shape)}")
 
 
-def _product_head(t, name, w8, plan):
-    """(leading dimensions of the weights, experts, dtype code, pointer of offsets)."""
-    lead = w8.values.shape[:-2]
-    n_experts = lead[0] if lead else 1
-    dt = _first(name, t)[0]
-    if plan is None:
-        if lead:
-            raise ValueError("plan is None: with a matrix for each expert it says which rows are whose")
-        return lead, n_experts, dt, 0
+def _offsets(plan, n_experts, like):
+    """Pointer of a plan's offsets."""
     offsets = plan.offsets
-    if offsets.dtype is not torch.int32 or offsets.get_device() != t.get_device() or not offsets.is_contiguous():
+    if offsets.dtype is not torch.int32 or offsets.get_device() != like.get_device() or not offsets.is_contiguous():
         raise ValueError("plan.offsets must be a contiguous int32 tensor on the call's device")
     if offsets.shape != (n_experts + 1,):
         raise ValueError(f"plan.offsets has shape {tuple(offsets.shape)}, expected ({n_experts + 1},)")
-    return lead, n_experts, dt, offsets.data_ptr()
+    return offsets.data_ptr()
+
+
+def _lead(w8, plan):
+    """Leading dimensions of the weights (none, or experts) and how many matrices they are."""
+    lead = w8.values.shape[:-2]
+    if len(lead) > 1:
+        raise ValueError(f"w8.values has shape {tuple(w8.values.shape)}: one matrix, or one for each expert")
+    if plan is None:
+        if lead:
+            raise ValueError("plan is None: with a matrix for each expert it says which rows are whose")
+        return lead, 1
+    return lead, lead[0] if lead else 1
 
 
 def product8_forward(x, w8, plan=None, gather=False, save=False):
@@ -285,22 +297,22 @@ def product8_forward(x, w8, plan=None, gather=False, save=False):
     out]; rows behind the last expert's are 0. With `save` returns (y, saved), saved being what
     `product8_backward` needs for dw (an opaque tensor: x in 8 bits by 128 rows of a column)."""
     n_in, n_out = w8.n_in, w8.n_out
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D (rows, width), got shape {tuple(x.shape)}")
-    x_rows, source, slots, rows, slot_rows = x.shape[0], 0, 1, x.shape[0], 0
-    if gather:
-        if plan is None:
-            raise ValueError("gather needs a plan")
-        slot_rows, x_rows, slots = _plan_rows(plan, x)
-        rows = x_rows * slots
-        if plan.source.dtype is not torch.int32 or plan.source.get_device() != x.get_device() or plan.source.shape != (rows,) or \
-                not plan.source.is_contiguous():
-            raise ValueError(f"plan.source must be a contiguous int32 tensor of {rows} elements on the call's device")
-        source = plan.source.data_ptr()
-    elif plan is not None:
-        _, tokens, slots = _plan_rows(plan, x)
-        x_rows = rows = tokens * slots
-    lead, n_experts, dt, offsets = _product_head(x, "x", w8, plan)
+    dt, x_rows, _ = _first("x", x)
+    lead, n_experts = _lead(w8, plan)
+    rows, offsets, source, slots, slot_rows = x_rows, 0, 0, 1, 0
+    if plan is not None:
+        offsets = _offsets(plan, n_experts, x)
+        slot_rows, tokens, slots = _plan_rows(plan, x)
+        rows = tokens * slots
+        if gather:
+            x_rows, src = tokens, plan.source
+            if src.dtype is not torch.int32 or src.get_device() != x.get_device() or src.shape != (rows,) or not src.is_contiguous():
+                raise ValueError(f"plan.source must be a contiguous int32 tensor of {rows} elements on the call's device")
+            source = src.data_ptr() or 256
+        else:
+            x_rows = rows
+    elif gather:
+        raise ValueError("gather needs a plan")
     px, lx = _matrix("x", x, x_rows, n_in, x)
     values, scales = _weight_pointers("w8.", w8.values, w8.scales, lead, n_in, n_out, x)
     y = x.new_empty((rows, n_out))
@@ -311,12 +323,16 @@ def product8_forward(x, w8, plan=None, gather=False, save=False):
         size = _known_size(("saved", key), "shampoo_product8_saved_size", _PRODUCT.pack(*head, *_NO_PRODUCT))
         saved = torch.empty(size, dtype=torch.uint8, device=x.device)
     args = _PRODUCT.pack(*head, values, scales, 0, 0, px, lx, y.data_ptr(), n_out, saved.data_ptr() if save else 0, 0, 0, 0, 0, 0, 0, 0)
-    size = _known_size(("forward", key, save), "shampoo_product8_workspace_size", args, 0)
-    ws, keep = _workspace(size, x)
+    if rows <= _FEW_ROWS and not save:
+        size = ws = 0
+    else:
+        size = _known_size(("forward", key, save), "shampoo_product8_workspace_size", args, 0)
+        ws, keep = _workspace(size, x)
     _call("shampoo_product8_forward", args, x.get_device(), ws, size)
     return (y, saved) if save else y
 
 
+_FEW_ROWS = 64  # up to here a call that saves nothing needs no workspace
 _NO_PRODUCT = (0,) * 16
 
 
@@ -326,13 +342,13 @@ def product8_backward(dy, w8, saved, plan=None, need_dx=True, need_dw=True):
     128 rows of a column, in w's shape and dy's dtype. The roundings of x, W and dy themselves have gradient 1.
     need_dx (needs w8.back_values) / need_dw (needs saved): None is returned for what is not needed."""
     n_in, n_out = w8.n_in, w8.n_out
-    if dy.dim() != 2:
-        raise ValueError(f"dy must be 2-D (rows, width), got shape {tuple(dy.shape)}")
-    rows = dy.shape[0]
+    dt, rows, _ = _first("dy", dy)
+    lead, n_experts = _lead(w8, plan)
+    offsets = 0
     if plan is not None:
+        offsets = _offsets(plan, n_experts, dy)
         _, tokens, slots = _plan_rows(plan, dy)
         rows = tokens * slots
-    lead, n_experts, dt, offsets = _product_head(dy, "dy", w8, plan)
     pdy, ldy = _matrix("dy", dy, rows, n_out, dy)
     back = (0, 0)
     if need_dx:
@@ -347,7 +363,7 @@ def product8_backward(dy, w8, saved, plan=None, need_dx=True, need_dw=True):
     psaved = 0
     if need_dw:
         size = _known_size(("saved", key), "shampoo_product8_saved_size", _PRODUCT.pack(*head, *_NO_PRODUCT))
-        if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or saved.numel() != size or saved.get_device() != dy.get_device():
+        if not isinstance(saved, torch.Tensor) or saved.dtype is not torch.uint8 or saved.numel() != size or saved.get_device() != dy.get_device() or not saved.is_contiguous():
             raise ValueError("saved is not what product8_forward kept for these sizes")
         psaved = saved.data_ptr()
         dw = dy.new_empty((*lead, n_in, n_out))

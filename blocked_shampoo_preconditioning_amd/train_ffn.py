@@ -1,13 +1,18 @@
 """A stack of feed-forward half-layers trained with the Shampoo step.
 
     python -m blocked_shampoo_preconditioning_amd.train_ffn --layers 4 --steps 20
+    python -m blocked_shampoo_preconditioning_amd.train_ffn --experts 8 --top 2 --dtype bf16
 
 Every half-layer is norm -> gated feed-forward block -> dropout, gate, norm
 and residual (the entry points of `layer`); its three weight matrices' gradients
 go to `shampoo.Shampoo.step` as they come out of the backward pass, its vectors
-(norm weights and gate) take plain gradient steps. The task is synthetic: the
-residual stream after the last layer has to match a fixed random linear map of
-the input. Prints the loss every few steps and the time of a training step.
+(norm weights and gate) take plain gradient steps. With --experts the block is one
+of several for each token: a router's softmax over its `--top` likeliest experts,
+tokens sorted by expert and back, and the three products in 8 bits (the entry
+points of `experts`); the experts' matrices and the router's go to the Shampoo
+step. The task is synthetic: the residual stream after the last layer has to match
+a fixed random linear map of the input. Prints the loss every few steps and the
+time of a training step.
 """
 from __future__ import annotations
 
@@ -16,6 +21,7 @@ import time
 
 import torch
 
+from . import experts as _experts
 from . import layer
 from .shampoo import Shampoo
 
@@ -29,6 +35,9 @@ class HalfLayer:
         def normal(rows, cols):
             return (torch.randn(rows, cols, generator=gen, device="cuda") * rows ** -0.5).to(dtype)
         self.matrices = [normal(d, f), normal(d, f), normal(f, d)]
+        self._make_vectors(d, dtype, activation, dropout)
+
+    def _make_vectors(self, d, dtype, activation, dropout):
         self.vectors = {k: torch.ones(d, dtype=dtype, device="cuda") for k in ("pre", "post")}
         self.vectors["gate"] = torch.full((1, d), 0.5, dtype=dtype, device="cuda")
         self.activation, self.dropout = activation, dropout
@@ -37,9 +46,18 @@ class HalfLayer:
         return dict(post="rms", post_weight=self.vectors["post"], gate=self.vectors["gate"], dropout=self.dropout,
                     seed=seed, offset=offset, next="none")
 
+    def block_forward(self, a):
+        """(z, what block_backward needs) of the block behind the norm."""
+        return layer.ffn_forward(a, *self.matrices, activation=self.activation, save=True)
+
+    def block_backward(self, dz, a, saved):
+        """(gradient of a, gradients of the matrices)."""
+        da, *matrices = layer.ffn_backward(dz, a, *self.matrices, saved, activation=self.activation)
+        return da, matrices
+
     def forward(self, x, seed, offset):
         a, a_stats = layer.norm_forward(x, "rms", self.vectors["pre"])
-        z, saved = layer.ffn_forward(a, *self.matrices, activation=self.activation, save=True)
+        z, saved = self.block_forward(a)
         settings = self._settings(seed, offset)
         r, _, r_stats = layer.residual_forward(x, z, **settings)
         return r, (x, a, a_stats, z, saved, r, r_stats, settings)
@@ -48,17 +66,59 @@ class HalfLayer:
         """(gradient of the input, of the matrices, of the vectors)."""
         x, a, a_stats, z, saved, r, r_stats, settings = kept
         g = layer.residual_backward(dr, None, r, z, r_stats, **settings)
-        da, *matrices = layer.ffn_backward(g["z"], a, *self.matrices, saved, activation=self.activation)
+        da, matrices = self.block_backward(g["z"], a, saved)
         pre = layer.norm_backward(da, x, a_stats, dr=g["x"], kind="rms", weight=self.vectors["pre"])
         return pre["x"], matrices, {"pre": pre["weight"], "post": g["post_weight"], "gate": g["gate"]}
 
 
+class ExpertsHalfLayer(HalfLayer):
+    """A half-layer whose block is a gated block for each expert, with SiLU; a token goes to `top` of them. The router's
+    weights are the softmax over the chosen experts' scores."""
+
+    def __init__(self, d, f, gen, dtype, n_experts, top, dropout=0.1):
+        def normal(rows, cols, *lead):
+            return (torch.randn(*lead, rows, cols, generator=gen, device="cuda") * rows ** -0.5).to(dtype)
+        self.n_experts, self.top = n_experts, top
+        self.router = normal(d, n_experts)
+        self.stacked = [normal(d, f, n_experts), normal(d, f, n_experts), normal(f, d, n_experts)]
+        self.matrices = [self.router] + [w[e] for w in self.stacked for e in range(n_experts)]
+        self._make_vectors(d, dtype, "silu", dropout)
+
+    def block_forward(self, a):
+        scores, ids = (a.float() @ self.router.float()).topk(self.top, dim=1)
+        weights = scores.softmax(1)
+        plan = _experts.sort_tokens(ids, self.n_experts)
+        gate, up, down = (_experts.quantize_weight(w, backward=True) for w in self.stacked)
+        g, saved_g = _experts.product8_forward(a, gate, plan, gather=True, save=True)
+        u, saved_u = _experts.product8_forward(a, up, plan, gather=True, save=True)
+        h = torch.nn.functional.silu(g) * u
+        ys, saved_h = _experts.product8_forward(h, down, plan, save=True)
+        return _experts.combine(ys, plan, weights), (ids, weights, plan, gate, up, down, g, u, saved_g, saved_u, ys, saved_h)
+
+    def block_backward(self, dz, a, saved):
+        ids, weights, plan, gate, up, down, g, u, saved_g, saved_u, ys, saved_h = saved
+        dys, dweights = _experts.combine_backward(dz, ys, plan, weights)
+        dh, d_down = _experts.product8_backward(dys, down, saved_h, plan)
+        gf, dhf = g.float(), dh.float()
+        s = torch.sigmoid(gf)
+        dg = (dhf * u.float() * s * (1 + gf * (1 - s))).to(g.dtype)
+        du = (dhf * gf * s).to(g.dtype)
+        dxg, d_gate = _experts.product8_backward(dg, gate, saved_g, plan)
+        dxu, d_up = _experts.product8_backward(du, up, saved_u, plan)
+        da = _experts.dispatch_backward(dxg, plan).float() + _experts.dispatch_backward(dxu, plan).float()
+        dscores = weights * (dweights - (dweights * weights).sum(1, keepdim=True))
+        dense = torch.zeros(a.shape[0], self.n_experts, device=a.device).scatter_(1, ids, dscores)
+        da = (da + dense @ self.router.float().t()).to(a.dtype)
+        d_router = (a.float().t() @ dense).to(a.dtype)
+        return da, [d_router, *d_gate.unbind(0), *d_up.unbind(0), *d_down.unbind(0)]
+
+
 def train(layers=4, d=512, f=1536, tokens=2048, steps=20, lr=1e-3, vector_lr=1e-2, block=512, root_every=5, dtype="f32",
-          seed=0, log=print):
-    """Runs the training; returns the losses."""
+          seed=0, log=print, n_experts=0, top=2):
+    """Runs the training (with n_experts, a block for each of them); returns the losses."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     dt = DTYPES[dtype]
-    stack = [HalfLayer(d, f, gen, dt) for _ in range(layers)]
+    stack = [ExpertsHalfLayer(d, f, gen, dt, n_experts, top) if n_experts else HalfLayer(d, f, gen, dt) for _ in range(layers)]
     x = torch.randn(tokens, d, generator=gen, device="cuda").to(dt)
     goal = x.float() @ (torch.randn(d, d, generator=gen, device="cuda") * d ** -0.5)
     matrices = [w for h in stack for w in h.matrices]
@@ -102,8 +162,10 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--lr", type=float, default=1e-3)
     ap.add_argument("--dtype", choices=sorted(DTYPES), default="f32")
+    ap.add_argument("--experts", type=int, default=0, help="blocks of a half-layer (0: one for all tokens)")
+    ap.add_argument("--top", type=int, default=2, help="experts of a token")
     a = ap.parse_args(argv)
-    train(a.layers, a.width, a.hidden, a.tokens, a.steps, a.lr, dtype=a.dtype)
+    train(a.layers, a.width, a.hidden, a.tokens, a.steps, a.lr, dtype=a.dtype, n_experts=a.experts, top=a.top)
 
 
 if __name__ == "__main__":
