@@ -120,9 +120,13 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM;
-  // Workgroups go round the 8 XCDs; this one has every stride-th tile of its XCD's.
-  const int stride = static_cast<int>(gridDim.x / 8);
+  // Workgroups go round the 8 XCDs, and through the list of their XCD's tiles to and
+  // fro: one that has the first of a round has the last of the next.
   const WorkRecord* mine = all.work + static_cast<int64_t>(blockIdx.x % 8) * all.per;
+  auto place = [&](int round) {
+    const int stride = static_cast<int>(gridDim.x / 8), nth = static_cast<int>(blockIdx.x / 8);
+    return round & 1 ? (round + 1) * stride - 1 - nth : round * stride + nth;
+  };
 
   // A load instruction covers eight rows of 128 bytes: row (instruction * NW + wave)
   // * 8 + lane / 8, place lane % 8. A row's chunk c of 16 bytes sits at place c ^
@@ -147,15 +151,15 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
   const bool b_scales = wave & 1;
   int4v ra = make_rsrc(0, 0), rb = ra, rs = ra;
   uint32_t vs = 0, scale_step = 0;
-  int lnext = static_cast<int>(blockIdx.x / 8), lproduct = -1, lstep = 0, lturns = 0;
+  int lround = 0, lproduct = -1, lstep = 0, lturns = 0;
   bool lwords = false, lwords_mine = false;
   auto enter = [&]() __attribute__((always_inline)) {  // the next tile that has steps
     int16v w = {};
     int turns = kNoTileNorBehind;
     do {
-      if (lnext < all.per) w = scalar_load<int16v>(mine + lnext);
-      turns = lnext < all.per ? w[14] : kNoTileNorBehind;
-      lnext += stride;
+      const int at = place(lround++);
+      if (at < all.per) w = scalar_load<int16v>(mine + at);
+      turns = at < all.per ? w[14] : kNoTileNorBehind;
     } while (turns == 0 || turns == kNoTile);
     const bool more = turns > 0;
     const int product = more ? w[15] >> 22 : 0;
@@ -299,13 +303,13 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
   const std::integral_constant<int, 1> second{};
 
   // the tile that is multiplied: c, turns and shape of its record
-  int cnext = static_cast<int>(blockIdx.x / 8), turns = kNoTileNorBehind, turn = 0;
+  int round = 0, turns = kNoTileNorBehind, turn = 0;
   int4v c{};
   auto next_tile = [&]() __attribute__((always_inline)) {
     do {
-      if (cnext < all.per) c = scalar_load<int4v>(&mine[cnext].c);
-      turns = cnext < all.per ? c[2] : kNoTileNorBehind;
-      cnext += stride;
+      const int at = place(round++);
+      if (at < all.per) c = scalar_load<int4v>(&mine[at].c);
+      turns = at < all.per ? c[2] : kNoTileNorBehind;
     } while (turns == kNoTile);
     turn = 0;
   };

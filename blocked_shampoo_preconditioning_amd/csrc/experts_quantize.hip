@@ -213,17 +213,44 @@ __device__ __forceinline__ void write_tables(const Groups& g, int per_tile, int*
 // product's tiles, in groups of four row tiles, so that those in flight on one XCD
 // share their operands in its L2. Experts have sums of different length: each XCD
 // takes its part of every expert's tiles, another one for each (dW of eight experts of
-// 16384 x 2048 x 2048 bf16: 88 us; with an expert an XCD 126).
-__device__ __forceinline__ void write_work(const Products& all, const Groups& g, int which, int* first_tile, int* first_block) {
+// 16384 x 2048 x 2048 bf16: 88 us; with an expert an XCD 126). dW, the last product,
+// goes by length, longest first, and the first product before the experts whose sums
+// are shorter than its own: workgroups take the list to and fro, which then evens
+// out (dx and dW of eight experts, three batches: 157, 142 and 145 us, in the experts'
+// order 153, 160 and 164).
+__device__ __forceinline__ void write_work(const Products& all, const Groups& g, int which, int* first_tile, int* first_block, int* order) {
   const int side = product_tile(static_cast<ProductTile>(all.tile)), per_tile = side / kBlock;
   if (g.offsets) write_tables(g, per_tile, first_tile, first_block);
+  const ProductArgs& last = all.p[all.count > 0 ? all.count - 1 : 0];
+  const uint32_t last_tiles = static_cast<uint32_t>((last.M + side - 1) / side) * ((last.N + side - 1) / side), last_per = (last_tiles + 7) / 8;
+  const bool sorted = g.offsets && all.count > 0 && last.by_expert && last_tiles >= 16 && all.experts <= kThreads;
+  uint32_t head = 0;  // experts in front of the first product
+  if (sorted) {
+    const int e = threadIdx.x;
+    bool longer = false;
+    if (e < all.experts) {
+      const int mine = first_block[e + 1] - first_block[e];
+      int rank = 0;
+      for (int j = 0; j < all.experts; ++j) {
+        const int its = first_block[j + 1] - first_block[j];
+        rank += its > mine || (its == mine && j < e);
+      }
+      order[rank] = e;
+      longer = all.count == 1 || mine > all.p[0].k_blocks;
+    }
+    head = static_cast<uint32_t>(__syncthreads_count(longer));
+  }
   const int64_t record = static_cast<int64_t>(which) * kThreads + threadIdx.x;
   if (record >= 8ll * all.per) return;
   const uint32_t xcd = static_cast<uint32_t>(record / all.per);
   uint32_t n = static_cast<uint32_t>(record - static_cast<int64_t>(xcd) * all.per);
   WorkRecord w{};
   w.turns = kNoTileNorBehind;
-  for (int q = 0; q < all.count; ++q) {
+  int q = 0;
+  const bool front = sorted && n < head * last_per;
+  if (front) q = all.count - 1;
+  else if (sorted && all.count > 1) n -= head * last_per;
+  for (; q < all.count; ++q) {
     const ProductArgs& p = all.p[q];
     const uint32_t tn = (p.N + side - 1) / side, experts = p.by_expert ? all.experts : 1;
     uint32_t tm = (p.M + side - 1) / side;
@@ -235,6 +262,7 @@ __device__ __forceinline__ void write_work(const Products& all, const Groups& g,
     const uint32_t tiles = tm * tn, per = (tiles + 7) / 8;  // of an XCD, of each expert
     const bool round = tiles < 16;                          // fewer than two of an expert an XCD: all experts' in turn
     const uint32_t length = round ? (tiles * experts + 7) / 8 : per * experts;
+    if (sorted && all.count > 1 && q == 1 && !front) n += head * last_per;  // the experts behind the first product
     if (n >= length) {
       n -= length;
       continue;
@@ -247,9 +275,10 @@ __device__ __forceinline__ void write_work(const Products& all, const Groups& g,
       expert = at / tiles;
       id = at - expert * tiles;
     } else {
-      expert = n / per;
-      id = (xcd + expert) % 8 * per + (n - expert * per);
+      const uint32_t nth = n / per;
+      id = (xcd + nth) % 8 * per + (n - nth * per);
       if (id >= tiles) break;
+      expert = p.by_expert && sorted ? static_cast<uint32_t>(order[nth]) : nth;
     }
     const uint32_t group = id / (4 * tn), in_group = min(4u, tm - 4 * group);
     id -= group * 4 * tn;
@@ -308,7 +337,7 @@ __device__ __forceinline__ void write_work(const Products& all, const Groups& g,
 }
 
 constexpr int kMaxExperts = 1024;
-constexpr int kTables = 2 * (kMaxExperts + 1), kLds = kBlock * kBlock;
+constexpr int kTables = 2 * (kMaxExperts + 1) + kThreads, kLds = kBlock * kBlock;
 static_assert(kLds >= 4 * kTables, "");
 
 template <bool F32>
@@ -320,7 +349,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a) {
   const uint32_t writers = (8 * static_cast<uint32_t>(a.products.per) + kThreads - 1) / kThreads;
   if (blockIdx.x < writers) {
     int* tables = reinterpret_cast<int*>(lds);
-    write_work(a.products, a.g, static_cast<int>(blockIdx.x), tables, tables + kMaxExperts + 1);
+    write_work(a.products, a.g, static_cast<int>(blockIdx.x), tables, tables + kMaxExperts + 1, tables + 2 * (kMaxExperts + 1));
     return;
   }
   const uint32_t block = blockIdx.x - writers;
@@ -407,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(QuantizeArgs a) {
   __shared__ int first_row[kMaxExperts + 1], first_block[kMaxExperts + 1], places[kScatterRows * kMaxScatter];
   const uint32_t writers = (8 * static_cast<uint32_t>(a.products.per) + kThreads - 1) / kThreads;
   if (blockIdx.x < writers) {
-    write_work(a.products, a.g, static_cast<int>(blockIdx.x), first_row, first_block);
+    write_work(a.products, a.g, static_cast<int>(blockIdx.x), first_row, first_block, places);
     return;
   }
   const uint32_t block = blockIdx.x - writers;

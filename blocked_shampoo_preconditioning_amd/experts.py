@@ -126,9 +126,8 @@ def sort_tokens(ids, n_experts):
         raise ValueError(f"n_experts must be in [1, {MAX_EXPERTS}], got {n_experts}")
     tokens, slots = ids.shape
     ptr, ld = _matrix("ids", ids, tokens, slots, ids)
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device)
-    rows = torch.empty((tokens, slots), dtype=torch.int32, device=ids.device)
-    source = torch.empty(tokens * slots, dtype=torch.int32, device=ids.device)
+    rows = torch.empty_like(ids, dtype=torch.int32, memory_format=torch.contiguous_format)
+    offsets, source = rows.new_empty(n_experts + 1), rows.new_empty(tokens * slots)
     args = _SORT.pack(tokens, slots, n_experts, size, ptr, ld, offsets.data_ptr(), rows.data_ptr(), source.data_ptr())
     need = _known_size(("sort", tokens, slots, n_experts), "shampoo_sort_workspace_size", args)
     ws, keep = _workspace(need, ids)
