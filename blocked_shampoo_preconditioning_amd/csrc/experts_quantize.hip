@@ -570,8 +570,11 @@ int64_t work_length(const Products& a, int64_t rows, bool grouped) {
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
   const uint32_t writers = (8 * static_cast<uint32_t>(a.products.per) + kThreads - 1) / kThreads;
   const int tiles = a.slot_rows ? (a.rows_in + kScatterRows - 1) / kScatterRows : a.g.blocks;
-  const uint32_t grid = static_cast<uint32_t>(a.col_blocks) * static_cast<uint32_t>(tiles) + writers;
-  if (grid == 0) return hipSuccess;
+  const int64_t all = static_cast<int64_t>(a.col_blocks) * tiles + writers;
+  if (all == 0) return hipSuccess;
+  // a launch has fewer than 2^32 threads; of so many tiles the values alone are 2^37 bytes and more
+  if (all >= (int64_t(1) << 32) / kThreads) return hipErrorInvalidConfiguration;
+  const uint32_t grid = static_cast<uint32_t>(all);
   if (a.slot_rows)
     a.f32 ? scatter_kernel<true><<<grid, kThreads, 0, s>>>(a) : scatter_kernel<false><<<grid, kThreads, 0, s>>>(a);
   else

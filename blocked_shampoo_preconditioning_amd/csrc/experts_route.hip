@@ -413,9 +413,28 @@ int columns_per_wave(const RouteArgs& a) {
   return groups >= 2 && a.tokens * ((groups + 1) / 2) >= 4096 ? 2 : 1;
 }
 
+// A launch has fewer than 2^32 threads: at most this many tokens each.
+constexpr int64_t kTokensALaunch = int64_t(1) << 23;
+template <class F>
+hipError_t in_parts(const RouteArgs& a, F&& f) {
+  const int64_t e = a.f32 ? 4 : 2;
+  for (int64_t t = 0; t < a.tokens; t += kTokensALaunch) {
+    RouteArgs part = a;
+    part.tokens = min(a.tokens - t, kTokensALaunch);
+    part.rows = a.rows + t * a.slots;
+    if (a.weights) part.weights = a.weights + t * a.slots;
+    if (a.dweights) part.dweights = a.dweights + t * a.slots;
+    if (a.x) part.x = static_cast<const char*>(a.x) + t * a.ld_x * e;
+    if (a.y) part.y = static_cast<char*>(a.y) + t * a.ld_y * e;
+    const hipError_t err = f(part);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
 template <class F>
 hipError_t by_columns(const RouteArgs& a, F&& f) {
-  if (a.tokens == 0 || a.width == 0) return hipSuccess;
+  if (a.width == 0) return hipSuccess;
   const int nc = columns_per_wave(a);
   const dim3 grid(static_cast<uint32_t>((a.tokens + kRouteWaves - 1) / kRouteWaves), static_cast<uint32_t>((a.width + 512 * nc - 1) / (512 * nc)));
   if (nc == 4)
@@ -450,26 +469,29 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_dispatch(const RouteArgs& a, hipStream_t s) {
-  return by_columns(a, [&](auto nc, dim3 grid) {
-    if (a.f32)
-      dispatch_kernel<true, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
-    else
-      dispatch_kernel<false, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+hipError_t launch_dispatch(const RouteArgs& all, hipStream_t s) {
+  return in_parts(all, [&](const RouteArgs& a) {
+    return by_columns(a, [&](auto nc, dim3 grid) {
+      if (a.f32)
+        dispatch_kernel<true, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+      else
+        dispatch_kernel<false, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+    });
   });
 }
 
-hipError_t launch_combine(const RouteArgs& a, hipStream_t s) {
-  return by_columns(a, [&](auto nc, dim3 grid) {
-    if (a.f32)
-      combine_kernel<true, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
-    else
-      combine_kernel<false, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+hipError_t launch_combine(const RouteArgs& all, hipStream_t s) {
+  return in_parts(all, [&](const RouteArgs& a) {
+    return by_columns(a, [&](auto nc, dim3 grid) {
+      if (a.f32)
+        combine_kernel<true, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+      else
+        combine_kernel<false, decltype(nc)::value><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+    });
   });
 }
 
-hipError_t launch_combine_backward(const RouteArgs& a, hipStream_t s) {
-  if (a.tokens == 0) return hipSuccess;
+static hipError_t launch_combine_backward_part(const RouteArgs& a, hipStream_t s) {
   auto start = [&](auto nc, auto w) {
     constexpr int NC = decltype(nc)::value, W = decltype(w)::value;
     const uint32_t grid = static_cast<uint32_t>(W == 1 ? (a.tokens + kRouteWaves - 1) / kRouteWaves : a.tokens);
@@ -494,6 +516,10 @@ hipError_t launch_combine_backward(const RouteArgs& a, hipStream_t s) {
     start(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   }
   return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const RouteArgs& all, hipStream_t s) {
+  return in_parts(all, [&](const RouteArgs& a) { return launch_combine_backward_part(a, s); });
 }
 
 }  // namespace she

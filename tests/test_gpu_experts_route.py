@@ -176,6 +176,26 @@ def test_offsets_past_32_bits():
     assert ((dw[-5:].double() - want).abs() <= (width + 2) * 2.0 ** -24 * want).all()
 
 
+def test_more_tokens_than_a_launch_has_threads_for():
+    """2^26 tokens and some, four to a workgroup of 256: over 2^32 threads in all. (In torch too an index of so many rows
+    gives five rows and nothing else: the rows are taken in parts.)"""
+    tokens, width = 2 ** 26 + 5, 8
+    log(f"routes {tokens} x 1 x {width}")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(-1, 4, (tokens, 1), generator=g, device="cuda", dtype=torch.int32)
+    plan = experts.sort_tokens(ids, 4)
+    x = torch.randint(-4, 5, (tokens, width), generator=g, device="cuda").bfloat16()
+    want = torch.cat([x[torch.where(s < 0, ~s, s)] * (s >= 0)[:, None] for s in plan.source.long().split(2 ** 24)])
+    assert torch.equal(plan.offsets[1:].long(), torch.stack([(ids[:, 0] == e).sum() for e in range(4)]).cumsum(0))
+    xs = experts.dispatch(x, plan)
+    assert torch.equal(xs, want)
+    kept = x * (ids >= 0)
+    assert torch.equal(experts.combine(xs, plan), kept)
+    dys, dw = experts.combine_backward(x, xs, plan, torch.full((tokens, 1), 2.0, device="cuda"))
+    assert torch.equal(dys, 2 * want)
+    assert torch.equal(dw[:, 0], kept.float().square().sum(1))  # small integers: exact
+
+
 def test_streams_and_graphs():
     """On another stream, and captured into a graph that is replayed with eager work between."""
     ids, dev = make_ids(3, 3000, 2, 8, 0.1)
