@@ -11,7 +11,16 @@
 // hundredth of what rounding to bf16 leaves, and where one term stands out, less
 // than a seventieth of what its own rounding to 8 bits does. It is too much for
 // fp32 results: those come from the bf16 instruction with both operands widened,
-// scales included, which is exact, at a quarter of the rate.
+// scales included, which is exact, at a quarter of the rate. There 64 instructions of
+// a step come with 128 that widen, two behind each; bytes are read a phase before
+// (1536 x 4096 x 2688: 41 us, widened as they are read 47).
+//
+// What bounds it: large bf16 products the power limit, at the rate of the library's
+// 8-bit product without blocks' scales (y of 8192 x 2048 x 8192 112 us, 2.4 PFLOP/s,
+// the library 107; of 4096 x 8192 x 2048 62, the library 65; dx and dW of the former
+// 203, 2.7 PFLOP/s). Where each CU has one 128 tile, the L2s: 33 KB a step and CU
+// in 0.53 us are 15 TB/s. fp32: the issue of one wave's instructions, a step of one
+// tile 1.0 us alone on a CU, 0.75 with two, 0.45 were it the matrix cores.
 //
 // Operands go from HBM to LDS by direct loads of 16 bytes a lane, a K block a step;
 // the scales of a step go the same way, 256 bytes an operand. A step's products are
@@ -113,10 +122,26 @@ __device__ __forceinline__ V scalar_load(const void* p) {
 }
 __device__ __forceinline__ uint64_t address(int low, int high) { return static_cast<uint64_t>(static_cast<uint32_t>(high)) << 32 | static_cast<uint32_t>(low); }
 
+// Where a wave turns its fp32 results: eight rows of 64.
+constexpr int kTurnedPitch = 272, kTurned = 8 * kTurnedPitch;
+
+// Four fp32 of a row, or its last n < 4.
+__device__ __forceinline__ void store4(char* p, int64_t off, int n, const floatx4& v) {
+  float* q = reinterpret_cast<float*>(p) + off;
+  if (n == 4) {
+    __builtin_memcpy(q, &v, 16);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < n) q[k] = v[k];
+}
+
 template <class T>
 __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) {
   constexpr bool F32 = T::F32;
   __shared__ __attribute__((aligned(1024))) char lds[T::ST * T::STAGE];
+  __shared__ __attribute__((aligned(16))) char turned[F32 ? T::NW * kTurned : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM;
@@ -240,18 +265,9 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
   auto scale_a = [&](int i) { return value_of(sa2[i >> 2] >> (8 * (i & 3)) & 255u); };
   auto scale_b = [&](int j) { return value_of(__builtin_amdgcn_perm(sb2[j >> 2], sb2[j >> 2], picks[0]) >> (8 * (j & 3)) & 255u); };
   // half of operand f: chunk q4 or q4 + 4 of its row
-  auto fetch = [&](Fragment<F32>& x, uint32_t base, int f, int half, float scale) {
+  auto fetch = [&](uint32_t base, int f, int half) {
     const uint32_t from = base + (64 * (f >> 2) + 4 * (f & 3)) * 128;
-    const int4v v = *reinterpret_cast<lds_int4>(half ? from ^ 64u : from);
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        widen(v[2 * i], scale, x.k[2 * half + i], 0);
-        widen(v[2 * i + 1], scale, x.k[2 * half + i], 4);
-      }
-    } else {
-      (half ? x.hi : x.lo) = v;
-    }
+    return *reinterpret_cast<lds_int4>(half ? from ^ 64u : from);
   };
 
   floatx4 acc[T::FM][T::FN];
@@ -264,23 +280,20 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
 
   constexpr int HA = T::FM / 2, HB = T::FN / 2, kMma = HA * HB;
   Fragment<F32> a0[HA], a1[HA], b0[HB], b1[HB];
-  auto product = [&](auto i_, auto j_, const Fragment<F32>& x, const Fragment<F32>& y) {
-    constexpr int i = decltype(i_)::value, j = decltype(j_)::value;
-    if constexpr (F32) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y.k[k], x.k[k], acc[i][j], 0, 0, 0);
-    } else {
-      const int8v av = __builtin_shufflevector(x.lo, x.hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      const int8v bv = __builtin_shufflevector(y.lo, y.hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[i][j], 0, 0, j & 3, static_cast<int>(sb[j >> 2]), i & 3,
-                                                                   static_cast<int>(sa[i >> 2]));
-    }
-  };
-  // One phase: products of half IH of A and half JH of B, with more(q) behind the q-th.
+  // One phase: products of half IH of A and half JH of B, with more(q) behind the q-th
+  // instruction. fp32: four an operand pair, those of one pair not behind each other.
+  constexpr int kSlots = F32 ? 4 * kMma : kMma;
   auto phase = [&](auto ih, auto jh, const Fragment<F32>(&x)[HA], const Fragment<F32>(&y)[HB], auto&& more) {
-    each<kMma>([&](auto q) {
-      constexpr int Q = decltype(q)::value, i = Q / HB, j = Q % HB;
-      product(std::integral_constant<int, decltype(ih)::value * HA + i>{}, std::integral_constant<int, decltype(jh)::value * HB + j>{}, x[i], y[j]);
+    each<kSlots>([&](auto q) {
+      constexpr int Q = decltype(q)::value, i = Q % kMma / HB, j = Q % HB, I = decltype(ih)::value * HA + i, J = decltype(jh)::value * HB + j;
+      if constexpr (F32) {
+        acc[I][J] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[j].k[Q / kMma], x[i].k[Q / kMma], acc[I][J], 0, 0, 0);
+      } else {
+        const int8v av = __builtin_shufflevector(x[i].lo, x[i].hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        const int8v bv = __builtin_shufflevector(y[j].lo, y[j].hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[I][J], 0, 0, J & 3, static_cast<int>(sb[J >> 2]), I & 3,
+                                                                     static_cast<int>(sa[I >> 2]));
+      }
       more(Q);
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -294,10 +307,30 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
       if (r * SPAN / N == q) read(r >> 1, r & 1);
   };
   auto read_a = [&](Fragment<F32>(&x)[HA], int first, int q) {
-    reads(std::integral_constant<int, HA>{}, q, [&](int i, int half) { fetch(x[i], fa, first + i, half, F32 ? scale_a(first + i) : 0.f); });
+    if constexpr (!F32) reads(std::integral_constant<int, HA>{}, q, [&](int i, int half) { (half ? x[i].hi : x[i].lo) = fetch(fa, first + i, half); });
   };
   auto read_b = [&](Fragment<F32>(&x)[HB], int first, int q) {
-    reads(std::integral_constant<int, HB>{}, q, [&](int j, int half) { fetch(x[j], fb, first + j, half, F32 ? scale_b(first + j) : 0.f); });
+    if constexpr (!F32) reads(std::integral_constant<int, HB>{}, q, [&](int j, int half) { (half ? x[j].hi : x[j].lo) = fetch(fb, first + j, half); });
+  };
+  // fp32: bytes are read a phase before they are widened, four reads a half of an
+  // operand, and widened a word (of 4 HA) at a time, as many as go behind an instruction.
+  static_assert(!F32 || HA == HB, "");
+  constexpr int kHeld = F32 ? 2 * HA : 1, kWords = 4 * kHeld;
+  int4v held[2][kHeld];
+  auto hold_a = [&](int4v(&v)[kHeld], int first, int r) {
+    if (r >= 0 && r < kHeld) v[r] = fetch(fa, first + r / 2, r & 1);
+  };
+  auto hold_b = [&](int4v(&v)[kHeld], int first, int r) {
+    if (r >= 0 && r < kHeld) v[r] = fetch(fb, first + r / 2, r & 1);
+  };
+  auto widen_word = [&](Fragment<F32>& x, const int4v& v, int half, int w, float scale) {
+    if constexpr (F32) widen(v[w], scale, x.k[2 * half + w / 2], 4 * (w & 1));
+  };
+  auto widen_a = [&](Fragment<F32>(&x)[HA], const int4v(&v)[kHeld], int first, int w) {
+    if (w >= 0 && w < kWords) widen_word(x[w / 8], v[w / 4], w / 4 & 1, w & 3, scale_a(first + w / 8));
+  };
+  auto widen_b = [&](Fragment<F32>(&x)[HB], const int4v(&v)[kHeld], int first, int w) {
+    if (w >= 0 && w < kWords) widen_word(x[w / 8], v[w / 4], w / 4 & 1, w & 3, scale_b(first + w / 8));
   };
   const std::integral_constant<int, 0> first{};
   const std::integral_constant<int, 1> second{};
@@ -327,12 +360,21 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
   }
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((T::ST - 1) * kLoads) : "memory");
   read_scales();
+  if constexpr (F32) {
 #pragma unroll
-  for (int q = 0; q < kMma; ++q) {
-    read_a(a0, 0, q);
-    read_b(b0, 0, q);
+    for (int r = 0; r < kHeld; ++r) hold_a(held[0], 0, r), hold_b(held[1], 0, r);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) widen_a(a0, held[0], 0, w), widen_b(b0, held[1], 0, w);
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) hold_b(held[0], HB, r);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kMma; ++q) {
+      read_a(a0, 0, q);
+      read_b(b0, 0, q);
+    }
+    use_scales();
   }
-  use_scales();
   __builtin_amdgcn_sched_barrier(0);
   int buf = 0;
   bool stores = false;  // whether some may be behind the loads that are out
@@ -348,9 +390,19 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
       for (; turn < until; ++turn) {
         phase(first, first, a0, b0, [&](int q) {
           if (q == 0) aim(buf);
-          read_b(b1, HB, q);
+          if constexpr (F32) {
+            hold_a(held[1], HA, q);
+            widen_b(b1, held[0], HB, q);
+          } else {
+            read_b(b1, HB, q);
+          }
         });
-        phase(first, second, a0, b1, [&](int q) { read_a(a1, HA, q); });
+        phase(first, second, a0, b1, [&](int q) {
+          if constexpr (F32)
+            widen_a(a1, held[1], HA, q);
+          else
+            read_a(a1, HA, q);
+        });
         other_buffer();
         // the next step has landed: what is still out are the loads of those behind it
         if (T::ST > 2 && !stores)
@@ -362,20 +414,32 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
         auto loads_at = [&](int q) {
 #pragma unroll
           for (int e = 0; e < kLoads; ++e)
-            if (e * 2 * kMma / kLoads == q) load(e);
+            if (e * 2 * kSlots / kLoads == q) load(e);
         };
         if (++buf == T::ST) buf = 0;
         next_pick();
         phase(second, first, a1, b0, [&](int q) {
           if (q == 0) read_scales();
-          read_a(a0, 0, q);
+          if constexpr (F32) {
+            hold_a(held[0], 0, q);
+            hold_b(held[1], 0, q - kHeld);
+            const int w = 2 * (q - kSlots / 2);
+            widen_a(a0, held[0], 0, w), widen_a(a0, held[0], 0, w < 0 ? -1 : w + 1);
+          } else {
+            read_a(a0, 0, q);
+          }
           loads_at(q);
         });
         phase(second, second, a1, b1, [&](int q) {
-          read_b(b0, 0, q);
-          loads_at(kMma + q);
+          if constexpr (F32) {
+            hold_b(held[0], HB, q);
+            widen_b(b0, held[1], 0, q);
+          } else {
+            read_b(b0, 0, q);
+          }
+          loads_at(kSlots + q);
         });
-        use_scales();
+        if constexpr (!F32) use_scales();
       }
     }
 
@@ -383,23 +447,59 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void product_kernel(Products all) 
     char* out = reinterpret_cast<char*>(address(c[0], c[1]));
     const int rows = c[3] & 1023, cols = c[3] >> 10 & 1023;
     const int64_t ldc = all.p[c[3] >> 22].ldc;
-    // (not to be worked out ahead of the loop: registers are for its operands)
-    int row0 = wm * T::FM * 16 + lane_row, col0 = wn * T::FN * 16 + 16 * q4;
-    asm volatile("" : "+v"(row0), "+v"(col0));
+    if constexpr (F32) {
+      // By way of LDS, so that 16 lanes write a row's 256 bytes at once: four pieces of
+      // 16 bytes out of every 64, as they lie in the accumulators, are four requests
+      // to the L2 (3000 x 128 x 2688: 12.4 us, without 17.5). 32 bytes of bf16 are not
+      // worth the way.
+      int from = lane >> 4, col0 = wn * T::FN * 16 + (lane & 15) * 4;
+      asm volatile("" : "+v"(from), "+v"(col0));
+      char* mine = turned + wave * kTurned;
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) {
-      const int row = row0 + 64 * (i >> 2) + 4 * (i & 3);
-      if (row >= rows) continue;
+      for (int i = 0; i < T::FM; ++i) {
+        const int row0 = wm * T::FM * 16 + 64 * (i >> 2) + 4 * (i & 3);
+        if (row0 >= rows) continue;
 #pragma unroll
-      for (int J = 0; J < T::FN / 4; ++J) {
-        const int col = col0 + 64 * J;
+        for (int J = 0; J < T::FN / 4; ++J) {
+          const int col = col0 + 64 * J, n = min(4, cols - col);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
+          for (int part = 0; part < 2; ++part) {  // eight of the operand's rows
+            if (r16 >> 3 == part) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = acc[i][4 * J + 2 * h + q / 4][q % 4];
-          const int n = min(8, cols - col - 8 * h);
-          if (n > 0) store8(out, row * ldc + col + 8 * h, n, F32, v);
+              for (int h = 0; h < 4; ++h) *reinterpret_cast<floatx4*>(mine + (r16 & 7) * kTurnedPitch + q4 * 64 + 16 * h) = acc[i][4 * J + h];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r = 8 * part + 4 * k + from, row = row0 + 16 * (r >> 2) + (r & 3);
+              const floatx4 v = *reinterpret_cast<const floatx4*>(mine + (4 * k + from) * kTurnedPitch + (lane & 15) * 16);
+              if (row < rows && n > 0) store4(out, row * ldc + col, n, v);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+          }
+        }
+      }
+    } else {
+      // (not to be worked out ahead of the loop: registers are for its operands)
+      int row0 = wm * T::FM * 16 + lane_row, col0 = wn * T::FN * 16 + 16 * q4;
+      asm volatile("" : "+v"(row0), "+v"(col0));
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i) {
+        const int row = row0 + 64 * (i >> 2) + 4 * (i & 3);
+        if (row >= rows) continue;
+#pragma unroll
+        for (int J = 0; J < T::FN / 4; ++J) {
+          const int col = col0 + 64 * J;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = acc[i][4 * J + 2 * h + q / 4][q % 4];
+            const int n = min(8, cols - col - 8 * h);
+            if (n > 0) store8(out, row * ldc + col + 8 * h, n, false, v);
+          }
         }
       }
     }

@@ -6,6 +6,10 @@
 // go by token: a token's row is read once for all its slots, and since a slot
 // that is left out has a row too, behind the experts', every row is written by
 // exactly one slot and none needs clearing first.
+//
+// Memory bounds the copies, a few launches' length the sort: 16384 tokens x 8 x 2048
+// bf16 sort 9 us, dispatch 120 (604 MB, 5.0 TB/s), combine 117 (5.2 TB/s), its
+// gradient 233 (1.14 GB, 4.9 TB/s); of a single token every kernel takes 3 to 4.
 #include "experts_kernels.h"
 #include "layer_device.h"
 
