@@ -168,11 +168,11 @@ int64_t row_blocks(const shampoo_product8_t* a) {
 // block takes a 256 tile alone on its CU 1.5, each of two 128 tiles on one 1.0; a tile
 // costs 2 besides, the launch 5. 256 tiles go in whole rounds over the CUs, while
 // 128 tiles that are left alone on a CU go faster. Of an expert's rows the last tile
-// is half empty in the mean. Measured, 256 and 128, us: y of 8192 x 2048 x 8192 118
-// and 145, dx and dW of it 212 and 260; y of 4096 x 8192 x 2048 - and 62, of 16384
-// rows of 64 experts x 2048 x 768 51 and 36, of eight x 2048 x 2048 81 and 74, dx and dW of
-// those 151 and 163. Where 128 tiles are no more than CUs, four steps of each are on
-// their way (dx and dW of 1024 x 768 x 2048: 15 us, with two 18).
+// is half empty in the mean. Measured, 256 and 128, us: y of 8192 x 2048 x 8192 128
+// and 151, dx and dW of it 220 and 281; y of 4096 x 8192 x 2048 83 and 63, of 16384
+// rows of 64 experts x 2048 x 768 51 and 37, of eight x 2048 x 2048 81 and 77, dx and dW of
+// those 157 and 170; of 1024 x 768 x 2048 15 and 9, 25 and 14. Where 128 tiles are no
+// more than CUs, four steps of each are on their way (the last 14, with two 18).
 she::ProductTile choose_tile(const shampoo_product8_t* a, bool backward) {
   const bool dx = !backward || a->dx, dw = backward && a->dw;
   const double experts = a->experts, rows = static_cast<double>(a->rows);
