@@ -335,3 +335,31 @@ def test_there_and_back():
         off = ((got.double().cpu() - want).norm() / want.norm()).item()
         log(f"  whole path, {name}: {off:.4f}")
         assert off <= 2.0 ** -4 / 3 ** 0.5 * 6 ** 0.5, name
+
+
+def test_two_graphs_of_inference():
+    """Gathered rows that nothing is kept of, few and many, in two graphs whose replays take turns with eager calls."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w8 = experts.quantize_weight(torch.randn(8, 256, 384, generator=g, device="cuda").bfloat16())
+    sides = []
+    for tokens in (9, 700):
+        _, dev = make_ids(30, tokens, 4, 8, 0.1)
+        x = torch.randn(tokens, 256, generator=g, device="cuda").bfloat16()
+        weights = torch.rand(tokens, 4, generator=g, device="cuda")
+
+        def run(x=x, dev=dev, weights=weights):
+            plan = experts.sort_tokens(dev, 8)
+            return experts.combine(experts.product8_forward(x, w8, plan, gather=True), plan, weights)
+        run()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            out = run()
+        sides.append((tokens, x, dev, run, graph, out))
+    for turn in range(3):
+        for tokens, x, dev, _, graph, _ in sides:
+            x.copy_(torch.randn(tokens, 256, generator=g, device="cuda").bfloat16())
+            dev.copy_(torch.from_numpy(make_ids(40 + turn, tokens, 4, 8, 0.1)[0]).cuda())
+            graph.replay()
+        for _, _, _, run, _, out in sides:
+            assert torch.equal(out, run()), turn
