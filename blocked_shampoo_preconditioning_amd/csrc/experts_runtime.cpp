@@ -131,10 +131,13 @@ int check_aligned(const char* name, const void* p, int64_t a) {
   return SHAMPOO_OK;
 }
 
+// Matrices one behind the other, or side by side in rows that hold a row of each.
 int check_matrices(const char* name, const void* p, int64_t experts, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int64_t esize) {
   RC(check_array(name, p, rows, cols, ld, esize));
-  if (experts > 1 && (stride < (rows - 1) * ld + cols || stride > kAnyLd))
-    return invalid(std::string(name) + ": matrices overlap, or lie over 2^40 elements apart");
+  if (experts == 1) return SHAMPOO_OK;
+  const bool behind = stride >= (rows - 1) * ld + cols && stride <= kAnyLd;
+  const bool beside = stride >= cols && stride <= ld && (experts - 1) * stride + cols <= ld;
+  if (!behind && !beside) return invalid(std::string(name) + ": matrices overlap, or lie over 2^40 elements apart");
   return SHAMPOO_OK;
 }
 

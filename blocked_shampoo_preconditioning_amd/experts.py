@@ -225,7 +225,8 @@ def _weight_shapes(lead, n_in, n_out):
 
 
 def quantize_weight(w, backward=False):
-    """`Weight8` of w [in, out], or [n_experts, in, out] (contiguous rows; rows and matrices any distance apart):
+    """`Weight8` of w [in, out], or [n_experts, in, out] (contiguous rows, any distance apart; matrices one behind the
+    other, or side by side as in a transposed view of [in, n_experts, out], any distance apart):
     every block of 128 x 128 over the smallest power of two that brings it to 448 at most, rounded to e4m3.
     backward: also as dx needs it."""
     if not isinstance(w, torch.Tensor) or not w.is_cuda:

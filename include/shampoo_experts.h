@@ -92,7 +92,10 @@ typedef struct {
   int64_t in, out;    /* 1 .. 2^21                                        */
   int32_t experts;    /* matrices, 1 .. 1024                              */
   int32_t dtype;      /* shampoo_dtype_t of w                             */
-  const void* w;      /* experts x in x out, rows ld_w, matrices stride_w elements apart */
+  /* experts x in x out, rows ld_w, matrices stride_w elements apart: one behind the
+     other (stride_w >= (in - 1) * ld_w + out) or side by side (stride_w >= out,
+     (experts - 1) * stride_w + out <= ld_w). stride_w is read where experts > 1 */
+  const void* w;
   int64_t ld_w, stride_w;
   /* Results. values: out rows of in values rounded up to a multiple of 128, 0
      behind in, 16-byte aligned; scales (exponent + 127, 1 byte) of the blocks:
@@ -130,7 +133,7 @@ typedef struct {
   int64_t ld_dy;
   void* dx;
   int64_t ld_dx;
-  void* dw; /* experts x in x out */
+  void* dw; /* experts x in x out, apart as shampoo_weight8_t's w */
   int64_t ld_dw, stride_dw;
 } shampoo_product8_t;
 
