@@ -77,8 +77,8 @@ struct ProductArgs {
   void* c;
   int64_t ldc, c_stride;
 };
-// Rows and columns of a result tile. kProduct128Deep: one workgroup a CU with four
-// steps' operands in LDS, for few tiles.
+// Rows and columns of a result tile; fp32 results have kProduct128 alone.
+// kProduct128Deep: one workgroup a CU with four steps' operands in LDS, for few tiles.
 enum ProductTile { kProduct256, kProduct128, kProduct128Deep };
 constexpr int product_tile(ProductTile t) { return t == kProduct256 ? 256 : 128; }
 // One or two products in one launch, of one type. Their work, a record for each

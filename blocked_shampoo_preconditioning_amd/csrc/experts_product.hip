@@ -521,13 +521,14 @@ void start(const Products& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_products(const Products& a, hipStream_t s) {
-  const bool deep = a.tile == kProduct128Deep;
   if (a.f32)
-    deep ? start<Tile<4, 4, 2, 2, 4, true, 1>>(a, s) : start<Tile<4, 4, 2, 2, 2, true, 2>>(a, s);
+    start<Tile<4, 4, 2, 2, 2, true, 2>>(a, s);
   else if (a.tile == kProduct256)
     start<Tile<8, 8, 2, 2, 2, false, 1>>(a, s);
+  else if (a.tile == kProduct128Deep)
+    start<Tile<4, 4, 2, 2, 4, false, 1>>(a, s);
   else
-    deep ? start<Tile<4, 4, 2, 2, 4, false, 1>>(a, s) : start<Tile<4, 4, 2, 2, 2, false, 2>>(a, s);
+    start<Tile<4, 4, 2, 2, 2, false, 2>>(a, s);
   return hipGetLastError();
 }
 

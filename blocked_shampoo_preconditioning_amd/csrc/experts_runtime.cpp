@@ -171,11 +171,16 @@ int64_t row_blocks(const shampoo_product8_t* a) {
 // block takes a 256 tile alone on its CU 1.5, each of two 128 tiles on one 1.0; a tile
 // costs 2 besides, the launch 5. 256 tiles go in whole rounds over the CUs, while
 // 128 tiles that are left alone on a CU go faster. Of an expert's rows the last tile
-// is half empty in the mean. Measured, 256 and 128, us: y of 8192 x 2048 x 8192 128
-// and 151, dx and dW of it 220 and 281; y of 4096 x 8192 x 2048 83 and 63, of 16384
-// rows of 64 experts x 2048 x 768 51 and 37, of eight x 2048 x 2048 81 and 77, dx and dW of
-// those 157 and 170; of 1024 x 768 x 2048 15 and 9, 25 and 14. Where 128 tiles are no
-// more than CUs, four steps of each are on their way (the last 14, with two 18).
+// is half empty in the mean. Measured, both sides in turn on one card, median launch, 256
+// and 128, us: y of 8192 x 2048 x 8192 127 and 145, dx and dW of it 219 and 264; of
+// 4096 x 8192 x 2048 84 and 64, 118 and 143; of 16384 rows of 64 experts x 2048 x 768
+// 63 and 41, 133 and 142, of eight x 2048 x 2048 81 and 76, 152 and 164; of 1024 x 768 x
+// 2048 15 and 9, 25 and 14.
+// Where 128 tiles of bf16 are no more than CUs, four steps of each are on their way: for
+// long sums (four and two, y of 512 x 8192 x 512 34 and 41, of 256 x 2048 x 8192 14.5 and
+// 17.6; dx and dW of 1024 x 768 x 2048 13.6 and 14.2); short ones lose up to 0.7 (y of
+// 1024 x 512 x 1024 7.3 and 6.6). fp32 has no such tile, it was slower for long sums too
+// (512 x 8192 x 512 62 and 54, 1024 x 768 x 2048 13.9 and 12.4).
 she::ProductTile choose_tile(const shampoo_product8_t* a, bool backward) {
   const bool dx = !backward || a->dx, dw = backward && a->dw;
   const double experts = a->experts, rows = static_cast<double>(a->rows);
@@ -194,7 +199,7 @@ she::ProductTile choose_tile(const shampoo_product8_t* a, bool backward) {
   double large, small;
   const double us_large = estimate(256, 1.5, 256, large), us_small = estimate(128, 1.0, 512, small);
   if (a->dtype != SHAMPOO_F32 && us_large < us_small) return she::kProduct256;
-  return small <= 256 ? she::kProduct128Deep : she::kProduct128;
+  return a->dtype != SHAMPOO_F32 && small <= 256 ? she::kProduct128Deep : she::kProduct128;
 }
 
 // Quantized operands by rows and by columns in the workspace, and the products of a
