@@ -13,12 +13,14 @@
 // fp32 results: those come from the bf16 instruction with both operands widened,
 // scales included, which is exact, at a quarter of the rate. There 64 instructions of
 // a step come with 128 that widen, two behind each; bytes are read a phase before
-// (1536 x 4096 x 2688: 41 us, widened as they are read 47).
+// (1536 x 4096 x 2688: 38 us; with four steps in LDS 41, and 47 with bytes widened as
+// they are read).
 //
-// What bounds it: large bf16 products the power limit, at the rate of the library's
-// 8-bit product without blocks' scales (y of 8192 x 2048 x 8192 112 us, 2.4 PFLOP/s,
-// the library 107; of 4096 x 8192 x 2048 62, the library 65; dx and dW of the former
-// 203, 2.7 PFLOP/s). Where each CU has one 128 tile, the L2s: 33 KB a step and CU
+// What bounds it: large bf16 products the power limit, near the rate of the library's
+// 8-bit product without blocks' scales (in turn on one card, median launch: y of 8192 x
+// 2048 x 8192 132 us, 2.1 PFLOP/s, the library 125; of 4096 x 8192 x 2048 67, the library
+// 72). Under that limit launches of the former go from 116 us to 152; within a training step
+// it takes 123, and its dx and dW 213 (2.6 PFLOP/s). Where each CU has one 128 tile, the L2s: 33 KB a step and CU
 // in 0.53 us are 15 TB/s. fp32: the issue of one wave's instructions, a step of one
 // tile 1.0 us alone on a CU, 0.75 with two, 0.45 were it the matrix cores.
 //

@@ -11,7 +11,7 @@
 // the values by rows, by columns or both. What comes by columns is transposed
 // through LDS. Memory bounds it: 2 or 4 bytes in, 1 or 2 out an element. For that the
 // maxima are taken of two bf16 magnitudes a word, and the conversion divides.
-// 8192 x 8192 bf16 by rows and columns: 55 us, 4.9 TB/s (268 MB); 8192 x 2048 17.5;
+// 8192 x 8192 bf16 by rows and columns: 56 us, 4.8 TB/s (268 MB); 8192 x 2048 18;
 // a weight of 2048 x 8192 both ways 16; five of 1001 x 2730 fp32 16, 5.1 TB/s.
 #include "experts_device.h"
 

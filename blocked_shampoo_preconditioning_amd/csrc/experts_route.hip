@@ -8,8 +8,9 @@
 // exactly one slot and none needs clearing first.
 //
 // Memory bounds the copies, a few launches' length the sort: 16384 tokens x 8 x 2048
-// bf16 sort 9 us, dispatch 120 (604 MB, 5.0 TB/s), combine 117 (5.2 TB/s), its
-// gradient 233 (1.14 GB, 4.9 TB/s); of a single token every kernel takes 3 to 4.
+// bf16 sort 4.8 and 7.0 us, dispatch 117 (604 MB, 5.2 TB/s), combine 117 to 122 (5.0 to
+// 5.2 TB/s), its gradient 233 (1.14 GB, 4.9 TB/s); of a single token every kernel takes
+// 2.5 to 3.3.
 #include "experts_kernels.h"
 #include "layer_device.h"
 
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 }
 
 // Sort, second launch, or the only one where one workgroup does all: places.
-// 131072 slots of 64 experts: 64 workgroups; one token: what a launch costs.
+// 131072 slots of 64 experts: 128 workgroups; one token: what a launch costs.
 template <int KEEP>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ uint32_t count[kSortWaves * (kMaxExperts + 1)];
@@ -453,7 +454,9 @@ hipError_t by_columns(const RouteArgs& a, F&& f) {
 }  // namespace
 
 void sort_plan(int64_t total, uint32_t& blocks, uint32_t& per_block) {
-  // One workgroup up to 4096 slots (16384 of eight experts 22 us, two launches 10);
+  // One workgroup up to 4096 slots (one launch and two, us: 2048 slots of 2 to 256
+  // experts 4.8 to 5.5 and 6.5 to 7.3, 4096 6.2 to 7.2 and 6.6 to 7.5, 8192 11 to 14 and
+  // 6.9 to 8.2; of 1024 experts 4096 8.6 and 10, 8192 16 and 12);
   // then at least 1024 of them a workgroup, and at most 256 workgroups, whose counts
   // each of them sums.
   const int64_t each = total <= 4096 ? total : (total + 255) / 256;
