@@ -234,3 +234,65 @@ def test_sort_of_a_million_slots(tokens, slots, n_experts):
     """Over 4096 slots a workgroup: ids are read twice."""
     ids, dev = make_ids(slots, tokens, slots, n_experts, 0.02, torch.int32)
     check_plan(experts.sort_tokens(dev, n_experts), ids, n_experts)
+
+
+# -------------------------------------------------------------- largest sizes
+def signs(g, *shape, dtype=torch.bfloat16):
+    return torch.randint(-1, 2, shape, generator=g, device="cuda", dtype=torch.int8).to(dtype)
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(3, 5, 1 << 21), (3, 1 << 21, 5), (90, 5, 1 << 21), (90, 1 << 21, 5)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_widest_matrices(rows, n_in, n_out, dtype):
+    """Operands of -1, 0 and 1: every sum is a whole number under 2^24, so results are those numbers, rounded once."""
+    log(f"widest {rows} x {n_in} x {n_out} {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    dt = DT[dtype]
+    x, w, dy = signs(g, rows, n_in, dtype=dt), signs(g, n_in, n_out, dtype=dt), signs(g, rows, n_out, dtype=dt)
+    w8 = experts.quantize_weight(w, backward=True)
+    y, saved = experts.product8_forward(x, w8, save=True)
+    want_y, want_dx = x.double() @ w.double(), dy.double() @ w.double().t()
+    assert torch.equal(y, want_y.to(dt)) and torch.equal(experts.product8_forward(x, w8), y)
+    dx, dw = experts.product8_backward(dy, w8, saved)
+    assert torch.equal(dx, want_dx.to(dt)) and torch.equal(dw, (x.double().t() @ dy.double()).to(dt))
+    assert torch.equal(experts.product8_backward(dy, w8, None, need_dw=False)[0], dx)
+
+
+def test_most_rows_that_are_saved():
+    """2^23 - 2^18 rows, of one matrix and of three experts, with sums over all of them; and one row more is refused."""
+    rows, n_in, n_out = 2 ** 23 - 2 ** 18, 300, 260
+    log(f"most rows {rows} x {n_in} x {n_out}")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, dy = signs(g, rows, n_in), signs(g, rows, n_out)
+    for n_experts in (0, 3):
+        w = signs(g, *((n_experts,) if n_experts else ()), n_in, n_out)
+        plan, bounds = None, [0, rows]
+        if n_experts:
+            ids = torch.randint(0, n_experts, (rows, 1), generator=g, device="cuda", dtype=torch.int32)
+            ids[:2 ** 22] = 1
+            plan = experts.sort_tokens(ids, n_experts)
+            bounds = plan.offsets.tolist()
+        w8 = experts.quantize_weight(w, backward=True)
+        y, saved = experts.product8_forward(x, w8, plan, save=True)
+        dx, dw = experts.product8_backward(dy, w8, saved, plan)
+        for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+            we = w[e].float() if n_experts else w.float()
+            want = torch.zeros(n_in, n_out, dtype=torch.float64, device="cuda")
+            for a in range(lo, hi, 1 << 20):
+                part = slice(a, min(hi, a + (1 << 20)))
+                want += (x[part].float().t() @ dy[part].float()).double()
+                assert torch.equal(y[part], (x[part].float() @ we).bfloat16()) and torch.equal(dx[part], (dy[part].float() @ we.t()).bfloat16())
+            assert torch.equal(dw[e] if n_experts else dw, want.bfloat16())
+        del y, dx, saved
+    with pytest.raises(Exception, match="2\\^23 - 2\\^18"):
+        experts.product8_forward(torch.zeros(rows + 1, 8, device="cuda").bfloat16(), experts.quantize_weight(torch.zeros(8, 8, device="cuda").bfloat16()), save=True)
+
+
+def test_more_rows_than_are_saved():
+    rows, n_in, n_out = 20_000_003, 40, 24
+    log(f"more rows {rows} x {n_in} x {n_out}")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, w = signs(g, rows, n_in), signs(g, n_in, n_out)
+    y = experts.product8_forward(x, experts.quantize_weight(w))
+    for a in range(0, rows, 1 << 22):
+        assert torch.equal(y[a:a + (1 << 22)], (x[a:a + (1 << 22)].float() @ w.float()).bfloat16())
