@@ -20,9 +20,10 @@
 // 8-bit product without blocks' scales (in turn on one card, median launch: y of 8192 x
 // 2048 x 8192 132 us, 2.1 PFLOP/s, the library 125; of 4096 x 8192 x 2048 67, the library
 // 72). Under that limit launches of the former go from 116 us to 152; within a training step
-// it takes 123, and its dx and dW 213 (2.6 PFLOP/s). Where each CU has one 128 tile, the L2s: 33 KB a step and CU
-// in 0.53 us are 15 TB/s. fp32: the issue of one wave's instructions, a step of one
-// tile 1.0 us alone on a CU, 0.75 with two, 0.45 were it the matrix cores.
+// it takes 123, and its dx and dW 213 (2.6 PFLOP/s). Where each CU has one 128 tile, the
+// L2s: 33 KB a step and CU in 0.53 us are 15 TB/s. fp32: the issue of one wave's
+// instructions, a step of one tile 1.0 us alone on a CU, 0.75 with two, 0.45 were it the
+// matrix cores.
 //
 // Operands go from HBM to LDS by direct loads of 16 bytes a lane, a K block a step;
 // the scales of a step go the same way, 256 bytes an operand. A step's products are
